@@ -153,6 +153,141 @@ int dsa_quantize_fp8(const float *x, int64_t rows, int64_t cols, int scale_mode,
                      void *codes, float *scale, dsa_stream_t stream);
 
 /*
+ * dsa_rmsnorm: residual addition, root-mean-square norm and FP8 output, the
+ * step in front of a layer's projections (the pages name the FP8 arithmetic it
+ * feeds: "AMD Instinct MI355X GPUs Power DeepSeek-V3.2-Exp", section "DeepSeek
+ * Sparse Attention (DSA)", item 1; the norm itself has no counterpart there).
+ * For each row r, in fp32,
+ *     h = x + residual (x when residual is NULL)
+ *     y = h / sqrt(mean_c(h^2) + eps) * weight
+ * residual_out = h and out = y, each rounded once to the tensors' type; codes
+ * and scale are the FP8 form of the fp32 y: E4M3 nearest to y / scale (fp32
+ * division, ties to even, saturated), with, per row (block = 0) or per 128
+ * consecutive columns (block = 128; the last block may be short), scale =
+ * amax / 448 or the power of two of dsa_quantize_fp8's scale_mode.
+ *
+ *   x, residual, residual_out, out: [rows, cols] of `dtype` (DSA_BF16 or
+ *             DSA_FP32), rows ldx, ldr, ldh, ldo elements apart (>= cols);
+ *   weight    [cols] of `weight_dtype`
+ *   codes     [rows, cols] uint8, contiguous;  scale [rows, n] fp32 with n = 1
+ *             (block = 0) or ceil(cols / 128)
+ * residual, residual_out, out and codes (with scale) may each be NULL, the last
+ * three not all.  residual_out may be residual or x itself, and out may be x.
+ * 1 <= cols <= 16384; rows = 0 is a no-op; eps >= 0.  Inputs must be finite.  Any
+ * alignment works; 16-byte aligned rows, with cols a multiple of 8, take the
+ * vector path.
+ */
+#define DSA_BF16 0
+#define DSA_FP32 1
+int dsa_rmsnorm(const void *x, int64_t ldx, const void *residual, int64_t ldr, const void *weight,
+                int64_t rows, int cols, int dtype, int weight_dtype, float eps,
+                void *residual_out, int64_t ldh, void *out, int64_t ldo,
+                void *codes, float *scale, int block, int scale_mode, dsa_stream_t stream);
+
+/*
+ * dsa_rmsnorm_backward: gradients of dsa_rmsnorm (the FP8 output passes
+ * gradients straight through, as in dsa_indexer_warmup; no counterpart on the
+ * pages).  With h the saved residual_out (x where there was no residual),
+ * xhat = h / sqrt(mean(h^2) + eps) and g = dy * weight, per row
+ *     dx = (g - xhat mean_c(g xhat)) / sqrt(mean(h^2) + eps) + dres
+ *     dweight[c] = sum over rows of dy xhat
+ * dx is the gradient of x and of the residual alike; dres is the gradient that
+ * reaches residual_out from elsewhere (NULL: none).
+ *
+ *   dy, h, dres, dx: [rows, cols] of `dtype`, contiguous;  weight [cols] of
+ *   `weight_dtype`;  dweight [cols] fp32, overwritten (zeros when rows = 0)
+ *   workspace: dsa_rmsnorm_backward_workspace_size(rows, cols) bytes, 16-byte
+ *   aligned, owned by the caller, used only while the call's kernels run
+ *   (calls sharing one must be ordered).
+ * dx may be dy, dres or h itself.  1 <= cols <= 16384.  All sums are fp32 in an order fixed
+ * by the sizes: results repeat bit for bit on one kind of device.
+ */
+int dsa_rmsnorm_backward(const void *dy, const void *h, const void *weight, const void *dres,
+                         int64_t rows, int cols, int dtype, int weight_dtype, float eps,
+                         void *dx, float *dweight, void *workspace, size_t workspace_bytes, dsa_stream_t stream);
+
+/* Bytes of workspace dsa_rmsnorm_backward needs on the current device (0 on bad input). */
+size_t dsa_rmsnorm_backward_workspace_size(int64_t rows, int cols);
+
+/*
+ * dsa_cache_append: writes new tokens into the paged caches that the paged
+ * entry points read, applying the position rotation on the way ("DeepSeek-
+ * V3.2-Exp: Boosting Long-Context Efficiency with DeepSeek Sparse Attention",
+ * section "Key claims": the indexer's RoPE is non-interleaved, the MLA's is
+ * interleaved).  Token t goes to logical position p = pos[t] of the sequence
+ * whose pages block_table row seq[t] lists (row t when seq is NULL), i.e. to
+ * slot p % page_size of pool page block_table[seq[t]*max_pages + p/page_size]:
+ *   kv_pool  columns [0, 512): kv[t, 0:512], or its RMS norm
+ *            c / sqrt(mean(c^2) + eps) * kv_weight when kv_weight is given;
+ *            columns [512, 576): kv[t, 512:576] with the pairs (2i, 2i + 1)
+ *            rotated by p * inv_freq[i]; rounded once to bf16
+ *   k8_pool, ks_pool: kI[t] with the pairs (i, i + 32) of its first 64 columns
+ *            rotated by p * inv_freq[i], as E4M3 codes and one scale per token
+ *            (scale_mode as in dsa_quantize_fp8, from the unrounded values)
+ * A rotation takes (a, b) to (a cos - b sin, a sin + b cos).
+ *
+ *   pos [T] int32;  seq [T] int32 or NULL;  block_table [num_seqs, max_pages]
+ *   inv_freq [32] fp64, radians per position
+ *   kv  [T, 576] bf16, rows ld_kv elements apart;  kv_weight [512] bf16/fp32
+ *       (`weight_dtype`) or NULL;  kv_pool [num_pages, page_size, 576] bf16
+ *   kI  [T, 128] bf16/fp32 (`k_dtype`), rows ld_kI elements apart;
+ *       k8_pool [num_pages, page_size, 128], ks_pool [num_pages, page_size]
+ * kv (with kv_pool) or kI (with k8_pool and ks_pool) may be NULL: that cache is
+ * left alone.  page_size in {32, 64, 128}.  T = 0 is a no-op.  kv, kv_weight,
+ * kI, the pools' bases and the row strides in bytes are multiples of 16.
+ * A token with pos < 0 is padding: nothing is written for it.  A position past
+ * the table's last page or a seq outside [0, num_seqs) is skipped and flagged
+ * DSA_DEV_BAD_POSITION, a page id outside [0, num_pages) skipped and flagged
+ * DSA_DEV_BAD_PAGE.  Slots no token names keep their bytes.  Two tokens of one
+ * call must not name the same slot (that slot's bytes are then unspecified).
+ */
+int dsa_cache_append(const int32_t *pos, const int32_t *seq, int T,
+                     const int32_t *block_table, int num_seqs, int max_pages, int num_pages, int page_size,
+                     const double *inv_freq,
+                     const void *kv, int64_t ld_kv, const void *kv_weight, int weight_dtype, float eps, void *kv_pool,
+                     const void *kI, int64_t ld_kI, int k_dtype, int scale_mode, void *k8_pool, float *ks_pool,
+                     dsa_stream_t stream);
+
+/*
+ * dsa_rope_queries: the queries' side of dsa_cache_append (same rotations, same
+ * page and section).  For each token t at position p = pos[t]:
+ *   q[t, h, 512:576] = q_rope[t, h, :] with the pairs (2i, 2i + 1) rotated by
+ *            p * inv_freq[i], rounded once to bf16 (the other 512 columns are
+ *            left alone)
+ *   q8, q_scale: the index queries qI[t] with the pairs (i, i + 32) of each
+ *            head's first 64 columns rotated, as E4M3 codes with one scale per
+ *            token over its H_I * 128 values (scale_mode as in dsa_quantize_fp8)
+ *
+ *   pos [T] int32;  inv_freq [32] fp64, radians per position
+ *   q_rope [T, H, 64] bf16, strides st_t and st_h in elements;  q [T, H, 576] bf16
+ *   qI [T, H_I, 128] bf16/fp32 (`i_dtype`);  q8 [T, H_I, 128];  q_scale [T] fp32
+ * q_rope (with q) or qI (with q8 and q_scale) may be NULL.  1 <= H <= 128 and
+ * 1 <= H_I <= 64 where used; T = 0 is a no-op.  q_rope, q, qI and q8 are 16-byte
+ * aligned, st_t and st_h multiples of 8.  q_rope may be q[:, :, 512:576] itself (the
+ * rotation is then in place) and must not overlap q otherwise.  A negative
+ * position is padding: that token's outputs are left alone.
+ */
+int dsa_rope_queries(const int32_t *pos, const double *inv_freq, int T,
+                     const void *q_rope, int64_t st_t, int64_t st_h, int H, void *q,
+                     const void *qI, int H_I, int i_dtype, int scale_mode, void *q8, float *q_scale,
+                     dsa_stream_t stream);
+
+/*
+ * dsa_index_rope_backward: gradient of the index rotation, for training the
+ * indexer's projections from dsa_indexer_warmup's dq (H_I heads) and dk (H_I =
+ * 1), which are gradients of the rotated vectors (same page and section as
+ * dsa_cache_append; the FP8 quantiser passes gradients straight through):
+ *     dx[t, j, :] = g[t, j, :] with the pairs (i, i + 32) of the first 64
+ *                   columns rotated by -pos[t] * inv_freq[i]
+ *   g [T, H_I, 128] fp32;  pos [T] int32;  inv_freq [32] fp64;
+ *   dx [T, H_I, 128] bf16/fp32 (`dtype`); fp32 dx may be g itself.
+ * g and dx 16-byte aligned; 1 <= H_I <= 64; T = 0 is a no-op.  For pos < 0, dx
+ * is zero (such a token was never rotated or used).
+ */
+int dsa_index_rope_backward(const float *g, const int32_t *pos, const double *inv_freq, int T, int H_I,
+                            void *dx, int dtype, dsa_stream_t stream);
+
+/*
  * dsa_topk: fine-grained token selection (stage 2).
  *
  * For each row t with n = valid_len[t] candidates logits[t*ld + s], s in [0, n):
@@ -431,6 +566,43 @@ int dsa_sparse_mla_decode_paged_noalloc(const void *q, const void *kv_pool, int 
  * 2 * clusters * H * 513 * 4, with clusters = min(SM pairs, B * ceil(k / 64)).
  * 0 on bad input. */
 size_t dsa_sparse_mla_decode_workspace_size(int B, int H, int k);
+
+/*
+ * dsa_mla_decode_paged: dense MLA of single tokens over the paged latent cache,
+ * for layers, steps and contexts that select nothing (the attention that DSA's
+ * selection narrows and its warm-up trains against: "DeepSeek-V3.2-Exp:
+ * Boosting Long-Context Efficiency with DeepSeek Sparse Attention", section
+ * "Method").  Row b's query attends over every position s < ctx_len[b] of the
+ * sequence whose pages block_table row b lists:
+ *     S_s = sm_scale * sum_{d<576} q[b,h,d] * kv[s,d]
+ *     out[b,h,v] = sum_s softmax(S)_s * kv[s,v]  (v < 512),  lse = ln sum_s exp(S_s)
+ * Rows are independent (one new token per sequence, several positions of one
+ * sequence, or a ragged batch, as in dsa_sparse_mla_decode_paged).  A row with
+ * ctx_len <= 0, or no valid page, gets out = 0 and lse = -inf.  A ctx_len past
+ * the block table's last page is clamped to it and flagged
+ * DSA_DEV_BAD_POSITION; keys on a page id outside [0, num_pages) are skipped and flagged
+ * DSA_DEV_BAD_PAGE.  Slots past ctx_len are never used, whatever they hold.
+ *
+ * Precision: scores and softmax in fp32; out rounded once to bf16.  The keys of
+ * a row are split over the SMs and joined by their LSEs in a fixed order, so
+ * results repeat bit for bit on one kind of device.
+ *
+ *   q [B, H, 576] bf16;  kv_pool [num_pages, page_size, 576] bf16
+ *   block_table [B, max_pages] int32;  ctx_len [B] int32
+ *   out [B, H, 512] bf16;  lse [B, H] fp32
+ *   workspace: dsa_mla_decode_workspace_size(B, H) bytes, 256-byte aligned,
+ *   owned by the caller, used only while the call's kernels run on `stream`
+ *   (calls sharing one must be ordered).
+ * 1 <= H <= 128; page_size in {32, 64, 128}; 0 <= B <= 65535 (0 is a no-op);
+ * q, kv_pool and out 16-byte aligned.
+ */
+int dsa_mla_decode_paged(const void *q, const void *kv_pool, int num_pages, int page_size,
+                         const int32_t *block_table, int max_pages, const int32_t *ctx_len,
+                         int B, int H, float sm_scale, void *out, float *lse,
+                         void *workspace, size_t workspace_bytes, dsa_stream_t stream);
+
+/* Bytes of workspace dsa_mla_decode_paged needs on the current device (0 on bad input). */
+size_t dsa_mla_decode_workspace_size(int B, int H);
 
 #ifdef __cplusplus
 }

@@ -69,7 +69,18 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.dsa_indexer_warmup_workspace_size.argtypes = [i32, i32, i32, i32]
     lib.dsa_indexer_topk_workspace_size.restype = sz
     lib.dsa_indexer_topk_workspace_size.argtypes = [i32, i32, i32, i32, i32]
-    for name in ("dsa_quantize_fp8", "dsa_indexer_logits", "dsa_topk", "dsa_indexer_topk", "dsa_indexer_warmup",
+    lib.dsa_rmsnorm.argtypes = [P, i64, P, i64, P, i64, i32, i32, i32, f32, P, i64, P, i64, P, P, i32, i32, P]
+    lib.dsa_rmsnorm_backward.argtypes = [P, P, P, P, i64, i32, i32, i32, f32, P, P, P, sz, P]
+    lib.dsa_rmsnorm_backward_workspace_size.restype = sz
+    lib.dsa_rmsnorm_backward_workspace_size.argtypes = [i64, i32]
+    lib.dsa_cache_append.argtypes = [P, P, i32, P, i32, i32, i32, i32, P, P, i64, P, i32, f32, P, P, i64, i32, i32, P, P, P]
+    lib.dsa_rope_queries.argtypes = [P, P, i32, P, i64, i64, i32, P, P, i32, i32, i32, P, P, P]
+    lib.dsa_index_rope_backward.argtypes = [P, P, P, i32, i32, P, i32, P]
+    lib.dsa_mla_decode_paged.argtypes = [P, P, i32, i32, P, i32, P, i32, i32, f32, P, P, P, sz, P]
+    lib.dsa_mla_decode_workspace_size.restype = sz
+    lib.dsa_mla_decode_workspace_size.argtypes = [i32, i32]
+    for name in ("dsa_rmsnorm", "dsa_rmsnorm_backward", "dsa_cache_append", "dsa_rope_queries",
+                 "dsa_index_rope_backward", "dsa_mla_decode_paged", "dsa_quantize_fp8", "dsa_indexer_logits", "dsa_topk", "dsa_indexer_topk", "dsa_indexer_warmup",
                  "dsa_sparse_mla_prefill",
                  "dsa_sparse_mla_decode_paged",
                  "dsa_sparse_mla_decode_paged_noalloc", "dsa_prefill_host", "dsa_prefill_host_trace",
@@ -181,6 +192,189 @@ def dsa_indexer_logits(q8, q_scale, w, k8, k_scale, q_pos, logits, block_table=N
                                   _ptr(block_table), mp, npg, ps, _ptr(q_pos), _ptr(logits), logits.stride(0),
                                   _stream(stream)))
     return logits
+
+
+DSA_BF16 = 0
+DSA_FP32 = 1
+_DTYPE = {torch.bfloat16: DSA_BF16, torch.float32: DSA_FP32}
+
+
+def _arg(t, cur: int, name: str, dtype, shape, rows: bool = False, optional: bool = False):
+    """Address of a CUDA tensor of the current device ``cur``: ``dtype`` (or one of a tuple), ``shape``,
+    contiguous or, with ``rows``, with rows any distance >= their width apart; None where ``optional``."""
+    if t is None and optional:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype and not (type(dtype) is tuple and t.dtype in dtype):
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != cur:
+        raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{cur}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+    if rows:
+        if (shape[1] > 1 and t.stride(1) != 1) or (shape[0] > 1 and t.stride(0) < shape[1]):
+            raise ValueError(f"{name}: rows must be contiguous with a leading dimension >= width")
+    elif not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _ld(t) -> int:
+    """Distance of a 2-D tensor's rows (a single row's stride says nothing)."""
+    return 0 if t is None else max(t.stride(0), t.shape[1]) if t.shape[0] > 1 else t.shape[1]
+
+
+def _workspace(workspace, need: int, cur: int, stream):
+    """(address, bytes, tensor to keep until the launch) of a call's workspace: the caller's, or one from
+    PyTorch's allocator, taken on the stream that the call runs on."""
+    if workspace is None:
+        if not need:
+            return None, 0, None
+        if stream is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=cur)
+        else:
+            with torch.cuda.stream(stream):
+                workspace = torch.empty(need, dtype=torch.uint8, device=cur)
+    elif not workspace.is_cuda or not workspace.is_contiguous() or workspace.get_device() != cur:
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{cur}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+_TYPES = (torch.bfloat16, torch.float32)
+
+
+def dsa_rmsnorm(x, weight, eps: float, out=None, residual=None, residual_out=None, codes=None, scale=None,
+                block: int = 0, scale_mode: int = DSA_SCALE_AMAX, stream=None):
+    """h = x + residual; y = h / sqrt(mean(h^2) + eps) * weight, over the rows of x [rows, cols] (bf16 or fp32).
+
+    residual_out gets h, out gets y (both of x's type); codes uint8 [rows, cols] and scale fp32 [rows] or
+    [rows, n] get y as E4M3 codes with one scale per row (block = 0) or per 128 columns (block = 128,
+    n = ceil(cols / 128)).  weight [cols] is bf16 or fp32.  Rows of x, residual, residual_out and out may be
+    strided.  Returns (residual_out, out, codes, scale) as given."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise TypeError("x must be a 2-D torch.Tensor")
+    cur, shape, t = torch.cuda.current_device(), tuple(x.shape), x.dtype
+    rows, cols = shape
+    n = -(-cols // block) if block else 1
+    a_scale = None
+    if scale is not None:
+        a_scale = _arg(scale, cur, "scale", torch.float32, (rows,) if n == 1 and scale.dim() == 1 else (rows, n))
+    _check(load_library().dsa_rmsnorm(
+        _arg(x, cur, "x", _TYPES, shape, True), _ld(x), _arg(residual, cur, "residual", t, shape, True, True),
+        _ld(residual), _arg(weight, cur, "weight", _TYPES, (cols,)), rows, cols, _DTYPE[t], _DTYPE[weight.dtype], eps,
+        _arg(residual_out, cur, "residual_out", t, shape, True, True), _ld(residual_out),
+        _arg(out, cur, "out", t, shape, True, True), _ld(out), _arg(codes, cur, "codes", torch.uint8, shape, False, True),
+        a_scale, block, scale_mode, _stream(stream)))
+    return residual_out, out, codes, scale
+
+
+def dsa_rmsnorm_backward_workspace_size(rows: int, cols: int) -> int:
+    return int(load_library().dsa_rmsnorm_backward_workspace_size(rows, cols))
+
+
+def dsa_rmsnorm_backward(dy, h, weight, eps: float, dx, dweight, dres=None, workspace=None, stream=None):
+    """Gradients of dsa_rmsnorm: dy, h, dres (or None) and dx [rows, cols] bf16 or fp32, h the saved residual_out
+    (x without a residual); dx is the gradient of x and of the residual; dweight fp32 [cols].  ``workspace``: a
+    CUDA tensor of at least dsa_rmsnorm_backward_workspace_size(rows, cols) bytes; taken from PyTorch when None."""
+    if not isinstance(h, torch.Tensor) or h.dim() != 2:
+        raise TypeError("h must be a 2-D torch.Tensor")
+    cur, shape, t = torch.cuda.current_device(), tuple(h.shape), h.dtype
+    rows, cols = shape
+    lib = load_library()
+    args = (_arg(dy, cur, "dy", t, shape), _arg(h, cur, "h", _TYPES, shape), _arg(weight, cur, "weight", _TYPES, (cols,)),
+            _arg(dres, cur, "dres", t, shape, False, True), rows, cols, _DTYPE[t], _DTYPE[weight.dtype], eps,
+            _arg(dx, cur, "dx", t, shape), _arg(dweight, cur, "dweight", torch.float32, (cols,)))
+    need = 0 if workspace is not None else lib.dsa_rmsnorm_backward_workspace_size(rows, cols)
+    ws, ws_bytes, keep = _workspace(workspace, need, cur, stream)
+    _check(lib.dsa_rmsnorm_backward(*args, ws, ws_bytes, _stream(stream)))
+    return dx, dweight
+
+
+def dsa_cache_append(pos, block_table, inv_freq, kv=None, kv_pool=None, kI=None, k8_pool=None, ks_pool=None, seq=None,
+                     kv_weight=None, eps: float = 1e-6, scale_mode: int = DSA_SCALE_AMAX, stream=None):
+    """Writes T tokens into the paged caches, rotating them on the way.
+
+    pos int32 [T] (negative: padding, nothing written); block_table int32 [num_seqs, max_pages]; seq int32 [T] names
+    each token's block-table row (None: token t has row t); inv_freq fp64 [32] radians per position.  Latent cache:
+    kv bf16 [T, 576] (rows may be strided) into kv_pool bf16 [P, page, 576], columns [0, 512) RMS-normed with
+    kv_weight [512] (bf16 or fp32) when given, columns [512, 576) rotated in pairs (2i, 2i + 1).  Index cache: kI
+    bf16 or fp32 [T, 128] (rows may be strided), pairs (i, i + 32) of its first 64 columns rotated, into k8_pool
+    uint8 [P, page, 128] (E4M3 codes) and ks_pool fp32 [P, page].  Either cache may be left out."""
+    if kv is None and kI is None:
+        raise ValueError("kv or kI is needed")
+    if not isinstance(pos, torch.Tensor) or pos.dim() != 1 or not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise TypeError("pos must be a 1-D and block_table a 2-D torch.Tensor")
+    pool, name = (kv_pool, "kv_pool") if kv is not None else (k8_pool, "k8_pool")
+    if not isinstance(pool, torch.Tensor) or pool.dim() != 3:
+        raise TypeError(f"{name} must be a 3-D torch.Tensor")
+    cur, T, (P, ps) = torch.cuda.current_device(), pos.shape[0], pool.shape[:2]
+    w, k = _TYPES[0] if kv_weight is None else kv_weight.dtype, _TYPES[0] if kI is None else kI.dtype
+    a_kv = a_pool = a_w = a_k = a_k8 = a_ks = None
+    if kv is not None:
+        a_kv, a_pool = _arg(kv, cur, "kv", torch.bfloat16, (T, 576), True), _arg(kv_pool, cur, "kv_pool", torch.bfloat16, (P, ps, 576))
+        a_w = _arg(kv_weight, cur, "kv_weight", _TYPES, (512,), False, True)
+    if kI is not None:
+        a_k, a_k8 = _arg(kI, cur, "kI", _TYPES, (T, 128), True), _arg(k8_pool, cur, "k8_pool", torch.uint8, (P, ps, 128))
+        a_ks = _arg(ks_pool, cur, "ks_pool", torch.float32, (P, ps))
+    _check(load_library().dsa_cache_append(
+        _arg(pos, cur, "pos", torch.int32, (T,)), _arg(seq, cur, "seq", torch.int32, (T,), False, True), T,
+        _arg(block_table, cur, "block_table", torch.int32, tuple(block_table.shape)), block_table.shape[0],
+        block_table.shape[1], P, ps, _arg(inv_freq, cur, "inv_freq", torch.float64, (32,)), a_kv, _ld(kv), a_w, _DTYPE[w],
+        eps, a_pool, a_k, _ld(kI), _DTYPE[k], scale_mode, a_k8, a_ks, _stream(stream)))
+
+
+def dsa_rope_queries(pos, inv_freq, q_rope=None, q=None, qI=None, q8=None, q_scale=None,
+                     scale_mode: int = DSA_SCALE_AMAX, stream=None):
+    """Rotates the queries of T tokens: q_rope bf16 [T, H, 64] (any strides over tokens and heads) into columns
+    [512, 576) of q bf16 [T, H, 576]; the index queries qI bf16 or fp32 [T, H_I, 128] into q8 uint8 (E4M3 codes) and
+    q_scale fp32 [T].  pos int32 [T] (negative: padding, outputs left alone), inv_freq fp64 [32].  Either part may be
+    left out; q_rope may be q[:, :, 512:]."""
+    if not isinstance(pos, torch.Tensor) or pos.dim() != 1:
+        raise TypeError("pos must be a 1-D torch.Tensor")
+    cur, T = torch.cuda.current_device(), pos.shape[0]
+    a_r = a_q = a_i = a_8 = a_s = None
+    st_t = st_h = H = HI = i_type = 0
+    if q_rope is not None:
+        if not isinstance(q_rope, torch.Tensor) or q_rope.dtype != torch.bfloat16 or not q_rope.is_cuda or q_rope.dim() != 3:
+            raise TypeError("q_rope: expected a 3-D CUDA bf16 tensor")
+        H = q_rope.shape[1]
+        if q_rope.get_device() != cur:
+            raise ValueError(f"q_rope is on {q_rope.device}, but the current device is cuda:{cur}")
+        if q_rope.shape[0] != T or q_rope.shape[2] != 64 or q_rope.stride(2) != 1:
+            raise ValueError("q_rope must be [T, H, 64] with contiguous last dimension")
+        a_r, st_t, st_h = q_rope.data_ptr(), q_rope.stride(0) if T > 1 else 0, q_rope.stride(1) if H > 1 else 0
+        a_q = _arg(q, cur, "q", torch.bfloat16, (T, H, 576))
+    if qI is not None:
+        if not isinstance(qI, torch.Tensor) or qI.dim() != 3:
+            raise TypeError("qI must be a 3-D torch.Tensor")
+        HI = qI.shape[1]
+        a_i = _arg(qI, cur, "qI", _TYPES, (T, HI, 128))
+        i_type = _DTYPE[qI.dtype]
+        a_8, a_s = _arg(q8, cur, "q8", torch.uint8, (T, HI, 128)), _arg(q_scale, cur, "q_scale", torch.float32, (T,))
+    if q_rope is None and qI is None:
+        raise ValueError("q_rope or qI is needed")
+    _check(load_library().dsa_rope_queries(
+        _arg(pos, cur, "pos", torch.int32, (T,)), _arg(inv_freq, cur, "inv_freq", torch.float64, (32,)), T, a_r, st_t, st_h,
+        H, a_q, a_i, HI, i_type, scale_mode, a_8, a_s, _stream(stream)))
+
+
+def dsa_index_rope_backward(g, pos, inv_freq, dx, stream=None):
+    """Gradient of the index rotation: g fp32 [T, H_I, 128] (or [T, 128], keys), the gradient of the rotated vectors
+    (dsa_indexer_warmup's dq or dk), turned back by the tokens' angles into dx (bf16 or fp32, g's shape)."""
+    if not isinstance(g, torch.Tensor) or g.dim() not in (2, 3):
+        raise TypeError("g must be a 2-D or 3-D torch.Tensor")
+    cur, shape = torch.cuda.current_device(), tuple(g.shape)
+    if shape[-1] != 128:
+        raise ValueError("g must be [T, H_I, 128] or [T, 128]")
+    T, HI = shape[0], shape[1] if len(shape) == 3 else 1
+    _check(load_library().dsa_index_rope_backward(
+        _arg(g, cur, "g", torch.float32, shape), _arg(pos, cur, "pos", torch.int32, (T,)),
+        _arg(inv_freq, cur, "inv_freq", torch.float64, (32,)), T, HI, _arg(dx, cur, "dx", _TYPES, shape), _DTYPE[dx.dtype],
+        _stream(stream)))
+    return dx
 
 
 def dsa_topk(logits, valid_len, k: int, idx, stream=None):
@@ -353,6 +547,29 @@ def dsa_sparse_mla_decode_paged_noalloc(q, kv_pool, block_table, ctx_len, idx, s
                                                               block_table.shape[1], _ptr(ctx_len), _ptr(idx), B, H,
                                                               k, float(sm_scale), _ptr(out), _ptr(lse),
                                                               _stream(stream)))
+    return out, lse
+
+
+def dsa_mla_decode_workspace_size(B: int, H: int) -> int:
+    return int(load_library().dsa_mla_decode_workspace_size(B, H))
+
+
+def dsa_mla_decode_paged(q, kv_pool, block_table, ctx_len, sm_scale: float, out, lse, workspace=None, stream=None):
+    """Dense paged decode attention over every position below ctx_len: q bf16 [B, H, 576], kv_pool bf16
+    [P, page, 576], block_table int32 [B, max_pages], ctx_len int32 [B] -> out bf16 [B, H, 512], lse fp32 [B, H].
+    ``workspace``: a CUDA tensor of at least dsa_mla_decode_workspace_size(B, H) bytes; taken from PyTorch's
+    allocator when None."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3 or not isinstance(kv_pool, torch.Tensor) or kv_pool.dim() != 3 \
+            or not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise TypeError("q and kv_pool must be 3-D, block_table a 2-D torch.Tensor")
+    cur, (B, H, _), (P, ps, _), mp = torch.cuda.current_device(), q.shape, kv_pool.shape, block_table.shape[1]
+    lib = load_library()
+    args = (_arg(q, cur, "q", torch.bfloat16, (B, H, 576)), _arg(kv_pool, cur, "kv_pool", torch.bfloat16, (P, ps, 576)), P, ps,
+            _arg(block_table, cur, "block_table", torch.int32, (B, mp)), mp, _arg(ctx_len, cur, "ctx_len", torch.int32, (B,)), B,
+            H, sm_scale, _arg(out, cur, "out", torch.bfloat16, (B, H, 512)), _arg(lse, cur, "lse", torch.float32, (B, H)))
+    need = 0 if workspace is not None else lib.dsa_mla_decode_workspace_size(B, H)
+    ws, ws_bytes, keep = _workspace(workspace, need, cur, stream)
+    _check(lib.dsa_mla_decode_paged(*args, ws, ws_bytes, _stream(stream)))
     return out, lse
 
 

@@ -276,6 +276,225 @@ int dsa_quantize_fp8(const float *x, int64_t rows, int64_t cols, int scale_mode,
     return rc == DSA_OK ? ok() : rc;
 }
 
+namespace {
+
+constexpr int kNormMaxCols = 16384;
+
+bool bad_dtype(int t) { return t != DSA_BF16 && t != DSA_FP32; }
+bool bad_scale_mode(int m) { return m != DSA_SCALE_AMAX && m != DSA_SCALE_POW2; }
+bool bad_page_size(int n) { return n != 32 && n != 64 && n != 128; }
+
+// rows * cols values of a tensor whose rows are ld apart stay addressable
+bool too_large(int64_t rows, int64_t ld) { return rows > (int64_t(1) << 40) / ld; }
+
+} // namespace
+
+int dsa_rmsnorm(const void *x, int64_t ldx, const void *residual, int64_t ldr, const void *weight, int64_t rows, int cols,
+                int dtype, int weight_dtype, float eps, void *residual_out, int64_t ldh, void *out, int64_t ldo, void *codes,
+                float *scale, int block, int scale_mode, dsa_stream_t stream)
+{
+    if (rows < 0 || cols < 1)
+        return fail(DSA_ERR_INVALID_ARG, "rows must be >= 0 and cols >= 1");
+    if (cols > kNormMaxCols)
+        return fail(DSA_ERR_UNSUPPORTED, "cols must be at most %d", kNormMaxCols);
+    if (bad_dtype(dtype) || bad_dtype(weight_dtype))
+        return fail(DSA_ERR_INVALID_ARG, "dtype and weight_dtype must be DSA_BF16 or DSA_FP32");
+    if (!(eps >= 0.f) || eps > 1e30f)
+        return fail(DSA_ERR_INVALID_ARG, "eps must be finite and not negative");
+    if (bad_scale_mode(scale_mode))
+        return fail(DSA_ERR_INVALID_ARG, "scale_mode must be DSA_SCALE_AMAX or DSA_SCALE_POW2");
+    if (block != 0 && block != 128)
+        return fail(DSA_ERR_INVALID_ARG, "block must be 0 (one scale per row) or 128");
+    if (rows == 0)
+        return ok();
+    if (!x || !weight)
+        return fail(DSA_ERR_INVALID_ARG, "null pointer argument");
+    if ((codes == nullptr) != (scale == nullptr))
+        return fail(DSA_ERR_INVALID_ARG, "codes and scale go together");
+    if (!residual_out && !out && !codes)
+        return fail(DSA_ERR_INVALID_ARG, "no output given");
+    if (ldx < cols || (residual && ldr < cols) || (residual_out && ldh < cols) || (out && ldo < cols))
+        return fail(DSA_ERR_INVALID_ARG, "a row stride is below cols");
+    if (rows > (int64_t)INT32_MAX || too_large(rows, ldx) || (residual && too_large(rows, ldr)) ||
+        (residual_out && too_large(rows, ldh)) || (out && too_large(rows, ldo)))
+        return fail(DSA_ERR_UNSUPPORTED, "rows too large");
+    RmsNormArgs a{x, residual, weight, rows, cols, ldx, ldr, ldh, ldo, dtype == DSA_FP32, weight_dtype == DSA_FP32, eps,
+                  residual_out, out, static_cast<uint8_t *>(codes), scale, block, scale_mode};
+    int rc = launch_rmsnorm(a, reinterpret_cast<cudaStream_t>(stream), t_err, sizeof t_err);
+    return rc == DSA_OK ? ok() : rc;
+}
+
+size_t dsa_rmsnorm_backward_workspace_size(int64_t rows, int cols)
+{
+    if (rows < 0 || rows > (int64_t)INT32_MAX || cols < 1 || cols > kNormMaxCols)
+        return 0;
+    return rmsnorm_backward_workspace_bytes(rows, cols);
+}
+
+int dsa_rmsnorm_backward(const void *dy, const void *h, const void *weight, const void *dres, int64_t rows, int cols,
+                         int dtype, int weight_dtype, float eps, void *dx, float *dweight, void *workspace,
+                         size_t workspace_bytes, dsa_stream_t stream)
+{
+    if (rows < 0 || cols < 1)
+        return fail(DSA_ERR_INVALID_ARG, "rows must be >= 0 and cols >= 1");
+    if (cols > kNormMaxCols)
+        return fail(DSA_ERR_UNSUPPORTED, "cols must be at most %d", kNormMaxCols);
+    if (bad_dtype(dtype) || bad_dtype(weight_dtype))
+        return fail(DSA_ERR_INVALID_ARG, "dtype and weight_dtype must be DSA_BF16 or DSA_FP32");
+    if (!(eps >= 0.f) || eps > 1e30f)
+        return fail(DSA_ERR_INVALID_ARG, "eps must be finite and not negative");
+    if (!dweight || (rows > 0 && (!dy || !h || !weight || !dx)))
+        return fail(DSA_ERR_INVALID_ARG, "null pointer argument");
+    if (rows > (int64_t)INT32_MAX)
+        return fail(DSA_ERR_UNSUPPORTED, "rows too large");
+    const size_t need = rmsnorm_backward_workspace_bytes(rows, cols);
+    if (need > 0 && (!workspace || workspace_bytes < need))
+        return fail(DSA_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace ? workspace_bytes : 0);
+    if (!aligned16(workspace))
+        return fail(DSA_ERR_ALIGNMENT, "workspace must be 16-byte aligned");
+    RmsNormBackwardArgs a{dy, h, weight, dres, rows, cols, dtype == DSA_FP32, weight_dtype == DSA_FP32, eps, dx, dweight,
+                          workspace};
+    int rc = launch_rmsnorm_backward(a, reinterpret_cast<cudaStream_t>(stream), t_err, sizeof t_err);
+    return rc == DSA_OK ? ok() : rc;
+}
+
+int dsa_cache_append(const int32_t *pos, const int32_t *seq, int T, const int32_t *block_table, int num_seqs, int max_pages,
+                     int num_pages, int page_size, const double *inv_freq, const void *kv, int64_t ld_kv,
+                     const void *kv_weight, int weight_dtype, float eps, void *kv_pool, const void *kI, int64_t ld_kI,
+                     int k_dtype, int scale_mode, void *k8_pool, float *ks_pool, dsa_stream_t stream)
+{
+    if (T < 0)
+        return fail(DSA_ERR_INVALID_ARG, "T < 0");
+    if (bad_page_size(page_size))
+        return fail(DSA_ERR_UNSUPPORTED, "page_size must be 32, 64 or 128");
+    if (bad_dtype(weight_dtype) || bad_dtype(k_dtype))
+        return fail(DSA_ERR_INVALID_ARG, "weight_dtype and k_dtype must be DSA_BF16 or DSA_FP32");
+    if (bad_scale_mode(scale_mode))
+        return fail(DSA_ERR_INVALID_ARG, "scale_mode must be DSA_SCALE_AMAX or DSA_SCALE_POW2");
+    if (!(eps >= 0.f) || eps > 1e30f)
+        return fail(DSA_ERR_INVALID_ARG, "eps must be finite and not negative");
+    if (T == 0)
+        return ok();
+    if (!pos || !block_table || !inv_freq)
+        return fail(DSA_ERR_INVALID_ARG, "null pointer argument");
+    if (!kv && !kI)
+        return fail(DSA_ERR_INVALID_ARG, "neither kv nor kI given");
+    if ((kv && !kv_pool) || (kI && (!k8_pool || !ks_pool)))
+        return fail(DSA_ERR_INVALID_ARG, "kv needs kv_pool, kI needs k8_pool and ks_pool");
+    if (num_seqs <= 0 || max_pages <= 0 || num_pages <= 0)
+        return fail(DSA_ERR_INVALID_ARG, "num_seqs, max_pages and num_pages must be positive");
+    if (!seq && T > num_seqs)
+        return fail(DSA_ERR_INVALID_ARG, "without seq the block table needs a row per token");
+    if ((kv && ld_kv < 576) || (kI && ld_kI < 128))
+        return fail(DSA_ERR_INVALID_ARG, "a row stride is below the row's width");
+    if ((kv && too_large(T, ld_kv)) || (kI && too_large(T, ld_kI)))
+        return fail(DSA_ERR_UNSUPPORTED, "row stride too large");
+    if (kv && (!aligned16(kv) || !aligned16(kv_pool) || !aligned16(kv_weight) || ld_kv % 8))
+        return fail(DSA_ERR_ALIGNMENT, "kv, its row stride, kv_weight and kv_pool must be 16-byte aligned");
+    if (kI && (!aligned16(kI) || !aligned16(k8_pool) || ld_kI % (k_dtype == DSA_FP32 ? 4 : 8)))
+        return fail(DSA_ERR_ALIGNMENT, "kI, its row stride and k8_pool must be 16-byte aligned");
+    CacheAppendArgs a{pos, seq, block_table, T, num_seqs, max_pages, num_pages, page_size, inv_freq, kv, ld_kv, kv_weight,
+                      weight_dtype == DSA_FP32, eps, kv_pool, kI, ld_kI, k_dtype == DSA_FP32, scale_mode,
+                      static_cast<uint8_t *>(k8_pool), ks_pool};
+    int rc = launch_cache_append(a, reinterpret_cast<cudaStream_t>(stream), t_err, sizeof t_err);
+    return rc == DSA_OK ? ok() : rc;
+}
+
+int dsa_rope_queries(const int32_t *pos, const double *inv_freq, int T, const void *q_rope, int64_t st_t, int64_t st_h, int H,
+                     void *q, const void *qI, int H_I, int i_dtype, int scale_mode, void *q8, float *q_scale,
+                     dsa_stream_t stream)
+{
+    if (T < 0)
+        return fail(DSA_ERR_INVALID_ARG, "T < 0");
+    if (bad_dtype(i_dtype))
+        return fail(DSA_ERR_INVALID_ARG, "i_dtype must be DSA_BF16 or DSA_FP32");
+    if (bad_scale_mode(scale_mode))
+        return fail(DSA_ERR_INVALID_ARG, "scale_mode must be DSA_SCALE_AMAX or DSA_SCALE_POW2");
+    if (T == 0)
+        return ok();
+    if (!pos || !inv_freq)
+        return fail(DSA_ERR_INVALID_ARG, "null pointer argument");
+    if (!q_rope && !qI)
+        return fail(DSA_ERR_INVALID_ARG, "neither q_rope nor qI given");
+    if ((q_rope && !q) || (qI && (!q8 || !q_scale)))
+        return fail(DSA_ERR_INVALID_ARG, "q_rope needs q, qI needs q8 and q_scale");
+    if (q_rope && (H < 1 || H > 128))
+        return fail(DSA_ERR_UNSUPPORTED, "H must be in [1, 128]");
+    if (qI && (H_I < 1 || H_I > 64))
+        return fail(DSA_ERR_UNSUPPORTED, "H_I must be in [1, 64]");
+    if (q_rope && (st_t < 0 || st_h < 0 || too_large(T, st_t + 1) || too_large(H, st_h + 1)))
+        return fail(DSA_ERR_INVALID_ARG, "q_rope strides out of range");
+    if (q_rope && (!aligned16(q_rope) || !aligned16(q) || st_t % 8 || st_h % 8))
+        return fail(DSA_ERR_ALIGNMENT, "q_rope, its strides and q must be 16-byte aligned");
+    if (qI && (!aligned16(qI) || !aligned16(q8)))
+        return fail(DSA_ERR_ALIGNMENT, "qI and q8 must be 16-byte aligned");
+    RopeQueriesArgs a{pos, inv_freq, T, H, H_I, q_rope, st_t, st_h, q, qI, i_dtype == DSA_FP32, scale_mode,
+                      static_cast<uint8_t *>(q8), q_scale};
+    int rc = launch_rope_queries(a, reinterpret_cast<cudaStream_t>(stream), t_err, sizeof t_err);
+    return rc == DSA_OK ? ok() : rc;
+}
+
+int dsa_index_rope_backward(const float *g, const int32_t *pos, const double *inv_freq, int T, int H_I, void *dx, int dtype,
+                            dsa_stream_t stream)
+{
+    if (T < 0)
+        return fail(DSA_ERR_INVALID_ARG, "T < 0");
+    if (bad_dtype(dtype))
+        return fail(DSA_ERR_INVALID_ARG, "dtype must be DSA_BF16 or DSA_FP32");
+    if (H_I < 1 || H_I > 64)
+        return fail(DSA_ERR_UNSUPPORTED, "H_I must be in [1, 64]");
+    if (T == 0)
+        return ok();
+    if (!g || !pos || !inv_freq || !dx)
+        return fail(DSA_ERR_INVALID_ARG, "null pointer argument");
+    if (!aligned16(g) || !aligned16(dx))
+        return fail(DSA_ERR_ALIGNMENT, "g and dx must be 16-byte aligned");
+    IndexRopeBackwardArgs a{g, pos, inv_freq, T, H_I, dx, dtype == DSA_FP32};
+    int rc = launch_index_rope_backward(a, reinterpret_cast<cudaStream_t>(stream), t_err, sizeof t_err);
+    return rc == DSA_OK ? ok() : rc;
+}
+
+size_t dsa_mla_decode_workspace_size(int B, int H)
+{
+    if (B < 1 || B > 65535 || H < 1 || H > 128)
+        return 0;
+    return dense_mla_workspace_bytes(B, H);
+}
+
+int dsa_mla_decode_paged(const void *q, const void *kv_pool, int num_pages, int page_size, const int32_t *block_table,
+                         int max_pages, const int32_t *ctx_len, int B, int H, float sm_scale, void *out, float *lse,
+                         void *workspace, size_t workspace_bytes, dsa_stream_t stream)
+{
+    if (B < 0)
+        return fail(DSA_ERR_INVALID_ARG, "B < 0");
+    if (B > 65535)
+        return fail(DSA_ERR_UNSUPPORTED, "B must be at most 65535");
+    if (H < 1 || H > 128)
+        return fail(DSA_ERR_UNSUPPORTED, "H must be in [1, 128]");
+    if (B == 0)
+        return ok();
+    if (!q || !kv_pool || !block_table || !ctx_len || !out || !lse)
+        return fail(DSA_ERR_INVALID_ARG, "null pointer argument");
+    if (num_pages <= 0 || max_pages <= 0)
+        return fail(DSA_ERR_INVALID_ARG, "num_pages and max_pages must be positive");
+    if (bad_page_size(page_size))
+        return fail(DSA_ERR_UNSUPPORTED, "page_size must be 32, 64 or 128");
+    if ((int64_t)num_pages * page_size > (int64_t)INT32_MAX || (int64_t)max_pages * page_size > (int64_t)INT32_MAX)
+        return fail(DSA_ERR_UNSUPPORTED, "pool or block table too large");
+    if (!aligned16(q) || !aligned16(kv_pool) || !aligned16(out))
+        return fail(DSA_ERR_ALIGNMENT, "q, kv_pool and out must be 16-byte aligned");
+    if (!(sm_scale > 0.f) || sm_scale > 1e30f)
+        return fail(DSA_ERR_INVALID_ARG, "sm_scale must be positive and finite");
+    const size_t need = dense_mla_workspace_bytes(B, H);
+    if (need > 0 && (!workspace || workspace_bytes < need))
+        return fail(DSA_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace ? workspace_bytes : 0);
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+        return fail(DSA_ERR_ALIGNMENT, "workspace must be 256-byte aligned");
+    DenseMlaArgs a{q, kv_pool, num_pages, page_size, block_table, max_pages, ctx_len, B, H, sm_scale, out, lse, workspace};
+    int rc = launch_dense_mla(a, reinterpret_cast<cudaStream_t>(stream), t_err, sizeof t_err);
+    return rc == DSA_OK ? ok() : rc;
+}
+
 int dsa_topk(const float *logits, int64_t ld, int T, const int32_t *valid_len, int k, int32_t *idx,
              dsa_stream_t stream)
 {

@@ -1,0 +1,40 @@
+// E4M3 helpers shared by the kernels that write FP8 codes.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace dsa {
+
+// Smallest power of two not below a positive finite fp32 r (exact, bit level).
+__device__ __forceinline__ float pow2_ceil(float r)
+{
+    const uint32_t u = __float_as_uint(r);
+    const uint32_t ex = u & 0x7F800000u, man = u & 0x007FFFFFu;
+    if (ex != 0u) // normal: r itself when the mantissa is zero, else the next exponent
+        return man == 0u ? r : __uint_as_float(ex + 0x00800000u);
+    // subnormal r = man * 2^-149: the next power of two of man, in the same units
+    const uint32_t p = (man & (man - 1u)) == 0u ? man : (1u << (32 - __clz(man - 1u)));
+    return __uint_as_float(p);
+}
+
+// Two fp32 -> two E4M3 codes (round to nearest even, saturating), lo in byte 0.
+__device__ __forceinline__ uint16_t e4m3x2(float lo, float hi)
+{
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Scale of values whose largest magnitude is amax: amax / 448, or the smallest
+// power of two not below it (mode 1); 1 for zeros and where the quotient is
+// below the smallest fp32.
+__device__ __forceinline__ float fp8_scale(float amax, int mode)
+{
+    const float ratio = amax / 448.f;
+    if (!(ratio > 0.f))
+        return 1.f;
+    return mode == 0 ? ratio : pow2_ceil(ratio);
+}
+
+} // namespace dsa

@@ -80,6 +80,83 @@ struct QuantizeArgs {
 };
 int launch_quantize(const QuantizeArgs &a, cudaStream_t stream, char *err, size_t errlen);
 
+struct RmsNormArgs {
+    const void *x;        // [rows, cols], row stride ldx; bf16, or fp32 with x32
+    const void *residual; // like x (stride ldr), or null
+    const void *weight;   // [cols] bf16, or fp32 with w32
+    int64_t rows;
+    int cols;
+    int64_t ldx, ldr, ldh, ldo;
+    bool x32, w32;
+    float eps;
+    void *residual_out; // like x (stride ldh), or null
+    void *out;          // like x (stride ldo), or null
+    uint8_t *codes;     // [rows, cols], or null
+    float *scale;       // [rows, 1 or ceil(cols / 128)]
+    int block;          // 0: one scale a row, 128: one per 128 columns
+    int scale_mode;
+};
+int launch_rmsnorm(const RmsNormArgs &a, cudaStream_t stream, char *err, size_t errlen);
+
+struct RmsNormBackwardArgs {
+    const void *dy, *h, *weight, *dres; // [rows, cols] (dres or null); weight [cols]
+    int64_t rows;
+    int cols;
+    bool x32, w32;
+    float eps;
+    void *dx;
+    float *dweight;
+    void *workspace;
+};
+int launch_rmsnorm_backward(const RmsNormBackwardArgs &a, cudaStream_t stream, char *err, size_t errlen);
+size_t rmsnorm_backward_workspace_bytes(int64_t rows, int cols);
+
+struct CacheAppendArgs {
+    const int32_t *pos;       // [T]
+    const int32_t *seq;       // [T] block-table row of each token, or null: its own index
+    const int32_t *block_table;
+    int T, num_seqs, max_pages, num_pages, page_size;
+    const double *inv_freq;   // [32]
+    const void *kv;           // [T, 576] bf16, row stride ld_kv, or null
+    int64_t ld_kv;
+    const void *kv_weight;    // [512], or null
+    bool w32;
+    float eps;
+    void *kv_pool;
+    const void *kI;           // [T, 128], row stride ld_kI, or null
+    int64_t ld_kI;
+    bool k32;
+    int scale_mode;
+    uint8_t *k8_pool;
+    float *ks_pool;
+};
+int launch_cache_append(const CacheAppendArgs &a, cudaStream_t stream, char *err, size_t errlen);
+
+struct RopeQueriesArgs {
+    const int32_t *pos; // [T]
+    const double *inv_freq;
+    int T, H, HI;
+    const void *q_rope; // [T, H, 64] bf16, strides st_t, st_h, or null
+    int64_t st_t, st_h;
+    void *q;            // [T, H, 576] bf16
+    const void *qI;     // [T, HI, 128], or null
+    bool i32;           // fp32 qI
+    int scale_mode;
+    uint8_t *q8;
+    float *q_scale;
+};
+int launch_rope_queries(const RopeQueriesArgs &a, cudaStream_t stream, char *err, size_t errlen);
+
+struct IndexRopeBackwardArgs {
+    const float *g;     // [T, HI, 128]
+    const int32_t *pos; // [T]
+    const double *inv_freq;
+    int T, HI;
+    void *dx;           // [T, HI, 128] bf16, or fp32 with o32
+    bool o32;
+};
+int launch_index_rope_backward(const IndexRopeBackwardArgs &a, cudaStream_t stream, char *err, size_t errlen);
+
 struct IndexerArgs {
     const void *q8;
     const float *q_scale;
@@ -184,5 +261,21 @@ struct MlaArgs {
 int launch_mla_prefill(const MlaArgs &a, cudaStream_t stream, char *err, size_t errlen);
 int launch_mla_decode(const MlaArgs &a, cudaStream_t stream, char *err, size_t errlen);
 size_t mla_decode_workspace_bytes(int B, int H, int k);
+
+struct DenseMlaArgs {
+    const void *q;       // [B, H, 576] bf16
+    const void *kv_pool; // [num_pages, page_size, 576] bf16
+    int num_pages, page_size;
+    const int32_t *block_table;
+    int max_pages;
+    const int32_t *ctx_len;
+    int B, H;
+    float sm_scale;
+    void *out;           // [B, H, 512] bf16
+    float *lse;          // [B, H]
+    void *workspace;
+};
+int launch_dense_mla(const DenseMlaArgs &a, cudaStream_t stream, char *err, size_t errlen);
+size_t dense_mla_workspace_bytes(int B, int H);
 
 } // namespace dsa

@@ -17,6 +17,7 @@
 // pass takes the amax with 16-byte loads, a second pass re-reads the row (now
 // in L1/L2), divides, and converts pairs with cvt.rn.satfinite.e4m3x2.f32.
 #include "common.cuh"
+#include "fp8.cuh"
 #include "launch.h"
 
 #include <stdio.h>
@@ -25,26 +26,6 @@ namespace dsa {
 namespace {
 
 constexpr int kQThreads = 256;
-
-// Smallest power of two not below a positive finite fp32 r (exact, bit level).
-__device__ __forceinline__ float pow2_ceil(float r)
-{
-    const uint32_t u = __float_as_uint(r);
-    const uint32_t ex = u & 0x7F800000u, man = u & 0x007FFFFFu;
-    if (ex != 0u) // normal: r itself when the mantissa is zero, else the next exponent
-        return man == 0u ? r : __uint_as_float(ex + 0x00800000u);
-    // subnormal r = man * 2^-149: the next power of two of man, in the same units
-    const uint32_t p = (man & (man - 1u)) == 0u ? man : (1u << (32 - __clz(man - 1u)));
-    return __uint_as_float(p);
-}
-
-// Two fp32 -> two E4M3 codes (round to nearest even, saturating), lo in byte 0.
-__device__ __forceinline__ uint16_t e4m3x2(float lo, float hi)
-{
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-    return r;
-}
 
 template <int GROUP>
 __global__ void __launch_bounds__(kQThreads)

@@ -1,0 +1,533 @@
+// Residual addition, root-mean-square norm and FP8 output on sm_103a, and the
+// norm's backward.
+//
+// The step in front of a layer's projections: the indexer's and the main
+// attention's inputs are projections of the normalised hidden state, and the
+// indexer runs in FP8 ("AMD Instinct MI355X GPUs Power DeepSeek-V3.2-Exp",
+// section "DeepSeek Sparse Attention (DSA)", item 1).  For each row
+//     h = x + residual (fp32),  r = 1 / sqrt(mean(h^2) + eps),  y = h r weight
+// with h and y rounded once, to the tensors' type, and the FP8 codes taken from
+// the fp32 y (scale = amax / 448 or its power of two, per row or per 128
+// columns, as dsa_quantize_fp8).  Backward, with xhat = h r and g = dy weight:
+//     dx = r (g - xhat mean(g xhat)) + dres,   dweight = sum over rows of dy xhat
+//
+// Both are HBM-bound: every value is read once, kept in registers, and written
+// once.  A group of G threads (a warp, or the CTA) owns a row; thread g holds
+// the 8-value chunks c G + g, so a warp's loads are 32 consecutive 16-byte
+// words and 16 neighbouring lanes hold one 128-column FP8 block.  Sums are
+// fp32, first within a thread, then by shuffles and shared memory, in an order
+// that depends on the sizes alone: results repeat bit for bit.
+#include "common.cuh"
+#include "fp8.cuh"
+#include "launch.h"
+
+#include <stdio.h>
+#include <type_traits>
+
+namespace dsa {
+namespace {
+
+constexpr int kRowThreads = 128; // threads of a CTA whose warps each own rows
+
+template <typename T> struct Vec8; // eight values as loaded
+
+template <> struct Vec8<__nv_bfloat16> {
+    uint4 v;
+    __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { v = *reinterpret_cast<const uint4 *>(p); }
+    __device__ __forceinline__ void load_n(const __nv_bfloat16 *p, int n)
+    {
+        uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n)
+                w[i >> 1] |= (uint32_t)reinterpret_cast<const uint16_t *>(p)[i] << (16 * (i & 1));
+        v = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __device__ __forceinline__ void get(float (&f)[8]) const
+    {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    }
+    __device__ __forceinline__ void set(const float (&f)[8])
+    {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(f[2 * i + 1]), "f"(f[2 * i]));
+        v = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __device__ __forceinline__ void store(__nv_bfloat16 *p) const { *reinterpret_cast<uint4 *>(p) = v; }
+    __device__ __forceinline__ void store_n(__nv_bfloat16 *p, int n) const
+    {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n)
+                reinterpret_cast<uint16_t *>(p)[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+    }
+};
+
+template <> struct Vec8<float> {
+    float4 a, b;
+    __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ void load(const float *p)
+    {
+        a = reinterpret_cast<const float4 *>(p)[0];
+        b = reinterpret_cast<const float4 *>(p)[1];
+    }
+    __device__ __forceinline__ void load_n(const float *p, int n)
+    {
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            f[i] = i < n ? p[i] : 0.f;
+        set(f);
+    }
+    __device__ __forceinline__ void get(float (&f)[8]) const
+    {
+        f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+    }
+    __device__ __forceinline__ void set(const float (&f)[8])
+    {
+        a = make_float4(f[0], f[1], f[2], f[3]);
+        b = make_float4(f[4], f[5], f[6], f[7]);
+    }
+    __device__ __forceinline__ void store(float *p) const
+    {
+        reinterpret_cast<float4 *>(p)[0] = a;
+        reinterpret_cast<float4 *>(p)[1] = b;
+    }
+    __device__ __forceinline__ void store_n(float *p, int n) const
+    {
+        float f[8];
+        get(f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n)
+                p[i] = f[i];
+    }
+};
+
+// Chunk of a row at column c0 (n valid columns of it): whole-chunk 16-byte
+// accesses when the call's rows allow them, else one value at a time.
+template <typename T>
+__device__ __forceinline__ void load_chunk(Vec8<T> &v, const T *row, int c0, int n, bool vec)
+{
+    if (n <= 0)
+        v.zero();
+    else if (vec)
+        v.load(row + c0);
+    else
+        v.load_n(row + c0, n);
+}
+
+template <typename T>
+__device__ __forceinline__ void store_chunk(const Vec8<T> &v, T *row, int c0, int n, bool vec)
+{
+    if (n <= 0)
+        return;
+    if (vec)
+        v.store(row + c0);
+    else
+        v.store_n(row + c0, n);
+}
+
+// Two sums (or maxima) over the row's group; every thread gets the result.
+// red: 2 x 32 floats of shared memory, only used when the group is the CTA.
+template <bool WARP, bool MAX>
+__device__ __forceinline__ float2 group_reduce(float a, float b, float *red)
+{
+    auto op = [](float x, float y) { return MAX ? fmaxf(x, y) : x + y; };
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        a = op(a, __shfl_xor_sync(0xffffffffu, a, o));
+        b = op(b, __shfl_xor_sync(0xffffffffu, b, o));
+    }
+    if (!WARP) {
+        const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+        if (lane == 0) {
+            red[threadIdx.x >> 5] = a;
+            red[32 + (threadIdx.x >> 5)] = b;
+        }
+        __syncthreads();
+        a = lane < warps ? red[lane] : 0.f; // 0 leaves a maximum of magnitudes alone
+        b = lane < warps ? red[32 + lane] : 0.f;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            a = op(a, __shfl_xor_sync(0xffffffffu, a, o));
+            b = op(b, __shfl_xor_sync(0xffffffffu, b, o));
+        }
+        __syncthreads(); // red is reused by the next reduction
+    }
+    return make_float2(a, b);
+}
+
+template <typename T, typename W, int NV, bool WARP>
+__global__ void __launch_bounds__(WARP ? kRowThreads : NV == 4 ? 256 : 1024)
+    rmsnorm_kernel(RmsNormArgs a, bool vec)
+{
+    __shared__ float red[64];
+    grid_dep_wait();
+    grid_dep_launch();
+    const int G = WARP ? 32 : blockDim.x;
+    const int g = WARP ? (threadIdx.x & 31) : threadIdx.x;
+    const int64_t row0 = WARP ? (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5) : blockIdx.x;
+    const int64_t step = (int64_t)gridDim.x * (WARP ? kRowThreads / 32 : 1);
+    const int cols = a.cols;
+    const W *weight = static_cast<const W *>(a.weight);
+    for (int64_t row = row0; row < a.rows; row += step) {
+        const T *x = static_cast<const T *>(a.x) + row * a.ldx;
+        Vec8<T> xv[NV], rv[NV];
+#pragma unroll
+        for (int c = 0; c < NV; ++c) {
+            const int c0 = (c * G + g) * 8;
+            load_chunk(xv[c], x, c0, cols - c0, vec);
+        }
+        if (a.residual) {
+            const T *res = static_cast<const T *>(a.residual) + row * a.ldr;
+#pragma unroll
+            for (int c = 0; c < NV; ++c) {
+                const int c0 = (c * G + g) * 8;
+                load_chunk(rv[c], res, c0, cols - c0, vec);
+            }
+        }
+        float h[NV][8];
+        float ss = 0.f;
+#pragma unroll
+        for (int c = 0; c < NV; ++c) {
+            xv[c].get(h[c]);
+            if (a.residual) {
+                float r[8];
+                rv[c].get(r);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    h[c][i] += r[i];
+            }
+            float s = 0.f; // 8 values at a time, so no long fp32 chain
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                s = fmaf(h[c][i], h[c][i], s);
+            ss += s;
+        }
+        // a tensor may be overwritten in place: each chunk is written by the
+        // thread that read it
+        if (a.residual_out) {
+            T *ho = static_cast<T *>(a.residual_out) + row * a.ldh;
+#pragma unroll
+            for (int c = 0; c < NV; ++c) {
+                const int c0 = (c * G + g) * 8;
+                Vec8<T> v;
+                v.set(h[c]);
+                store_chunk(v, ho, c0, cols - c0, vec);
+            }
+        }
+        ss = group_reduce<WARP, false>(ss, 0.f, red).x;
+        const float r = 1.f / sqrtf(ss / (float)cols + a.eps);
+#pragma unroll
+        for (int c = 0; c < NV; ++c) {
+            const int c0 = (c * G + g) * 8;
+            Vec8<W> wv;
+            load_chunk(wv, weight, c0, cols - c0, vec);
+            float w[8];
+            wv.get(w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                h[c][i] = h[c][i] * r * w[i];
+        }
+        if (a.out) {
+            T *out = static_cast<T *>(a.out) + row * a.ldo;
+#pragma unroll
+            for (int c = 0; c < NV; ++c) {
+                const int c0 = (c * G + g) * 8;
+                Vec8<T> v;
+                v.set(h[c]);
+                store_chunk(v, out, c0, cols - c0, vec);
+            }
+        }
+        if (!a.codes)
+            continue;
+        uint8_t *codes = a.codes + row * cols;
+        const int nblk = a.block ? (cols + a.block - 1) / a.block : 1;
+        float *scale = a.scale + row * nblk;
+        float s = 1.f;
+        if (!a.block) {
+            float m = 0.f;
+#pragma unroll
+            for (int c = 0; c < NV; ++c)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    m = fmaxf(m, fabsf(h[c][i]));
+            m = group_reduce<WARP, true>(m, 0.f, red).x;
+            s = fp8_scale(m, a.scale_mode);
+            if (g == 0)
+                scale[0] = s;
+        }
+#pragma unroll
+        for (int c = 0; c < NV; ++c) {
+            const int c0 = (c * G + g) * 8;
+            if (a.block) { // 16 lanes x 8 values = one 128-column block
+                float m = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    m = fmaxf(m, fabsf(h[c][i]));
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1)
+                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                s = fp8_scale(m, a.scale_mode);
+                if ((g & 15) == 0 && c0 < cols)
+                    scale[c0 / 128] = s;
+            }
+            uint32_t lo = e4m3x2(h[c][0] / s, h[c][1] / s) | ((uint32_t)e4m3x2(h[c][2] / s, h[c][3] / s) << 16);
+            uint32_t hi = e4m3x2(h[c][4] / s, h[c][5] / s) | ((uint32_t)e4m3x2(h[c][6] / s, h[c][7] / s) << 16);
+            if (cols - c0 <= 0)
+                continue;
+            if (vec) {
+                *reinterpret_cast<uint2 *>(codes + c0) = make_uint2(lo, hi);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i < cols - c0)
+                        codes[c0 + i] = (uint8_t)((i < 4 ? lo : hi) >> (8 * (i & 3)));
+            }
+        }
+    }
+}
+
+// Backward.  Each CTA walks rows b, b + grid, ... with its dweight sums in
+// registers and leaves them as one fp32 row of the workspace (warps of a CTA
+// first add theirs up in shared memory, warp by warp).
+template <typename T, typename W, int NV, bool WARP>
+__global__ void __launch_bounds__(WARP ? kRowThreads : NV == 4 ? 256 : 1024)
+    rmsnorm_backward_kernel(RmsNormBackwardArgs a, float *part, bool vec)
+{
+    __shared__ float red[64];
+    __shared__ float dws[WARP ? 32 * 8 * NV : 1];
+    grid_dep_wait();
+    grid_dep_launch();
+    const int G = WARP ? 32 : blockDim.x;
+    const int g = WARP ? (threadIdx.x & 31) : threadIdx.x;
+    const int64_t row0 = WARP ? (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5) : blockIdx.x;
+    const int64_t step = (int64_t)gridDim.x * (WARP ? kRowThreads / 32 : 1);
+    const int cols = a.cols;
+    Vec8<W> wv[NV];
+#pragma unroll
+    for (int c = 0; c < NV; ++c) {
+        const int c0 = (c * G + g) * 8;
+        load_chunk(wv[c], static_cast<const W *>(a.weight), c0, cols - c0, vec);
+    }
+    float dw[NV][8] = {};
+    for (int64_t row = row0; row < a.rows; row += step) {
+        Vec8<T> hv[NV], dv[NV], ev[NV];
+#pragma unroll
+        for (int c = 0; c < NV; ++c) {
+            const int c0 = (c * G + g) * 8;
+            load_chunk(hv[c], static_cast<const T *>(a.h) + row * cols, c0, cols - c0, vec);
+            load_chunk(dv[c], static_cast<const T *>(a.dy) + row * cols, c0, cols - c0, vec);
+            if (a.dres)
+                load_chunk(ev[c], static_cast<const T *>(a.dres) + row * cols, c0, cols - c0, vec);
+        }
+        float ss = 0.f, sg = 0.f;
+#pragma unroll
+        for (int c = 0; c < NV; ++c) {
+            float h[8], d[8], w[8], s = 0.f, t = 0.f;
+            hv[c].get(h);
+            dv[c].get(d);
+            wv[c].get(w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                s = fmaf(h[i], h[i], s);
+                t = fmaf(d[i] * w[i], h[i], t);
+            }
+            ss += s;
+            sg += t;
+        }
+        const float2 sums = group_reduce<WARP, false>(ss, sg, red);
+        const float r = 1.f / sqrtf(sums.x / (float)cols + a.eps);
+        const float k = sums.y * r * r / (float)cols; // mean(g xhat) r
+#pragma unroll
+        for (int c = 0; c < NV; ++c) {
+            const int c0 = (c * G + g) * 8;
+            float h[8], d[8], w[8], e[8], o[8];
+            hv[c].get(h);
+            dv[c].get(d);
+            wv[c].get(w);
+            if (a.dres)
+                ev[c].get(e);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                o[i] = r * (d[i] * w[i] - h[i] * k);
+                if (a.dres)
+                    o[i] += e[i];
+                dw[c][i] = fmaf(d[i], h[i] * r, dw[c][i]);
+            }
+            Vec8<T> v;
+            v.set(o);
+            store_chunk(v, static_cast<T *>(a.dx) + row * cols, c0, cols - c0, vec);
+        }
+    }
+    if (WARP) { // this CTA's warps add theirs up in turn
+        for (int w = 0; w < kRowThreads / 32; ++w) {
+            if ((threadIdx.x >> 5) == w) {
+#pragma unroll
+                for (int c = 0; c < NV; ++c)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        float &d = dws[(c * 8 + i) * 32 + g];
+                        d = w == 0 ? dw[c][i] : d + dw[c][i];
+                    }
+            }
+            __syncthreads();
+        }
+        if (threadIdx.x >= 32)
+            return;
+#pragma unroll
+        for (int c = 0; c < NV; ++c)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                dw[c][i] = dws[(c * 8 + i) * 32 + g];
+    }
+#pragma unroll
+    for (int c = 0; c < NV; ++c) {
+        const int c0 = (c * G + g) * 8;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (c0 + i < cols)
+                part[(int64_t)blockIdx.x * cols + c0 + i] = dw[c][i];
+    }
+}
+
+// dweight[c] = sum of the nparts partial rows: 32 columns a CTA, the rows
+// dealt to 8 warps, whose sums are added in order.
+__global__ void __launch_bounds__(256) dweight_kernel(const float *part, int nparts, int cols, float *dweight)
+{
+    __shared__ float s[8][32];
+    grid_dep_wait();
+    grid_dep_launch();
+    const int c = blockIdx.x * 32 + (threadIdx.x & 31), w = threadIdx.x >> 5;
+    float t = 0.f;
+    if (c < cols)
+        for (int p = w; p < nparts; p += 8)
+            t += part[(int64_t)p * cols + c];
+    s[w][threadIdx.x & 31] = t;
+    __syncthreads();
+    if (w == 0 && c < cols) {
+        t = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            t += s[i][threadIdx.x];
+        dweight[c] = t;
+    }
+}
+
+bool chunked(const void *p, int64_t ld_bytes) { return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)ld_bytes) & 15) == 0; }
+
+struct Shape {
+    int nv;      // chunks per thread
+    int threads; // per CTA
+    bool warp;   // a warp per row
+};
+
+// Threads per row.  Rows of at most 1024 values go to single warps (several
+// rows a CTA, no barrier), up to 8192 to CTAs of 64 to 256 threads with four
+// chunks each, longer ones to 1024 threads with two (four would spill).
+Shape shape_of(int cols)
+{
+    if (cols <= 1024)
+        return {cols <= 256 ? 1 : 4, kRowThreads, true};
+    if (cols > 8192)
+        return {2, 1024, false};
+    int threads = 64;
+    while (threads * 4 * 8 < cols)
+        threads *= 2;
+    return {4, threads, false};
+}
+
+template <typename F>
+cudaError_t dispatch(const Shape &s, bool x32, bool w32, F &&f)
+{
+    using std::integral_constant;
+    using bf16 = __nv_bfloat16;
+    auto go = [&](auto nv, auto warp) {
+        if (x32)
+            return w32 ? f((float *)0, (float *)0, nv, warp) : f((float *)0, (bf16 *)0, nv, warp);
+        return w32 ? f((bf16 *)0, (float *)0, nv, warp) : f((bf16 *)0, (bf16 *)0, nv, warp);
+    };
+    if (s.warp)
+        return s.nv == 1 ? go(integral_constant<int, 1>(), std::true_type()) : go(integral_constant<int, 4>(), std::true_type());
+    return s.nv == 2 ? go(integral_constant<int, 2>(), std::false_type()) : go(integral_constant<int, 4>(), std::false_type());
+}
+
+int64_t rows_grid(int64_t rows, const Shape &s, int64_t most)
+{
+    const int64_t per = s.warp ? s.threads / 32 : 1;
+    const int64_t n = (rows + per - 1) / per;
+    return n < most ? n : most;
+}
+
+int backward_ctas(int64_t rows, int cols)
+{
+    return (int)rows_grid(rows, shape_of(cols), 2LL * num_sms());
+}
+
+} // namespace
+
+int launch_rmsnorm(const RmsNormArgs &a, cudaStream_t stream, char *err, size_t errlen)
+{
+    const int e = a.x32 ? 4 : 2;
+    const bool vec = a.cols % 8 == 0 && chunked(a.x, a.ldx * e) && chunked(a.weight, 0) &&
+                     (!a.residual || chunked(a.residual, a.ldr * e)) &&
+                     (!a.residual_out || chunked(a.residual_out, a.ldh * e)) && (!a.out || chunked(a.out, a.ldo * e)) &&
+                     (!a.codes || (reinterpret_cast<uintptr_t>(a.codes) & 7) == 0);
+    const Shape s = shape_of(a.cols);
+    const int64_t grid = rows_grid(a.rows, s, 1 << 30);
+    cudaError_t rc = dispatch(s, a.x32, a.w32, [&](auto t, auto w, auto nv, auto warp) {
+        using T = std::remove_pointer_t<decltype(t)>;
+        using W = std::remove_pointer_t<decltype(w)>;
+        return launch_pdl(rmsnorm_kernel<T, W, decltype(nv)::value, decltype(warp)::value>, dim3((unsigned)grid),
+                          dim3(s.threads), 0, stream, 1, a, vec);
+    });
+    if (rc != cudaSuccess) {
+        snprintf(err, errlen, "rmsnorm launch: %s", cudaGetErrorString(rc));
+        return DSA_ERR_CUDA;
+    }
+    return DSA_OK;
+}
+
+size_t rmsnorm_backward_workspace_bytes(int64_t rows, int cols)
+{
+    return (size_t)backward_ctas(rows, cols) * cols * sizeof(float);
+}
+
+int launch_rmsnorm_backward(const RmsNormBackwardArgs &a, cudaStream_t stream, char *err, size_t errlen)
+{
+    const int e = a.x32 ? 4 : 2;
+    const int64_t ld = (int64_t)a.cols * e;
+    const bool vec = a.cols % 8 == 0 && chunked(a.h, ld) && chunked(a.dy, ld) && chunked(a.dx, ld) && chunked(a.weight, 0) &&
+                     (!a.dres || chunked(a.dres, ld));
+    const Shape s = shape_of(a.cols);
+    const int grid = backward_ctas(a.rows, a.cols);
+    float *part = static_cast<float *>(a.workspace);
+    cudaError_t rc = cudaSuccess;
+    if (grid > 0)
+        rc = dispatch(s, a.x32, a.w32, [&](auto t, auto w, auto nv, auto warp) {
+            using T = std::remove_pointer_t<decltype(t)>;
+            using W = std::remove_pointer_t<decltype(w)>;
+            return launch_pdl(rmsnorm_backward_kernel<T, W, decltype(nv)::value, decltype(warp)::value>,
+                              dim3((unsigned)grid), dim3(s.threads), 0, stream, 1, a, part, vec);
+        });
+    if (rc == cudaSuccess) // no rows: the sum of nothing, zeros
+        rc = launch_pdl(dweight_kernel, dim3((unsigned)((a.cols + 31) / 32)), dim3(256), 0, stream, 1, (const float *)part,
+                        grid, a.cols, a.dweight);
+    if (rc != cudaSuccess) {
+        snprintf(err, errlen, "rmsnorm backward launch: %s", cudaGetErrorString(rc));
+        return DSA_ERR_CUDA;
+    }
+    return DSA_OK;
+}
+
+} // namespace dsa

@@ -1,0 +1,414 @@
+// Position rotation on the way into the caches and the attention, on sm_103a:
+// appending tokens to the paged caches, preparing the queries, and the
+// backward of the index rotation.
+//
+// The two rotations differ in which columns form a pair (release summary
+// "DeepSeek-V3.2-Exp: Boosting Long-Context Efficiency with DeepSeek Sparse
+// Attention", section "Key claims": the indexer's RoPE is non-interleaved, the
+// MLA's interleaved).  With angle t_i = pos * inv_freq[i], i < 32:
+//     main   (64 columns)         pairs (2i, 2i + 1)
+//     index  (first 64 of 128)    pairs (i, i + 32)
+//     (a, b) -> (a cos t - b sin t, a sin t + b cos t)
+// The index vector then becomes E4M3 codes with one scale per token, as
+// dsa_quantize_fp8, from the fp32 rotated values (no rounding in between).
+//
+// Angles.  pos * inv_freq in fp32 is off by up to pos * 2^-24 radians (0.008 at
+// 131072).  Here inv_freq / (2 pi) becomes a 64-bit fixed-point fraction of a
+// turn, once per lane; pos times it modulo 2^64 is then the angle's fraction of
+// a turn with nothing rounded, and only that fraction is taken to fp32 for sine
+// and cosine.  The same product in fp64 cost five fp64 operations an angle, on
+// a GPU with 1/64 of its fp32 rate.
+//
+// All three kernels move each byte once and are HBM-bound (or, for a decode
+// step, bound by launch and load latency).
+#include "common.cuh"
+#include "fp8.cuh"
+#include "launch.h"
+
+#include <stdio.h>
+
+namespace dsa {
+namespace {
+
+constexpr int kLatent = 576, kValue = 512, kIndex = 128;
+
+// A frequency (radians per position) as a 2^-64 fraction of a turn per position.
+__device__ __forceinline__ uint64_t turn_step(double freq)
+{
+    double f = freq * 0.15915494309189533577; // 1 / (2 pi)
+    f -= floor(f);
+    return (uint64_t)(f * 18446744073709551616.0);
+}
+
+// (cos, sin) at position pos >= 0.
+__device__ __forceinline__ float2 rotation(int pos, uint64_t step)
+{
+    const uint64_t p = step * (uint32_t)pos + 0x80000000u;
+    const float half_turns = (float)(int32_t)(p >> 32) * 4.656612873077393e-10f; // 2^-31
+    float2 r;
+    sincospif(half_turns, &r.y, &r.x);
+    return r;
+}
+
+__device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
+
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ void unpack8(const uint4 &v, float (&f)[8])
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = bf16_lo(w[i]);
+        f[2 * i + 1] = bf16_hi(w[i]);
+    }
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&f)[8])
+{
+    return make_uint4(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7]));
+}
+
+// ------------------------------------------------------------- cache append
+// One warp per token.  Lane l holds latent chunks l and l + 32 (8 columns
+// each); lanes 0-7 the rotated columns' chunks; every lane 4 index columns, so
+// the index pair (i, i + 32) sits 8 lanes apart.  Lane i computes angle i; a
+// lane of either rotation needs angles 4 (l & 7) .. + 3.
+constexpr int kAppendThreads = 128;
+
+template <typename K, bool W32>
+__global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(CacheAppendArgs a, unsigned *status)
+{
+    grid_dep_wait();
+    grid_dep_launch();
+    const int lane = threadIdx.x & 31;
+    const uint64_t freq = turn_step(a.inv_freq[lane]);
+    const int step = gridDim.x * (kAppendThreads / 32);
+    for (int t = blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5); t < a.T; t += step) {
+        const int pos = a.pos[t];
+        if (pos < 0) // a padded row
+            continue;
+        const int s = a.seq ? a.seq[t] : t;
+        const int lp = pos / a.page_size;
+        if (s < 0 || s >= a.num_seqs || lp >= a.max_pages) {
+            if (lane == 0)
+                atomicOr(status, DSA_DEV_BAD_POSITION);
+            continue;
+        }
+        const int page = a.block_table[(int64_t)s * a.max_pages + lp];
+        if (page < 0 || page >= a.num_pages) {
+            if (lane == 0)
+                atomicOr(status, DSA_DEV_BAD_PAGE);
+            continue;
+        }
+        const int64_t slot = (int64_t)page * a.page_size + pos % a.page_size;
+        uint4 v0, v1, vr = make_uint4(0, 0, 0, 0);
+        if (a.kv) {
+            const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.kv) + t * a.ld_kv);
+            v0 = src[lane];
+            v1 = src[lane + 32];
+            if (lane < 8)
+                vr = src[64 + lane];
+        }
+        float k[4] = {};
+        if (a.kI) {
+            const K *src = static_cast<const K *>(a.kI) + t * a.ld_kI + 4 * lane;
+            if (sizeof(K) == 4) {
+                const float4 f = *reinterpret_cast<const float4 *>(src);
+                k[0] = f.x, k[1] = f.y, k[2] = f.z, k[3] = f.w;
+            } else {
+                const uint2 f = *reinterpret_cast<const uint2 *>(src);
+                k[0] = bf16_lo(f.x), k[1] = bf16_hi(f.x), k[2] = bf16_lo(f.y), k[3] = bf16_hi(f.y);
+            }
+        }
+        const float2 mine = rotation(pos, freq);
+        float c[4], n[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            c[i] = __shfl_sync(0xffffffffu, mine.x, 4 * (lane & 7) + i);
+            n[i] = __shfl_sync(0xffffffffu, mine.y, 4 * (lane & 7) + i);
+        }
+        if (a.kv) {
+            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.kv_pool) + slot * kLatent);
+            if (a.kv_weight) {
+                float f0[8], f1[8], ss = 0.f, w0[8], w1[8];
+                unpack8(v0, f0);
+                unpack8(v1, f1);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    ss = fmaf(f0[i], f0[i], fmaf(f1[i], f1[i], ss));
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1)
+                    ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                const float r = 1.f / sqrtf(ss / (float)kValue + a.eps);
+                if (W32) {
+                    const float *w = static_cast<const float *>(a.kv_weight) + 8 * lane;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        w0[i] = w[i];
+                        w1[i] = w[256 + i];
+                    }
+                } else {
+                    const uint4 *w = static_cast<const uint4 *>(a.kv_weight) + lane;
+                    unpack8(w[0], w0);
+                    unpack8(w[32], w1);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    f0[i] = f0[i] * r * w0[i];
+                    f1[i] = f1[i] * r * w1[i];
+                }
+                v0 = pack8(f0);
+                v1 = pack8(f1);
+            }
+            dst[lane] = v0;
+            dst[lane + 32] = v1;
+            if (lane < 8) {
+                float f[8], o[8];
+                unpack8(vr, f);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    o[2 * i] = f[2 * i] * c[i] - f[2 * i + 1] * n[i];
+                    o[2 * i + 1] = f[2 * i] * n[i] + f[2 * i + 1] * c[i];
+                }
+                dst[64 + lane] = pack8(o);
+            }
+        }
+        if (a.kI) {
+            float m = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float other = __shfl_xor_sync(0xffffffffu, k[i], 8);
+                if (lane < 8)
+                    k[i] = k[i] * c[i] - other * n[i];
+                else if (lane < 16)
+                    k[i] = other * n[i] + k[i] * c[i];
+                m = fmaxf(m, fabsf(k[i]));
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            const float sc = fp8_scale(m, a.scale_mode);
+            reinterpret_cast<uint32_t *>(a.k8_pool + slot * kIndex)[lane] =
+                e4m3x2(k[0] / sc, k[1] / sc) | ((uint32_t)e4m3x2(k[2] / sc, k[3] / sc) << 16);
+            if (lane == 0)
+                a.ks_pool[slot] = sc;
+        }
+    }
+}
+
+// ------------------------------------------------------------------ queries
+// One CTA per token.  Index queries: thread t holds chunks t, t + 256, ... of
+// the token's H_I x 128 values (8 columns each, 16 chunks a head), its pair's
+// other half 4 lanes away; at most 64 heads, so four chunks a thread stay in
+// registers while the token's amax is found.
+constexpr int kQueryThreads = 256;
+constexpr int kIndexChunks = 4;
+
+// Rotates chunk c (0 .. 15) of a 128-wide index vector; other: the 8 values 4
+// lanes away.  back turns by the negative angle.
+__device__ __forceinline__ void rotate_index(float (&f)[8], int c, const float2 *cs, bool back)
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float other = __shfl_xor_sync(0xffffffffu, f[i], 4);
+        if (c < 8) {
+            const float2 r = cs[8 * (c & 3) + i];
+            const float sn = ((c < 4) != back) ? -r.y : r.y;
+            f[i] = f[i] * r.x + other * sn;
+        }
+    }
+}
+
+template <typename K>
+__device__ __forceinline__ void load8(const K *p, float (&f)[8])
+{
+    if (sizeof(K) == 4) {
+        const float4 u = reinterpret_cast<const float4 *>(p)[0], v = reinterpret_cast<const float4 *>(p)[1];
+        f[0] = u.x, f[1] = u.y, f[2] = u.z, f[3] = u.w, f[4] = v.x, f[5] = v.y, f[6] = v.z, f[7] = v.w;
+    } else {
+        unpack8(*reinterpret_cast<const uint4 *>(p), f);
+    }
+}
+
+template <typename K>
+__global__ void __launch_bounds__(kQueryThreads) rope_queries_kernel(RopeQueriesArgs a)
+{
+    __shared__ float2 cs[32];
+    __shared__ float red[kQueryThreads / 32];
+    grid_dep_wait();
+    grid_dep_launch();
+    const int t = blockIdx.x, tid = threadIdx.x;
+    const int pos = a.pos[t];
+    if (pos < 0) // a padded row
+        return;
+    if (tid < 32)
+        cs[tid] = rotation(pos, turn_step(a.inv_freq[tid]));
+    float f[kIndexChunks][8];
+    const int chunks = a.qI ? a.HI * 16 : 0;
+#pragma unroll
+    for (int j = 0; j < kIndexChunks; ++j) {
+        const int c = j * kQueryThreads + tid;
+        if (c < chunks)
+            load8(static_cast<const K *>(a.qI) + ((int64_t)t * a.HI * 16 + c) * 8, f[j]);
+        else
+            for (int i = 0; i < 8; ++i)
+                f[j][i] = 0.f;
+    }
+    __syncthreads();
+    if (a.q_rope) {
+        const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(a.q_rope) + t * a.st_t;
+        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.q) + (int64_t)t * a.H * kLatent + kValue;
+        for (int c = tid; c < a.H * 8; c += kQueryThreads) {
+            const int h = c >> 3, p = c & 7;
+            float x[8], o[8];
+            unpack8(*reinterpret_cast<const uint4 *>(src + h * a.st_h + 8 * p), x);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 r = cs[4 * p + i];
+                o[2 * i] = x[2 * i] * r.x - x[2 * i + 1] * r.y;
+                o[2 * i + 1] = x[2 * i] * r.y + x[2 * i + 1] * r.x;
+            }
+            *reinterpret_cast<uint4 *>(dst + (int64_t)h * kLatent + 8 * p) = pack8(o);
+        }
+    }
+    if (!a.qI)
+        return;
+    float m = 0.f;
+#pragma unroll
+    for (int j = 0; j < kIndexChunks; ++j) {
+        rotate_index(f[j], tid & 15, cs, false);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            m = fmaxf(m, fabsf(f[j][i]));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if ((tid & 31) == 0)
+        red[tid >> 5] = m;
+    __syncthreads();
+    m = red[0];
+#pragma unroll
+    for (int w = 1; w < kQueryThreads / 32; ++w)
+        m = fmaxf(m, red[w]);
+    const float sc = fp8_scale(m, a.scale_mode);
+    if (tid == 0)
+        a.q_scale[t] = sc;
+#pragma unroll
+    for (int j = 0; j < kIndexChunks; ++j) {
+        const int c = j * kQueryThreads + tid;
+        if (c >= chunks)
+            continue;
+        const uint32_t lo = e4m3x2(f[j][0] / sc, f[j][1] / sc) | ((uint32_t)e4m3x2(f[j][2] / sc, f[j][3] / sc) << 16);
+        const uint32_t hi = e4m3x2(f[j][4] / sc, f[j][5] / sc) | ((uint32_t)e4m3x2(f[j][6] / sc, f[j][7] / sc) << 16);
+        reinterpret_cast<uint2 *>(a.q8)[(int64_t)t * a.HI * 16 + c] = make_uint2(lo, hi);
+    }
+}
+
+// ------------------------------------------------- backward of the rotation
+// dx = R(pos)^T g per index vector.  Each CTA takes 64 consecutive vectors, of
+// one token (64 heads) to 64 (keys, one vector a token), and first computes
+// the angles of the tokens it meets, 32 each.
+constexpr int kBackVecs = kQueryThreads * kIndexChunks / 16;
+
+template <typename O>
+__global__ void __launch_bounds__(kQueryThreads) index_rope_backward_kernel(IndexRopeBackwardArgs a)
+{
+    __shared__ float2 cs[kBackVecs][32];
+    __shared__ bool padded[kBackVecs];
+    grid_dep_wait();
+    grid_dep_launch();
+    const int64_t v0 = (int64_t)blockIdx.x * kBackVecs, vecs = (int64_t)a.T * a.HI;
+    const int64_t vlast = (v0 + kBackVecs < vecs ? v0 + kBackVecs : vecs) - 1;
+    const int t0 = (int)(v0 / a.HI), ntok = (int)(vlast / a.HI) - t0 + 1;
+    float f[kIndexChunks][8];
+#pragma unroll
+    for (int j = 0; j < kIndexChunks; ++j) {
+        const int64_t c = v0 * 16 + j * kQueryThreads + threadIdx.x;
+        if (c < vecs * 16)
+            load8(a.g + c * 8, f[j]);
+        else
+            for (int i = 0; i < 8; ++i)
+                f[j][i] = 0.f;
+    }
+    const uint64_t step = turn_step(a.inv_freq[threadIdx.x & 31]);
+    for (int t = threadIdx.x >> 5; t < ntok; t += kQueryThreads / 32) {
+        const int pos = a.pos[t0 + t];
+        cs[t][threadIdx.x & 31] = rotation(pos, step);
+        if ((threadIdx.x & 31) == 0)
+            padded[t] = pos < 0;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kIndexChunks; ++j) {
+        const int64_t c = v0 * 16 + j * kQueryThreads + threadIdx.x;
+        const int64_t v = c >> 4 < vecs ? c >> 4 : vecs - 1;
+        const int t = (int)(v / a.HI) - t0;
+        rotate_index(f[j], threadIdx.x & 15, cs[t], true);
+        if (c >= vecs * 16)
+            continue;
+        if (padded[t])
+            for (int i = 0; i < 8; ++i)
+                f[j][i] = 0.f;
+        if (sizeof(O) == 4) {
+            float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(a.dx) + c * 8);
+            o[0] = make_float4(f[j][0], f[j][1], f[j][2], f[j][3]);
+            o[1] = make_float4(f[j][4], f[j][5], f[j][6], f[j][7]);
+        } else {
+            reinterpret_cast<uint4 *>(a.dx)[c] = pack8(f[j]);
+        }
+    }
+}
+
+int finish(cudaError_t e, const char *what, char *err, size_t errlen)
+{
+    if (e == cudaSuccess)
+        return DSA_OK;
+    snprintf(err, errlen, "%s launch: %s", what, cudaGetErrorString(e));
+    return DSA_ERR_CUDA;
+}
+
+} // namespace
+
+int launch_cache_append(const CacheAppendArgs &a, cudaStream_t stream, char *err, size_t errlen)
+{
+    unsigned *status = device_status_ptr();
+    if (!status) {
+        snprintf(err, errlen, "device status word unavailable");
+        return DSA_ERR_CUDA;
+    }
+    const int per = kAppendThreads / 32;
+    const int want = (a.T + per - 1) / per, most = 16 * num_sms();
+    auto go = [&](auto kernel) {
+        return launch_pdl(kernel, dim3((unsigned)(want < most ? want : most)), dim3(kAppendThreads), 0, stream, 1, a, status);
+    };
+    cudaError_t e;
+    if (a.k32)
+        e = a.w32 ? go(cache_append_kernel<float, true>) : go(cache_append_kernel<float, false>);
+    else
+        e = a.w32 ? go(cache_append_kernel<__nv_bfloat16, true>) : go(cache_append_kernel<__nv_bfloat16, false>);
+    return finish(e, "cache append", err, errlen);
+}
+
+int launch_rope_queries(const RopeQueriesArgs &a, cudaStream_t stream, char *err, size_t errlen)
+{
+    auto go = [&](auto kernel) { return launch_pdl(kernel, dim3((unsigned)a.T), dim3(kQueryThreads), 0, stream, 1, a); };
+    return finish(a.i32 ? go(rope_queries_kernel<float>) : go(rope_queries_kernel<__nv_bfloat16>), "query rotation", err, errlen);
+}
+
+int launch_index_rope_backward(const IndexRopeBackwardArgs &a, cudaStream_t stream, char *err, size_t errlen)
+{
+    const unsigned grid = (unsigned)(((int64_t)a.T * a.HI + kBackVecs - 1) / kBackVecs);
+    auto go = [&](auto kernel) { return launch_pdl(kernel, dim3(grid), dim3(kQueryThreads), 0, stream, 1, a); };
+    return finish(a.o32 ? go(index_rope_backward_kernel<float>) : go(index_rope_backward_kernel<__nv_bfloat16>),
+                  "index rotation backward", err, errlen);
+}
+
+} // namespace dsa
