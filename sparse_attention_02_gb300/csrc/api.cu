@@ -92,9 +92,10 @@ int num_sms()
     return g_sms[d];
 }
 
-bool encode_tmap_2d(CUtensorMap *map, CUtensorMapDataType dtype, const void *base, uint64_t inner, uint64_t rows,
-                    uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swizzle,
-                    char *err, size_t errlen)
+namespace {
+
+bool encode_tmap(CUtensorMap *map, CUtensorMapDataType dtype, const void *base, int rank, const cuuint64_t *dims,
+                 const cuuint64_t *strides, const cuuint32_t *box, CUtensorMapSwizzle swizzle, char *err, size_t errlen)
 {
     {
         std::lock_guard<std::mutex> lk(g_mu);
@@ -110,20 +111,38 @@ bool encode_tmap_2d(CUtensorMap *map, CUtensorMapDataType dtype, const void *bas
             g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
         }
     }
-    cuuint64_t dims[2] = {inner, rows > 0 ? rows : 1};
-    cuuint64_t strides[1] = {row_stride_bytes};
-    cuuint32_t box[2] = {box_inner, box_rows};
-    cuuint32_t estr[2] = {1, 1};
-    CUresult r = g_encode(map, dtype, 2, const_cast<void *>(base), dims, strides, box, estr,
+    const cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = g_encode(map, dtype, rank, const_cast<void *>(base), dims, strides, box, estr,
                           CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) {
         snprintf(err, errlen, "cuTensorMapEncodeTiled failed (%d): inner=%llu rows=%llu stride=%llu box=%ux%u", (int)r,
-                 (unsigned long long)inner, (unsigned long long)rows, (unsigned long long)row_stride_bytes, box_inner,
-                 box_rows);
+                 (unsigned long long)dims[0], (unsigned long long)dims[1], (unsigned long long)strides[0], box[0], box[1]);
         return false;
     }
     return true;
+}
+
+} // namespace
+
+bool encode_tmap_2d(CUtensorMap *map, CUtensorMapDataType dtype, const void *base, uint64_t inner, uint64_t rows,
+                    uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swizzle,
+                    char *err, size_t errlen)
+{
+    const cuuint64_t dims[2] = {inner, rows > 0 ? rows : 1};
+    const cuuint64_t strides[1] = {row_stride_bytes};
+    const cuuint32_t box[2] = {box_inner, box_rows};
+    return encode_tmap(map, dtype, base, 2, dims, strides, box, swizzle, err, errlen);
+}
+
+bool encode_tmap_blocks(CUtensorMap *map, CUtensorMapDataType dtype, const void *base, uint64_t inner, uint64_t rows,
+                        uint64_t blocks, uint64_t row_stride_bytes, uint64_t block_stride_bytes, uint32_t box_rows,
+                        uint32_t box_blocks, CUtensorMapSwizzle swizzle, char *err, size_t errlen)
+{
+    const cuuint64_t dims[3] = {inner, rows > 0 ? rows : 1, blocks};
+    const cuuint64_t strides[2] = {row_stride_bytes, block_stride_bytes};
+    const cuuint32_t box[3] = {(cuuint32_t)inner, box_rows, box_blocks};
+    return encode_tmap(map, dtype, base, 3, dims, strides, box, swizzle, err, errlen);
 }
 
 } // namespace dsa

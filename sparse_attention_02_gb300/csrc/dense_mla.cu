@@ -61,38 +61,37 @@ constexpr int kAtom = 64 * 128;           // 64 rows x 64 bf16 columns, SW128
 constexpr int kAtoms = 9;
 constexpr int kStage = kAtoms * kAtom;
 constexpr int kStages = 2;
-constexpr int kThreads = 256;
-constexpr int kSoftWarp0 = 4;
+constexpr int kGroups = 4;                // groups a stage's atoms arrive in: 0-1, 2-3, 4-5, 6-8
+constexpr int kSoftWarp0 = 4, kSoftWarps = 8;
+constexpr int kThreads = 32 * (kSoftWarp0 + kSoftWarps);
 constexpr int kBatch = 16;                // tiles whose pages a warp looks up at once (two half-blocks a tile)
-constexpr int kPrefetch = 6;              // tiles ahead of the loads that are pulled into L2
+constexpr int kPrefetch = 1;              // tiles ahead of the loads that are pulled into L2
 constexpr float kRescaleLog2 = 8.f;
 
 // shared memory
 constexpr int OFF_Q = 0;
 constexpr int OFF_KV = OFF_Q + kStage;
 constexpr int OFF_P1 = OFF_KV + kStages * kStage; // P of the tile's second 64 keys (the first's takes the spent RoPE atom)
-constexpr int OFF_X = OFF_P1 + kAtom;             // per-thread maxima (two buffers of 128) and sums (128)
-constexpr int OFF_BAR = OFF_X + 3 * 128 * 4;
-constexpr int NBAR = 30;
+constexpr int OFF_X = OFF_P1 + kAtom;             // per-thread maxima (two buffers); the first also takes the sums
+constexpr int OFF_BAR = OFF_X + 2 * 256 * 4;
+constexpr int NBAR = 36;
 constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
-constexpr int kSmem = OFF_MISC + 64 + 1024; // with room to start at a multiple of 1024
+constexpr int kSmem = OFF_MISC + 64;
 static_assert(kSmem <= 232448, "dynamic shared memory above the 227 KB a CTA may hold");
 
 // barriers (L: used in the leader CTA only; both CTAs' roles arrive there)
-constexpr int B_KF = 0,  // L [stage][group]: both CTAs' atoms 0-3 / 4-8 landed
-              B_E = 4,   // [stage][half]: PV of the tile's first / second 64 keys done
-              B_SF = 8,  // [buffer]: scores done
-              B_SE = 10, // L [buffer]: scores read
-              B_QD = 12, // [stage]: the score MMAs over atoms 0-3 done
-              B_VL = 14, // [stage]: this CTA's swapped-in columns landed
-              B_P0 = 16, // L [buffer]: P of the first 64 keys written and O rescaled
-              B_P1 = 18, // L [buffer]: P of the second 64 keys written
-              B_OF = 20, // O of a unit complete
-              B_OE = 21, // L: O read
-              B_QF = 22, // L: Q landed
-              B_DONE = 23,
-              B_RB = 24, // [pair][parity]: the two warps of 32 heads swapped their maxima
-              B_RL = 28; // [pair]: ... their sums
+constexpr int B_KF = 0,  // L [stage][group]: both CTAs' atoms landed
+              B_E = 8,   // [stage][half]: PV of the tile's first / second 64 keys done
+              B_SF = 12, // [buffer]: scores done
+              B_QD = 16, // [stage]: the score MMAs over atoms 0-3 done
+              B_VL = 18, // [stage]: this CTA's swapped-in columns landed
+              B_P = 20,  // L [buffer]: scores read, P written, O rescaled, value columns in place
+              B_OF = 24, // O of a unit complete
+              B_OE = 25, // L: O read
+              B_QF = 26, // L: Q landed
+              B_DONE = 27,
+              B_RB = 28, // [pair][parity]: the four warps of 32 heads swapped their maxima
+              B_RL = 32; // [pair][0/1]: ... their sums / read them
 
 constexpr uint32_t TM_O = 0, TM_S = 256, kTmemCols = 512;
 
@@ -147,6 +146,14 @@ struct Walk {
         ++row;
         tile = 0;
         return true;
+    }
+    __device__ bool next_filled(const Params &p, int cid, Unit &u) // skips empty rows
+    {
+        while (next(p, cid, u))
+            if (u.ctx > 0)
+                return true;
+        u.jb = u.je = 0;
+        return false;
     }
 };
 
@@ -209,12 +216,32 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi)
     return r;
 }
 
-// 2-D tiled load into this CTA's shared memory, completion counted on a barrier of either CTA of the pair.
-__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap *map, uint32_t bar, int32_t c0, int32_t c1)
+// True in one lane of the warp.  The compiler keeps the operands of what this
+// lane issues in uniform registers: the MMAs then go out at the tensor pipe's own
+// rate (32 cycles for N = 128, 64 for N = 256), which a plain lane == 0 does
+// not reach (54 cycles for N = 128 in a loop of MMAs alone).
+__device__ __forceinline__ bool elect_one()
 {
-    asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
-                 "[%1, {%2, %3}], [%4];" ::"r"(dst),
-                 "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
+// Arrive on a barrier of either CTA of the pair, releasing at CTA scope: what
+// it announces lies in this CTA's shared or tensor memory.  A release at cluster
+// scope waits for more than that and took most of a tile's time.
+__device__ __forceinline__ void arrive_pair(uint32_t cluster_bar)
+{
+    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+
+// Atoms of 64 columns (block, block + 1, ... as the map's box has) of consecutive rows into this CTA's shared memory.
+// The barrier may be either CTA's of the pair.
+__device__ __forceinline__ void load_atoms(uint32_t dst, const CUtensorMap *map, uint32_t bar, int32_t block, int32_t row)
+{
+    asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+                 "[%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(block), "r"(bar)
                  : "memory");
 }
 
@@ -252,10 +279,10 @@ __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    dense_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv, Params p)
+    dense_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv2,
+                     const __grid_constant__ CUtensorMap tm_kv3, Params p)
 {
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) uint8_t smem[]; // the swizzle's period; no other shared memory in this kernel
     const uint32_t sbase = smem_u32(smem);
     const uint32_t bar0 = sbase + OFF_BAR;
     auto bar = [&](int i) { return bar0 + 8u * i; };
@@ -268,24 +295,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int cid = blockIdx.x >> 1;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kStages * kGroups; ++i)
             mbar_init(bar(B_KF + i), 1);
+        for (int i = 0; i < 4; ++i) {
             mbar_init(bar(B_E + i), 1);
-            mbar_init(bar(B_RB + i), 2);
+            mbar_init(bar(B_RB + i), kSoftWarps / 2);
+            mbar_init(bar(B_RL + i), kSoftWarps / 2);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(B_SF + i), 1);
-            mbar_init(bar(B_SE + i), 8);
             mbar_init(bar(B_QD + i), 1);
             mbar_init(bar(B_VL + i), 1);
-            mbar_init(bar(B_P0 + i), 8);
-            mbar_init(bar(B_P1 + i), 4);
-            mbar_init(bar(B_RL + i), 2);
+            mbar_init(bar(B_P + i), 2 * kSoftWarps);
         }
         mbar_init(bar(B_OF), 1);
-        mbar_init(bar(B_OE), 8);
+        mbar_init(bar(B_OE), 2 * kSoftWarps);
         mbar_init(bar(B_QF), 1);
-        mbar_init(bar(B_DONE), 1);
+        mbar_init(bar(B_DONE), 2);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -374,45 +400,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 ok = false;
                 break;
             }
-            if (lane == 0) {
+            if (elect_one()) {
                 if (rank == 0)
                     mbar_arrive_expect_tx(bar(B_QF), 2 * kStage);
-                for (int a = 0; a < kAtoms; ++a)
-                    tma_load_2d_pair(sbase + OFF_Q + a * kAtom, &tm_q, lead(B_QF), 64 * a, un.row * p.H + 64 * (int)rank);
+                load_atoms(sbase + OFF_Q, &tm_q, lead(B_QF), 0, un.row * p.H + 64 * (int)rank);
             }
+            __syncwarp();
             ++u;
             for (int j = un.jb; j < un.je; ++j, ++i) {
                 const int st = i & 1;
                 pg.advance(p, un, j);
                 int r[2] = {pg.get(j, 0), pg.get(j, 1)};
-                // prefetch: the unit's first tiles at once, then one a tile
-                for (int f = j == un.jb ? j + 1 : j + kPrefetch; f <= j + kPrefetch && f < un.je; ++f) {
-                    const int r0 = pg.get(f, 0), r1 = pg.get(f, 1);
-                    if (lane == 0 && r0 >= 0)
-                        prefetch_l2(p.pool + (int64_t)r0 * kD, kStage / boxes);
-                    if (lane == 0 && boxes == 2 && r1 >= 0)
-                        prefetch_l2(p.pool + (int64_t)r1 * kD, kStage / 2);
-                }
                 if (lane == 0 && (r[0] == -2 || (boxes == 2 && r[1] == -2)))
                     atomicOr(p.status, DSA_DEV_BAD_PAGE);
-                for (int g = 0; g < 2 && ok; ++g) {
-                    if (i >= 2 && !mbar_wait_warp(bar(B_E + 2 * st + g), ((i >> 1) - 1) & 1, abort_flag, p.status)) {
+                for (int g = 0; g < kGroups; ++g) {
+                    // atoms 0-3 hold the value columns of the first 64 keys, 4-7 of the second
+                    if ((g & 1) == 0 && i >= 2 &&
+                        !mbar_wait_warp(bar(B_E + 2 * st + (g >> 1)), ((i >> 1) - 1) & 1, abort_flag, p.status)) {
                         ok = false;
                         break;
                     }
-                    if (lane == 0) {
-                        const int a0 = g ? 4 : 0, a1 = g ? kAtoms : 4;
+                    if (elect_one()) {
+                        const int n = g == kGroups - 1 ? 3 : 2, per = boxes == 2 ? 1 : n;
                         if (rank == 0)
-                            mbar_arrive_expect_tx(bar(B_KF + 2 * st + g), 2 * (a1 - a0) * kAtom);
-                        for (int a = a0; a < a1; ++a)
+                            mbar_arrive_expect_tx(bar(B_KF + kGroups * st + g), 2 * n * kAtom);
+                        for (int a = 0; a < n; a += per)
                             for (int b = 0; b < boxes; ++b)
-                                tma_load_2d_pair(sbase + OFF_KV + st * kStage + a * kAtom + b * box_bytes, &tm_kv,
-                                                 lead(B_KF + 2 * st + g), 64 * a, r[b] >= 0 ? r[b] : oob);
+                                load_atoms(sbase + OFF_KV + st * kStage + (2 * g + a) * kAtom + b * box_bytes,
+                                           n == 3 ? &tm_kv3 : &tm_kv2, lead(B_KF + kGroups * st + g), 2 * g + a,
+                                           r[b] >= 0 ? r[b] : oob);
                     }
                     __syncwarp();
                 }
                 if (!ok)
                     break;
+                // behind this tile's loads, the one after the next: the copy engine takes requests in order
+                if (j + kPrefetch < un.je) {
+                    const int r0 = pg.get(j + kPrefetch, 0), r1 = pg.get(j + kPrefetch, 1);
+                    if (elect_one()) {
+                        if (r0 >= 0)
+                            prefetch_l2(p.pool + (int64_t)r0 * kD, kStage / boxes);
+                        if (boxes == 2 && r1 >= 0)
+                            prefetch_l2(p.pool + (int64_t)r1 * kD, kStage / 2);
+                    }
+                    __syncwarp();
+                }
             }
         }
     } else if (warp == 2) {
@@ -436,12 +468,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     ok = false;
                     break;
                 }
-                if (lane == 0) {
+                if (elect_one()) {
                     mbar_arrive_expect_tx(bar(B_VL + st), 4 * kAtom);
-                    for (int a = 0; a < 4; ++a)
+                    for (int a = 0; a < 4; a += boxes == 2 ? 1 : 2)
                         for (int b = 0; b < boxes; ++b)
-                            tma_load_2d(sbase + OFF_KV + st * kStage + (y0 + a) * kAtom + b * box_bytes, &tm_kv, bar(B_VL + st),
-                                        64 * (a0 + a), r[b] >= 0 ? r[b] : oob);
+                            load_atoms(sbase + OFF_KV + st * kStage + (y0 + a) * kAtom + b * box_bytes, &tm_kv2, bar(B_VL + st),
+                                       a0 + a, r[b] >= 0 ? r[b] : oob);
                 }
                 __syncwarp();
             }
@@ -450,97 +482,94 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_drain(bar(B_VL + ((i - 1) & 1)), ((i - 1) >> 1) & 1);
         __syncwarp();
     } else if (warp == 1 && rank == 0) {
-        // ------------------------------------------------------------- MMAs
-        constexpr uint32_t idesc_qk = idesc_f32acc(128, 128, 1u, false, false);
-        constexpr uint32_t idesc_pv = idesc_f32acc(128, 256, 1u, false, true);
-        const uint64_t qd = sdesc(sbase + OFF_Q, 16, 1024, 2), kd = sdesc(sbase + OFF_KV, 16, 1024, 2);
-        const uint64_t vd = sdesc(sbase + OFF_KV, kAtom, 1024, 2);
-        const uint64_t pd0 = sdesc(sbase + OFF_KV + 8 * kAtom, 16, 1024, 2), pd1 = sdesc(sbase + OFF_P1, 16, 1024, 2);
-        uint32_t i = 0;
-        int u = 0;
-        bool ok = true;
-        auto scores = [&](bool first) { // of tile i
-            const int st = i & 1;
-            const uint64_t so = (uint64_t)((st * kStage) >> 4);
-            if ((first && !mbar_wait_warp(bar(B_QF), u & 1, abort_flag, p.status)) ||
-                (i >= 2 && !mbar_wait_warp<true>(bar(B_SE + st), ((i >> 1) - 1) & 1, abort_flag, p.status)) ||
-                !mbar_wait_warp(bar(B_KF + 2 * st), (i >> 1) & 1, abort_flag, p.status))
-                return false;
-            tc_fence_after();
-            if (lane == 0) {
+        // ----------------------------------------------------- score MMAs
+        // KF of a tile implies that its stage's last P, and with it the scores
+        // that this buffer held, have been consumed.
+        if (elect_one()) {
+            constexpr uint32_t idesc = idesc_f32acc(128, 128, 1u, false, false);
+            const uint64_t qd = sdesc(sbase + OFF_Q, 16, 1024, 2), kd = sdesc(sbase + OFF_KV, 16, 1024, 2);
+            Walk it(*share);
+            Unit un;
+            uint32_t t = 0;
+            bool ok = true;
+            for (int u = 0; ok && it.next_filled(p, cid, un); ++u) {
+                ok = mbar_wait(bar(B_QF), u & 1, abort_flag, p.status);
+                for (int j = un.jb; ok && j < un.je; ++j, ++t) {
+                    const int st = t & 1;
+                    const uint64_t so = (uint64_t)((st * kStage) >> 4);
 #pragma unroll
-                for (int s = 0; s < 16; ++s)
-                    umma_f16_pair(tmem + TM_S + 64 * st, qd + (((s >> 2) * kAtom + (s & 3) * 32) >> 4),
-                                  kd + so + (((s >> 2) * kAtom + (s & 3) * 32) >> 4), idesc_qk, s > 0);
-                umma_commit_pair(bar(B_QD + st));
+                    for (int g = 0; g < kGroups; ++g) {
+                        if (!mbar_wait(bar(B_KF + kGroups * st + g), (t >> 1) & 1, abort_flag, p.status)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+#pragma unroll
+                        for (int s = 8 * g; s < (g == kGroups - 1 ? 36 : 8 * g + 8); ++s)
+                            umma_f16_pair(tmem + TM_S + 64 * st, qd + (((s >> 2) * kAtom + (s & 3) * 32) >> 4),
+                                          kd + so + (((s >> 2) * kAtom + (s & 3) * 32) >> 4), idesc, s > 0);
+                        if (g == 1)
+                            umma_commit_pair(bar(B_QD + st));
+                        if (g == kGroups - 1)
+                            umma_commit_pair(bar(B_SF + st));
+                    }
+                }
             }
-            __syncwarp();
-            if (!mbar_wait_warp(bar(B_KF + 2 * st + 1), (i >> 1) & 1, abort_flag, p.status))
-                return false;
-            if (lane == 0) {
+            umma_commit_pair(bar(B_DONE));
+            mbar_drain(bar(B_DONE), 0);
+        }
+        __syncwarp();
+    } else if (warp == 3 && rank == 0) {
+        // -------------------------------------------------------- PV MMAs
+        // A thread of its own: neither its waits nor the score MMAs' hold the
+        // other up, and a PV frees the stage that the loads wait for.
+        if (elect_one()) {
+            constexpr uint32_t idesc = idesc_f32acc(128, 256, 1u, false, true);
+            const uint64_t vd = sdesc(sbase + OFF_KV, kAtom, 1024, 2);
+            const uint64_t pd0 = sdesc(sbase + OFF_KV + 8 * kAtom, 16, 1024, 2), pd1 = sdesc(sbase + OFF_P1, 16, 1024, 2);
+            Walk it(*share);
+            Unit un;
+            uint32_t t = 0;
+            bool ok = true;
+            for (int u = 0; ok && it.next_filled(p, cid, un); ++u) {
+                // a unit's first PV overwrites O: the previous unit's must have been read
+                ok = u == 0 || mbar_wait(bar(B_OE), (u - 1) & 1, abort_flag, p.status);
+                for (int j = un.jb; ok && j < un.je; ++j, ++t) {
+                    const int st = t & 1;
+                    const uint64_t so = (uint64_t)((st * kStage) >> 4);
+                    if (!mbar_wait(bar(B_P + st), (t >> 1) & 1, abort_flag, p.status)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
 #pragma unroll
-                for (int s = 16; s < 36; ++s)
-                    umma_f16_pair(tmem + TM_S + 64 * st, qd + (((s >> 2) * kAtom + (s & 3) * 32) >> 4),
-                                  kd + so + (((s >> 2) * kAtom + (s & 3) * 32) >> 4), idesc_qk, 1u);
-                umma_commit_pair(bar(B_SF + st));
-            }
-            __syncwarp();
-            return true;
-        };
-        auto values = [&](uint32_t t, bool first, bool last) { // of tile t
-            const int st = t & 1;
-            const uint64_t so = (uint64_t)((st * kStage) >> 4);
-            // a unit's first PV overwrites O: the previous unit's must have been read
-            if (first && u > 0 && !mbar_wait_warp<true>(bar(B_OE), (u - 1) & 1, abort_flag, p.status))
-                return false;
-            for (int kb = 0; kb < 2; ++kb) {
-                if (!mbar_wait_warp<true>(bar((kb ? B_P1 : B_P0) + st), (t >> 1) & 1, abort_flag, p.status))
-                    return false;
-                tc_fence_after();
-                if (lane == 0) {
-                    const uint64_t pd = kb ? pd1 : pd0 + so;
+                    for (int kb = 0; kb < 2; ++kb) {
 #pragma unroll
-                    for (int n = 0; n < 2; ++n)
+                        for (int n = 0; n < 2; ++n)
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            umma_f16_pair(tmem + TM_O + 128 * n, pd + 2 * k,
-                                          vd + so + (((4 * kb + 2 * n) * kAtom + 16 * 128 * k) >> 4), idesc_pv,
-                                          !(first && kb == 0 && k == 0));
-                    umma_commit_pair(bar(B_E + 2 * st + kb));
-                    if (kb == 1 && last)
+                            for (int k = 0; k < 4; ++k)
+                                umma_f16_pair(tmem + TM_O + 128 * n, (kb ? pd1 : pd0 + so) + 2 * k,
+                                              vd + so + (((4 * kb + 2 * n) * kAtom + 16 * 128 * k) >> 4), idesc,
+                                              kb || k || j > un.jb);
+                        umma_commit_pair(bar(B_E + 2 * st + kb));
+                    }
+                    if (j == un.je - 1)
                         umma_commit_pair(bar(B_OF));
                 }
-                __syncwarp();
             }
-            return true;
-        };
-        Walk it(*share);
-        Unit un;
-        while (ok && it.next(p, cid, un)) {
-            if (un.ctx == 0)
-                continue;
-            const int n = un.je - un.jb;
-            for (int j = 0; j <= n && ok; ++j) {
-                if (j < n)
-                    ok = scores(j == 0);
-                if (ok && j > 0)
-                    ok = values(i - 1, j == 1, j == n);
-                if (j < n)
-                    ++i;
-            }
-            ++u;
-        }
-        if (lane == 0) {
             umma_commit_pair(bar(B_DONE));
             mbar_drain(bar(B_DONE), 0);
         }
         __syncwarp();
     } else if (warp >= kSoftWarp0) {
         // ---------------------------------------------------------- softmax
-        const int quad = warp & 3, kb = quad >> 1, pair = quad & 1;
-        const int t128 = 32 * quad + lane, hl = t128 & 63, h = 64 * (int)rank + hl;
+        // Warp: TMEM lane quadrant, and 32 of its 64 score columns.  Thread:
+        // head hl of this CTA, keys [64 kb + 32 part, + 32) of the tile.
+        const int quad = warp & 3, part = (warp - kSoftWarp0) >> 2, kb = quad >> 1, pair = quad & 1;
+        const int hl = 32 * pair + lane, h = 64 * (int)rank + hl;
         const uint32_t lane_off = (uint32_t)(32 * quad) << 16;
         const bool swapped = kb != (int)rank; // this CTA's value columns of key block kb are swapped in
+        float *xrow = xs + hl * 4, *xmine = xrow + 2 * kb + part;
         uint32_t i = 0;
         int u = 0;
         bool ok = true;
@@ -550,12 +579,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         while (ok && it.next(p, cid, un)) {
             float m = -INFINITY, l = 0.f;
             const int64_t orow = (int64_t)un.row * p.H + h, prow = (int64_t)un.slot * p.H + h;
+            const int col0 = 256 * kb + 128 * part; // of O: lanes 0-63 hold columns [0, 256), lanes 64-127 the others
             if (un.ctx == 0) {
                 if (h < p.H) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(p.out + orow * kDv + 256 * kb);
-                    for (int c = 0; c < 32; ++c)
+                    uint4 *dst = reinterpret_cast<uint4 *>(p.out + orow * kDv + col0);
+                    for (int c = 0; c < 16; ++c)
                         dst[c] = make_uint4(0, 0, 0, 0);
-                    if (kb == 0)
+                    if (col0 == 0)
                         p.lse[orow] = -INFINITY;
                 }
                 continue;
@@ -564,35 +594,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int j = un.jb; j < un.je; ++j, ++i) {
                 const int st = i & 1;
                 pg.advance(p, un, j);
-                const bool bad0 = pg.get(j, 0) < 0, bad1 = boxes == 2 ? pg.get(j, 1) < 0 : bad0;
-                const int64_t left = (int64_t)un.ctx - (int64_t)j * kTile - 64 * kb;
-                const int valid = left < 0 ? 0 : left < 64 ? (int)left : 64;
+                const bool bad = pg.get(j, boxes == 2 ? part : 0) < 0;
+                const int64_t left = (int64_t)un.ctx - (int64_t)j * kTile - 64 * kb - 32 * part;
+                const int valid = bad || left < 0 ? 0 : left < 32 ? (int)left : 32;
                 if (!mbar_wait_warp(bar(B_SF + st), (i >> 1) & 1, abort_flag, p.status)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                uint32_t s[2][32];
-                tmem_ld32(tmem + lane_off + TM_S + 64 * st, s[0]);
-                tmem_ld32(tmem + lane_off + TM_S + 64 * st + 32, s[1]);
+                uint32_t s[32];
+                tmem_ld32(tmem + lane_off + TM_S + 64 * st + 32 * part, s);
                 tmem_ld_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive_remote(lead(B_SE + st));
-                float mx = -INFINITY;
-                if (valid < 64 || bad0 || bad1) {
+                if (valid < 32) {
 #pragma unroll
-                    for (int c = 0; c < 64; ++c)
-                        if (c >= valid || (c < 32 ? bad0 : bad1))
-                            s[c >> 5][c & 31] = 0xFF800000u;
+                    for (int c = 0; c < 32; ++c)
+                        if (c >= valid)
+                            s[c] = 0xFF800000u;
                 }
+                float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int c = 0; c < 64; ++c)
-                    mx = fmaxf(mx, __uint_as_float(s[c >> 5][c & 31]));
-                mx *= p.scale_log2; // scale > 0; -inf stays
-                // the head's other thread
-                xs[128 * (i & 1) + t128] = mx;
+                for (int c = 0; c < 32; ++c)
+                    mx4[c & 3] = fmaxf(mx4[c & 3], __uint_as_float(s[c]));
+                // the head's four threads; scale > 0, and -inf stays
+                xmine[256 * (i & 1)] = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * p.scale_log2;
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(bar(B_RB + 2 * pair + (i & 1)));
@@ -600,7 +624,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     ok = false;
                     break;
                 }
-                mx = fmaxf(mx, xs[128 * (i & 1) + (t128 ^ 64)]);
+                const float4 x4 = *reinterpret_cast<const float4 *>(xrow + 256 * (i & 1));
+                const float mx = fmaxf(fmaxf(x4.x, x4.y), fmaxf(x4.z, x4.w));
                 const bool first = j == un.jb;
                 const bool move = mx > m + kRescaleLog2 || (m == -INFINITY && mx > m);
                 const bool rescale = !first && __any_sync(0xffffffffu, move);
@@ -615,38 +640,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     const float f = move ? exp2_fast(m - mx) : 1.f;
                     l *= f;
 #pragma unroll 1
-                    for (int c = 0; c < 256; c += 32) {
+                    for (int c = 0; c < 128; c += 32) {
                         uint32_t o[32];
-                        tmem_ld32(tmem + lane_off + TM_O + c, o);
+                        tmem_ld32(tmem + lane_off + TM_O + 128 * part + c, o);
                         tmem_ld_wait();
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
                             o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                        tmem_st32(tmem + lane_off + TM_O + c, o);
+                        tmem_st32(tmem + lane_off + TM_O + 128 * part + c, o);
                     }
                     tmem_st_wait();
-                    tc_fence_before();
                 }
                 if (move)
                     m = mx;
-                if (kb == 1) { // O is as the first PV of this tile wants it
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive_remote(lead(B_P0 + st));
-                }
                 const float ms = m == -INFINITY ? 0.f : m;
                 uint8_t *prow_s = smem + (kb ? OFF_P1 : OFF_KV + st * kStage + 8 * kAtom) + hl * 128;
                 float sum = 0.f;
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
+                for (int c = 0; c < 4; ++c) {
                     float e[8];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const int x = 8 * c + k;
-                        e[k] = exp2_fast(fmaf(__uint_as_float(s[x >> 5][x & 31]), p.scale_log2, -ms));
-                    }
+                    for (int k = 0; k < 8; ++k)
+                        e[k] = exp2_fast(fmaf(__uint_as_float(s[8 * c + k]), p.scale_log2, -ms));
                     sum += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
-                    *reinterpret_cast<uint4 *>(prow_s + ((c ^ (hl & 7)) << 4)) =
+                    *reinterpret_cast<uint4 *>(prow_s + (((4 * part + c) ^ (hl & 7)) << 4)) =
                         make_uint4(pack2(e[0], e[1]), pack2(e[2], e[3]), pack2(e[4], e[5]), pack2(e[6], e[7]));
                 }
                 l += sum;
@@ -654,44 +671,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     ok = false;
                     break;
                 }
-                if (valid < 64) { // value rows past the end
-                    for (int x = valid * 8 + 32 * pair + lane; x < 64 * 8; x += 64)
+                if (left < 32) { // value rows past the end, of this warp's 32 keys
+                    const int from = 32 * part + (left < 0 ? 0 : (int)left);
+                    for (int x = from * 8 + 32 * pair + lane; x < (32 * part + 32) * 8; x += 64)
 #pragma unroll
                         for (int a = 0; a < 4; ++a)
                             *reinterpret_cast<uint4 *>(smem + OFF_KV + st * kStage + (4 * kb + a) * kAtom + x * 16) =
                                 make_uint4(0, 0, 0, 0);
                 }
+                tc_fence_before();
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive_remote(lead((kb ? B_P1 : B_P0) + st));
+                    arrive_pair(lead(B_P + st));
             }
             if (!ok)
                 break;
             // ---- the unit's output
-            xs[256 + t128] = l;
+            // the sums go where the next tile's maxima do: all four threads have read the ones before
+            xmine[256 * (i & 1)] = l;
             __syncwarp();
             if (lane == 0)
-                mbar_arrive(bar(B_RL + pair));
-            if (!mbar_wait_warp(bar(B_RL + pair), u & 1, abort_flag, p.status) ||
+                mbar_arrive(bar(B_RL + 2 * pair));
+            if (!mbar_wait_warp(bar(B_RL + 2 * pair), u & 1, abort_flag, p.status)) {
+                ok = false;
+                break;
+            }
+            const float4 l4 = *reinterpret_cast<const float4 *>(xrow + 256 * (i & 1));
+            l = (l4.x + l4.y) + (l4.z + l4.w);
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(bar(B_RL + 2 * pair + 1)); // read
+            if (!mbar_wait_warp(bar(B_RL + 2 * pair + 1), u & 1, abort_flag, p.status) ||
                 !mbar_wait_warp(bar(B_OF), u & 1, abort_flag, p.status)) {
                 ok = false;
                 break;
             }
             ++u;
-            l += xs[256 + (t128 ^ 64)];
             const float inv = l > 0.f ? 1.f / l : 0.f;
             tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < 256; c += 32) {
+            for (int c = 0; c < 128; c += 32) {
                 uint32_t o[32];
-                tmem_ld32(tmem + lane_off + TM_O + c, o);
+                tmem_ld32(tmem + lane_off + TM_O + 128 * part + c, o);
                 tmem_ld_wait();
                 if (h >= p.H)
                     continue;
-                // lanes 0-63: columns [0, 256); lanes 64-127: [256, 512)
                 if (un.slot < 0) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(p.out + orow * kDv + 256 * kb + c);
+                    uint4 *dst = reinterpret_cast<uint4 *>(p.out + orow * kDv + col0 + c);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         uint32_t w[4];
@@ -701,7 +728,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 } else {
-                    float4 *dst = reinterpret_cast<float4 *>(p.ws_o + prow * kDv + 256 * kb + c);
+                    float4 *dst = reinterpret_cast<float4 *>(p.ws_o + prow * kDv + col0 + c);
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
                         dst[e] = make_float4(__uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
@@ -711,8 +738,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0)
-                mbar_arrive_remote(lead(B_OE));
-            if (h < p.H && kb == 0) {
+                arrive_pair(lead(B_OE));
+            if (h < p.H && col0 == 0) {
                 const float v = l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
                 if (un.slot < 0)
                     p.lse[orow] = v;
@@ -845,16 +872,21 @@ int launch_dense_mla(const DenseMlaArgs &a, cudaStream_t stream, char *err, size
     p.ws_o = reinterpret_cast<float *>(ws);
     p.ws_lse = reinterpret_cast<float *>(ws + align256(parts * kDv * sizeof(float)));
     p.row_start = reinterpret_cast<int64_t *>(ws + align256(parts * kDv * sizeof(float)) + align256(parts * sizeof(float)));
-    CUtensorMap tq, tkv;
-    if (!encode_tmap_2d(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, kD, (uint64_t)a.B * a.H, kD * 2, 64, 64,
-                        CU_TENSOR_MAP_SWIZZLE_128B, err, errlen) ||
-        !encode_tmap_2d(&tkv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.kv_pool, kD, (uint64_t)a.num_pages * a.page_size, kD * 2, 64,
-                        a.page_size < 64 ? a.page_size : 64, CU_TENSOR_MAP_SWIZZLE_128B, err, errlen))
+    CUtensorMap tq, tkv2, tkv3;
+    const uint64_t rows = (uint64_t)a.num_pages * a.page_size;
+    const uint32_t box = a.page_size < 64 ? a.page_size : 64;
+    auto map = [&](CUtensorMap *m, const void *base, uint64_t n, uint32_t box_rows, uint32_t atoms) {
+        return encode_tmap_blocks(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, 64, n, kAtoms, kD * 2, 128, box_rows, atoms,
+                                  CU_TENSOR_MAP_SWIZZLE_128B, err, errlen);
+    };
+    // pages of 32: an atom takes two boxes, so a box holds one atom
+    if (!map(&tq, a.q, (uint64_t)a.B * a.H, 64, kAtoms) || !map(&tkv2, a.kv_pool, rows, box, box < 64 ? 1 : 2) ||
+        !map(&tkv3, a.kv_pool, rows, box, box < 64 ? 1 : 3))
         return DSA_ERR_CUDA;
     static std::atomic<bool> raised[64];
     cudaError_t e = raise_smem_limit_once(dense_mla_kernel, kSmem, raised);
     if (e == cudaSuccess)
-        e = launch_pdl(dense_mla_kernel, dim3(2 * p.clusters), dim3(kThreads), kSmem, stream, 1, tq, tkv, p);
+        e = launch_pdl(dense_mla_kernel, dim3(2 * p.clusters), dim3(kThreads), kSmem, stream, 1, tq, tkv2, tkv3, p);
     if (e == cudaSuccess)
         e = launch_pdl(dense_mla_join_kernel, dim3(a.B, a.H), dim3(256), 0, stream, 1, p);
     if (e != cudaSuccess) {

@@ -15,6 +15,12 @@ bool encode_tmap_2d(CUtensorMap *map, CUtensorMapDataType dtype, const void *bas
                     uint64_t rows, uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_rows,
                     CUtensorMapSwizzle swizzle, char *err, size_t errlen);
 
+// The same over rows of `blocks` column blocks of `inner` elements each: a box
+// is box_blocks blocks of box_rows rows, laid out block by block.
+bool encode_tmap_blocks(CUtensorMap *map, CUtensorMapDataType dtype, const void *base, uint64_t inner, uint64_t rows,
+                        uint64_t blocks, uint64_t row_stride_bytes, uint64_t block_stride_bytes, uint32_t box_rows,
+                        uint32_t box_blocks, CUtensorMapSwizzle swizzle, char *err, size_t errlen);
+
 int num_sms();
 
 // Records a message for dsa_last_error() on this host thread and returns `code`.
