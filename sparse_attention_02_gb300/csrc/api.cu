@@ -111,7 +111,7 @@ bool encode_tmap(CUtensorMap *map, CUtensorMapDataType dtype, const void *base, 
             g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
         }
     }
-    const cuuint32_t estr[3] = {1, 1, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
     CUresult r = g_encode(map, dtype, rank, const_cast<void *>(base), dims, strides, box, estr,
                           CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -136,13 +136,13 @@ bool encode_tmap_2d(CUtensorMap *map, CUtensorMapDataType dtype, const void *bas
 }
 
 bool encode_tmap_blocks(CUtensorMap *map, CUtensorMapDataType dtype, const void *base, uint64_t inner, uint64_t rows,
-                        uint64_t blocks, uint64_t row_stride_bytes, uint64_t block_stride_bytes, uint32_t box_rows,
-                        uint32_t box_blocks, CUtensorMapSwizzle swizzle, char *err, size_t errlen)
+                        uint64_t blocks, uint64_t groups, uint64_t row_stride_bytes, uint64_t block_stride_bytes,
+                        uint32_t box_rows, uint32_t box_blocks, CUtensorMapSwizzle swizzle, char *err, size_t errlen)
 {
-    const cuuint64_t dims[3] = {inner, rows > 0 ? rows : 1, blocks};
-    const cuuint64_t strides[2] = {row_stride_bytes, block_stride_bytes};
-    const cuuint32_t box[3] = {(cuuint32_t)inner, box_rows, box_blocks};
-    return encode_tmap(map, dtype, base, 3, dims, strides, box, swizzle, err, errlen);
+    const cuuint64_t dims[4] = {inner, rows, blocks, groups};
+    const cuuint64_t strides[3] = {row_stride_bytes, block_stride_bytes, rows * row_stride_bytes};
+    const cuuint32_t box[4] = {(cuuint32_t)inner, box_rows, box_blocks, 1};
+    return encode_tmap(map, dtype, base, 4, dims, strides, box, swizzle, err, errlen);
 }
 
 } // namespace dsa

@@ -237,11 +237,12 @@ __device__ __forceinline__ void arrive_pair(uint32_t cluster_bar)
 
 // Atoms of 64 columns (block, block + 1, ... as the map's box has) of consecutive rows into this CTA's shared memory.
 // The barrier may be either CTA's of the pair.
-__device__ __forceinline__ void load_atoms(uint32_t dst, const CUtensorMap *map, uint32_t bar, int32_t block, int32_t row)
+__device__ __forceinline__ void load_atoms(uint32_t dst, const CUtensorMap *map, uint32_t bar, int32_t block, int32_t row,
+                                           int32_t group = 0)
 {
-    asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
-                 "[%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-                 "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(block), "r"(bar)
+    asm volatile("cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+                 "[%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(block), "r"(group), "r"(bar)
                  : "memory");
 }
 
@@ -403,7 +404,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (elect_one()) {
                 if (rank == 0)
                     mbar_arrive_expect_tx(bar(B_QF), 2 * kStage);
-                load_atoms(sbase + OFF_Q, &tm_q, lead(B_QF), 0, un.row * p.H + 64 * (int)rank);
+                load_atoms(sbase + OFF_Q, &tm_q, lead(B_QF), 0, 64 * (int)rank, un.row); // heads past H: zeros
             }
             __syncwarp();
             ++u;
@@ -596,7 +597,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 pg.advance(p, un, j);
                 const bool bad = pg.get(j, boxes == 2 ? part : 0) < 0;
                 const int64_t left = (int64_t)un.ctx - (int64_t)j * kTile - 64 * kb - 32 * part;
-                const int valid = bad || left < 0 ? 0 : left < 32 ? (int)left : 32;
+                // heads past H have Q = 0; P = 0 too costs the MMAs the least power
+                const int valid = bad || left < 0 || h >= p.H ? 0 : left < 32 ? (int)left : 32;
                 if (!mbar_wait_warp(bar(B_SF + st), (i >> 1) & 1, abort_flag, p.status)) {
                     ok = false;
                     break;
@@ -875,13 +877,13 @@ int launch_dense_mla(const DenseMlaArgs &a, cudaStream_t stream, char *err, size
     CUtensorMap tq, tkv2, tkv3;
     const uint64_t rows = (uint64_t)a.num_pages * a.page_size;
     const uint32_t box = a.page_size < 64 ? a.page_size : 64;
-    auto map = [&](CUtensorMap *m, const void *base, uint64_t n, uint32_t box_rows, uint32_t atoms) {
-        return encode_tmap_blocks(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, 64, n, kAtoms, kD * 2, 128, box_rows, atoms,
-                                  CU_TENSOR_MAP_SWIZZLE_128B, err, errlen);
+    auto map = [&](CUtensorMap *m, const void *base, uint64_t n, uint64_t groups, uint32_t box_rows, uint32_t atoms) {
+        return encode_tmap_blocks(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, 64, n, kAtoms, groups, kD * 2, 128, box_rows,
+                                  atoms, CU_TENSOR_MAP_SWIZZLE_128B, err, errlen);
     };
     // pages of 32: an atom takes two boxes, so a box holds one atom
-    if (!map(&tq, a.q, (uint64_t)a.B * a.H, 64, kAtoms) || !map(&tkv2, a.kv_pool, rows, box, box < 64 ? 1 : 2) ||
-        !map(&tkv3, a.kv_pool, rows, box, box < 64 ? 1 : 3))
+    if (!map(&tq, a.q, a.H, a.B, 64, kAtoms) || !map(&tkv2, a.kv_pool, rows, 1, box, box < 64 ? 1 : 2) ||
+        !map(&tkv3, a.kv_pool, rows, 1, box, box < 64 ? 1 : 3))
         return DSA_ERR_CUDA;
     static std::atomic<bool> raised[64];
     cudaError_t e = raise_smem_limit_once(dense_mla_kernel, kSmem, raised);

@@ -15,11 +15,13 @@ bool encode_tmap_2d(CUtensorMap *map, CUtensorMapDataType dtype, const void *bas
                     uint64_t rows, uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_rows,
                     CUtensorMapSwizzle swizzle, char *err, size_t errlen);
 
-// The same over rows of `blocks` column blocks of `inner` elements each: a box
-// is box_blocks blocks of box_rows rows, laid out block by block.
+// `groups` groups of `rows` rows, each row `blocks` column blocks of `inner`
+// elements: a box is box_blocks blocks of box_rows rows of one group, laid out
+// block by block; rows past a group's end arrive as zeros.  Coordinates: column
+// in the block, row, block, group.
 bool encode_tmap_blocks(CUtensorMap *map, CUtensorMapDataType dtype, const void *base, uint64_t inner, uint64_t rows,
-                        uint64_t blocks, uint64_t row_stride_bytes, uint64_t block_stride_bytes, uint32_t box_rows,
-                        uint32_t box_blocks, CUtensorMapSwizzle swizzle, char *err, size_t errlen);
+                        uint64_t blocks, uint64_t groups, uint64_t row_stride_bytes, uint64_t block_stride_bytes,
+                        uint32_t box_rows, uint32_t box_blocks, CUtensorMapSwizzle swizzle, char *err, size_t errlen);
 
 int num_sms();
 
