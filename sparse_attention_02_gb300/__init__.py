@@ -199,32 +199,66 @@ DSA_FP32 = 1
 _DTYPE = {torch.bfloat16: DSA_BF16, torch.float32: DSA_FP32}
 
 
-def _arg(t, cur: int, name: str, dtype, shape, rows: bool = False, optional: bool = False):
-    """Address of a CUDA tensor of the current device ``cur``: ``dtype`` (or one of a tuple), ``shape``,
-    contiguous or, with ``rows``, with rows any distance >= their width apart; None where ``optional``."""
-    if t is None and optional:
-        return None
+def _device() -> int:
+    try:
+        return torch._C._cuda_getDevice()  # torch.cuda.current_device() without its initialisation check
+    except (AttributeError, RuntimeError):
+        return torch.cuda.current_device()
+
+
+def _raw_stream(stream, cur: int) -> int:
+    """The CUDA stream handle of ``stream``, or of the device's current stream."""
+    if stream is not None:
+        return stream.cuda_stream
+    try:
+        return torch._C._cuda_getCurrentRawStream(cur)
+    except AttributeError:
+        return torch.cuda.current_stream().cuda_stream
+
+
+def _refuse(t, cur: int, name: str, dtype, shape, rows: bool = False):
+    """The error for an argument that is not what its call needs."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype is not dtype and not (type(dtype) is tuple and t.dtype in dtype):
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.get_device() != cur:
         raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{cur}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if rows:
-        if (shape[1] > 1 and t.stride(1) != 1) or (shape[0] > 1 and t.stride(0) < shape[1]):
-            raise ValueError(f"{name}: rows must be contiguous with a leading dimension >= width")
-    elif not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+        raise ValueError(f"{name}: rows must be contiguous with a leading dimension >= width")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _ld(t) -> int:
-    """Distance of a 2-D tensor's rows (a single row's stride says nothing)."""
-    return 0 if t is None else max(t.stride(0), t.shape[1]) if t.shape[0] > 1 else t.shape[1]
+# The checks below are one expression each: a call on a few tokens costs the host more than the GPU.
+def _at(t, cur: int, name: str, dtype, shape) -> int:
+    """Address of a contiguous CUDA tensor of the current device ``cur``."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == cur and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(t, cur, name, dtype, shape)
+
+
+def _at_rows(t, cur: int, name: str, dtype, shape):
+    """(address, distance of the rows) of a 2-D CUDA tensor whose rows may be apart."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == cur and t.shape == shape:
+        if t.is_contiguous():
+            return t.data_ptr(), shape[1]
+        ld = t.stride(0) if shape[0] > 1 else shape[1]  # a single row's stride says nothing
+        if (shape[1] == 1 or t.stride(1) == 1) and ld >= shape[1]:
+            return t.data_ptr(), ld
+    _refuse(t, cur, name, dtype, shape, True)
+
+
+def _dtype_of(t, name: str):
+    """bf16 or fp32."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in _DTYPE:
+        raise TypeError(f"{name}: expected {_TYPES}, got {t.dtype}")
+    return t.dtype
 
 
 def _workspace(workspace, need: int, cur: int, stream):
@@ -238,7 +272,7 @@ def _workspace(workspace, need: int, cur: int, stream):
         else:
             with torch.cuda.stream(stream):
                 workspace = torch.empty(need, dtype=torch.uint8, device=cur)
-    elif not workspace.is_cuda or not workspace.is_contiguous() or workspace.get_device() != cur:
+    elif not isinstance(workspace, torch.Tensor) or workspace.get_device() != cur or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on cuda:{cur}")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
@@ -254,20 +288,29 @@ def dsa_rmsnorm(x, weight, eps: float, out=None, residual=None, residual_out=Non
     [rows, n] get y as E4M3 codes with one scale per row (block = 0) or per 128 columns (block = 128,
     n = ceil(cols / 128)).  weight [cols] is bf16 or fp32.  Rows of x, residual, residual_out and out may be
     strided.  Returns (residual_out, out, codes, scale) as given."""
-    if not isinstance(x, torch.Tensor) or x.dim() != 2:
-        raise TypeError("x must be a 2-D torch.Tensor")
-    cur, shape, t = torch.cuda.current_device(), tuple(x.shape), x.dtype
+    t = _dtype_of(x, "x")
+    if x.dim() != 2:
+        raise TypeError("x must be 2-D")
+    cur, shape, f32 = _device(), x.shape, torch.float32
     rows, cols = shape
-    n = -(-cols // block) if block else 1
-    a_scale = None
+    wt = _dtype_of(weight, "weight")
+    a_x, ldx = _at_rows(x, cur, "x", t, shape)
+    a_r = a_h = a_o = a_c = a_s = None
+    ldr = ldh = ldo = 0
+    if residual is not None:
+        a_r, ldr = _at_rows(residual, cur, "residual", t, shape)
+    if residual_out is not None:
+        a_h, ldh = _at_rows(residual_out, cur, "residual_out", t, shape)
+    if out is not None:
+        a_o, ldo = _at_rows(out, cur, "out", t, shape)
+    if codes is not None:
+        a_c = _at(codes, cur, "codes", torch.uint8, shape)
     if scale is not None:
-        a_scale = _arg(scale, cur, "scale", torch.float32, (rows,) if n == 1 and scale.dim() == 1 else (rows, n))
-    _check(load_library().dsa_rmsnorm(
-        _arg(x, cur, "x", _TYPES, shape, True), _ld(x), _arg(residual, cur, "residual", t, shape, True, True),
-        _ld(residual), _arg(weight, cur, "weight", _TYPES, (cols,)), rows, cols, _DTYPE[t], _DTYPE[weight.dtype], eps,
-        _arg(residual_out, cur, "residual_out", t, shape, True, True), _ld(residual_out),
-        _arg(out, cur, "out", t, shape, True, True), _ld(out), _arg(codes, cur, "codes", torch.uint8, shape, False, True),
-        a_scale, block, scale_mode, _stream(stream)))
+        n = -(-cols // block) if block > 0 else 1
+        a_s = _at(scale, cur, "scale", f32, (rows,) if n == 1 and isinstance(scale, torch.Tensor) and scale.dim() == 1 else (rows, n))
+    _check((_lib or load_library()).dsa_rmsnorm(
+        a_x, ldx, a_r, ldr, _at(weight, cur, "weight", wt, (cols,)), rows, cols, _DTYPE[t], _DTYPE[wt], eps, a_h, ldh, a_o, ldo,
+        a_c, a_s, block, scale_mode, _raw_stream(stream, cur)))
     return residual_out, out, codes, scale
 
 
@@ -279,17 +322,19 @@ def dsa_rmsnorm_backward(dy, h, weight, eps: float, dx, dweight, dres=None, work
     """Gradients of dsa_rmsnorm: dy, h, dres (or None) and dx [rows, cols] bf16 or fp32, h the saved residual_out
     (x without a residual); dx is the gradient of x and of the residual; dweight fp32 [cols].  ``workspace``: a
     CUDA tensor of at least dsa_rmsnorm_backward_workspace_size(rows, cols) bytes; taken from PyTorch when None."""
-    if not isinstance(h, torch.Tensor) or h.dim() != 2:
-        raise TypeError("h must be a 2-D torch.Tensor")
-    cur, shape, t = torch.cuda.current_device(), tuple(h.shape), h.dtype
+    t = _dtype_of(h, "h")
+    if h.dim() != 2:
+        raise TypeError("h must be 2-D")
+    cur, shape, wt = _device(), h.shape, _dtype_of(weight, "weight")
     rows, cols = shape
-    lib = load_library()
-    args = (_arg(dy, cur, "dy", t, shape), _arg(h, cur, "h", _TYPES, shape), _arg(weight, cur, "weight", _TYPES, (cols,)),
-            _arg(dres, cur, "dres", t, shape, False, True), rows, cols, _DTYPE[t], _DTYPE[weight.dtype], eps,
-            _arg(dx, cur, "dx", t, shape), _arg(dweight, cur, "dweight", torch.float32, (cols,)))
+    lib = _lib or load_library()
+    a_dy, a_h, a_w = _at(dy, cur, "dy", t, shape), _at(h, cur, "h", t, shape), _at(weight, cur, "weight", wt, (cols,))
+    a_e = None if dres is None else _at(dres, cur, "dres", t, shape)
+    a_dx, a_dw = _at(dx, cur, "dx", t, shape), _at(dweight, cur, "dweight", torch.float32, (cols,))
     need = 0 if workspace is not None else lib.dsa_rmsnorm_backward_workspace_size(rows, cols)
     ws, ws_bytes, keep = _workspace(workspace, need, cur, stream)
-    _check(lib.dsa_rmsnorm_backward(*args, ws, ws_bytes, _stream(stream)))
+    _check(lib.dsa_rmsnorm_backward(a_dy, a_h, a_w, a_e, rows, cols, _DTYPE[t], _DTYPE[wt], eps, a_dx, a_dw, ws, ws_bytes,
+                                    _raw_stream(stream, cur)))
     return dx, dweight
 
 
@@ -310,20 +355,27 @@ def dsa_cache_append(pos, block_table, inv_freq, kv=None, kv_pool=None, kI=None,
     pool, name = (kv_pool, "kv_pool") if kv is not None else (k8_pool, "k8_pool")
     if not isinstance(pool, torch.Tensor) or pool.dim() != 3:
         raise TypeError(f"{name} must be a 3-D torch.Tensor")
-    cur, T, (P, ps) = torch.cuda.current_device(), pos.shape[0], pool.shape[:2]
-    w, k = _TYPES[0] if kv_weight is None else kv_weight.dtype, _TYPES[0] if kI is None else kI.dtype
+    cur, T, i32, bf16 = _device(), pos.shape[0], torch.int32, torch.bfloat16
+    P, ps, _ = pool.shape
+    table = block_table.shape
     a_kv = a_pool = a_w = a_k = a_k8 = a_ks = None
+    ld_kv = ld_kI = w = k = 0
     if kv is not None:
-        a_kv, a_pool = _arg(kv, cur, "kv", torch.bfloat16, (T, 576), True), _arg(kv_pool, cur, "kv_pool", torch.bfloat16, (P, ps, 576))
-        a_w = _arg(kv_weight, cur, "kv_weight", _TYPES, (512,), False, True)
+        a_kv, ld_kv = _at_rows(kv, cur, "kv", bf16, (T, 576))
+        a_pool = _at(kv_pool, cur, "kv_pool", bf16, (P, ps, 576))
+        if kv_weight is not None:
+            w = _dtype_of(kv_weight, "kv_weight")
+            a_w, w = _at(kv_weight, cur, "kv_weight", w, (512,)), _DTYPE[w]
     if kI is not None:
-        a_k, a_k8 = _arg(kI, cur, "kI", _TYPES, (T, 128), True), _arg(k8_pool, cur, "k8_pool", torch.uint8, (P, ps, 128))
-        a_ks = _arg(ks_pool, cur, "ks_pool", torch.float32, (P, ps))
-    _check(load_library().dsa_cache_append(
-        _arg(pos, cur, "pos", torch.int32, (T,)), _arg(seq, cur, "seq", torch.int32, (T,), False, True), T,
-        _arg(block_table, cur, "block_table", torch.int32, tuple(block_table.shape)), block_table.shape[0],
-        block_table.shape[1], P, ps, _arg(inv_freq, cur, "inv_freq", torch.float64, (32,)), a_kv, _ld(kv), a_w, _DTYPE[w],
-        eps, a_pool, a_k, _ld(kI), _DTYPE[k], scale_mode, a_k8, a_ks, _stream(stream)))
+        k = _dtype_of(kI, "kI")
+        a_k, ld_kI = _at_rows(kI, cur, "kI", k, (T, 128))
+        k = _DTYPE[k]
+        a_k8, a_ks = _at(k8_pool, cur, "k8_pool", torch.uint8, (P, ps, 128)), _at(ks_pool, cur, "ks_pool", torch.float32, (P, ps))
+    _check((_lib or load_library()).dsa_cache_append(
+        _at(pos, cur, "pos", i32, (T,)), None if seq is None else _at(seq, cur, "seq", i32, (T,)), T,
+        _at(block_table, cur, "block_table", i32, table), table[0], table[1], P, ps,
+        _at(inv_freq, cur, "inv_freq", torch.float64, (32,)), a_kv, ld_kv, a_w, w, eps, a_pool, a_k, ld_kI, k, scale_mode, a_k8,
+        a_ks, _raw_stream(stream, cur)))
 
 
 def dsa_rope_queries(pos, inv_freq, q_rope=None, q=None, qI=None, q8=None, q_scale=None,
@@ -334,31 +386,32 @@ def dsa_rope_queries(pos, inv_freq, q_rope=None, q=None, qI=None, q8=None, q_sca
     left out; q_rope may be q[:, :, 512:]."""
     if not isinstance(pos, torch.Tensor) or pos.dim() != 1:
         raise TypeError("pos must be a 1-D torch.Tensor")
-    cur, T = torch.cuda.current_device(), pos.shape[0]
+    if q_rope is None and qI is None:
+        raise ValueError("q_rope or qI is needed")
+    cur, T, bf16 = _device(), pos.shape[0], torch.bfloat16
     a_r = a_q = a_i = a_8 = a_s = None
     st_t = st_h = H = HI = i_type = 0
     if q_rope is not None:
-        if not isinstance(q_rope, torch.Tensor) or q_rope.dtype != torch.bfloat16 or not q_rope.is_cuda or q_rope.dim() != 3:
-            raise TypeError("q_rope: expected a 3-D CUDA bf16 tensor")
+        if not isinstance(q_rope, torch.Tensor) or q_rope.dim() != 3:
+            raise TypeError("q_rope must be a 3-D torch.Tensor")
         H = q_rope.shape[1]
-        if q_rope.get_device() != cur:
-            raise ValueError(f"q_rope is on {q_rope.device}, but the current device is cuda:{cur}")
-        if q_rope.shape[0] != T or q_rope.shape[2] != 64 or q_rope.stride(2) != 1:
-            raise ValueError("q_rope must be [T, H, 64] with contiguous last dimension")
-        a_r, st_t, st_h = q_rope.data_ptr(), q_rope.stride(0) if T > 1 else 0, q_rope.stride(1) if H > 1 else 0
-        a_q = _arg(q, cur, "q", torch.bfloat16, (T, H, 576))
+        st_t, st_h, st_d = q_rope.stride()
+        if q_rope.dtype is not bf16 or q_rope.get_device() != cur or q_rope.shape != (T, H, 64) or st_d != 1:
+            _refuse(q_rope, cur, "q_rope", bf16, (T, H, 64), True)
+        # a single token's or head's stride says nothing
+        a_r, st_t, st_h = q_rope.data_ptr(), st_t if T > 1 else 0, st_h if H > 1 else 0
+        a_q = _at(q, cur, "q", bf16, (T, H, 576))
     if qI is not None:
-        if not isinstance(qI, torch.Tensor) or qI.dim() != 3:
-            raise TypeError("qI must be a 3-D torch.Tensor")
+        i_type = _dtype_of(qI, "qI")
+        if qI.dim() != 3:
+            raise TypeError("qI must be 3-D")
         HI = qI.shape[1]
-        a_i = _arg(qI, cur, "qI", _TYPES, (T, HI, 128))
-        i_type = _DTYPE[qI.dtype]
-        a_8, a_s = _arg(q8, cur, "q8", torch.uint8, (T, HI, 128)), _arg(q_scale, cur, "q_scale", torch.float32, (T,))
-    if q_rope is None and qI is None:
-        raise ValueError("q_rope or qI is needed")
-    _check(load_library().dsa_rope_queries(
-        _arg(pos, cur, "pos", torch.int32, (T,)), _arg(inv_freq, cur, "inv_freq", torch.float64, (32,)), T, a_r, st_t, st_h,
-        H, a_q, a_i, HI, i_type, scale_mode, a_8, a_s, _stream(stream)))
+        shape = (T, HI, 128)
+        a_i, i_type = _at(qI, cur, "qI", i_type, shape), _DTYPE[i_type]
+        a_8, a_s = _at(q8, cur, "q8", torch.uint8, shape), _at(q_scale, cur, "q_scale", torch.float32, (T,))
+    _check((_lib or load_library()).dsa_rope_queries(
+        _at(pos, cur, "pos", torch.int32, (T,)), _at(inv_freq, cur, "inv_freq", torch.float64, (32,)), T, a_r, st_t, st_h, H, a_q,
+        a_i, HI, i_type, scale_mode, a_8, a_s, _raw_stream(stream, cur)))
 
 
 def dsa_index_rope_backward(g, pos, inv_freq, dx, stream=None):
@@ -366,14 +419,14 @@ def dsa_index_rope_backward(g, pos, inv_freq, dx, stream=None):
     (dsa_indexer_warmup's dq or dk), turned back by the tokens' angles into dx (bf16 or fp32, g's shape)."""
     if not isinstance(g, torch.Tensor) or g.dim() not in (2, 3):
         raise TypeError("g must be a 2-D or 3-D torch.Tensor")
-    cur, shape = torch.cuda.current_device(), tuple(g.shape)
+    shape = g.shape
     if shape[-1] != 128:
         raise ValueError("g must be [T, H_I, 128] or [T, 128]")
-    T, HI = shape[0], shape[1] if len(shape) == 3 else 1
-    _check(load_library().dsa_index_rope_backward(
-        _arg(g, cur, "g", torch.float32, shape), _arg(pos, cur, "pos", torch.int32, (T,)),
-        _arg(inv_freq, cur, "inv_freq", torch.float64, (32,)), T, HI, _arg(dx, cur, "dx", _TYPES, shape), _DTYPE[dx.dtype],
-        _stream(stream)))
+    cur, T, HI, t = _device(), shape[0], shape[1] if len(shape) == 3 else 1, _dtype_of(dx, "dx")
+    _check((_lib or load_library()).dsa_index_rope_backward(
+        _at(g, cur, "g", torch.float32, shape), _at(pos, cur, "pos", torch.int32, (T,)),
+        _at(inv_freq, cur, "inv_freq", torch.float64, (32,)), T, HI, _at(dx, cur, "dx", t, shape), _DTYPE[t],
+        _raw_stream(stream, cur)))
     return dx
 
 
@@ -562,14 +615,17 @@ def dsa_mla_decode_paged(q, kv_pool, block_table, ctx_len, sm_scale: float, out,
     if not isinstance(q, torch.Tensor) or q.dim() != 3 or not isinstance(kv_pool, torch.Tensor) or kv_pool.dim() != 3 \
             or not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
         raise TypeError("q and kv_pool must be 3-D, block_table a 2-D torch.Tensor")
-    cur, (B, H, _), (P, ps, _), mp = torch.cuda.current_device(), q.shape, kv_pool.shape, block_table.shape[1]
-    lib = load_library()
-    args = (_arg(q, cur, "q", torch.bfloat16, (B, H, 576)), _arg(kv_pool, cur, "kv_pool", torch.bfloat16, (P, ps, 576)), P, ps,
-            _arg(block_table, cur, "block_table", torch.int32, (B, mp)), mp, _arg(ctx_len, cur, "ctx_len", torch.int32, (B,)), B,
-            H, sm_scale, _arg(out, cur, "out", torch.bfloat16, (B, H, 512)), _arg(lse, cur, "lse", torch.float32, (B, H)))
+    cur, bf16, i32, mp = _device(), torch.bfloat16, torch.int32, block_table.shape[1]
+    B, H, _ = q.shape
+    P, ps, _ = kv_pool.shape
+    lib = _lib or load_library()
+    a_q, a_kv = _at(q, cur, "q", bf16, (B, H, 576)), _at(kv_pool, cur, "kv_pool", bf16, (P, ps, 576))
+    a_bt, a_ctx = _at(block_table, cur, "block_table", i32, (B, mp)), _at(ctx_len, cur, "ctx_len", i32, (B,))
+    a_out, a_lse = _at(out, cur, "out", bf16, (B, H, 512)), _at(lse, cur, "lse", torch.float32, (B, H))
     need = 0 if workspace is not None else lib.dsa_mla_decode_workspace_size(B, H)
     ws, ws_bytes, keep = _workspace(workspace, need, cur, stream)
-    _check(lib.dsa_mla_decode_paged(*args, ws, ws_bytes, _stream(stream)))
+    _check(lib.dsa_mla_decode_paged(a_q, a_kv, P, ps, a_bt, mp, a_ctx, B, H, sm_scale, a_out, a_lse, ws, ws_bytes,
+                                    _raw_stream(stream, cur)))
     return out, lse
 
 
