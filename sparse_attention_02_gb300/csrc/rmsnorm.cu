@@ -11,16 +11,22 @@
 // columns, as dsa_quantize_fp8).  Backward, with xhat = h r and g = dy weight:
 //     dx = r (g - xhat mean(g xhat)) + dres,   dweight = sum over rows of dy xhat
 //
-// Both are HBM-bound: every value is read once, kept in registers, and written
-// once.  A group of G threads (a warp, or the CTA) owns a row; thread g holds
-// the 8-value chunks c G + g, so a warp's loads are 32 consecutive 16-byte
-// words and 16 neighbouring lanes hold one 128-column FP8 block.  Sums are
-// fp32, first within a thread, then by shuffles and shared memory, in an order
-// that depends on the sizes alone: results repeat bit for bit.
+// Both are HBM-bound: every value is read once and written once.  A group of G
+// threads (a warp, or the CTA) owns a row; thread g holds the 8-value chunks
+// c G + g, so a warp's loads are 32 consecutive 16-byte words and 16
+// neighbouring lanes hold one 128-column FP8 block.  Where rows are aligned,
+// long and many, persistent CTAs (two an SM) take them through a ring in shared
+// memory that bulk copies fill while earlier rows are worked on: with the row's
+// values and sums in registers, direct loads left an SM too few threads to keep
+// HBM busy (8191 x 8192 bf16 with residual and block codes: 141 us; backward:
+// 166 us).  Sums are fp32, first within a thread, then by shuffles and shared
+// memory, in an order that depends on the sizes alone: results repeat bit for
+// bit.
 #include "common.cuh"
 #include "fp8.cuh"
 #include "launch.h"
 
+#include <atomic>
 #include <stdio.h>
 #include <type_traits>
 
@@ -167,142 +173,306 @@ __device__ __forceinline__ float2 group_reduce(float a, float b, float *red)
     return make_float2(a, b);
 }
 
+// One row: x and res (null: none) point at it, in global or shared memory.
 template <typename T, typename W, int NV, bool WARP>
-__global__ void __launch_bounds__(WARP ? kRowThreads : NV == 4 ? 256 : 1024)
-    rmsnorm_kernel(RmsNormArgs a, bool vec)
+__device__ __forceinline__ void rmsnorm_row(const RmsNormArgs &a, const T *x, const T *res, int64_t row, float *red, bool vec)
 {
-    __shared__ float red[64];
-    grid_dep_wait();
-    grid_dep_launch();
     const int G = WARP ? 32 : blockDim.x;
     const int g = WARP ? (threadIdx.x & 31) : threadIdx.x;
-    const int64_t row0 = WARP ? (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5) : blockIdx.x;
-    const int64_t step = (int64_t)gridDim.x * (WARP ? kRowThreads / 32 : 1);
     const int cols = a.cols;
     const W *weight = static_cast<const W *>(a.weight);
-    for (int64_t row = row0; row < a.rows; row += step) {
-        const T *x = static_cast<const T *>(a.x) + row * a.ldx;
-        Vec8<T> xv[NV], rv[NV];
+    Vec8<T> xv[NV], rv[NV];
+#pragma unroll
+    for (int c = 0; c < NV; ++c) {
+        const int c0 = (c * G + g) * 8;
+        load_chunk(xv[c], x, c0, cols - c0, vec);
+    }
+    if (res) {
 #pragma unroll
         for (int c = 0; c < NV; ++c) {
             const int c0 = (c * G + g) * 8;
-            load_chunk(xv[c], x, c0, cols - c0, vec);
+            load_chunk(rv[c], res, c0, cols - c0, vec);
         }
-        if (a.residual) {
-            const T *res = static_cast<const T *>(a.residual) + row * a.ldr;
+    }
+    float h[NV][8];
+    float ss = 0.f;
 #pragma unroll
-            for (int c = 0; c < NV; ++c) {
-                const int c0 = (c * G + g) * 8;
-                load_chunk(rv[c], res, c0, cols - c0, vec);
-            }
-        }
-        float h[NV][8];
-        float ss = 0.f;
-#pragma unroll
-        for (int c = 0; c < NV; ++c) {
-            xv[c].get(h[c]);
-            if (a.residual) {
-                float r[8];
-                rv[c].get(r);
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    h[c][i] += r[i];
-            }
-            float s = 0.f; // 8 values at a time, so no long fp32 chain
+    for (int c = 0; c < NV; ++c) {
+        xv[c].get(h[c]);
+        if (res) {
+            float r[8];
+            rv[c].get(r);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                s = fmaf(h[c][i], h[c][i], s);
-            ss += s;
+                h[c][i] += r[i];
         }
-        // a tensor may be overwritten in place: each chunk is written by the
-        // thread that read it
-        if (a.residual_out) {
-            T *ho = static_cast<T *>(a.residual_out) + row * a.ldh;
+        float s = 0.f; // 8 values at a time, so no long fp32 chain
 #pragma unroll
-            for (int c = 0; c < NV; ++c) {
-                const int c0 = (c * G + g) * 8;
-                Vec8<T> v;
-                v.set(h[c]);
-                store_chunk(v, ho, c0, cols - c0, vec);
-            }
-        }
-        ss = group_reduce<WARP, false>(ss, 0.f, red).x;
-        const float r = 1.f / sqrtf(ss / (float)cols + a.eps);
+        for (int i = 0; i < 8; ++i)
+            s = fmaf(h[c][i], h[c][i], s);
+        ss += s;
+    }
+    // a tensor may be overwritten in place: each chunk is written by the
+    // thread that read it
+    if (a.residual_out) {
+        T *ho = static_cast<T *>(a.residual_out) + row * a.ldh;
 #pragma unroll
         for (int c = 0; c < NV; ++c) {
             const int c0 = (c * G + g) * 8;
-            Vec8<W> wv;
-            load_chunk(wv, weight, c0, cols - c0, vec);
-            float w[8];
-            wv.get(w);
+            Vec8<T> v;
+            v.set(h[c]);
+            store_chunk(v, ho, c0, cols - c0, vec);
+        }
+    }
+    ss = group_reduce<WARP, false>(ss, 0.f, red).x;
+    const float r = 1.f / sqrtf(ss / (float)cols + a.eps);
+#pragma unroll
+    for (int c = 0; c < NV; ++c) {
+        const int c0 = (c * G + g) * 8;
+        Vec8<W> wv;
+        load_chunk(wv, weight, c0, cols - c0, vec);
+        float w[8];
+        wv.get(w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            h[c][i] = h[c][i] * r * w[i];
+    }
+    if (a.out) {
+        T *out = static_cast<T *>(a.out) + row * a.ldo;
+#pragma unroll
+        for (int c = 0; c < NV; ++c) {
+            const int c0 = (c * G + g) * 8;
+            Vec8<T> v;
+            v.set(h[c]);
+            store_chunk(v, out, c0, cols - c0, vec);
+        }
+    }
+    if (!a.codes)
+        return;
+    uint8_t *codes = a.codes + row * cols;
+    const int nblk = a.block ? (cols + a.block - 1) / a.block : 1;
+    float *scale = a.scale + row * nblk;
+    float s = 1.f;
+    if (!a.block) {
+        float m = 0.f;
+#pragma unroll
+        for (int c = 0; c < NV; ++c)
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                h[c][i] = h[c][i] * r * w[i];
-        }
-        if (a.out) {
-            T *out = static_cast<T *>(a.out) + row * a.ldo;
+                m = fmaxf(m, fabsf(h[c][i]));
+        m = group_reduce<WARP, true>(m, 0.f, red).x;
+        s = fp8_scale(m, a.scale_mode);
+        if (g == 0)
+            scale[0] = s;
+    }
 #pragma unroll
-            for (int c = 0; c < NV; ++c) {
-                const int c0 = (c * G + g) * 8;
-                Vec8<T> v;
-                v.set(h[c]);
-                store_chunk(v, out, c0, cols - c0, vec);
-            }
-        }
-        if (!a.codes)
-            continue;
-        uint8_t *codes = a.codes + row * cols;
-        const int nblk = a.block ? (cols + a.block - 1) / a.block : 1;
-        float *scale = a.scale + row * nblk;
-        float s = 1.f;
-        if (!a.block) {
+    for (int c = 0; c < NV; ++c) {
+        const int c0 = (c * G + g) * 8;
+        if (a.block) { // 16 lanes x 8 values = one 128-column block
             float m = 0.f;
 #pragma unroll
-            for (int c = 0; c < NV; ++c)
+            for (int i = 0; i < 8; ++i)
+                m = fmaxf(m, fabsf(h[c][i]));
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    m = fmaxf(m, fabsf(h[c][i]));
-            m = group_reduce<WARP, true>(m, 0.f, red).x;
+            for (int o = 8; o > 0; o >>= 1)
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
             s = fp8_scale(m, a.scale_mode);
-            if (g == 0)
-                scale[0] = s;
+            if ((g & 15) == 0 && c0 < cols)
+                scale[c0 / 128] = s;
         }
+        uint32_t lo = e4m3x2(h[c][0] / s, h[c][1] / s) | ((uint32_t)e4m3x2(h[c][2] / s, h[c][3] / s) << 16);
+        uint32_t hi = e4m3x2(h[c][4] / s, h[c][5] / s) | ((uint32_t)e4m3x2(h[c][6] / s, h[c][7] / s) << 16);
+        if (cols - c0 <= 0)
+            continue;
+        if (vec) {
+            *reinterpret_cast<uint2 *>(codes + c0) = make_uint2(lo, hi);
+        } else {
 #pragma unroll
-        for (int c = 0; c < NV; ++c) {
-            const int c0 = (c * G + g) * 8;
-            if (a.block) { // 16 lanes x 8 values = one 128-column block
-                float m = 0.f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    m = fmaxf(m, fabsf(h[c][i]));
-#pragma unroll
-                for (int o = 8; o > 0; o >>= 1)
-                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                s = fp8_scale(m, a.scale_mode);
-                if ((g & 15) == 0 && c0 < cols)
-                    scale[c0 / 128] = s;
-            }
-            uint32_t lo = e4m3x2(h[c][0] / s, h[c][1] / s) | ((uint32_t)e4m3x2(h[c][2] / s, h[c][3] / s) << 16);
-            uint32_t hi = e4m3x2(h[c][4] / s, h[c][5] / s) | ((uint32_t)e4m3x2(h[c][6] / s, h[c][7] / s) << 16);
-            if (cols - c0 <= 0)
-                continue;
-            if (vec) {
-                *reinterpret_cast<uint2 *>(codes + c0) = make_uint2(lo, hi);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (i < cols - c0)
-                        codes[c0 + i] = (uint8_t)((i < 4 ? lo : hi) >> (8 * (i & 3)));
-            }
+            for (int i = 0; i < 8; ++i)
+                if (i < cols - c0)
+                    codes[c0 + i] = (uint8_t)((i < 4 ? lo : hi) >> (8 * (i & 3)));
         }
     }
 }
 
-// Backward.  Each CTA walks rows b, b + grid, ... with its dweight sums in
-// registers and leaves them as one fp32 row of the workspace (warps of a CTA
-// first add theirs up in shared memory, warp by warp).
 template <typename T, typename W, int NV, bool WARP>
-__global__ void __launch_bounds__(WARP ? kRowThreads : NV == 4 ? 256 : 1024)
+__global__ void __launch_bounds__(WARP ? kRowThreads : 1024) rmsnorm_kernel(RmsNormArgs a, bool vec)
+{
+    __shared__ float red[64];
+    grid_dep_wait();
+    grid_dep_launch();
+    const int64_t row0 = WARP ? (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5) : blockIdx.x;
+    const int64_t step = (int64_t)gridDim.x * (WARP ? kRowThreads / 32 : 1);
+    for (int64_t row = row0; row < a.rows; row += step)
+        rmsnorm_row<T, W, NV, WARP>(a, static_cast<const T *>(a.x) + row * a.ldx,
+                                    a.residual ? static_cast<const T *>(a.residual) + row * a.ldr : nullptr, row, red, vec);
+}
+
+// ---- the ring of rows in shared memory
+constexpr int kRingMost = 8; // stages at most
+constexpr int kRingBars = 128; // bytes in front of the stages: barriers and the abort flag
+constexpr int kRingSmemMost = 222 << 10;
+
+// Thread 0 copies row `row` of up to three tensors into a stage.
+struct RingRows {
+    const uint8_t *src[3];
+    int64_t ld[3]; // bytes
+};
+
+__device__ __forceinline__ void ring_load(const RingRows &r, int n, int64_t row, int bytes, uint32_t dst, uint32_t bar)
+{
+    mbar_arrive_expect_tx(bar, n * bytes);
+    for (int k = 0; k < n; ++k)
+        asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                         dst + k * bytes),
+                     "l"(r.src[k] + row * r.ld[k]), "r"(bytes), "r"(bar)
+                     : "memory");
+}
+
+// Walks rows blockIdx.x, + gridDim.x, ... through the ring; row_fn(stage
+// pointer, row) works on one with every thread of the CTA and ends with the
+// stage's values in registers or written.  All threads meet before a stage is
+// filled again.
+template <typename F>
+__device__ __forceinline__ void ring_walk(const RingRows &r, int n, int64_t rows, int bytes, int stages, uint8_t *smem,
+                                          unsigned *status, F &&row_fn)
+{
+    const uint32_t bar0 = smem_u32(smem);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + 8 * kRingMost);
+    uint8_t *data = smem + kRingBars;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < stages; ++i)
+            mbar_init(bar0 + 8 * i, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    __syncthreads();
+    grid_dep_wait();
+    grid_dep_launch();
+    const int64_t step = gridDim.x;
+    if (threadIdx.x == 0)
+        for (int i = 0; i < stages; ++i)
+            if (blockIdx.x + i * step < rows)
+                ring_load(r, n, blockIdx.x + i * step, bytes, smem_u32(data) + i * n * bytes, bar0 + 8 * i);
+    int st = 0, phase = 0;
+    for (int64_t row = blockIdx.x; row < rows; row += step) {
+        const bool ok = mbar_wait(bar0 + 8 * st, phase, abort_flag, status);
+        if (!__syncthreads_and(ok))
+            break;
+        row_fn(data + st * n * bytes, row);
+        __syncthreads();
+        if (threadIdx.x == 0 && row + stages * step < rows)
+            ring_load(r, n, row + stages * step, bytes, smem_u32(data) + st * n * bytes, bar0 + 8 * st);
+        if (++st == stages) {
+            st = 0;
+            phase ^= 1;
+        }
+    }
+    // after a wait that gave up: a millisecond is far longer than any copy in flight takes
+    if (*abort_flag) {
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < 1000000ull) {
+        }
+    }
+}
+
+template <typename T, typename W>
+__global__ void __launch_bounds__(512) rmsnorm_ring_kernel(RmsNormArgs a, int stages, unsigned *status)
+{
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ float red[64];
+    const RingRows r{{static_cast<const uint8_t *>(a.x), static_cast<const uint8_t *>(a.residual), nullptr},
+                     {a.ldx * (int64_t)sizeof(T), a.ldr * (int64_t)sizeof(T), 0}};
+    const int bytes = a.cols * (int)sizeof(T);
+    ring_walk(r, a.residual ? 2 : 1, a.rows, bytes, stages, smem, status, [&](uint8_t *stage, int64_t row) {
+        rmsnorm_row<T, W, 4, false>(a, reinterpret_cast<const T *>(stage),
+                                    a.residual ? reinterpret_cast<const T *>(stage + bytes) : nullptr, row, red, true);
+    });
+}
+
+// One row of the backward; dw: this thread's dweight sums.
+template <typename T, typename W, int NV, bool WARP>
+__device__ __forceinline__ void rmsnorm_backward_row(const RmsNormBackwardArgs &a, const T *hp, const T *dp, const T *ep,
+                                                     int64_t row, float (&dw)[NV][8], float *red, bool vec)
+{
+    const int G = WARP ? 32 : blockDim.x;
+    const int g = WARP ? (threadIdx.x & 31) : threadIdx.x;
+    const int cols = a.cols;
+    Vec8<T> hv[NV], dv[NV];
+    float ss = 0.f, sg = 0.f;
+#pragma unroll
+    for (int c = 0; c < NV; ++c) {
+        const int c0 = (c * G + g) * 8;
+        load_chunk(hv[c], hp, c0, cols - c0, vec);
+        load_chunk(dv[c], dp, c0, cols - c0, vec);
+    }
+#pragma unroll
+    for (int c = 0; c < NV; ++c) {
+        const int c0 = (c * G + g) * 8;
+        float h[8], d[8], w[8], s = 0.f, t = 0.f;
+        Vec8<W> wv;
+        load_chunk(wv, static_cast<const W *>(a.weight), c0, cols - c0, vec);
+        hv[c].get(h);
+        dv[c].get(d);
+        wv.get(w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            s = fmaf(h[i], h[i], s);
+            t = fmaf(d[i] * w[i], h[i], t);
+        }
+        ss += s;
+        sg += t;
+    }
+    const float2 sums = group_reduce<WARP, false>(ss, sg, red);
+    const float r = 1.f / sqrtf(sums.x / (float)cols + a.eps);
+    const float k = sums.y * r * r / (float)cols; // mean(g xhat) r
+#pragma unroll
+    for (int c = 0; c < NV; ++c) {
+        const int c0 = (c * G + g) * 8;
+        float h[8], d[8], w[8], o[8];
+        Vec8<W> wv;
+        load_chunk(wv, static_cast<const W *>(a.weight), c0, cols - c0, vec);
+        hv[c].get(h);
+        dv[c].get(d);
+        wv.get(w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            o[i] = r * (d[i] * w[i] - h[i] * k);
+            dw[c][i] = fmaf(d[i], h[i] * r, dw[c][i]);
+        }
+        if (ep) {
+            float e[8];
+            Vec8<T> ev;
+            load_chunk(ev, ep, c0, cols - c0, vec);
+            ev.get(e);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                o[i] += e[i];
+        }
+        Vec8<T> v;
+        v.set(o);
+        store_chunk(v, static_cast<T *>(a.dx) + row * cols, c0, cols - c0, vec);
+    }
+}
+
+// A CTA's dweight sums as one fp32 row of the workspace.
+template <int NV>
+__device__ __forceinline__ void store_part(float *part, const float (&dw)[NV][8], int G, int g, int cols, bool vec)
+{
+    float *row = part + (int64_t)blockIdx.x * cols;
+#pragma unroll
+    for (int c = 0; c < NV; ++c) {
+        const int c0 = (c * G + g) * 8;
+        Vec8<float> v;
+        v.set(dw[c]);
+        store_chunk(v, row, c0, cols - c0, vec);
+    }
+}
+
+// Backward.  Each CTA walks rows b, b + grid, ... with its dweight sums in
+// registers (warps of a CTA first add theirs up in shared memory, in turn).
+template <typename T, typename W, int NV, bool WARP>
+__global__ void __launch_bounds__(WARP ? kRowThreads : 1024)
     rmsnorm_backward_kernel(RmsNormBackwardArgs a, float *part, bool vec)
 {
     __shared__ float red[64];
@@ -314,63 +484,12 @@ __global__ void __launch_bounds__(WARP ? kRowThreads : NV == 4 ? 256 : 1024)
     const int64_t row0 = WARP ? (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5) : blockIdx.x;
     const int64_t step = (int64_t)gridDim.x * (WARP ? kRowThreads / 32 : 1);
     const int cols = a.cols;
-    Vec8<W> wv[NV];
-#pragma unroll
-    for (int c = 0; c < NV; ++c) {
-        const int c0 = (c * G + g) * 8;
-        load_chunk(wv[c], static_cast<const W *>(a.weight), c0, cols - c0, vec);
-    }
     float dw[NV][8] = {};
-    for (int64_t row = row0; row < a.rows; row += step) {
-        Vec8<T> hv[NV], dv[NV], ev[NV];
-#pragma unroll
-        for (int c = 0; c < NV; ++c) {
-            const int c0 = (c * G + g) * 8;
-            load_chunk(hv[c], static_cast<const T *>(a.h) + row * cols, c0, cols - c0, vec);
-            load_chunk(dv[c], static_cast<const T *>(a.dy) + row * cols, c0, cols - c0, vec);
-            if (a.dres)
-                load_chunk(ev[c], static_cast<const T *>(a.dres) + row * cols, c0, cols - c0, vec);
-        }
-        float ss = 0.f, sg = 0.f;
-#pragma unroll
-        for (int c = 0; c < NV; ++c) {
-            float h[8], d[8], w[8], s = 0.f, t = 0.f;
-            hv[c].get(h);
-            dv[c].get(d);
-            wv[c].get(w);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                s = fmaf(h[i], h[i], s);
-                t = fmaf(d[i] * w[i], h[i], t);
-            }
-            ss += s;
-            sg += t;
-        }
-        const float2 sums = group_reduce<WARP, false>(ss, sg, red);
-        const float r = 1.f / sqrtf(sums.x / (float)cols + a.eps);
-        const float k = sums.y * r * r / (float)cols; // mean(g xhat) r
-#pragma unroll
-        for (int c = 0; c < NV; ++c) {
-            const int c0 = (c * G + g) * 8;
-            float h[8], d[8], w[8], e[8], o[8];
-            hv[c].get(h);
-            dv[c].get(d);
-            wv[c].get(w);
-            if (a.dres)
-                ev[c].get(e);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                o[i] = r * (d[i] * w[i] - h[i] * k);
-                if (a.dres)
-                    o[i] += e[i];
-                dw[c][i] = fmaf(d[i], h[i] * r, dw[c][i]);
-            }
-            Vec8<T> v;
-            v.set(o);
-            store_chunk(v, static_cast<T *>(a.dx) + row * cols, c0, cols - c0, vec);
-        }
-    }
-    if (WARP) { // this CTA's warps add theirs up in turn
+    for (int64_t row = row0; row < a.rows; row += step)
+        rmsnorm_backward_row<T, W, NV, WARP>(a, static_cast<const T *>(a.h) + row * cols,
+                                             static_cast<const T *>(a.dy) + row * cols,
+                                             a.dres ? static_cast<const T *>(a.dres) + row * cols : nullptr, row, dw, red, vec);
+    if (WARP) {
         for (int w = 0; w < kRowThreads / 32; ++w) {
             if ((threadIdx.x >> 5) == w) {
 #pragma unroll
@@ -391,37 +510,48 @@ __global__ void __launch_bounds__(WARP ? kRowThreads : NV == 4 ? 256 : 1024)
             for (int i = 0; i < 8; ++i)
                 dw[c][i] = dws[(c * 8 + i) * 32 + g];
     }
-#pragma unroll
-    for (int c = 0; c < NV; ++c) {
-        const int c0 = (c * G + g) * 8;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (c0 + i < cols)
-                part[(int64_t)blockIdx.x * cols + c0 + i] = dw[c][i];
-    }
+    store_part<NV>(part, dw, G, g, cols, cols % 4 == 0);
+}
+
+template <typename T, typename W>
+__global__ void __launch_bounds__(512, 1)
+    rmsnorm_backward_ring_kernel(RmsNormBackwardArgs a, float *part, int stages, unsigned *status)
+{
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ float red[64];
+    const int bytes = a.cols * (int)sizeof(T);
+    const RingRows r{{static_cast<const uint8_t *>(a.h), static_cast<const uint8_t *>(a.dy), static_cast<const uint8_t *>(a.dres)},
+                     {bytes, bytes, bytes}};
+    float dw[4][8] = {};
+    ring_walk(r, a.dres ? 3 : 2, a.rows, bytes, stages, smem, status, [&](uint8_t *stage, int64_t row) {
+        rmsnorm_backward_row<T, W, 4, false>(a, reinterpret_cast<const T *>(stage), reinterpret_cast<const T *>(stage + bytes),
+                                             a.dres ? reinterpret_cast<const T *>(stage + 2 * bytes) : nullptr, row, dw, red,
+                                             true);
+    });
+    store_part<4>(part, dw, blockDim.x, threadIdx.x, a.cols, true);
 }
 
 // dweight[c] = sum of the nparts partial rows: 32 columns a CTA, the rows
-// dealt to 8 warps, whose sums are added in order.
-__global__ void __launch_bounds__(256) dweight_kernel(const float *part, int nparts, int cols, float *dweight)
+// dealt to 32 warps, whose sums are added in order.
+__global__ void __launch_bounds__(1024) dweight_kernel(const float *part, int nparts, int cols, float *dweight)
 {
-    __shared__ float s[8][32];
+    __shared__ float s[32][33];
     grid_dep_wait();
     grid_dep_launch();
-    const int c = blockIdx.x * 32 + (threadIdx.x & 31), w = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     float t = 0.f;
     if (c < cols)
-        for (int p = w; p < nparts; p += 8)
+#pragma unroll 8
+        for (int p = w; p < nparts; p += 32)
             t += part[(int64_t)p * cols + c];
-    s[w][threadIdx.x & 31] = t;
+    s[w][lane] = t;
     __syncthreads();
-    if (w == 0 && c < cols) {
-        t = 0.f;
+    t = s[lane][w]; // warp w: the 32 sums of column w
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            t += s[i][threadIdx.x];
-        dweight[c] = t;
-    }
+    for (int o = 16; o > 0; o >>= 1)
+        t += __shfl_xor_sync(0xffffffffu, t, o);
+    if (lane == 0 && blockIdx.x * 32 + w < cols)
+        dweight[blockIdx.x * 32 + w] = t;
 }
 
 bool chunked(const void *p, int64_t ld_bytes) { return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)ld_bytes) & 15) == 0; }
@@ -430,36 +560,55 @@ struct Shape {
     int nv;      // chunks per thread
     int threads; // per CTA
     bool warp;   // a warp per row
+    int stages;  // > 0: the ring (nv = 4)
+    int ctas;    // ring: CTAs per SM
+    size_t smem; // ring
 };
 
-// Threads per row.  Rows of at most 1024 values go to single warps (several
-// rows a CTA, no barrier), up to 8192 to CTAs of 64 to 256 threads with four
-// chunks each, longer ones to 1024 threads with two (four would spill).
-Shape shape_of(int cols)
+// Threads per row, and whether rows (of n tensors of esize-byte values) go
+// through the ring: where they are aligned, longer than a warp's and at least
+// four for each SM.  Its CTAs per SM are as many as leave each two stages.
+Shape shape_of(int64_t rows, int cols, int n, int esize, bool vec)
 {
-    if (cols <= 1024)
-        return {cols <= 256 ? 1 : 4, kRowThreads, true};
-    if (cols > 8192)
-        return {2, 1024, false};
-    int threads = 64;
-    while (threads * 4 * 8 < cols)
+    if (cols <= 1024) // rows of single warps: several a CTA, no barrier
+        return {cols <= 256 ? 1 : 4, kRowThreads, true, 0, 0, 0};
+    const size_t stage = (size_t)n * cols * esize;
+    if (vec && rows >= 4LL * num_sms()) {
+        const int threads = cols > 8192 ? 512 : cols > 4096 ? 256 : 128;
+        for (int ctas = 512 / threads; ctas > 0; ctas /= 2) {
+            const size_t room = (size_t)kRingSmemMost / ctas - 1024 - kRingBars;
+            const size_t stages = room / stage < 4 ? room / stage : 4;
+            if (stages >= 2)
+                return {4, threads, false, (int)stages, ctas, kRingBars + stages * stage};
+        }
+    }
+    // one chunk a thread up to the 8192 values that 1024 threads then hold
+    int threads = 128;
+    while (threads < 1024 && threads * 8 < cols)
         threads *= 2;
-    return {4, threads, false};
+    return {cols > 8192 ? 2 : 1, threads, false, 0, 0, 0};
+}
+
+template <typename F>
+cudaError_t dispatch_types(bool x32, bool w32, F &&f)
+{
+    using bf16 = __nv_bfloat16;
+    if (x32)
+        return w32 ? f((float *)0, (float *)0) : f((float *)0, (bf16 *)0);
+    return w32 ? f((bf16 *)0, (float *)0) : f((bf16 *)0, (bf16 *)0);
 }
 
 template <typename F>
 cudaError_t dispatch(const Shape &s, bool x32, bool w32, F &&f)
 {
     using std::integral_constant;
-    using bf16 = __nv_bfloat16;
-    auto go = [&](auto nv, auto warp) {
-        if (x32)
-            return w32 ? f((float *)0, (float *)0, nv, warp) : f((float *)0, (bf16 *)0, nv, warp);
-        return w32 ? f((bf16 *)0, (float *)0, nv, warp) : f((bf16 *)0, (bf16 *)0, nv, warp);
-    };
-    if (s.warp)
-        return s.nv == 1 ? go(integral_constant<int, 1>(), std::true_type()) : go(integral_constant<int, 4>(), std::true_type());
-    return s.nv == 2 ? go(integral_constant<int, 2>(), std::false_type()) : go(integral_constant<int, 4>(), std::false_type());
+    return dispatch_types(x32, w32, [&](auto t, auto w) {
+        if (s.warp)
+            return s.nv == 1 ? f(t, w, integral_constant<int, 1>(), std::true_type())
+                             : f(t, w, integral_constant<int, 4>(), std::true_type());
+        return s.nv == 1 ? f(t, w, integral_constant<int, 1>(), std::false_type())
+                         : f(t, w, integral_constant<int, 2>(), std::false_type());
+    });
 }
 
 int64_t rows_grid(int64_t rows, const Shape &s, int64_t most)
@@ -469,9 +618,10 @@ int64_t rows_grid(int64_t rows, const Shape &s, int64_t most)
     return n < most ? n : most;
 }
 
-int backward_ctas(int64_t rows, int cols)
+// CTAs of a backward: a row of the workspace each.
+int64_t backward_ctas(int64_t rows, const Shape &s)
 {
-    return (int)rows_grid(rows, shape_of(cols), 2LL * num_sms());
+    return rows_grid(rows, s, (int64_t)(s.stages ? s.ctas : s.warp ? 4 : 2) * num_sms());
 }
 
 } // namespace
@@ -483,14 +633,31 @@ int launch_rmsnorm(const RmsNormArgs &a, cudaStream_t stream, char *err, size_t 
                      (!a.residual || chunked(a.residual, a.ldr * e)) &&
                      (!a.residual_out || chunked(a.residual_out, a.ldh * e)) && (!a.out || chunked(a.out, a.ldo * e)) &&
                      (!a.codes || (reinterpret_cast<uintptr_t>(a.codes) & 7) == 0);
-    const Shape s = shape_of(a.cols);
-    const int64_t grid = rows_grid(a.rows, s, 1 << 30);
-    cudaError_t rc = dispatch(s, a.x32, a.w32, [&](auto t, auto w, auto nv, auto warp) {
-        using T = std::remove_pointer_t<decltype(t)>;
-        using W = std::remove_pointer_t<decltype(w)>;
-        return launch_pdl(rmsnorm_kernel<T, W, decltype(nv)::value, decltype(warp)::value>, dim3((unsigned)grid),
-                          dim3(s.threads), 0, stream, 1, a, vec);
-    });
+    const Shape s = shape_of(a.rows, a.cols, a.residual ? 2 : 1, e, vec);
+    unsigned *status = device_status_ptr();
+    if (!status) {
+        snprintf(err, errlen, "device status word unavailable");
+        return DSA_ERR_CUDA;
+    }
+    cudaError_t rc;
+    if (s.stages)
+        rc = dispatch_types(a.x32, a.w32, [&](auto t, auto w) {
+            using T = std::remove_pointer_t<decltype(t)>;
+            using W = std::remove_pointer_t<decltype(w)>;
+            static std::atomic<bool> raised[64];
+            cudaError_t r = raise_smem_limit_once(rmsnorm_ring_kernel<T, W>, kRingSmemMost, raised);
+            if (r != cudaSuccess)
+                return r;
+            return launch_pdl(rmsnorm_ring_kernel<T, W>, dim3((unsigned)rows_grid(a.rows, s, (int64_t)s.ctas * num_sms())),
+                              dim3(s.threads), s.smem, stream, 1, a, s.stages, status);
+        });
+    else
+        rc = dispatch(s, a.x32, a.w32, [&](auto t, auto w, auto nv, auto warp) {
+            using T = std::remove_pointer_t<decltype(t)>;
+            using W = std::remove_pointer_t<decltype(w)>;
+            return launch_pdl(rmsnorm_kernel<T, W, decltype(nv)::value, decltype(warp)::value>,
+                              dim3((unsigned)rows_grid(a.rows, s, 1 << 30)), dim3(s.threads), 0, stream, 1, a, vec);
+        });
     if (rc != cudaSuccess) {
         snprintf(err, errlen, "rmsnorm launch: %s", cudaGetErrorString(rc));
         return DSA_ERR_CUDA;
@@ -498,9 +665,18 @@ int launch_rmsnorm(const RmsNormArgs &a, cudaStream_t stream, char *err, size_t 
     return DSA_OK;
 }
 
+// The most that any alignment, type and dres needs: which of them a call has is
+// not known here.
 size_t rmsnorm_backward_workspace_bytes(int64_t rows, int cols)
 {
-    return (size_t)backward_ctas(rows, cols) * cols * sizeof(float);
+    int64_t most = 0;
+    for (int esize = 2; esize <= 4; esize += 2)
+        for (int n = 2; n <= 3; ++n)
+            for (int vec = 0; vec < 2; ++vec) {
+                const int64_t c = backward_ctas(rows, shape_of(rows, cols, n, esize, vec != 0));
+                most = c > most ? c : most;
+            }
+    return (size_t)most * cols * sizeof(float);
 }
 
 int launch_rmsnorm_backward(const RmsNormBackwardArgs &a, cudaStream_t stream, char *err, size_t errlen)
@@ -509,11 +685,27 @@ int launch_rmsnorm_backward(const RmsNormBackwardArgs &a, cudaStream_t stream, c
     const int64_t ld = (int64_t)a.cols * e;
     const bool vec = a.cols % 8 == 0 && chunked(a.h, ld) && chunked(a.dy, ld) && chunked(a.dx, ld) && chunked(a.weight, 0) &&
                      (!a.dres || chunked(a.dres, ld));
-    const Shape s = shape_of(a.cols);
-    const int grid = backward_ctas(a.rows, a.cols);
+    const Shape s = shape_of(a.rows, a.cols, a.dres ? 3 : 2, e, vec);
+    const int grid = (int)backward_ctas(a.rows, s);
     float *part = static_cast<float *>(a.workspace);
+    unsigned *status = device_status_ptr();
+    if (!status) {
+        snprintf(err, errlen, "device status word unavailable");
+        return DSA_ERR_CUDA;
+    }
     cudaError_t rc = cudaSuccess;
-    if (grid > 0)
+    if (grid > 0 && s.stages)
+        rc = dispatch_types(a.x32, a.w32, [&](auto t, auto w) {
+            using T = std::remove_pointer_t<decltype(t)>;
+            using W = std::remove_pointer_t<decltype(w)>;
+            static std::atomic<bool> raised[64];
+            cudaError_t r = raise_smem_limit_once(rmsnorm_backward_ring_kernel<T, W>, kRingSmemMost, raised);
+            if (r != cudaSuccess)
+                return r;
+            return launch_pdl(rmsnorm_backward_ring_kernel<T, W>, dim3((unsigned)grid), dim3(s.threads), s.smem, stream, 1, a,
+                              part, s.stages, status);
+        });
+    else if (grid > 0)
         rc = dispatch(s, a.x32, a.w32, [&](auto t, auto w, auto nv, auto warp) {
             using T = std::remove_pointer_t<decltype(t)>;
             using W = std::remove_pointer_t<decltype(w)>;
@@ -521,7 +713,7 @@ int launch_rmsnorm_backward(const RmsNormBackwardArgs &a, cudaStream_t stream, c
                               dim3((unsigned)grid), dim3(s.threads), 0, stream, 1, a, part, vec);
         });
     if (rc == cudaSuccess) // no rows: the sum of nothing, zeros
-        rc = launch_pdl(dweight_kernel, dim3((unsigned)((a.cols + 31) / 32)), dim3(256), 0, stream, 1, (const float *)part,
+        rc = launch_pdl(dweight_kernel, dim3((unsigned)((a.cols + 31) / 32)), dim3(1024), 0, stream, 1, (const float *)part,
                         grid, a.cols, a.dweight);
     if (rc != cudaSuccess) {
         snprintf(err, errlen, "rmsnorm backward launch: %s", cudaGetErrorString(rc));
