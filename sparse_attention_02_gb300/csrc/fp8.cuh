@@ -37,4 +37,31 @@ __device__ __forceinline__ float fp8_scale(float amax, int mode)
     return mode == 0 ? ratio : pow2_ceil(ratio);
 }
 
+// Division of many values by one scale, each quotient correctly rounded (the
+// same bits as y / s): with inv = RN(1 / s), q0 = RN(y inv) and the remainder
+// y - q0 s, exact in an fma, RN(q0 + remainder inv) is RN(y / s) (P. Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000 processor",
+// 1990), as long as nothing under- or overflows on the way; scales so small
+// that 1 / s might, divide.  Three operations for the ten or so of a division,
+// which bounded the norm's FP8 output (115 us for 92 with a bare product at
+// 8191 x 8192).
+struct ScaleDivider {
+    float s, inv;
+    bool plain;
+    __device__ __forceinline__ explicit ScaleDivider(float scale) : s(scale), inv(1.f / scale), plain(!(scale > 1e-30f)) {}
+    __device__ __forceinline__ float operator()(float y) const
+    {
+        if (plain)
+            return y / s;
+        const float q = y * inv;
+        return fmaf(fmaf(-q, s, y), inv, q);
+    }
+};
+
+// Four values as E4M3 codes over a scale, the first in byte 0.
+__device__ __forceinline__ uint32_t e4m3x4(const ScaleDivider &d, float a, float b, float c, float e)
+{
+    return e4m3x2(d(a), d(b)) | ((uint32_t)e4m3x2(d(c), d(e)) << 16);
+}
+
 } // namespace dsa

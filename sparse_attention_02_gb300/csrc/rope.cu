@@ -82,33 +82,12 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8])
 // lane of either rotation needs angles 4 (l & 7) .. + 3.
 constexpr int kAppendThreads = 128;
 
-template <typename K, bool W32>
-__global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(CacheAppendArgs a, unsigned *status)
-{
-    grid_dep_wait();
-    grid_dep_launch();
-    const int lane = threadIdx.x & 31;
-    const uint64_t freq = turn_step(a.inv_freq[lane]);
-    const int step = gridDim.x * (kAppendThreads / 32);
-    for (int t = blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5); t < a.T; t += step) {
-        const int pos = a.pos[t];
-        if (pos < 0) // a padded row
-            continue;
-        const int s = a.seq ? a.seq[t] : t;
-        const int lp = pos / a.page_size;
-        if (s < 0 || s >= a.num_seqs || lp >= a.max_pages) {
-            if (lane == 0)
-                atomicOr(status, DSA_DEV_BAD_POSITION);
-            continue;
-        }
-        const int page = a.block_table[(int64_t)s * a.max_pages + lp];
-        if (page < 0 || page >= a.num_pages) {
-            if (lane == 0)
-                atomicOr(status, DSA_DEV_BAD_PAGE);
-            continue;
-        }
-        const int64_t slot = (int64_t)page * a.page_size + pos % a.page_size;
-        uint4 v0, v1, vr = make_uint4(0, 0, 0, 0);
+// What a token's warp reads of it: nothing depends on where it goes, so it is
+// loaded while the position and page are looked up, and one token ahead.
+template <typename K> struct TokenRow {
+    uint4 v0, v1, vr, k;
+    __device__ __forceinline__ void load(const CacheAppendArgs &a, int t, int lane)
+    {
         if (a.kv) {
             const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.kv) + t * a.ld_kv);
             v0 = src[lane];
@@ -116,17 +95,57 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(CacheAppen
             if (lane < 8)
                 vr = src[64 + lane];
         }
-        float k[4] = {};
         if (a.kI) {
             const K *src = static_cast<const K *>(a.kI) + t * a.ld_kI + 4 * lane;
             if (sizeof(K) == 4) {
-                const float4 f = *reinterpret_cast<const float4 *>(src);
-                k[0] = f.x, k[1] = f.y, k[2] = f.z, k[3] = f.w;
+                k = *reinterpret_cast<const uint4 *>(src);
             } else {
                 const uint2 f = *reinterpret_cast<const uint2 *>(src);
-                k[0] = bf16_lo(f.x), k[1] = bf16_hi(f.x), k[2] = bf16_lo(f.y), k[3] = bf16_hi(f.y);
+                k.x = f.x, k.y = f.y;
             }
         }
+    }
+    __device__ __forceinline__ void index(float (&f)[4]) const
+    {
+        if (sizeof(K) == 4) {
+            f[0] = __uint_as_float(k.x), f[1] = __uint_as_float(k.y), f[2] = __uint_as_float(k.z), f[3] = __uint_as_float(k.w);
+        } else {
+            f[0] = bf16_lo(k.x), f[1] = bf16_hi(k.x), f[2] = bf16_lo(k.y), f[3] = bf16_hi(k.y);
+        }
+    }
+};
+
+template <typename K, bool W32>
+__global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(CacheAppendArgs a, unsigned *status)
+{
+    grid_dep_wait();
+    grid_dep_launch();
+    const int lane = threadIdx.x & 31;
+    const int step = gridDim.x * (kAppendThreads / 32);
+    int t = blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
+    if (t >= a.T)
+        return;
+    TokenRow<K> next;
+    next.load(a, t, lane);
+    int next_pos = a.pos[t], next_seq = a.seq ? a.seq[t] : t;
+    const uint64_t freq = turn_step(a.inv_freq[lane]);
+    for (; t < a.T; t += step) {
+        const TokenRow<K> row = next;
+        const int pos = next_pos, s = next_seq;
+        if (t < a.T - step) {
+            next.load(a, t + step, lane);
+            next_pos = a.pos[t + step];
+            next_seq = a.seq ? a.seq[t + step] : t + step;
+        }
+        if (pos < 0) // a padded row
+            continue;
+        const int lp = pos / a.page_size;
+        if (s < 0 || s >= a.num_seqs || lp >= a.max_pages) {
+            if (lane == 0)
+                atomicOr(status, DSA_DEV_BAD_POSITION);
+            continue;
+        }
+        const int page = a.block_table[(int64_t)s * a.max_pages + lp];
         const float2 mine = rotation(pos, freq);
         float c[4], n[4];
 #pragma unroll
@@ -134,8 +153,15 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(CacheAppen
             c[i] = __shfl_sync(0xffffffffu, mine.x, 4 * (lane & 7) + i);
             n[i] = __shfl_sync(0xffffffffu, mine.y, 4 * (lane & 7) + i);
         }
+        if (page < 0 || page >= a.num_pages) {
+            if (lane == 0)
+                atomicOr(status, DSA_DEV_BAD_PAGE);
+            continue;
+        }
+        const int64_t slot = (int64_t)page * a.page_size + pos % a.page_size;
         if (a.kv) {
             uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.kv_pool) + slot * kLatent);
+            uint4 v0 = row.v0, v1 = row.v1;
             if (a.kv_weight) {
                 float f0[8], f1[8], ss = 0.f, w0[8], w1[8];
                 unpack8(v0, f0);
@@ -171,7 +197,7 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(CacheAppen
             dst[lane + 32] = v1;
             if (lane < 8) {
                 float f[8], o[8];
-                unpack8(vr, f);
+                unpack8(row.vr, f);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     o[2 * i] = f[2 * i] * c[i] - f[2 * i + 1] * n[i];
@@ -181,7 +207,8 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(CacheAppen
             }
         }
         if (a.kI) {
-            float m = 0.f;
+            float k[4], m = 0.f;
+            row.index(k);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float other = __shfl_xor_sync(0xffffffffu, k[i], 8);
@@ -195,8 +222,7 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(CacheAppen
             for (int o = 16; o > 0; o >>= 1)
                 m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
             const float sc = fp8_scale(m, a.scale_mode);
-            reinterpret_cast<uint32_t *>(a.k8_pool + slot * kIndex)[lane] =
-                e4m3x2(k[0] / sc, k[1] / sc) | ((uint32_t)e4m3x2(k[2] / sc, k[3] / sc) << 16);
+            reinterpret_cast<uint32_t *>(a.k8_pool + slot * kIndex)[lane] = e4m3x4(ScaleDivider(sc), k[0], k[1], k[2], k[3]);
             if (lane == 0)
                 a.ks_pool[slot] = sc;
         }
@@ -204,10 +230,12 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(CacheAppen
 }
 
 // ------------------------------------------------------------------ queries
-// One CTA per token.  Index queries: thread t holds chunks t, t + 256, ... of
-// the token's H_I x 128 values (8 columns each, 16 chunks a head), its pair's
-// other half 4 lanes away; at most 64 heads, so four chunks a thread stay in
-// registers while the token's amax is found.
+// Two CTAs per token, one for each part that is asked for.  Everything a thread
+// reads is in flight before the token's position and angles are there.  Index
+// queries: thread t holds chunks t, t + 256, ... of the token's H_I x 128 values
+// (8 columns each, 16 chunks a head), its pair's other half 4 lanes away; at
+// most 64 heads, so four chunks a thread stay in registers while the token's
+// amax is found.
 constexpr int kQueryThreads = 256;
 constexpr int kIndexChunks = 4;
 
@@ -245,41 +273,59 @@ __global__ void __launch_bounds__(kQueryThreads) rope_queries_kernel(RopeQueries
     grid_dep_wait();
     grid_dep_launch();
     const int t = blockIdx.x, tid = threadIdx.x;
-    const int pos = a.pos[t];
-    if (pos < 0) // a padded row
+    if (a.q_rope && blockIdx.y == 0) {
+        const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(a.q_rope) + t * a.st_t;
+        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.q) + (int64_t)t * a.H * kLatent + kValue;
+        constexpr int kMost = 128 * 8 / kQueryThreads; // chunks of a thread
+        const int h0 = tid >> 3, p = tid & 7;
+        uint4 v[kMost];
+#pragma unroll
+        for (int j = 0; j < kMost; ++j)
+            if (h0 + j * (kQueryThreads / 8) < a.H)
+                v[j] = *reinterpret_cast<const uint4 *>(src + (h0 + j * (kQueryThreads / 8)) * a.st_h + 8 * p);
+        const int pos = a.pos[t];
+        if (pos < 0) // a padded row
+            return;
+        if (tid < 32)
+            cs[tid] = rotation(pos, turn_step(a.inv_freq[tid]));
+        __syncthreads();
+        float2 r[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            r[i] = cs[4 * p + i];
+#pragma unroll
+        for (int j = 0; j < kMost; ++j) {
+            const int h = h0 + j * (kQueryThreads / 8);
+            if (h >= a.H)
+                continue;
+            float x[8], o[8];
+            unpack8(v[j], x);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                o[2 * i] = x[2 * i] * r[i].x - x[2 * i + 1] * r[i].y;
+                o[2 * i + 1] = x[2 * i] * r[i].y + x[2 * i + 1] * r[i].x;
+            }
+            *reinterpret_cast<uint4 *>(dst + (int64_t)h * kLatent + 8 * p) = pack8(o);
+        }
         return;
-    if (tid < 32)
-        cs[tid] = rotation(pos, turn_step(a.inv_freq[tid]));
+    }
     float f[kIndexChunks][8];
-    const int chunks = a.qI ? a.HI * 16 : 0;
+    const int chunks = a.HI * 16;
 #pragma unroll
     for (int j = 0; j < kIndexChunks; ++j) {
         const int c = j * kQueryThreads + tid;
         if (c < chunks)
-            load8(static_cast<const K *>(a.qI) + ((int64_t)t * a.HI * 16 + c) * 8, f[j]);
+            load8(static_cast<const K *>(a.qI) + ((int64_t)t * chunks + c) * 8, f[j]);
         else
             for (int i = 0; i < 8; ++i)
                 f[j][i] = 0.f;
     }
-    __syncthreads();
-    if (a.q_rope) {
-        const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(a.q_rope) + t * a.st_t;
-        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.q) + (int64_t)t * a.H * kLatent + kValue;
-        for (int c = tid; c < a.H * 8; c += kQueryThreads) {
-            const int h = c >> 3, p = c & 7;
-            float x[8], o[8];
-            unpack8(*reinterpret_cast<const uint4 *>(src + h * a.st_h + 8 * p), x);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 r = cs[4 * p + i];
-                o[2 * i] = x[2 * i] * r.x - x[2 * i + 1] * r.y;
-                o[2 * i + 1] = x[2 * i] * r.y + x[2 * i + 1] * r.x;
-            }
-            *reinterpret_cast<uint4 *>(dst + (int64_t)h * kLatent + 8 * p) = pack8(o);
-        }
-    }
-    if (!a.qI)
+    const int pos = a.pos[t];
+    if (pos < 0)
         return;
+    if (tid < 32)
+        cs[tid] = rotation(pos, turn_step(a.inv_freq[tid]));
+    __syncthreads();
     float m = 0.f;
 #pragma unroll
     for (int j = 0; j < kIndexChunks; ++j) {
@@ -299,6 +345,7 @@ __global__ void __launch_bounds__(kQueryThreads) rope_queries_kernel(RopeQueries
     for (int w = 1; w < kQueryThreads / 32; ++w)
         m = fmaxf(m, red[w]);
     const float sc = fp8_scale(m, a.scale_mode);
+    const ScaleDivider div(sc);
     if (tid == 0)
         a.q_scale[t] = sc;
 #pragma unroll
@@ -306,9 +353,9 @@ __global__ void __launch_bounds__(kQueryThreads) rope_queries_kernel(RopeQueries
         const int c = j * kQueryThreads + tid;
         if (c >= chunks)
             continue;
-        const uint32_t lo = e4m3x2(f[j][0] / sc, f[j][1] / sc) | ((uint32_t)e4m3x2(f[j][2] / sc, f[j][3] / sc) << 16);
-        const uint32_t hi = e4m3x2(f[j][4] / sc, f[j][5] / sc) | ((uint32_t)e4m3x2(f[j][6] / sc, f[j][7] / sc) << 16);
-        reinterpret_cast<uint2 *>(a.q8)[(int64_t)t * a.HI * 16 + c] = make_uint2(lo, hi);
+        const uint32_t lo = e4m3x4(div, f[j][0], f[j][1], f[j][2], f[j][3]);
+        const uint32_t hi = e4m3x4(div, f[j][4], f[j][5], f[j][6], f[j][7]);
+        reinterpret_cast<uint2 *>(a.q8)[(int64_t)t * chunks + c] = make_uint2(lo, hi);
     }
 }
 
@@ -399,7 +446,7 @@ int launch_cache_append(const CacheAppendArgs &a, cudaStream_t stream, char *err
 
 int launch_rope_queries(const RopeQueriesArgs &a, cudaStream_t stream, char *err, size_t errlen)
 {
-    auto go = [&](auto kernel) { return launch_pdl(kernel, dim3((unsigned)a.T), dim3(kQueryThreads), 0, stream, 1, a); };
+    auto go = [&](auto kernel) { return launch_pdl(kernel, dim3((unsigned)a.T, a.q_rope && a.qI ? 2 : 1), dim3(kQueryThreads), 0, stream, 1, a); };
     return finish(a.i32 ? go(rope_queries_kernel<float>) : go(rope_queries_kernel<__nv_bfloat16>), "query rotation", err, errlen);
 }
 
