@@ -104,7 +104,7 @@ struct Params {
     __nv_bfloat16 *out;
     float *lse;
     float *ws_o, *ws_lse; // [2 clusters, H, 512], [2 clusters, H]
-    int64_t *row_start;   // [B + 1] first tile of each row
+    int2 *row_parts;      // [B] slot of a row's first part (-1: it is whole), cluster of its last
     unsigned *status;
 };
 
@@ -316,6 +316,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         *abort_flag = 0;
         fence_mbar_init();
     }
+    // this CTA's barriers exist (thread 0 is past its fence when it arrives); the peer's are waited for below
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     if (warp == 1)
         tmem_alloc_pair(sbase + OFF_MISC, kTmemCols);
     grid_dep_wait(); // no global memory before this
@@ -349,34 +351,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 before += sums[w];
             total += sums[w];
         }
-        const int64_t g0 = total * cid / p.clusters, g1 = total * (cid + 1) / p.clusters;
+        // of as many clusters as there are tiles: none in between has nothing
+        const int n = total < p.clusters ? (int)total : p.clusters;
+        auto start = [&](int c) {
+            return total < (1 << 24) ? (int64_t)((uint32_t)total * (uint32_t)c / (uint32_t)n) : total * c / n;
+        };
+        const int64_t g0 = cid < n ? start(cid) : total, g1 = cid < n ? start(cid + 1) : total;
         if (threadIdx.x == 0)
             share->tiles = g1 - g0;
         if (g0 >= before && g0 < before + mine) {
             int64_t at = before;
             int r = r0;
             for (;; ++r) {
-                const int n = tiles_of(context(p, r));
-                if (g0 < at + n)
+                const int t = tiles_of(context(p, r));
+                if (g0 < at + t)
                     break;
-                at += n;
+                at += t;
             }
             share->row = r;
             share->tile = (int)(g0 - at);
         }
-        if (blockIdx.x == 0) { // for the joining kernel
-            int64_t at = before;
-            for (int r = r0; r < r1; ++r) {
-                p.row_start[r] = at;
-                at += tiles_of(context(p, r));
-            }
-            if (threadIdx.x == 0)
-                p.row_start[p.B] = total;
-        }
     }
     tc_fence_before();
     __syncthreads();
-    cluster_sync_all(); // both CTAs' barriers exist before any remote operation
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); // before any remote operation
     tc_fence_after();
     const uint32_t tmem = *tmem_holder;
     const uint32_t lead0 = mapa_shared(bar0, 0);
@@ -579,6 +577,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         Pages pg;
         while (ok && it.next(p, cid, un)) {
             float m = -INFINITY, l = 0.f;
+            if (rank == 0 && threadIdx.x == 32 * kSoftWarp0) { // for the joining kernel
+                if (un.jb == 0)
+                    p.row_parts[un.row].x = un.slot;
+                if (un.je == tiles_of(un.ctx))
+                    p.row_parts[un.row].y = cid;
+            }
             const int64_t orow = (int64_t)un.row * p.H + h, prow = (int64_t)un.slot * p.H + h;
             const int col0 = 256 * kb + 128 * part; // of O: lanes 0-63 hold columns [0, 256), lanes 64-127 the others
             if (un.ctx == 0) {
@@ -712,7 +716,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             ++u;
             const float inv = l > 0.f ? 1.f / l : 0.f;
             tc_fence_after();
-#pragma unroll 1
+#pragma unroll 2
             for (int c = 0; c < 128; c += 32) {
                 uint32_t o[32];
                 tmem_ld32(tmem + lane_off + TM_O + 128 * part + c, o);
@@ -768,72 +772,84 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
 }
 
-// Joins the parts of each split row: a CTA per (row, head), its 8 warps taking
-// parts w, w + 8, ... and adding up in order.  O = sum exp(LSE_i - LSE) O_i.
+// Joins the parts of each split row, O = sum exp(LSE_i - LSE) O_i, in the order
+// of the parts.  A CTA takes HEADS heads of a row: with eight and few parts a
+// warp each, else its warps take parts w, w + 8, ... of one head after the
+// other and add up.  A row's parts lie in consecutive clusters; in all but the
+// first the row is the share's first, so its slot is 2 cluster.
+template <int HEADS>
 __global__ void __launch_bounds__(256) dense_mla_join_kernel(Params p)
 {
     __shared__ float acc_s[8][kDv];
     __shared__ float sum_s[8];
     grid_dep_wait();
     grid_dep_launch();
-    const int row = blockIdx.x, h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t total = p.row_start[p.B], a = p.row_start[row], b = p.row_start[row + 1];
-    // cluster c holds tiles [floor(total c / C), floor(total (c + 1) / C))
-    auto cluster_of = [&](int64_t g) { return (int)(((g + 1) * p.clusters + total - 1) / total - 1); };
-    const int c0 = cluster_of(a), c1 = cluster_of(b - 1);
-    if (c0 == c1)
+    const int row = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int2 rp = p.row_parts[row];
+    if (rp.x < 0)
         return;
-    // the row is its cluster's first unless the cluster began with an earlier one; with fewer tiles than clusters some
-    // have none
-    auto slot = [&](int c) {
-        const int64_t g0 = total * c / p.clusters, g1 = total * (c + 1) / p.clusters;
-        return g0 == g1 ? -1 : 2 * c + (g0 < a);
-    };
-    float top = -INFINITY;
-    for (int c = c0 + lane; c <= c1; c += 32)
-        if (slot(c) >= 0)
-            top = fmaxf(top, p.ws_lse[(int64_t)slot(c) * p.H + h]);
+    const int c0 = rp.x >> 1, np = rp.y - c0 + 1;
+    auto slot = [&](int i) { return i == 0 ? rp.x : 2 * (c0 + i); };
+    const bool alone = HEADS > 1 && np <= 8; // a warp joins a head by itself
+    for (int k = alone ? warp : 0; k < HEADS; k += alone ? 8 : 1) {
+        const int h = blockIdx.y * HEADS + k;
+        if (h >= p.H)
+            break;
+        float top = -INFINITY;
+        for (int i = lane; i < np; i += 32)
+            top = fmaxf(top, p.ws_lse[(int64_t)slot(i) * p.H + h]);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    float acc[16] = {}, sum = 0.f;
-    if (top != -INFINITY)
-        for (int c = c0 + warp; c <= c1; c += 8) {
-            if (slot(c) < 0)
-                continue;
-            const int64_t r = (int64_t)slot(c) * p.H + h;
-            const float w = expf(p.ws_lse[r] - top);
+        for (int o = 16; o > 0; o >>= 1)
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        float4 acc[4] = {};
+        float sum = 0.f;
+        const int step = alone ? 1 : 8;
+#pragma unroll 4
+        for (int i = alone ? 0 : warp; i < np; i += step) {
+            const int64_t r = (int64_t)slot(i) * p.H + h;
             const float4 *src = reinterpret_cast<const float4 *>(p.ws_o + r * kDv) + lane;
+            const float w = top == -INFINITY ? 0.f : expf(p.ws_lse[r] - top);
             sum += w;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const float4 v = src[32 * e];
-                acc[4 * e] = fmaf(w, v.x, acc[4 * e]);
-                acc[4 * e + 1] = fmaf(w, v.y, acc[4 * e + 1]);
-                acc[4 * e + 2] = fmaf(w, v.z, acc[4 * e + 2]);
-                acc[4 * e + 3] = fmaf(w, v.w, acc[4 * e + 3]);
+                acc[e].x = fmaf(w, v.x, acc[e].x);
+                acc[e].y = fmaf(w, v.y, acc[e].y);
+                acc[e].z = fmaf(w, v.z, acc[e].z);
+                acc[e].w = fmaf(w, v.w, acc[e].w);
             }
         }
+        const int64_t orow = (int64_t)row * p.H + h;
+        if (alone) {
+            const float inv = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-        reinterpret_cast<float4 *>(acc_s[warp])[lane + 32 * e] =
-            make_float4(acc[4 * e], acc[4 * e + 1], acc[4 * e + 2], acc[4 * e + 3]);
-    if (lane == 0)
-        sum_s[warp] = sum;
-    __syncthreads();
-    float l = 0.f, x = 0.f, y = 0.f;
+            for (int e = 0; e < 4; ++e)
+                reinterpret_cast<uint2 *>(p.out)[orow * (kDv / 4) + lane + 32 * e] =
+                    make_uint2(pack2(acc[e].x * inv, acc[e].y * inv), pack2(acc[e].z * inv, acc[e].w * inv));
+            if (lane == 0)
+                p.lse[orow] = top == -INFINITY ? -INFINITY : top + logf(sum);
+            continue;
+        }
 #pragma unroll
-    for (int w = 0; w < 8; ++w) {
-        l += sum_s[w];
-        const float2 v = reinterpret_cast<const float2 *>(acc_s[w])[threadIdx.x];
-        x += v.x;
-        y += v.y;
+        for (int e = 0; e < 4; ++e)
+            reinterpret_cast<float4 *>(acc_s[warp])[lane + 32 * e] = acc[e];
+        if (lane == 0)
+            sum_s[warp] = sum;
+        __syncthreads();
+        float l = 0.f, x = 0.f, y = 0.f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+            l += sum_s[w];
+            const float2 v = reinterpret_cast<const float2 *>(acc_s[w])[threadIdx.x];
+            x += v.x;
+            y += v.y;
+        }
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        reinterpret_cast<uint32_t *>(p.out)[orow * (kDv / 2) + threadIdx.x] = pack2(x * inv, y * inv);
+        if (threadIdx.x == 0)
+            p.lse[orow] = top == -INFINITY ? -INFINITY : top + logf(l);
+        __syncthreads(); // the sums are used again for the next head
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    const int64_t orow = (int64_t)row * p.H + h;
-    reinterpret_cast<uint32_t *>(p.out)[orow * (kDv / 2) + threadIdx.x] = pack2(x * inv, y * inv);
-    if (threadIdx.x == 0)
-        p.lse[orow] = top == -INFINITY ? -INFINITY : top + logf(l);
 }
 
 int clusters() { return num_sms() / 2 > 0 ? num_sms() / 2 : 1; }
@@ -845,7 +861,7 @@ size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 size_t dense_mla_workspace_bytes(int B, int H)
 {
     const size_t parts = 2 * (size_t)clusters() * H;
-    return align256(parts * kDv * sizeof(float)) + align256(parts * sizeof(float)) + ((size_t)B + 1) * sizeof(int64_t);
+    return align256(parts * kDv * sizeof(float)) + align256(parts * sizeof(float)) + (size_t)B * sizeof(int2);
 }
 
 int launch_dense_mla(const DenseMlaArgs &a, cudaStream_t stream, char *err, size_t errlen)
@@ -873,7 +889,7 @@ int launch_dense_mla(const DenseMlaArgs &a, cudaStream_t stream, char *err, size
     uint8_t *ws = static_cast<uint8_t *>(a.workspace);
     p.ws_o = reinterpret_cast<float *>(ws);
     p.ws_lse = reinterpret_cast<float *>(ws + align256(parts * kDv * sizeof(float)));
-    p.row_start = reinterpret_cast<int64_t *>(ws + align256(parts * kDv * sizeof(float)) + align256(parts * sizeof(float)));
+    p.row_parts = reinterpret_cast<int2 *>(ws + align256(parts * kDv * sizeof(float)) + align256(parts * sizeof(float)));
     CUtensorMap tq, tkv2, tkv3;
     const uint64_t rows = (uint64_t)a.num_pages * a.page_size;
     const uint32_t box = a.page_size < 64 ? a.page_size : 64;
@@ -890,7 +906,9 @@ int launch_dense_mla(const DenseMlaArgs &a, cudaStream_t stream, char *err, size
     if (e == cudaSuccess)
         e = launch_pdl(dense_mla_kernel, dim3(2 * p.clusters), dim3(kThreads), kSmem, stream, 1, tq, tkv2, tkv3, p);
     if (e == cudaSuccess)
-        e = launch_pdl(dense_mla_join_kernel, dim3(a.B, a.H), dim3(256), 0, stream, 1, p);
+        e = (int64_t)a.B * a.H <= 8 * num_sms()
+                ? launch_pdl(dense_mla_join_kernel<1>, dim3(a.B, a.H), dim3(256), 0, stream, 1, p)
+                : launch_pdl(dense_mla_join_kernel<8>, dim3(a.B, (a.H + 7) / 8), dim3(256), 0, stream, 1, p);
     if (e != cudaSuccess) {
         snprintf(err, errlen, "dense MLA launch: %s", cudaGetErrorString(e));
         return DSA_ERR_CUDA;

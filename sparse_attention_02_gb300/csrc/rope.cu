@@ -116,7 +116,7 @@ template <typename K> struct TokenRow {
 };
 
 template <typename K, bool W32>
-__global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(CacheAppendArgs a, unsigned *status)
+__global__ void __launch_bounds__(kAppendThreads, 8) cache_append_kernel(CacheAppendArgs a, unsigned *status)
 {
     grid_dep_wait();
     grid_dep_launch();
@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(CacheAppen
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1)
                     ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                const float r = 1.f / sqrtf(ss / (float)kValue + a.eps);
+                const float r = rsqrtf(ss * (1.f / kValue) + a.eps);
                 if (W32) {
                     const float *w = static_cast<const float *>(a.kv_weight) + 8 * lane;
 #pragma unroll
