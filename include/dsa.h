@@ -199,8 +199,8 @@ int dsa_rmsnorm(const void *x, int64_t ldx, const void *residual, int64_t ldr, c
  *   workspace: dsa_rmsnorm_backward_workspace_size(rows, cols) bytes, 16-byte
  *   aligned, owned by the caller, used only while the call's kernels run
  *   (calls sharing one must be ordered).
- * dx may be dy, dres or h itself.  1 <= cols <= 16384.  All sums are fp32 in an order fixed
- * by the sizes: results repeat bit for bit on one kind of device.
+ * dx may be dy, dres or h itself.  1 <= cols <= 16384.  All sums are fp32 in an
+ * order fixed by sizes and alignment: results repeat bit for bit on one kind of device.
  */
 int dsa_rmsnorm_backward(const void *dy, const void *h, const void *weight, const void *dres,
                          int64_t rows, int cols, int dtype, int weight_dtype, float eps,

@@ -394,3 +394,95 @@ def test_streams_graphs_and_side_by_side_calls():
         o2, v2 = torch.empty_like(o), torch.empty_like(v)
         dsa.dsa_rmsnorm_backward(a, b, w[:1024].float().contiguous(), EPS, o2, v2)
         assert torch.equal(o, o2) and torch.equal(v, v2)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("rows,cols", [(5000, 40), (4999, 248), (6001, 256), (5003, 1000), (4900, 1024), (700, 1032), (613, 4096),
+                                       (640, 6000), (609, 8192), (700, 8200), (650, 16384), (3001, 1001), (700, 4001), (5001, 129)])
+def test_many_rows(rows, cols, dtype):
+    """Enough rows for the ring of rows in shared memory, of every width class, with and without a tensor that keeps
+    them out of it, against fp64 and against the same rows one at a time."""
+    dsa, g = lib(), gen(rows + cols)
+    x, res, w = normal(g, rows, cols, dtype=dtype), normal(g, rows, cols, dtype=dtype, std=2.0), normal(g, cols).to(dtype)
+    h, out = torch.empty_like(x), torch.empty_like(x)
+    codes, scale = torch.empty((rows, cols), dtype=U8, device=DEV), torch.empty((rows, -(-cols // 128)), device=DEV)
+    dsa.dsa_rmsnorm(x, w, EPS, out=out, residual=res, residual_out=h, codes=codes, scale=scale, block=128)
+    pick = sorted({0, 1, 7, 8, rows // 2, rows - 9, rows - 2, rows - 1})
+    rh, ry = R.rmsnorm(x[pick], res[pick], w, EPS)
+    R.check_close(h[pick], rh, rh.abs() * (R.half_step(dtype) + R.FP32) + 1e-30, "h")
+    R.check_close(out[pick], ry, ry.abs() * (R.half_step(dtype) + REL_Y) + 1e-30, "out")
+    for b in range(scale.shape[1]):
+        cut = slice(b * 128, (b + 1) * 128)
+        R.check_fp8(codes[pick][:, cut], scale[pick][:, b], ry[:, cut], REL_Y, 0, f"block {b}")
+    row_codes, row_scale = torch.empty((rows, cols), dtype=U8, device=DEV), torch.empty(rows, device=DEV)
+    out2 = torch.empty_like(out)
+    dsa.dsa_rmsnorm(x, w, EPS, out=out2, codes=row_codes, scale=row_scale)  # no residual, a scale a row
+    _, ry = R.rmsnorm(x[pick], None, w, EPS)
+    R.check_close(out2[pick], ry, ry.abs() * (R.half_step(dtype) + REL_Y) + 1e-30, "out without residual")
+    R.check_fp8(row_codes[pick], row_scale[pick], ry, REL_Y, 0, "row codes")
+    r2, x2 = res.clone(), x.clone()
+    dsa.dsa_rmsnorm(x2, w, EPS, out=x2, residual=r2, residual_out=r2)  # in place
+    assert torch.equal(r2, h) and torch.equal(x2, out)
+    # backward
+    dy, dres = normal(g, rows, cols, dtype=dtype), normal(g, rows, cols, dtype=dtype)
+    for extra in (None, dres):
+        dx, dw = torch.empty_like(h), torch.empty(cols, device=DEV)
+        dsa.dsa_rmsnorm_backward(dy, h, w, EPS, dx, dw, dres=extra)
+        rx, rw, mag, wmag = R.rmsnorm_backward(dy, h, w, extra, EPS)
+        R.check_close(dx, rx, rx.abs() * R.half_step(dtype) + 48 * R.FP32 * mag + 1e-30, "dx")
+        R.check_close(dw, rw, (rows / 100 + 128) * R.FP32 * wmag + 1e-30, "dweight")
+        hh, dw2 = h.clone(), torch.empty_like(dw)
+        dsa.dsa_rmsnorm_backward(dy, hh, w, EPS, hh, dw2, dres=extra)
+        assert torch.equal(hh, dx) and torch.equal(dw2, dw)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("cols", [9, 24, 127, 129, 520, 1111, 2049, 8190])
+def test_every_misalignment(cols, dtype):
+    """Rows at every element offset from 16 bytes, in every tensor: the values of the aligned call, and nothing beside
+    them."""
+    dsa, g = lib(), gen(cols)
+    rows = 3
+    x, res, w = normal(g, rows, cols, dtype=dtype), normal(g, rows, cols, dtype=dtype), normal(g, cols).to(dtype)
+    want = [torch.empty_like(x), torch.empty_like(x), torch.empty((rows, cols), dtype=U8, device=DEV), torch.empty(rows, device=DEV)]
+    dsa.dsa_rmsnorm(x, w, EPS, out=want[0], residual=res, residual_out=want[1], codes=want[2], scale=want[3])
+
+    def shifted(t, off, fill=None):
+        """A copy of t that begins `off` elements into a larger buffer, and that buffer."""
+        buf = torch.full((t.numel() + 48,), 7, dtype=t.dtype, device=DEV)
+        view = buf[off:off + t.numel()].view(t.shape)
+        view.copy_(t if fill is None else torch.full_like(t, fill))
+        return view, buf
+
+    for off in range(16):
+        (xs, _), (rs, _), (ws, _) = shifted(x, off), shifted(res, (off * 3) % 16), shifted(w, (off * 5) % 16)
+        outs = [shifted(t, (off * k) % 16, fill=5) for t, k in zip(want, (7, 1, 9, 1))]
+        (o, _), (h, _), (c, _), (s, _) = outs
+        dsa.dsa_rmsnorm(xs, ws, EPS, out=o, residual=rs, residual_out=h, codes=c, scale=s)
+        for (view, buf), ref, k in zip(outs, want, (7, 1, 9, 1)):
+            at = (off * k) % 16
+            assert torch.equal(view, ref)
+            assert (buf[:at] == 7).all() and (buf[at + ref.numel():] == 7).all()
+    dy, dw0, dx0 = normal(g, rows, cols, dtype=dtype), torch.empty(cols, device=DEV), torch.empty_like(x)
+    dsa.dsa_rmsnorm_backward(dy, x, w, EPS, dx0, dw0, dres=res)
+    for off in range(16):
+        dx, buf = shifted(x, (off * 3) % 16, fill=5)
+        dw = torch.empty_like(dw0)
+        dsa.dsa_rmsnorm_backward(shifted(dy, off)[0], shifted(x, (off * 7) % 16)[0], shifted(w, (off * 5) % 16)[0], EPS, dx, dw,
+                                 dres=shifted(res, (off * 9) % 16)[0])
+        at = (off * 3) % 16
+        assert torch.equal(dx, dx0) and torch.equal(dw, dw0)
+        assert (buf[:at] == 7).all() and (buf[at + dx.numel():] == 7).all()
+
+
+def test_quotients_are_those_of_a_division():
+    """Codes of the norm's fp32 output against dsa_quantize_fp8, which divides: equal bytes over many magnitudes."""
+    dsa, g = lib(), gen(77)
+    for k, std in enumerate((1e-35, 1e-20, 1e-3, 1.0, 1e4, 1e18)):
+        x = normal(g, 700, 4096)
+        w = torch.full((4096,), std, device=DEV)
+        out, codes, scale = torch.empty_like(x), torch.empty(x.shape, dtype=U8, device=DEV), torch.empty(700, device=DEV)
+        dsa.dsa_rmsnorm(x, w, EPS, out=out, codes=codes, scale=scale, scale_mode=k & 1)
+        qc, qs = torch.empty_like(codes), torch.empty_like(scale)
+        dsa.dsa_quantize_fp8(out, qc, qs, k & 1)
+        assert torch.equal(qc, codes) and torch.equal(qs, scale), std
