@@ -88,7 +88,23 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         getattr(lib, name).restype = i32
     if path is None:
         _lib = lib
+        _load_fastcall(p)
     return lib
+
+
+_fast = None  # the native call path (csrc/fastcall.c), loaded with the library
+
+
+def _load_fastcall(path: str):
+    global _fast
+    so = os.path.join(_HERE, "_fastcall.so")
+    if not os.path.exists(so):
+        raise RuntimeError(f"{so} is missing: build it with `python -m sparse_attention_02_gb300.build`")
+    from . import _fastcall
+
+    _fastcall.init(path, (torch.bfloat16, torch.float32, torch.float64, torch.int32, torch.uint8), torch._C._cuda_getDevice,
+                   torch._C._cuda_getCurrentRawStream, lambda n, cur: torch.empty(n, dtype=torch.uint8, device=cur))
+    _fast = _fastcall
 
 
 def _check(rc: int):
@@ -216,6 +232,18 @@ def _raw_stream(stream, cur: int) -> int:
         return torch.cuda.current_stream().cuda_stream
 
 
+def _native(name: str, *args) -> bool:
+    """Makes the call natively where its arguments are plainly right; False leaves it, and what is wrong with it, to
+    the Python form."""
+    if _fast is None:
+        load_library()
+    rc = getattr(_fast, name)(*args)
+    if rc is NotImplemented:
+        return False
+    _check(rc)
+    return True
+
+
 def _refuse(t, cur: int, name: str, dtype, shape, rows: bool = False):
     """The error for an argument that is not what its call needs."""
     if not isinstance(t, torch.Tensor):
@@ -288,6 +316,8 @@ def dsa_rmsnorm(x, weight, eps: float, out=None, residual=None, residual_out=Non
     [rows, n] get y as E4M3 codes with one scale per row (block = 0) or per 128 columns (block = 128,
     n = ceil(cols / 128)).  weight [cols] is bf16 or fp32.  Rows of x, residual, residual_out and out may be
     strided.  Returns (residual_out, out, codes, scale) as given."""
+    if _native("rmsnorm", x, weight, eps, out, residual, residual_out, codes, scale, block, scale_mode, stream):
+        return residual_out, out, codes, scale
     t = _dtype_of(x, "x")
     if x.dim() != 2:
         raise TypeError("x must be 2-D")
@@ -309,7 +339,7 @@ def dsa_rmsnorm(x, weight, eps: float, out=None, residual=None, residual_out=Non
         n = -(-cols // block) if block > 0 else 1
         a_s = _at(scale, cur, "scale", f32, (rows,) if n == 1 and isinstance(scale, torch.Tensor) and scale.dim() == 1 else (rows, n))
     _check((_lib or load_library()).dsa_rmsnorm(
-        a_x, ldx, a_r, ldr, _at(weight, cur, "weight", wt, (cols,)), rows, cols, _DTYPE[t], _DTYPE[wt], eps, a_h, ldh, a_o, ldo,
+        a_x, ldx, a_r, ldr, _at(weight, cur, "weight", wt, (cols,)), rows, cols, _DTYPE[t], _DTYPE[wt], float(eps), a_h, ldh, a_o, ldo,
         a_c, a_s, block, scale_mode, _raw_stream(stream, cur)))
     return residual_out, out, codes, scale
 
@@ -322,6 +352,8 @@ def dsa_rmsnorm_backward(dy, h, weight, eps: float, dx, dweight, dres=None, work
     """Gradients of dsa_rmsnorm: dy, h, dres (or None) and dx [rows, cols] bf16 or fp32, h the saved residual_out
     (x without a residual); dx is the gradient of x and of the residual; dweight fp32 [cols].  ``workspace``: a
     CUDA tensor of at least dsa_rmsnorm_backward_workspace_size(rows, cols) bytes; taken from PyTorch when None."""
+    if _native("rmsnorm_backward", dy, h, weight, eps, dx, dweight, dres, workspace, stream):
+        return dx, dweight
     t = _dtype_of(h, "h")
     if h.dim() != 2:
         raise TypeError("h must be 2-D")
@@ -333,7 +365,7 @@ def dsa_rmsnorm_backward(dy, h, weight, eps: float, dx, dweight, dres=None, work
     a_dx, a_dw = _at(dx, cur, "dx", t, shape), _at(dweight, cur, "dweight", torch.float32, (cols,))
     need = 0 if workspace is not None else lib.dsa_rmsnorm_backward_workspace_size(rows, cols)
     ws, ws_bytes, keep = _workspace(workspace, need, cur, stream)
-    _check(lib.dsa_rmsnorm_backward(a_dy, a_h, a_w, a_e, rows, cols, _DTYPE[t], _DTYPE[wt], eps, a_dx, a_dw, ws, ws_bytes,
+    _check(lib.dsa_rmsnorm_backward(a_dy, a_h, a_w, a_e, rows, cols, _DTYPE[t], _DTYPE[wt], float(eps), a_dx, a_dw, ws, ws_bytes,
                                     _raw_stream(stream, cur)))
     return dx, dweight
 
@@ -348,6 +380,9 @@ def dsa_cache_append(pos, block_table, inv_freq, kv=None, kv_pool=None, kI=None,
     kv_weight [512] (bf16 or fp32) when given, columns [512, 576) rotated in pairs (2i, 2i + 1).  Index cache: kI
     bf16 or fp32 [T, 128] (rows may be strided), pairs (i, i + 32) of its first 64 columns rotated, into k8_pool
     uint8 [P, page, 128] (E4M3 codes) and ks_pool fp32 [P, page].  Either cache may be left out."""
+    if _native("cache_append", pos, block_table, inv_freq, kv, kv_pool, kI, k8_pool, ks_pool, seq, kv_weight, eps, scale_mode,
+               stream):
+        return
     if kv is None and kI is None:
         raise ValueError("kv or kI is needed")
     if not isinstance(pos, torch.Tensor) or pos.dim() != 1 or not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
@@ -374,7 +409,7 @@ def dsa_cache_append(pos, block_table, inv_freq, kv=None, kv_pool=None, kI=None,
     _check((_lib or load_library()).dsa_cache_append(
         _at(pos, cur, "pos", i32, (T,)), None if seq is None else _at(seq, cur, "seq", i32, (T,)), T,
         _at(block_table, cur, "block_table", i32, table), table[0], table[1], P, ps,
-        _at(inv_freq, cur, "inv_freq", torch.float64, (32,)), a_kv, ld_kv, a_w, w, eps, a_pool, a_k, ld_kI, k, scale_mode, a_k8,
+        _at(inv_freq, cur, "inv_freq", torch.float64, (32,)), a_kv, ld_kv, a_w, w, float(eps), a_pool, a_k, ld_kI, k, scale_mode, a_k8,
         a_ks, _raw_stream(stream, cur)))
 
 
@@ -384,6 +419,8 @@ def dsa_rope_queries(pos, inv_freq, q_rope=None, q=None, qI=None, q8=None, q_sca
     [512, 576) of q bf16 [T, H, 576]; the index queries qI bf16 or fp32 [T, H_I, 128] into q8 uint8 (E4M3 codes) and
     q_scale fp32 [T].  pos int32 [T] (negative: padding, outputs left alone), inv_freq fp64 [32].  Either part may be
     left out; q_rope may be q[:, :, 512:]."""
+    if _native("rope_queries", pos, inv_freq, q_rope, q, qI, q8, q_scale, scale_mode, stream):
+        return
     if not isinstance(pos, torch.Tensor) or pos.dim() != 1:
         raise TypeError("pos must be a 1-D torch.Tensor")
     if q_rope is None and qI is None:
@@ -417,6 +454,8 @@ def dsa_rope_queries(pos, inv_freq, q_rope=None, q=None, qI=None, q8=None, q_sca
 def dsa_index_rope_backward(g, pos, inv_freq, dx, stream=None):
     """Gradient of the index rotation: g fp32 [T, H_I, 128] (or [T, 128], keys), the gradient of the rotated vectors
     (dsa_indexer_warmup's dq or dk), turned back by the tokens' angles into dx (bf16 or fp32, g's shape)."""
+    if _native("index_rope_backward", g, pos, inv_freq, dx, stream):
+        return dx
     if not isinstance(g, torch.Tensor) or g.dim() not in (2, 3):
         raise TypeError("g must be a 2-D or 3-D torch.Tensor")
     shape = g.shape
@@ -612,6 +651,8 @@ def dsa_mla_decode_paged(q, kv_pool, block_table, ctx_len, sm_scale: float, out,
     [P, page, 576], block_table int32 [B, max_pages], ctx_len int32 [B] -> out bf16 [B, H, 512], lse fp32 [B, H].
     ``workspace``: a CUDA tensor of at least dsa_mla_decode_workspace_size(B, H) bytes; taken from PyTorch's
     allocator when None."""
+    if _native("mla_decode_paged", q, kv_pool, block_table, ctx_len, sm_scale, out, lse, workspace, stream):
+        return out, lse
     if not isinstance(q, torch.Tensor) or q.dim() != 3 or not isinstance(kv_pool, torch.Tensor) or kv_pool.dim() != 3 \
             or not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
         raise TypeError("q and kv_pool must be 3-D, block_table a 2-D torch.Tensor")
@@ -624,7 +665,7 @@ def dsa_mla_decode_paged(q, kv_pool, block_table, ctx_len, sm_scale: float, out,
     a_out, a_lse = _at(out, cur, "out", bf16, (B, H, 512)), _at(lse, cur, "lse", torch.float32, (B, H))
     need = 0 if workspace is not None else lib.dsa_mla_decode_workspace_size(B, H)
     ws, ws_bytes, keep = _workspace(workspace, need, cur, stream)
-    _check(lib.dsa_mla_decode_paged(a_q, a_kv, P, ps, a_bt, mp, a_ctx, B, H, sm_scale, a_out, a_lse, ws, ws_bytes,
+    _check(lib.dsa_mla_decode_paged(a_q, a_kv, P, ps, a_bt, mp, a_ctx, B, H, float(sm_scale), a_out, a_lse, ws, ws_bytes,
                                     _raw_stream(stream, cur)))
     return out, lse
 

@@ -1,8 +1,10 @@
 """Build libdsa.so (sm_103a) in-tree with nvcc.
 
 Each translation unit under csrc/ compiles in parallel to an object file, then
-one link step makes ``sparse_attention_02_gb300/libdsa.so``.  Run as a script
-or call ``build()``.  Only the CUDA toolkit is needed (no torch, no cmake).
+one link step makes ``sparse_attention_02_gb300/libdsa.so``; the host compiler
+makes ``_fastcall.so``, the native part of the Python binding.  Run as a script
+or call ``build()``.  Only the CUDA toolkit, a C compiler and Python's headers
+are needed (no torch, no cmake).
 """
 from __future__ import annotations
 
@@ -11,11 +13,13 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(HERE, "_objs")
 LIB = os.path.join(HERE, "libdsa.so")
+FAST = os.path.join(HERE, "_fastcall.so")
 SOURCES = ["api.cu", "quantize.cu", "rmsnorm.cu", "rope.cu", "indexer.cu", "topk.cu", "indexer_topk.cu", "warmup.cu",
            "sparse_mla.cu", "dense_mla.cu", "prefill_host.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -48,8 +52,21 @@ def _compile(src: str, extra=()) -> str:
     return obj
 
 
+def _build_fastcall():
+    src, hdr = os.path.join(CSRC, "fastcall.c"), os.path.join(HERE, "..", "include", "dsa.h")
+    if os.path.exists(FAST) and os.path.getmtime(FAST) >= max(os.path.getmtime(src), os.path.getmtime(hdr)):
+        return
+    tmp = FAST + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CC", "gcc"), "-O2", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"], src, "-o", tmp, "-ldl"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed for fastcall.c:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, FAST)
+
+
 def build(verbose: bool = False, extra=()) -> str:
     os.makedirs(OBJ, exist_ok=True)
+    _build_fastcall()
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         objs = list(ex.map(lambda s: _compile(s, extra), SOURCES))
     if not os.path.exists(LIB) or os.path.getmtime(LIB) < max(os.path.getmtime(o) for o in objs):

@@ -1,0 +1,414 @@
+/* The calls of the Python binding that go out once per layer and token, with
+ * their argument checks in C: on a few tokens the interpreter's own checks and
+ * the marshalling of twenty arguments take the host longer than the kernels
+ * take the GPU (a decode step's cache append: 10.6 us of host time in Python).
+ *
+ * Every function takes the arguments of the binding's function of that name,
+ * in order, and either makes the call, returning the library's status, or
+ * returns NotImplemented without having done anything, where an argument is
+ * not plainly what the call needs; the Python form then finds out what is
+ * wrong and says so, or makes the call itself.
+ */
+#define PY_SSIZE_T_CLEAN
+#include <Python.h>
+#include <dlfcn.h>
+#include <stdint.h>
+
+#include "../../include/dsa.h"
+
+static PyObject *s_dtype, *s_shape, *s_get_device, *s_is_contiguous, *s_data_ptr, *s_stride, *s_cuda_stream;
+static PyObject *t_bf16, *t_fp32, *t_fp64, *t_int32, *t_uint8; /* torch dtypes */
+static PyObject *get_device_fn, *get_stream_fn, *empty_fn;     /* current device, its raw stream, empty(bytes, device) */
+
+static __typeof__(&dsa_rmsnorm) f_rmsnorm;
+static __typeof__(&dsa_rmsnorm_backward) f_rmsnorm_backward;
+static __typeof__(&dsa_rmsnorm_backward_workspace_size) f_rmsnorm_backward_ws;
+static __typeof__(&dsa_cache_append) f_cache_append;
+static __typeof__(&dsa_rope_queries) f_rope_queries;
+static __typeof__(&dsa_index_rope_backward) f_index_rope_backward;
+static __typeof__(&dsa_mla_decode_paged) f_mla_decode;
+static __typeof__(&dsa_mla_decode_workspace_size) f_mla_decode_ws;
+
+/* What is known of a tensor argument. */
+typedef struct {
+    int nd;
+    int64_t dim[3], stride[3]; /* stride only after strides() */
+    int dtype;                 /* DSA_BF16, DSA_FP32, or one of the below */
+    void *p;
+} Arg;
+enum { K_FP64 = 10, K_INT32, K_UINT8, K_ANY /* bf16 or fp32 */ };
+
+static int64_t as_int(PyObject *o, int *ok)
+{
+    int64_t v = o ? PyLong_AsLongLong(o) : -1;
+    if (!o || (v == -1 && PyErr_Occurred()))
+        *ok = 0;
+    Py_XDECREF(o);
+    return v;
+}
+
+/* Dtype, device, shape (up to 3 dimensions) and address of t; 0 where it is not a plain tensor of the device. */
+static int look(PyObject *t, long cur, int want, Arg *a)
+{
+    int ok = 1;
+    PyObject *d = PyObject_GetAttr(t, s_dtype);
+    if (!d)
+        return 0;
+    a->dtype = d == t_bf16 ? DSA_BF16 : d == t_fp32 ? DSA_FP32 : d == t_fp64 ? K_FP64 : d == t_int32 ? K_INT32 : d == t_uint8 ? K_UINT8 : -1;
+    Py_DECREF(d);
+    if (want == K_ANY ? (a->dtype != DSA_BF16 && a->dtype != DSA_FP32) : a->dtype != want)
+        return 0;
+    if (as_int(PyObject_CallMethodNoArgs(t, s_get_device), &ok) != cur || !ok)
+        return 0;
+    PyObject *shape = PyObject_GetAttr(t, s_shape);
+    if (!shape)
+        return 0;
+    ok = PyTuple_Check(shape) && PyTuple_GET_SIZE(shape) <= 3;
+    a->nd = ok ? (int)PyTuple_GET_SIZE(shape) : 0;
+    for (int i = 0; i < a->nd; ++i) {
+        a->dim[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(shape, i));
+        if (a->dim[i] < 0)
+            ok = 0;
+    }
+    Py_DECREF(shape);
+    a->p = (void *)(uintptr_t)as_int(PyObject_CallMethodNoArgs(t, s_data_ptr), &ok);
+    return ok && !PyErr_Occurred();
+}
+
+static int contiguous(PyObject *t)
+{
+    PyObject *c = PyObject_CallMethodNoArgs(t, s_is_contiguous);
+    int yes = c == Py_True;
+    Py_XDECREF(c);
+    return yes;
+}
+
+static int strides(PyObject *t, Arg *a)
+{
+    PyObject *s = PyObject_CallMethodNoArgs(t, s_stride);
+    int ok = s && PyTuple_Check(s) && PyTuple_GET_SIZE(s) == a->nd;
+    for (int i = 0; ok && i < a->nd; ++i)
+        a->stride[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(s, i));
+    Py_XDECREF(s);
+    return ok && !PyErr_Occurred();
+}
+
+/* A contiguous tensor of the shape (n1, n2 < 0: fewer dimensions). */
+static int at(PyObject *t, long cur, int want, int64_t n0, int64_t n1, int64_t n2, Arg *a)
+{
+    return look(t, cur, want, a) && a->nd == 1 + (n1 >= 0) + (n2 >= 0) && a->dim[0] == n0 && (n1 < 0 || a->dim[1] == n1) &&
+           (n2 < 0 || a->dim[2] == n2) && contiguous(t);
+}
+
+/* A 2-D tensor whose rows may be apart; *ld is their distance. */
+static int at_rows(PyObject *t, long cur, int want, int64_t n0, int64_t n1, Arg *a, int64_t *ld)
+{
+    if (!look(t, cur, want, a) || a->nd != 2 || a->dim[0] != n0 || a->dim[1] != n1 || !strides(t, a))
+        return 0;
+    *ld = n0 > 1 ? a->stride[0] : n1;
+    return (n1 == 1 || a->stride[1] == 1) && *ld >= n1;
+}
+
+/* Device, and the stream of the call: stream's, or the device's current one. */
+static int where(PyObject *stream, long *cur, dsa_stream_t *s)
+{
+    int ok = 1;
+    *cur = (long)as_int(PyObject_CallNoArgs(get_device_fn), &ok);
+    if (!ok)
+        return 0;
+    PyObject *v;
+    if (stream == Py_None) {
+        PyObject *c = PyLong_FromLong(*cur);
+        v = c ? PyObject_CallOneArg(get_stream_fn, c) : NULL;
+        Py_XDECREF(c);
+    } else {
+        v = PyObject_GetAttr(stream, s_cuda_stream);
+    }
+    *s = (dsa_stream_t)(uintptr_t)as_int(v, &ok);
+    return ok;
+}
+
+/* Workspace of `need` bytes: the caller's, or one of the allocator's on the current stream, kept until *keep is
+ * released (a call on another stream leaves it to the Python form). */
+static int workspace(PyObject *ws, PyObject *stream, long cur, size_t need, void **p, size_t *bytes, PyObject **keep)
+{
+    Arg a;
+    int ok = 1;
+    *keep = NULL;
+    *p = NULL;
+    *bytes = 0;
+    if (ws != Py_None) {
+        if (!look(ws, cur, K_UINT8, &a) || a.nd != 1 || !contiguous(ws))
+            return 0;
+        *p = a.p;
+        *bytes = (size_t)a.dim[0];
+        return 1;
+    }
+    if (!need)
+        return 1;
+    if (stream != Py_None)
+        return 0;
+    *keep = PyObject_CallFunction(empty_fn, "nl", (Py_ssize_t)need, cur);
+    if (!*keep)
+        return 0;
+    *p = (void *)(uintptr_t)as_int(PyObject_CallMethodNoArgs(*keep, s_data_ptr), &ok);
+    *bytes = need;
+    return ok;
+}
+
+/* Numbers: plain Python ones only. */
+static int number(PyObject *o, double *v)
+{
+    if (!PyFloat_Check(o) && !PyLong_Check(o))
+        return 0;
+    *v = PyFloat_AsDouble(o);
+    return !(*v == -1.0 && PyErr_Occurred());
+}
+
+static int integer(PyObject *o, int *v)
+{
+    if (!PyLong_Check(o))
+        return 0;
+    long x = PyLong_AsLong(o);
+    *v = (int)x;
+    return x >= INT32_MIN && x <= INT32_MAX && !PyErr_Occurred();
+}
+
+static PyObject *not_plain(PyObject *keep)
+{
+    Py_XDECREF(keep);
+    PyErr_Clear();
+    Py_RETURN_NOTIMPLEMENTED;
+}
+
+#define FITS(n) ((n) <= INT32_MAX)
+
+/* The library's call, with other Python threads free to run. */
+#define CALL(rc, expr)                                                                                                              \
+    do {                                                                                                                            \
+        Py_BEGIN_ALLOW_THREADS rc = (expr);                                                                                         \
+        Py_END_ALLOW_THREADS                                                                                                        \
+    } while (0)
+
+/* x, weight, eps, out, residual, residual_out, codes, scale, block, scale_mode, stream */
+static PyObject *py_rmsnorm(PyObject *m, PyObject *const *v, Py_ssize_t n)
+{
+    long cur;
+    dsa_stream_t st;
+    Arg x, w, o = {0}, r = {0}, h = {0}, c = {0}, s = {0};
+    int64_t ldx, ldo = 0, ldr = 0, ldh = 0;
+    double eps;
+    int block, mode;
+    if (n != 11 || !where(v[10], &cur, &st) || !number(v[2], &eps) || !integer(v[8], &block) || !integer(v[9], &mode) ||
+        !look(v[0], cur, K_ANY, &x) || x.nd != 2 || !FITS(x.dim[1]) || !strides(v[0], &x))
+        return not_plain(NULL);
+    const int64_t rows = x.dim[0], cols = x.dim[1];
+    ldx = rows > 1 ? x.stride[0] : cols;
+    if ((cols != 1 && x.stride[1] != 1) || ldx < cols || !at(v[1], cur, K_ANY, cols, -1, -1, &w) ||
+        (v[3] != Py_None && !at_rows(v[3], cur, x.dtype, rows, cols, &o, &ldo)) ||
+        (v[4] != Py_None && !at_rows(v[4], cur, x.dtype, rows, cols, &r, &ldr)) ||
+        (v[5] != Py_None && !at_rows(v[5], cur, x.dtype, rows, cols, &h, &ldh)) ||
+        (v[6] != Py_None && !at(v[6], cur, K_UINT8, rows, cols, -1, &c)))
+        return not_plain(NULL);
+    if (v[7] != Py_None) {
+        const int64_t parts = block > 0 ? (cols + block - 1) / block : 1;
+        if (!look(v[7], cur, DSA_FP32, &s) || s.dim[0] != rows || !contiguous(v[7]) ||
+            !((s.nd == 2 && s.dim[1] == parts) || (s.nd == 1 && parts == 1)))
+            return not_plain(NULL);
+    }
+    int rc;
+    CALL(rc, f_rmsnorm(x.p, ldx, r.p, ldr, w.p, rows, (int)cols, x.dtype, w.dtype, (float)eps, h.p, ldh, o.p, ldo,
+                                     c.p, s.p, block, mode, st));
+    return PyLong_FromLong(rc);
+}
+
+/* dy, h, weight, eps, dx, dweight, dres, workspace, stream */
+static PyObject *py_rmsnorm_backward(PyObject *m, PyObject *const *v, Py_ssize_t n)
+{
+    long cur;
+    dsa_stream_t st;
+    Arg dy, h, w, dx, dw, e = {0};
+    double eps;
+    void *ws;
+    size_t bytes;
+    PyObject *keep = NULL;
+    if (n != 9 || !where(v[8], &cur, &st) || !number(v[3], &eps) || !look(v[1], cur, K_ANY, &h) || h.nd != 2 ||
+        !FITS(h.dim[1]) || !contiguous(v[1]))
+        return not_plain(NULL);
+    const int64_t rows = h.dim[0], cols = h.dim[1];
+    if (!at(v[0], cur, h.dtype, rows, cols, -1, &dy) || !at(v[2], cur, K_ANY, cols, -1, -1, &w) ||
+        !at(v[4], cur, h.dtype, rows, cols, -1, &dx) || !at(v[5], cur, DSA_FP32, cols, -1, -1, &dw) ||
+        (v[6] != Py_None && !at(v[6], cur, h.dtype, rows, cols, -1, &e)) ||
+        !workspace(v[7], v[8], cur, v[7] == Py_None ? f_rmsnorm_backward_ws(rows, (int)cols) : 0, &ws, &bytes, &keep))
+        return not_plain(keep);
+    int rc;
+    CALL(rc, f_rmsnorm_backward(dy.p, h.p, w.p, e.p, rows, (int)cols, h.dtype, w.dtype, (float)eps, dx.p, dw.p, ws, bytes, st));
+    Py_XDECREF(keep);
+    return PyLong_FromLong(rc);
+}
+
+/* pos, block_table, inv_freq, kv, kv_pool, kI, k8_pool, ks_pool, seq, kv_weight, eps, scale_mode, stream */
+static PyObject *py_cache_append(PyObject *m, PyObject *const *v, Py_ssize_t n)
+{
+    long cur;
+    dsa_stream_t st;
+    Arg pos, bt, fr, kv = {0}, kp = {0}, k = {0}, k8 = {0}, ks = {0}, seq = {0}, w = {0};
+    int64_t ld = 0, ldI = 0;
+    double eps;
+    int mode;
+    const int with_kv = n == 13 && v[3] != Py_None, with_k = n == 13 && v[5] != Py_None;
+    if (n != 13 || (!with_kv && !with_k) || !where(v[12], &cur, &st) || !number(v[10], &eps) || !integer(v[11], &mode) ||
+        !look(v[0], cur, K_INT32, &pos) || pos.nd != 1 || !FITS(pos.dim[0]) || !contiguous(v[0]) ||
+        !look(v[1], cur, K_INT32, &bt) || bt.nd != 2 || !FITS(bt.dim[0]) || !FITS(bt.dim[1]) || !contiguous(v[1]) ||
+        !at(v[2], cur, K_FP64, 32, -1, -1, &fr))
+        return not_plain(NULL);
+    const int64_t T = pos.dim[0];
+    int64_t pages = 0, page = 0;
+    if (with_kv) {
+        if (!at_rows(v[3], cur, DSA_BF16, T, 576, &kv, &ld) || !look(v[4], cur, DSA_BF16, &kp) || kp.nd != 3 ||
+            kp.dim[2] != 576 || !contiguous(v[4]) || (v[9] != Py_None && !at(v[9], cur, K_ANY, 512, -1, -1, &w)))
+            return not_plain(NULL);
+        pages = kp.dim[0], page = kp.dim[1];
+    }
+    if (with_k) {
+        if (!at_rows(v[5], cur, K_ANY, T, 128, &k, &ldI) || !look(v[6], cur, K_UINT8, &k8) || k8.nd != 3 || k8.dim[2] != 128 ||
+            !contiguous(v[6]) || (with_kv && (k8.dim[0] != pages || k8.dim[1] != page)))
+            return not_plain(NULL);
+        pages = k8.dim[0], page = k8.dim[1];
+        if (!at(v[7], cur, DSA_FP32, pages, page, -1, &ks))
+            return not_plain(NULL);
+    }
+    if (!FITS(pages) || !FITS(page) || (v[8] != Py_None && !at(v[8], cur, K_INT32, T, -1, -1, &seq)))
+        return not_plain(NULL);
+    int rc;
+    CALL(rc, f_cache_append(pos.p, seq.p, (int)T, bt.p, (int)bt.dim[0], (int)bt.dim[1], (int)pages, (int)page, fr.p,
+                                          kv.p, ld, w.p, w.dtype, (float)eps, kp.p, k.p, ldI, k.dtype, mode, k8.p, ks.p, st));
+    return PyLong_FromLong(rc);
+}
+
+/* pos, inv_freq, q_rope, q, qI, q8, q_scale, scale_mode, stream */
+static PyObject *py_rope_queries(PyObject *m, PyObject *const *v, Py_ssize_t n)
+{
+    long cur;
+    dsa_stream_t st;
+    Arg pos, fr, r = {0}, q = {0}, qi = {0}, q8 = {0}, s = {0};
+    int64_t H = 0, HI = 0;
+    int mode;
+    const int with_r = n == 9 && v[2] != Py_None, with_i = n == 9 && v[4] != Py_None;
+    if (n != 9 || (!with_r && !with_i) || !where(v[8], &cur, &st) || !integer(v[7], &mode) || !look(v[0], cur, K_INT32, &pos) ||
+        pos.nd != 1 || !FITS(pos.dim[0]) || !contiguous(v[0]) || !at(v[1], cur, K_FP64, 32, -1, -1, &fr))
+        return not_plain(NULL);
+    const int64_t T = pos.dim[0];
+    if (with_r) {
+        if (!look(v[2], cur, DSA_BF16, &r) || r.nd != 3 || r.dim[0] != T || r.dim[2] != 64 || !strides(v[2], &r) || r.stride[2] != 1)
+            return not_plain(NULL);
+        H = r.dim[1];
+        if (!FITS(H) || !at(v[3], cur, DSA_BF16, T, H, 576, &q))
+            return not_plain(NULL);
+    }
+    if (with_i) {
+        if (!look(v[4], cur, K_ANY, &qi) || qi.nd != 3 || qi.dim[0] != T || qi.dim[2] != 128 || !contiguous(v[4]))
+            return not_plain(NULL);
+        HI = qi.dim[1];
+        if (!FITS(HI) || !at(v[5], cur, K_UINT8, T, HI, 128, &q8) || !at(v[6], cur, DSA_FP32, T, -1, -1, &s))
+            return not_plain(NULL);
+    }
+    int rc;
+    CALL(rc, f_rope_queries(pos.p, fr.p, (int)T, r.p, T > 1 ? r.stride[0] : 0, H > 1 ? r.stride[1] : 0, (int)H, q.p,
+                                          qi.p, (int)HI, with_i ? qi.dtype : DSA_BF16, mode, q8.p, s.p, st));
+    return PyLong_FromLong(rc);
+}
+
+/* g, pos, inv_freq, dx, stream */
+static PyObject *py_index_rope_backward(PyObject *m, PyObject *const *v, Py_ssize_t n)
+{
+    long cur;
+    dsa_stream_t st;
+    Arg g, pos, fr, dx;
+    if (n != 5 || !where(v[4], &cur, &st) || !look(v[0], cur, DSA_FP32, &g) || g.nd < 2 || g.dim[g.nd - 1] != 128 ||
+        !FITS(g.dim[0]) || !FITS(g.dim[1]) || !contiguous(v[0]) || !at(v[1], cur, K_INT32, g.dim[0], -1, -1, &pos) ||
+        !at(v[2], cur, K_FP64, 32, -1, -1, &fr) || !at(v[3], cur, K_ANY, g.dim[0], g.dim[1], g.nd == 3 ? 128 : -1, &dx))
+        return not_plain(NULL);
+    int rc;
+    CALL(rc, f_index_rope_backward(g.p, pos.p, fr.p, (int)g.dim[0], g.nd == 3 ? (int)g.dim[1] : 1, dx.p, dx.dtype, st));
+    return PyLong_FromLong(rc);
+}
+
+/* q, kv_pool, block_table, ctx_len, sm_scale, out, lse, workspace, stream */
+static PyObject *py_mla_decode_paged(PyObject *m, PyObject *const *v, Py_ssize_t n)
+{
+    long cur;
+    dsa_stream_t st;
+    Arg q, kv, bt, ctx, out, lse;
+    double scale;
+    void *ws;
+    size_t bytes;
+    PyObject *keep = NULL;
+    if (n != 9 || !where(v[8], &cur, &st) || !number(v[4], &scale) || !look(v[0], cur, DSA_BF16, &q) || q.nd != 3 ||
+        q.dim[2] != 576 || !FITS(q.dim[0]) || !FITS(q.dim[1]) || !contiguous(v[0]) || !look(v[1], cur, DSA_BF16, &kv) ||
+        kv.nd != 3 || kv.dim[2] != 576 || !FITS(kv.dim[0]) || !FITS(kv.dim[1]) || !contiguous(v[1]) ||
+        !look(v[2], cur, K_INT32, &bt) || bt.nd != 2 || bt.dim[0] != q.dim[0] || !FITS(bt.dim[1]) || !contiguous(v[2]) ||
+        !at(v[3], cur, K_INT32, q.dim[0], -1, -1, &ctx) || !at(v[5], cur, DSA_BF16, q.dim[0], q.dim[1], 512, &out) ||
+        !at(v[6], cur, DSA_FP32, q.dim[0], q.dim[1], -1, &lse) ||
+        !workspace(v[7], v[8], cur, v[7] == Py_None ? f_mla_decode_ws((int)q.dim[0], (int)q.dim[1]) : 0, &ws, &bytes, &keep))
+        return not_plain(keep);
+    int rc;
+    CALL(rc, f_mla_decode(q.p, kv.p, (int)kv.dim[0], (int)kv.dim[1], bt.p, (int)bt.dim[1], ctx.p, (int)q.dim[0],
+                                (int)q.dim[1], (float)scale, out.p, lse.p, ws, bytes, st));
+    Py_XDECREF(keep);
+    return PyLong_FromLong(rc);
+}
+
+/* init(path of the library, (bf16, fp32, fp64, int32, uint8), current device, raw stream of a device, empty(bytes, device)) */
+static PyObject *py_init(PyObject *m, PyObject *args)
+{
+    const char *path;
+    if (!PyArg_ParseTuple(args, "s(OOOOO)OOO", &path, &t_bf16, &t_fp32, &t_fp64, &t_int32, &t_uint8, &get_device_fn, &get_stream_fn,
+                          &empty_fn))
+        return NULL;
+    void *lib = dlopen(path, RTLD_NOW | RTLD_LOCAL);
+    if (!lib) {
+        PyErr_SetString(PyExc_RuntimeError, dlerror());
+        return NULL;
+    }
+    f_rmsnorm = (__typeof__(f_rmsnorm))dlsym(lib, "dsa_rmsnorm");
+    f_rmsnorm_backward = (__typeof__(f_rmsnorm_backward))dlsym(lib, "dsa_rmsnorm_backward");
+    f_rmsnorm_backward_ws = (__typeof__(f_rmsnorm_backward_ws))dlsym(lib, "dsa_rmsnorm_backward_workspace_size");
+    f_cache_append = (__typeof__(f_cache_append))dlsym(lib, "dsa_cache_append");
+    f_rope_queries = (__typeof__(f_rope_queries))dlsym(lib, "dsa_rope_queries");
+    f_index_rope_backward = (__typeof__(f_index_rope_backward))dlsym(lib, "dsa_index_rope_backward");
+    f_mla_decode = (__typeof__(f_mla_decode))dlsym(lib, "dsa_mla_decode_paged");
+    f_mla_decode_ws = (__typeof__(f_mla_decode_ws))dlsym(lib, "dsa_mla_decode_workspace_size");
+    if (!f_rmsnorm || !f_rmsnorm_backward || !f_rmsnorm_backward_ws || !f_cache_append || !f_rope_queries || !f_index_rope_backward ||
+        !f_mla_decode || !f_mla_decode_ws) {
+        PyErr_SetString(PyExc_RuntimeError, "the library lacks an entry point");
+        return NULL;
+    }
+    PyObject *kept[] = {t_bf16, t_fp32, t_fp64, t_int32, t_uint8, get_device_fn, get_stream_fn, empty_fn};
+    for (size_t i = 0; i < sizeof kept / sizeof *kept; ++i)
+        Py_INCREF(kept[i]);
+    Py_RETURN_NONE;
+}
+
+#define FAST(name) {#name, (PyCFunction)(void (*)(void))py_##name, METH_FASTCALL, NULL}
+static PyMethodDef methods[] = {FAST(rmsnorm),
+                                FAST(rmsnorm_backward),
+                                FAST(cache_append),
+                                FAST(rope_queries),
+                                FAST(index_rope_backward),
+                                FAST(mla_decode_paged),
+                                {"init", py_init, METH_VARARGS, NULL},
+                                {NULL, NULL, 0, NULL}};
+static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fastcall", NULL, -1, methods, NULL, NULL, NULL, NULL};
+
+PyMODINIT_FUNC PyInit__fastcall(void)
+{
+    s_dtype = PyUnicode_InternFromString("dtype");
+    s_shape = PyUnicode_InternFromString("shape");
+    s_get_device = PyUnicode_InternFromString("get_device");
+    s_is_contiguous = PyUnicode_InternFromString("is_contiguous");
+    s_data_ptr = PyUnicode_InternFromString("data_ptr");
+    s_stride = PyUnicode_InternFromString("stride");
+    s_cuda_stream = PyUnicode_InternFromString("cuda_stream");
+    return PyModule_Create(&module);
+}
