@@ -437,6 +437,8 @@ int dsa_rope_queries(const int32_t *pos, const double *inv_freq, int T, const vo
         return fail(DSA_ERR_INVALID_ARG, "neither q_rope nor qI given");
     if ((q_rope && !q) || (qI && (!q8 || !q_scale)))
         return fail(DSA_ERR_INVALID_ARG, "q_rope needs q, qI needs q8 and q_scale");
+    if (T > (1 << 30))
+        return fail(DSA_ERR_UNSUPPORTED, "T must be at most 2^30");
     if (q_rope && (H < 1 || H > 128))
         return fail(DSA_ERR_UNSUPPORTED, "H must be in [1, 128]");
     if (qI && (H_I < 1 || H_I > 64))

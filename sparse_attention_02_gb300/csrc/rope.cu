@@ -230,8 +230,11 @@ __global__ void __launch_bounds__(kAppendThreads, 8) cache_append_kernel(CacheAp
 }
 
 // ------------------------------------------------------------------ queries
-// Two CTAs per token, one for each part that is asked for.  Everything a thread
-// reads is in flight before the token's position and angles are there.  Index
+// A CTA per token for each part that is asked for, the two side by side.
+// Everything a thread reads is in flight before the token's position and angles
+// are there.  Five CTAs an SM (51 registers a thread): 42.9 us for 4096 tokens of
+// 128 and 64 heads, 81 % of measured HBM, 46.0 with four, 48 with all of one part
+// first.  Index
 // queries: thread t holds chunks t, t + 256, ... of the token's H_I x 128 values
 // (8 columns each, 16 chunks a head), its pair's other half 4 lanes away; at
 // most 64 heads, so four chunks a thread stay in registers while the token's
@@ -266,14 +269,15 @@ __device__ __forceinline__ void load8(const K *p, float (&f)[8])
 }
 
 template <typename K>
-__global__ void __launch_bounds__(kQueryThreads) rope_queries_kernel(RopeQueriesArgs a)
+__global__ void __launch_bounds__(kQueryThreads, 5) rope_queries_kernel(RopeQueriesArgs a)
 {
     __shared__ float2 cs[32];
     __shared__ float red[kQueryThreads / 32];
     grid_dep_wait();
     grid_dep_launch();
-    const int t = blockIdx.x, tid = threadIdx.x;
-    if (a.q_rope && blockIdx.y == 0) {
+    const bool both = a.q_rope && a.qI;
+    const int t = both ? blockIdx.x >> 1 : blockIdx.x, tid = threadIdx.x;
+    if (both ? blockIdx.x & 1 : a.q_rope != nullptr) {
         const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(a.q_rope) + t * a.st_t;
         __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.q) + (int64_t)t * a.H * kLatent + kValue;
         constexpr int kMost = 128 * 8 / kQueryThreads; // chunks of a thread
@@ -446,7 +450,7 @@ int launch_cache_append(const CacheAppendArgs &a, cudaStream_t stream, char *err
 
 int launch_rope_queries(const RopeQueriesArgs &a, cudaStream_t stream, char *err, size_t errlen)
 {
-    auto go = [&](auto kernel) { return launch_pdl(kernel, dim3((unsigned)a.T, a.q_rope && a.qI ? 2 : 1), dim3(kQueryThreads), 0, stream, 1, a); };
+    auto go = [&](auto kernel) { return launch_pdl(kernel, dim3((unsigned)a.T * (a.q_rope && a.qI ? 2 : 1)), dim3(kQueryThreads), 0, stream, 1, a); };
     return finish(a.i32 ? go(rope_queries_kernel<float>) : go(rope_queries_kernel<__nv_bfloat16>), "query rotation", err, errlen);
 }
 
