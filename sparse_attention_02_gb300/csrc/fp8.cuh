@@ -26,17 +26,6 @@ __device__ __forceinline__ uint16_t e4m3x2(float lo, float hi)
     return r;
 }
 
-// Scale of values whose largest magnitude is amax: amax / 448, or the smallest
-// power of two not below it (mode 1); 1 for zeros and where the quotient is
-// below the smallest fp32.
-__device__ __forceinline__ float fp8_scale(float amax, int mode)
-{
-    const float ratio = amax / 448.f;
-    if (!(ratio > 0.f))
-        return 1.f;
-    return mode == 0 ? ratio : pow2_ceil(ratio);
-}
-
 // Division of many values by one scale, each quotient correctly rounded (the
 // same bits as y / s): with inv = RN(1 / s), q0 = RN(y inv) and the remainder
 // y - q0 s, exact in an fma, RN(q0 + remainder inv) is RN(y / s) (P. Markstein,
@@ -49,14 +38,25 @@ struct ScaleDivider {
     float s, inv;
     bool plain;
     __device__ __forceinline__ explicit ScaleDivider(float scale) : s(scale), inv(1.f / scale), plain(!(scale > 1e-30f)) {}
-    __device__ __forceinline__ float operator()(float y) const
+    __device__ __forceinline__ float operator()(float y, bool in_range = true) const
     {
-        if (plain)
+        if (plain || !in_range)
             return y / s;
         const float q = y * inv;
         return fmaf(fmaf(-q, s, y), inv, q);
     }
 };
+
+// Scale of values whose largest magnitude is amax: amax / 448, or the smallest
+// power of two not below it (mode 1); 1 for zeros and where the quotient is
+// below the smallest fp32.
+__device__ __forceinline__ float fp8_scale(float amax, int mode)
+{
+    const float ratio = ScaleDivider(448.f)(amax, amax > 1e-30f && amax < 1e38f);
+    if (!(ratio > 0.f))
+        return 1.f;
+    return mode == 0 ? ratio : pow2_ceil(ratio);
+}
 
 // Four values as E4M3 codes over a scale, the first in byte 0.
 __device__ __forceinline__ uint32_t e4m3x4(const ScaleDivider &d, float a, float b, float c, float e)

@@ -76,47 +76,46 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8])
 }
 
 // ------------------------------------------------------------- cache append
-// One warp per token.  Lane l holds latent chunks l and l + 32 (8 columns
-// each); lanes 0-7 the rotated columns' chunks; every lane 4 index columns, so
-// the index pair (i, i + 32) sits 8 lanes apart.  Lane i computes angle i; a
-// lane of either rotation needs angles 4 (l & 7) .. + 3.
+// One warp per token.  Lane l holds latent chunks l and l + 32 (8 columns each),
+// the rotated pair (2l, 2l + 1), the index pair (l, l + 32) and the index columns
+// 64 + 2l and 65 + 2l: it computes the one angle that both its pairs turn by, and
+// no lane needs another's.  Instructions bound this kernel more than bytes (70 %
+// of issue slots with rotated chunks of 8 columns and angles handed around: 22 us
+// for 32768 tokens, 18 so), so the page size comes as a shift and quotients by
+// reciprocals.
 constexpr int kAppendThreads = 128;
 
 // What a token's warp reads of it: nothing depends on where it goes, so it is
 // loaded while the position and page are looked up, and one token ahead.
 template <typename K> struct TokenRow {
-    uint4 v0, v1, vr, k;
+    uint4 v0, v1;
+    uint32_t vr;
+    float k[4];
     __device__ __forceinline__ void load(const CacheAppendArgs &a, int t, int lane)
     {
         if (a.kv) {
-            const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.kv) + t * a.ld_kv);
-            v0 = src[lane];
-            v1 = src[lane + 32];
-            if (lane < 8)
-                vr = src[64 + lane];
+            const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(a.kv) + t * a.ld_kv;
+            v0 = reinterpret_cast<const uint4 *>(src)[lane];
+            v1 = reinterpret_cast<const uint4 *>(src)[lane + 32];
+            vr = reinterpret_cast<const uint32_t *>(src + kValue)[lane];
         }
         if (a.kI) {
-            const K *src = static_cast<const K *>(a.kI) + t * a.ld_kI + 4 * lane;
+            const K *src = static_cast<const K *>(a.kI) + t * a.ld_kI;
+            k[0] = (float)src[lane];
+            k[1] = (float)src[lane + 32];
             if (sizeof(K) == 4) {
-                k = *reinterpret_cast<const uint4 *>(src);
+                const float2 f = reinterpret_cast<const float2 *>(src + 64)[lane];
+                k[2] = f.x, k[3] = f.y;
             } else {
-                const uint2 f = *reinterpret_cast<const uint2 *>(src);
-                k.x = f.x, k.y = f.y;
+                const uint32_t f = reinterpret_cast<const uint32_t *>(src + 64)[lane];
+                k[2] = bf16_lo(f), k[3] = bf16_hi(f);
             }
-        }
-    }
-    __device__ __forceinline__ void index(float (&f)[4]) const
-    {
-        if (sizeof(K) == 4) {
-            f[0] = __uint_as_float(k.x), f[1] = __uint_as_float(k.y), f[2] = __uint_as_float(k.z), f[3] = __uint_as_float(k.w);
-        } else {
-            f[0] = bf16_lo(k.x), f[1] = bf16_hi(k.x), f[2] = bf16_lo(k.y), f[3] = bf16_hi(k.y);
         }
     }
 };
 
 template <typename K, bool W32>
-__global__ void __launch_bounds__(kAppendThreads, 8) cache_append_kernel(CacheAppendArgs a, unsigned *status)
+__global__ void __launch_bounds__(kAppendThreads, 8) cache_append_kernel(CacheAppendArgs a, int page_bits, unsigned *status)
 {
     grid_dep_wait();
     grid_dep_launch();
@@ -139,28 +138,23 @@ __global__ void __launch_bounds__(kAppendThreads, 8) cache_append_kernel(CacheAp
         }
         if (pos < 0) // a padded row
             continue;
-        const int lp = pos / a.page_size;
+        const int lp = pos >> page_bits;
         if (s < 0 || s >= a.num_seqs || lp >= a.max_pages) {
             if (lane == 0)
                 atomicOr(status, DSA_DEV_BAD_POSITION);
             continue;
         }
         const int page = a.block_table[(int64_t)s * a.max_pages + lp];
-        const float2 mine = rotation(pos, freq);
-        float c[4], n[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            c[i] = __shfl_sync(0xffffffffu, mine.x, 4 * (lane & 7) + i);
-            n[i] = __shfl_sync(0xffffffffu, mine.y, 4 * (lane & 7) + i);
-        }
+        const float2 turn = rotation(pos, freq);
         if (page < 0 || page >= a.num_pages) {
             if (lane == 0)
                 atomicOr(status, DSA_DEV_BAD_PAGE);
             continue;
         }
-        const int64_t slot = (int64_t)page * a.page_size + pos % a.page_size;
+        const int64_t slot = ((int64_t)page << page_bits) + (pos & ((1 << page_bits) - 1));
         if (a.kv) {
-            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.kv_pool) + slot * kLatent);
+            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.kv_pool) + slot * kLatent;
+            uint4 *dst = reinterpret_cast<uint4 *>(out);
             uint4 v0 = row.v0, v1 = row.v1;
             if (a.kv_weight) {
                 float f0[8], f1[8], ss = 0.f, w0[8], w1[8];
@@ -195,34 +189,22 @@ __global__ void __launch_bounds__(kAppendThreads, 8) cache_append_kernel(CacheAp
             }
             dst[lane] = v0;
             dst[lane + 32] = v1;
-            if (lane < 8) {
-                float f[8], o[8];
-                unpack8(row.vr, f);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    o[2 * i] = f[2 * i] * c[i] - f[2 * i + 1] * n[i];
-                    o[2 * i + 1] = f[2 * i] * n[i] + f[2 * i + 1] * c[i];
-                }
-                dst[64 + lane] = pack8(o);
-            }
+            const float x = bf16_lo(row.vr), y = bf16_hi(row.vr);
+            reinterpret_cast<uint32_t *>(out + kValue)[lane] =
+                bf16_pair(x * turn.x - y * turn.y, x * turn.y + y * turn.x);
         }
         if (a.kI) {
-            float k[4], m = 0.f;
-            row.index(k);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float other = __shfl_xor_sync(0xffffffffu, k[i], 8);
-                if (lane < 8)
-                    k[i] = k[i] * c[i] - other * n[i];
-                else if (lane < 16)
-                    k[i] = other * n[i] + k[i] * c[i];
-                m = fmaxf(m, fabsf(k[i]));
-            }
+            const float k0 = row.k[0] * turn.x - row.k[1] * turn.y, k1 = row.k[0] * turn.y + row.k[1] * turn.x;
+            float m = fmaxf(fmaxf(fabsf(k0), fabsf(k1)), fmaxf(fabsf(row.k[2]), fabsf(row.k[3])));
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1)
                 m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
             const float sc = fp8_scale(m, a.scale_mode);
-            reinterpret_cast<uint32_t *>(a.k8_pool + slot * kIndex)[lane] = e4m3x4(ScaleDivider(sc), k[0], k[1], k[2], k[3]);
+            const uint32_t c = e4m3x4(ScaleDivider(sc), k0, k1, row.k[2], row.k[3]);
+            uint8_t *codes = a.k8_pool + slot * kIndex;
+            codes[lane] = (uint8_t)c;
+            codes[lane + 32] = (uint8_t)(c >> 8);
+            reinterpret_cast<uint16_t *>(codes + 64)[lane] = (uint16_t)(c >> 16);
             if (lane == 0)
                 a.ks_pool[slot] = sc;
         }
@@ -436,9 +418,10 @@ int launch_cache_append(const CacheAppendArgs &a, cudaStream_t stream, char *err
         return DSA_ERR_CUDA;
     }
     const int per = kAppendThreads / 32;
-    const int want = (a.T + per - 1) / per, most = 16 * num_sms();
+    const int want = (a.T + per - 1) / per, most = 8 * num_sms(); // one wave
+    const int page_bits = a.page_size == 32 ? 5 : a.page_size == 64 ? 6 : 7;
     auto go = [&](auto kernel) {
-        return launch_pdl(kernel, dim3((unsigned)(want < most ? want : most)), dim3(kAppendThreads), 0, stream, 1, a, status);
+        return launch_pdl(kernel, dim3((unsigned)(want < most ? want : most)), dim3(kAppendThreads), 0, stream, 1, a, page_bits, status);
     };
     cudaError_t e;
     if (a.k32)
