@@ -172,9 +172,10 @@ int dsa_quantize_fp8(const float *x, int64_t rows, int64_t cols, int scale_mode,
  *   codes     [rows, cols] uint8, contiguous;  scale [rows, n] fp32 with n = 1
  *             (block = 0) or ceil(cols / 128)
  * residual, residual_out, out and codes (with scale) may each be NULL, the last
- * three not all.  residual_out may be residual or x itself, and out may be x.
+ * three not all.  residual_out may be residual or x itself, and out may be x; no
+ * other overlap of an output with another tensor.
  * 1 <= cols <= 16384; rows = 0 is a no-op; eps >= 0.  Inputs must be finite.  Any
- * alignment works; 16-byte aligned rows, with cols a multiple of 8, take the
+ * alignment of whole elements works; 16-byte aligned rows, with cols a multiple of 8, take the
  * vector path.
  */
 #define DSA_BF16 0

@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <initializer_list>
 #include <mutex>
 #include <stdarg.h>
 #include <stdio.h>
@@ -38,6 +39,13 @@ int ok()
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned_to(size_t n, std::initializer_list<const void *> ps)
+{
+    for (const void *p : ps)
+        if (reinterpret_cast<uintptr_t>(p) % n)
+            return false;
+    return true;
+}
 
 constexpr int kMaxDevices = 64;
 std::mutex g_mu;
@@ -337,6 +345,9 @@ int dsa_rmsnorm(const void *x, int64_t ldx, const void *residual, int64_t ldr, c
     if (rows > (int64_t)INT32_MAX || too_large(rows, ldx) || (residual && too_large(rows, ldr)) ||
         (residual_out && too_large(rows, ldh)) || (out && too_large(rows, ldo)))
         return fail(DSA_ERR_UNSUPPORTED, "rows too large");
+    if (!aligned_to(dtype == DSA_FP32 ? 4 : 2, {x, residual, residual_out, out}) ||
+        !aligned_to(weight_dtype == DSA_FP32 ? 4 : 2, {weight}) || !aligned_to(4, {scale}))
+        return fail(DSA_ERR_ALIGNMENT, "tensors must be aligned to their elements");
     RmsNormArgs a{x, residual, weight, rows, cols, ldx, ldr, ldh, ldo, dtype == DSA_FP32, weight_dtype == DSA_FP32, eps,
                   residual_out, out, static_cast<uint8_t *>(codes), scale, block, scale_mode};
     int rc = launch_rmsnorm(a, reinterpret_cast<cudaStream_t>(stream), t_err, sizeof t_err);
@@ -366,6 +377,9 @@ int dsa_rmsnorm_backward(const void *dy, const void *h, const void *weight, cons
         return fail(DSA_ERR_INVALID_ARG, "null pointer argument");
     if (rows > (int64_t)INT32_MAX)
         return fail(DSA_ERR_UNSUPPORTED, "rows too large");
+    if (!aligned_to(dtype == DSA_FP32 ? 4 : 2, {dy, h, dres, dx}) || !aligned_to(weight_dtype == DSA_FP32 ? 4 : 2, {weight}) ||
+        !aligned_to(4, {dweight}))
+        return fail(DSA_ERR_ALIGNMENT, "tensors must be aligned to their elements");
     const size_t need = rmsnorm_backward_workspace_bytes(rows, cols);
     if (need > 0 && (!workspace || workspace_bytes < need))
         return fail(DSA_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace ? workspace_bytes : 0);
@@ -406,8 +420,12 @@ int dsa_cache_append(const int32_t *pos, const int32_t *seq, int T, const int32_
         return fail(DSA_ERR_INVALID_ARG, "without seq the block table needs a row per token");
     if ((kv && ld_kv < 576) || (kI && ld_kI < 128))
         return fail(DSA_ERR_INVALID_ARG, "a row stride is below the row's width");
+    if (T > (1 << 30))
+        return fail(DSA_ERR_UNSUPPORTED, "T must be at most 2^30");
     if ((kv && too_large(T, ld_kv)) || (kI && too_large(T, ld_kI)))
         return fail(DSA_ERR_UNSUPPORTED, "row stride too large");
+    if (!aligned_to(4, {pos, seq, block_table, kI ? ks_pool : nullptr}) || !aligned_to(8, {inv_freq}))
+        return fail(DSA_ERR_ALIGNMENT, "tensors must be aligned to their elements");
     if (kv && (!aligned16(kv) || !aligned16(kv_pool) || !aligned16(kv_weight) || ld_kv % 8))
         return fail(DSA_ERR_ALIGNMENT, "kv, its row stride, kv_weight and kv_pool must be 16-byte aligned");
     if (kI && (!aligned16(kI) || !aligned16(k8_pool) || ld_kI % (k_dtype == DSA_FP32 ? 4 : 8)))
@@ -449,6 +467,8 @@ int dsa_rope_queries(const int32_t *pos, const double *inv_freq, int T, const vo
         return fail(DSA_ERR_ALIGNMENT, "q_rope, its strides and q must be 16-byte aligned");
     if (qI && (!aligned16(qI) || !aligned16(q8)))
         return fail(DSA_ERR_ALIGNMENT, "qI and q8 must be 16-byte aligned");
+    if (!aligned_to(4, {pos, qI ? q_scale : nullptr}) || !aligned_to(8, {inv_freq}))
+        return fail(DSA_ERR_ALIGNMENT, "tensors must be aligned to their elements");
     RopeQueriesArgs a{pos, inv_freq, T, H, H_I, q_rope, st_t, st_h, q, qI, i_dtype == DSA_FP32, scale_mode,
                       static_cast<uint8_t *>(q8), q_scale};
     int rc = launch_rope_queries(a, reinterpret_cast<cudaStream_t>(stream), t_err, sizeof t_err);
@@ -468,8 +488,12 @@ int dsa_index_rope_backward(const float *g, const int32_t *pos, const double *in
         return ok();
     if (!g || !pos || !inv_freq || !dx)
         return fail(DSA_ERR_INVALID_ARG, "null pointer argument");
+    if (T > (1 << 30))
+        return fail(DSA_ERR_UNSUPPORTED, "T must be at most 2^30");
     if (!aligned16(g) || !aligned16(dx))
         return fail(DSA_ERR_ALIGNMENT, "g and dx must be 16-byte aligned");
+    if (!aligned_to(4, {pos}) || !aligned_to(8, {inv_freq}))
+        return fail(DSA_ERR_ALIGNMENT, "tensors must be aligned to their elements");
     IndexRopeBackwardArgs a{g, pos, inv_freq, T, H_I, dx, dtype == DSA_FP32};
     int rc = launch_index_rope_backward(a, reinterpret_cast<cudaStream_t>(stream), t_err, sizeof t_err);
     return rc == DSA_OK ? ok() : rc;
@@ -504,6 +528,8 @@ int dsa_mla_decode_paged(const void *q, const void *kv_pool, int num_pages, int 
         return fail(DSA_ERR_UNSUPPORTED, "pool or block table too large");
     if (!aligned16(q) || !aligned16(kv_pool) || !aligned16(out))
         return fail(DSA_ERR_ALIGNMENT, "q, kv_pool and out must be 16-byte aligned");
+    if (!aligned_to(4, {block_table, ctx_len, lse}))
+        return fail(DSA_ERR_ALIGNMENT, "tensors must be aligned to their elements");
     if (!(sm_scale > 0.f) || sm_scale > 1e30f)
         return fail(DSA_ERR_INVALID_ARG, "sm_scale must be positive and finite");
     const size_t need = dense_mla_workspace_bytes(B, H);

@@ -125,3 +125,41 @@ def test_binding_refuses_host_tensors_and_wrong_shapes(monkeypatch):
         dsa.dsa_index_rope_backward(x, w, w, x)
     with pytest.raises(TypeError):
         dsa.dsa_mla_decode_paged(x, x, x, w, 1.0, x, x)
+
+
+def test_misaligned_elements_and_token_counts_are_refused(lib):
+    """Addresses that are no multiple of an element, which a kernel could only fault on."""
+    odd, two, four = P(4097), P(4098), P(4100)
+
+    def norm(x=fake, w=fake, res=None, dt=0, wt=0, h=None, out=fake, codes=None, scale=None):
+        return lib.dsa_rmsnorm(x, L(64), res, L(64), w, L(4), 64, dt, wt, F(1e-6), h, L(64), out, L(64), codes, scale, 0, 0, None)
+
+    assert norm(x=odd) == 3 and norm(res=odd) == 3 and norm(h=odd) == 3 and norm(out=odd) == 3 and norm(w=odd) == 3
+    assert norm(x=two, dt=1) == 3 and norm(w=two, wt=1) == 3 and norm(codes=odd, scale=two) == 3
+
+    def back(dy=fake, h=fake, w=fake, e=None, dt=0, wt=0, dx=fake, dw=fake):
+        return lib.dsa_rmsnorm_backward(dy, h, w, e, L(4), 64, dt, wt, F(1e-6), dx, dw, fake, 1 << 40, None)
+
+    assert back(dy=odd) == 3 and back(h=odd) == 3 and back(e=odd) == 3 and back(dx=odd) == 3 and back(dw=two) == 3
+    assert back(w=odd) == 3 and back(w=two, wt=1) == 3 and back(dx=two, dt=1) == 3
+
+    def append(pos=fake, seq=None, T=4, bt=fake, fr=fake, ks=fake):
+        return lib.dsa_cache_append(pos, seq, T, bt, T, 2, 8, 64, fr, None, L(0), None, 0, F(1e-6), None, fake, L(128), 0, 0, fake, ks, None)
+
+    assert append(pos=two) == 3 and append(seq=two) == 3 and append(bt=two) == 3 and append(fr=four) == 3 and append(ks=two) == 3
+    assert append(T=(1 << 30) + 1) == 2
+
+    def queries(pos=fake, fr=fake, qs=fake):
+        return lib.dsa_rope_queries(pos, fr, 4, None, L(0), L(0), 0, None, fake, 64, 0, 0, fake, qs, None)
+
+    assert queries(pos=two) == 3 and queries(fr=four) == 3 and queries(qs=two) == 3
+
+    def turn_back(pos=fake, fr=fake, T=4):
+        return lib.dsa_index_rope_backward(fake, pos, fr, T, 1, fake, 0, None)
+
+    assert turn_back(pos=two) == 3 and turn_back(fr=four) == 3 and turn_back(T=(1 << 30) + 1) == 2
+
+    def attend(bt=fake, ctx=fake, lse=fake):
+        return lib.dsa_mla_decode_paged(fake, fake, 8, 64, bt, 2, ctx, 2, 128, F(0.04), fake, lse, P(1 << 20), 1 << 40, None)
+
+    assert attend(bt=two) == 3 and attend(ctx=two) == 3 and attend(lse=two) == 3
