@@ -584,9 +584,15 @@ size_t dsa_sparse_mla_decode_workspace_size(int B, int H, int k);
  * DSA_DEV_BAD_POSITION; keys on a page id outside [0, num_pages) are skipped and flagged
  * DSA_DEV_BAD_PAGE.  Slots past ctx_len are never used, whatever they hold.
  *
- * Precision: scores and softmax in fp32; out rounded once to bf16.  The keys of
- * a row are split over the SMs and joined by their LSEs in a fixed order, so
- * results repeat bit for bit on one kind of device.
+ * A NaN in a used key or in a head's query makes out and lse of the rows or
+ * heads that use it NaN, and no others.
+ *
+ * Precision: scores and softmax in fp32; the weights exp(S - m) are rounded to
+ * bf16 for the product with the values (m is a running maximum, so they lie in
+ * (0, 2^8]; their sum is that of the unrounded ones), which the products
+ * accumulate in fp32; out rounded once to bf16.  The keys of a row are split
+ * over the SMs and joined by their LSEs in a fixed order, so results repeat bit
+ * for bit on one kind of device.
  *
  *   q [B, H, 576] bf16;  kv_pool [num_pages, page_size, 576] bf16
  *   block_table [B, max_pages] int32;  ctx_len [B] int32

@@ -714,7 +714,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 break;
             }
             ++u;
-            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const float inv = l == 0.f ? 0.f : 1.f / l; // a NaN key's l is NaN, and so its row
             tc_fence_after();
 #pragma unroll 2
             for (int c = 0; c < 128; c += 32) {
@@ -746,7 +746,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (lane == 0)
                 arrive_pair(lead(B_OE));
             if (h < p.H && col0 == 0) {
-                const float v = l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+                const float v = l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
                 if (un.slot < 0)
                     p.lse[orow] = v;
                 else
@@ -808,7 +808,7 @@ __global__ void __launch_bounds__(256) dense_mla_join_kernel(Params p)
         for (int i = alone ? 0 : warp; i < np; i += step) {
             const int64_t r = (int64_t)slot(i) * p.H + h;
             const float4 *src = reinterpret_cast<const float4 *>(p.ws_o + r * kDv) + lane;
-            const float w = top == -INFINITY ? 0.f : expf(p.ws_lse[r] - top);
+            const float part = p.ws_lse[r], w = part == -INFINITY ? 0.f : expf(part - top);
             sum += w;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -821,13 +821,13 @@ __global__ void __launch_bounds__(256) dense_mla_join_kernel(Params p)
         }
         const int64_t orow = (int64_t)row * p.H + h;
         if (alone) {
-            const float inv = sum > 0.f ? 1.f / sum : 0.f;
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 reinterpret_cast<uint2 *>(p.out)[orow * (kDv / 4) + lane + 32 * e] =
                     make_uint2(pack2(acc[e].x * inv, acc[e].y * inv), pack2(acc[e].z * inv, acc[e].w * inv));
             if (lane == 0)
-                p.lse[orow] = top == -INFINITY ? -INFINITY : top + logf(sum);
+                p.lse[orow] = sum == 0.f ? -INFINITY : top + logf(sum);
             continue;
         }
 #pragma unroll
@@ -844,10 +844,10 @@ __global__ void __launch_bounds__(256) dense_mla_join_kernel(Params p)
             x += v.x;
             y += v.y;
         }
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
         reinterpret_cast<uint32_t *>(p.out)[orow * (kDv / 2) + threadIdx.x] = pack2(x * inv, y * inv);
         if (threadIdx.x == 0)
-            p.lse[orow] = top == -INFINITY ? -INFINITY : top + logf(l);
+            p.lse[orow] = l == 0.f ? -INFINITY : top + logf(l);
         __syncthreads(); // the sums are used again for the next head
     }
 }
