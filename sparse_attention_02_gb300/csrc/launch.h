@@ -162,6 +162,7 @@ struct IndexRopeBackwardArgs {
     int T, HI;
     void *dx;           // [T, HI, 128] bf16, or fp32 with o32
     bool o32;
+    bool wide = false;  // g starts at 32 bytes (set by the launch)
 };
 int launch_index_rope_backward(const IndexRopeBackwardArgs &a, cudaStream_t stream, char *err, size_t errlen);
 

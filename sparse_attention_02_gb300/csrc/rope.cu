@@ -212,114 +212,122 @@ __global__ void __launch_bounds__(kAppendThreads, 8) cache_append_kernel(CacheAp
 }
 
 // ------------------------------------------------------------------ queries
-// A CTA per token for each part that is asked for, the two side by side.
-// Everything a thread reads is in flight before the token's position and angles
-// are there.  Five CTAs an SM (51 registers a thread): 42.9 us for 4096 tokens of
-// 128 and 64 heads, 81 % of measured HBM, 46.0 with four, 48 with all of one part
-// first.  Index
-// queries: thread t holds chunks t, t + 256, ... of the token's H_I x 128 values
-// (8 columns each, 16 chunks a head), its pair's other half 4 lanes away; at
-// most 64 heads, so four chunks a thread stay in registers while the token's
-// amax is found.
+// A CTA per token.  Everything a thread reads, of both parts, is in flight
+// before the token's position and angles are there.  Main part: eight threads a
+// head, 32 heads at a time.  Index part: four threads a head, thread r of them
+// with the chunks (8 columns) r and r + 4, which turn into each other, r + 8 and
+// r + 12; no value passes between threads but the token's amax.  HBM-bound: 37.2
+// us for 4096 tokens of 128 and 64 heads, 93 % of measured bandwidth; CTAs of one
+// part each 40.2 (the index part alone keeps too few bytes in flight), persistent
+// ones with the next token in registers 40.5, pairs of chunks four lanes apart
+// turned by shuffles 42.9.  Up to a token per SM each part has a CTA of its own:
+// 2.5 us instead of 2.8 for 64 tokens, 2.8 and 2.9 for 152, 3.8 and 3.6 for 304.
 constexpr int kQueryThreads = 256;
-constexpr int kIndexChunks = 4;
 
-// Rotates chunk c (0 .. 15) of a 128-wide index vector; other: the 8 values 4
-// lanes away.  back turns by the negative angle.
-__device__ __forceinline__ void rotate_index(float (&f)[8], int c, const float2 *cs, bool back)
+// Turns chunks a and b (columns 8 r ... and 32 + 8 r ...) into each other by the angles 8 r ... of cs; sign -1: back.
+__device__ __forceinline__ void turn_chunks(float (&a)[8], float (&b)[8], const float2 *cs, int r, float sign)
 {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float other = __shfl_xor_sync(0xffffffffu, f[i], 4);
-        if (c < 8) {
-            const float2 r = cs[8 * (c & 3) + i];
-            const float sn = ((c < 4) != back) ? -r.y : r.y;
-            f[i] = f[i] * r.x + other * sn;
+        const float2 t = cs[8 * r + i];
+        const float sn = sign * t.y, x = a[i], y = b[i];
+        a[i] = x * t.x - y * sn;
+        b[i] = x * sn + y * t.x;
+    }
+}
+
+template <typename K> struct IndexRow { // a thread's part of a token's index queries, as loaded
+    static constexpr int kWords = sizeof(K) == 4 ? 8 : 4;
+    uint4 v[kWords];
+    __device__ __forceinline__ void load(const K *src) // the thread's first chunk
+    {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int k = 0; k < kWords / 4; ++k)
+                v[kWords / 4 * j + k] = reinterpret_cast<const uint4 *>(src + 32 * j)[k];
+    }
+    __device__ __forceinline__ void get(int j, float (&f)[8]) const
+    {
+        if (sizeof(K) == 4) {
+            const uint4 x = v[kWords / 4 * j], y = v[kWords / 4 * j + kWords / 4 - 1];
+            const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                f[i] = __uint_as_float(w[i]);
+        } else {
+            unpack8(v[j], f);
         }
     }
-}
+};
 
 template <typename K>
-__device__ __forceinline__ void load8(const K *p, float (&f)[8])
+__global__ void __launch_bounds__(kQueryThreads, 4) rope_queries_kernel(RopeQueriesArgs a, bool split)
 {
-    if (sizeof(K) == 4) {
-        const float4 u = reinterpret_cast<const float4 *>(p)[0], v = reinterpret_cast<const float4 *>(p)[1];
-        f[0] = u.x, f[1] = u.y, f[2] = u.z, f[3] = u.w, f[4] = v.x, f[5] = v.y, f[6] = v.z, f[7] = v.w;
-    } else {
-        unpack8(*reinterpret_cast<const uint4 *>(p), f);
-    }
-}
-
-template <typename K>
-__global__ void __launch_bounds__(kQueryThreads, 5) rope_queries_kernel(RopeQueriesArgs a)
-{
-    __shared__ float2 cs[32];
+    __shared__ __align__(16) float2 cs[32];
     __shared__ float red[kQueryThreads / 32];
     grid_dep_wait();
     grid_dep_launch();
-    const bool both = a.q_rope && a.qI;
-    const int t = both ? blockIdx.x >> 1 : blockIdx.x, tid = threadIdx.x;
-    if (both ? blockIdx.x & 1 : a.q_rope != nullptr) {
-        const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(a.q_rope) + t * a.st_t;
-        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.q) + (int64_t)t * a.H * kLatent + kValue;
-        constexpr int kMost = 128 * 8 / kQueryThreads; // chunks of a thread
-        const int h0 = tid >> 3, p = tid & 7;
-        uint4 v[kMost];
+    const int t = split ? blockIdx.x >> 1 : blockIdx.x, tid = threadIdx.x;
+    const bool main_part = a.q_rope && (!split || (blockIdx.x & 1)), index_part = a.qI && (!split || !(blockIdx.x & 1));
+    const int pos = a.pos[t];
+    const double freq = a.inv_freq[tid & 31];
+    // main: eight threads a head, 32 heads at a time
+    constexpr int kMost = 128 * 8 / kQueryThreads, kHeads = kQueryThreads / 8;
+    const int h0 = tid >> 3, p = tid & 7;
+    uint4 v[kMost];
+    if (main_part) {
+        const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(a.q_rope) + t * a.st_t + 8 * p;
 #pragma unroll
         for (int j = 0; j < kMost; ++j)
-            if (h0 + j * (kQueryThreads / 8) < a.H)
-                v[j] = *reinterpret_cast<const uint4 *>(src + (h0 + j * (kQueryThreads / 8)) * a.st_h + 8 * p);
-        const int pos = a.pos[t];
-        if (pos < 0) // a padded row
-            return;
-        if (tid < 32)
-            cs[tid] = rotation(pos, turn_step(a.inv_freq[tid]));
-        __syncthreads();
-        float2 r[4];
+            if (h0 + j * kHeads < a.H)
+                v[j] = *reinterpret_cast<const uint4 *>(src + (h0 + j * kHeads) * a.st_h);
+    }
+    // index: four threads a head
+    const int h = tid >> 2, r = tid & 3;
+    const int64_t at = ((int64_t)t * a.HI + h) * kIndex + 8 * r;
+    const bool mine = index_part && h < a.HI;
+    IndexRow<K> row = {};
+    if (mine)
+        row.load(static_cast<const K *>(a.qI) + at);
+    if (pos < 0) // a padded row
+        return;
+    if (tid < 32)
+        cs[tid] = rotation(pos, turn_step(freq));
+    __syncthreads();
+    if (main_part) {
+        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.q) + (int64_t)t * a.H * kLatent + kValue + 8 * p;
+        float2 turn[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            r[i] = cs[4 * p + i];
+            turn[i] = cs[4 * p + i];
 #pragma unroll
         for (int j = 0; j < kMost; ++j) {
-            const int h = h0 + j * (kQueryThreads / 8);
-            if (h >= a.H)
+            if (h0 + j * kHeads >= a.H)
                 continue;
             float x[8], o[8];
             unpack8(v[j], x);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                o[2 * i] = x[2 * i] * r[i].x - x[2 * i + 1] * r[i].y;
-                o[2 * i + 1] = x[2 * i] * r[i].y + x[2 * i + 1] * r[i].x;
+                o[2 * i] = x[2 * i] * turn[i].x - x[2 * i + 1] * turn[i].y;
+                o[2 * i + 1] = x[2 * i] * turn[i].y + x[2 * i + 1] * turn[i].x;
             }
-            *reinterpret_cast<uint4 *>(dst + (int64_t)h * kLatent + 8 * p) = pack8(o);
+            *reinterpret_cast<uint4 *>(dst + (int64_t)(h0 + j * kHeads) * kLatent) = pack8(o);
         }
-        return;
     }
-    float f[kIndexChunks][8];
-    const int chunks = a.HI * 16;
+    if (!index_part)
+        return;
+    float f[4][8];
 #pragma unroll
-    for (int j = 0; j < kIndexChunks; ++j) {
-        const int c = j * kQueryThreads + tid;
-        if (c < chunks)
-            load8(static_cast<const K *>(a.qI) + ((int64_t)t * chunks + c) * 8, f[j]);
-        else
-            for (int i = 0; i < 8; ++i)
-                f[j][i] = 0.f;
-    }
-    const int pos = a.pos[t];
-    if (pos < 0)
-        return;
-    if (tid < 32)
-        cs[tid] = rotation(pos, turn_step(a.inv_freq[tid]));
-    __syncthreads();
+    for (int j = 0; j < 4; ++j)
+        row.get(j, f[j]);
+    turn_chunks(f[0], f[1], cs, r, 1.f);
     float m = 0.f;
 #pragma unroll
-    for (int j = 0; j < kIndexChunks; ++j) {
-        rotate_index(f[j], tid & 15, cs, false);
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             m = fmaxf(m, fabsf(f[j][i]));
-    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -334,68 +342,81 @@ __global__ void __launch_bounds__(kQueryThreads, 5) rope_queries_kernel(RopeQuer
     const ScaleDivider div(sc);
     if (tid == 0)
         a.q_scale[t] = sc;
+    if (!mine)
+        return;
 #pragma unroll
-    for (int j = 0; j < kIndexChunks; ++j) {
-        const int c = j * kQueryThreads + tid;
-        if (c >= chunks)
-            continue;
+    for (int j = 0; j < 4; ++j) {
         const uint32_t lo = e4m3x4(div, f[j][0], f[j][1], f[j][2], f[j][3]);
         const uint32_t hi = e4m3x4(div, f[j][4], f[j][5], f[j][6], f[j][7]);
-        reinterpret_cast<uint2 *>(a.q8)[(int64_t)t * chunks + c] = make_uint2(lo, hi);
+        *reinterpret_cast<uint2 *>(a.q8 + at + 32 * j) = make_uint2(lo, hi);
     }
 }
 
 // ------------------------------------------------- backward of the rotation
-// dx = R(pos)^T g per index vector.  Each CTA takes 64 consecutive vectors, of
-// one token (64 heads) to 64 (keys, one vector a token), and first computes
-// the angles of the tokens it meets, 32 each.
-constexpr int kBackVecs = kQueryThreads * kIndexChunks / 16;
+// dx = R(pos)^T g per index vector, four threads each as above.  Each CTA takes
+// kBackVecs consecutive vectors, of one token to kBackVecs (keys, one vector a
+// token), and first computes the angles of the tokens it meets, 32 each.  HBM-bound:
+// 30.2 us for 4096 tokens of 64 heads to bf16, 98 % of measured bandwidth (64 vectors
+// a CTA the same, 128 32.6; 16-byte loads of pairs turned by shuffles 36.3).
+constexpr int kBackVecs = 32, kBackThreads = 4 * kBackVecs;
+
+// 8 values; wide: p is a multiple of 32 bytes.
+__device__ __forceinline__ void load8(const float *p, float (&f)[8], bool wide)
+{
+    if (wide) {
+        asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]), "=f"(f[6]), "=f"(f[7])
+                     : "l"(p));
+    } else {
+        const float4 u = reinterpret_cast<const float4 *>(p)[0], v = reinterpret_cast<const float4 *>(p)[1];
+        f[0] = u.x, f[1] = u.y, f[2] = u.z, f[3] = u.w, f[4] = v.x, f[5] = v.y, f[6] = v.z, f[7] = v.w;
+    }
+}
 
 template <typename O>
-__global__ void __launch_bounds__(kQueryThreads) index_rope_backward_kernel(IndexRopeBackwardArgs a)
+__global__ void __launch_bounds__(kBackThreads) index_rope_backward_kernel(IndexRopeBackwardArgs a)
 {
-    __shared__ float2 cs[kBackVecs][32];
+    __shared__ __align__(16) float2 cs[kBackVecs][32];
     __shared__ bool padded[kBackVecs];
     grid_dep_wait();
     grid_dep_launch();
     const int64_t v0 = (int64_t)blockIdx.x * kBackVecs, vecs = (int64_t)a.T * a.HI;
     const int64_t vlast = (v0 + kBackVecs < vecs ? v0 + kBackVecs : vecs) - 1;
     const int t0 = (int)(v0 / a.HI), ntok = (int)(vlast / a.HI) - t0 + 1;
-    float f[kIndexChunks][8];
+    const int64_t v = v0 + (threadIdx.x >> 2);
+    const int r = threadIdx.x & 3;
+    const bool mine = v < vecs;
+    float f[4][8];
+    if (mine) {
 #pragma unroll
-    for (int j = 0; j < kIndexChunks; ++j) {
-        const int64_t c = v0 * 16 + j * kQueryThreads + threadIdx.x;
-        if (c < vecs * 16)
-            load8(a.g + c * 8, f[j]);
-        else
-            for (int i = 0; i < 8; ++i)
-                f[j][i] = 0.f;
+        for (int j = 0; j < 4; ++j)
+            load8(a.g + v * kIndex + 32 * j + 8 * r, f[j], a.wide);
     }
     const uint64_t step = turn_step(a.inv_freq[threadIdx.x & 31]);
-    for (int t = threadIdx.x >> 5; t < ntok; t += kQueryThreads / 32) {
+    for (int t = threadIdx.x >> 5; t < ntok; t += kBackThreads / 32) {
         const int pos = a.pos[t0 + t];
         cs[t][threadIdx.x & 31] = rotation(pos, step);
         if ((threadIdx.x & 31) == 0)
             padded[t] = pos < 0;
     }
     __syncthreads();
+    if (!mine)
+        return;
+    const int t = (int)(v / a.HI) - t0;
+    turn_chunks(f[0], f[1], cs[t], r, -1.f);
+    const bool zero = padded[t];
 #pragma unroll
-    for (int j = 0; j < kIndexChunks; ++j) {
-        const int64_t c = v0 * 16 + j * kQueryThreads + threadIdx.x;
-        const int64_t v = c >> 4 < vecs ? c >> 4 : vecs - 1;
-        const int t = (int)(v / a.HI) - t0;
-        rotate_index(f[j], threadIdx.x & 15, cs[t], true);
-        if (c >= vecs * 16)
-            continue;
-        if (padded[t])
+    for (int j = 0; j < 4; ++j) {
+        if (zero)
             for (int i = 0; i < 8; ++i)
                 f[j][i] = 0.f;
+        const int64_t c = v * kIndex + 32 * j + 8 * r;
         if (sizeof(O) == 4) {
-            float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(a.dx) + c * 8);
+            float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(a.dx) + c);
             o[0] = make_float4(f[j][0], f[j][1], f[j][2], f[j][3]);
             o[1] = make_float4(f[j][4], f[j][5], f[j][6], f[j][7]);
         } else {
-            reinterpret_cast<uint4 *>(a.dx)[c] = pack8(f[j]);
+            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.dx) + c) = pack8(f[j]);
         }
     }
 }
@@ -433,14 +454,17 @@ int launch_cache_append(const CacheAppendArgs &a, cudaStream_t stream, char *err
 
 int launch_rope_queries(const RopeQueriesArgs &a, cudaStream_t stream, char *err, size_t errlen)
 {
-    auto go = [&](auto kernel) { return launch_pdl(kernel, dim3((unsigned)a.T * (a.q_rope && a.qI ? 2 : 1)), dim3(kQueryThreads), 0, stream, 1, a); };
+    const bool split = a.q_rope && a.qI && a.T <= num_sms();
+    auto go = [&](auto kernel) { return launch_pdl(kernel, dim3((unsigned)a.T * (split ? 2 : 1)), dim3(kQueryThreads), 0, stream, 1, a, split); };
     return finish(a.i32 ? go(rope_queries_kernel<float>) : go(rope_queries_kernel<__nv_bfloat16>), "query rotation", err, errlen);
 }
 
 int launch_index_rope_backward(const IndexRopeBackwardArgs &a, cudaStream_t stream, char *err, size_t errlen)
 {
     const unsigned grid = (unsigned)(((int64_t)a.T * a.HI + kBackVecs - 1) / kBackVecs);
-    auto go = [&](auto kernel) { return launch_pdl(kernel, dim3(grid), dim3(kQueryThreads), 0, stream, 1, a); };
+    IndexRopeBackwardArgs b = a;
+    b.wide = (reinterpret_cast<uintptr_t>(a.g) & 31) == 0;
+    auto go = [&](auto kernel) { return launch_pdl(kernel, dim3(grid), dim3(kBackThreads), 0, stream, 1, b); };
     return finish(a.o32 ? go(index_rope_backward_kernel<float>) : go(index_rope_backward_kernel<__nv_bfloat16>),
                   "index rotation backward", err, errlen);
 }

@@ -171,3 +171,48 @@ def test_appends_whose_tokens_share_pages_and_sequences():
                 used[slot] = True
                 assert torch.equal(flat[slot, :512], kv[t, :512])
         assert (flat[~used] == 3.0).all()
+
+
+@pytest.mark.parametrize("T,HI", [(1, 1), (7, 33), (90, 1), (40, 64)])
+def test_index_gradients_that_start_at_16_bytes(T, HI):
+    """g and dx no multiple of 32 bytes, in place too, with padding between."""
+    dsa = lib()
+    g = torch.Generator().manual_seed(T)
+    pos = torch.randint(0, 9000, (T,), generator=g).to(I32)
+    pos[1::5] = -1
+    v = torch.randn((T, HI, 128), generator=g)
+    buf = torch.zeros(T * HI * 128 + 4, device=DEV)
+    src = buf[4:].view(T, HI, 128)
+    assert src.data_ptr() % 32 == 16
+    src.copy_(v)
+    freq = R.inv_freq()
+    ref = torch.where((pos < 0)[:, None, None], 0.0, R.rotate_index(R.d(v), -pos.clamp(min=0), freq))
+    pair = v.double()[..., :64].unflatten(-1, (2, 32)).abs().sum(-2)
+    mag = torch.cat([pair, pair, torch.zeros_like(pair), torch.zeros_like(pair)], -1)
+    dx = torch.empty((T, HI, 128), dtype=BF, device=DEV)
+    dsa.dsa_index_rope_backward(src, pos.to(DEV), freq.to(DEV), dx)
+    R.check_close(dx, ref, R.BF16 * ref.abs() + 8 * R.FP32 * mag, "bf16")
+    dsa.dsa_index_rope_backward(src, pos.to(DEV), freq.to(DEV), src)
+    R.check_close(src, ref, 8 * R.FP32 * mag, "fp32, in place")
+    assert (buf[:4] == 0).all()
+
+
+@pytest.mark.parametrize("T", [1, 152, 153, 1000])
+def test_query_parts_alone_and_together(T):
+    """Few tokens take a CTA for each part, many one for both: the results are those of the parts called alone."""
+    dsa = lib()
+    g = torch.Generator().manual_seed(T)
+    pos = torch.randint(-50, 5000, (T,), generator=g).to(I32).to(DEV)
+    fr = R.inv_freq().to(DEV)
+    qr, qI = torch.randn((T, 70, 64), generator=g).to(BF).to(DEV), torch.randn((T, 40, 128), generator=g).to(DEV)
+
+    def outs():
+        return (torch.zeros((T, 70, 576), dtype=BF, device=DEV), torch.zeros((T, 40, 128), dtype=torch.uint8, device=DEV),
+                torch.zeros(T, device=DEV))
+
+    a, b = outs(), outs()
+    dsa.dsa_rope_queries(pos, fr, qr, a[0], qI, a[1], a[2])
+    dsa.dsa_rope_queries(pos, fr, qr, b[0])
+    dsa.dsa_rope_queries(pos, fr, qI=qI, q8=b[1], q_scale=b[2])
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+    assert (a[2][pos < 0] == 0).all() and (a[2][pos >= 0] > 0).all()
