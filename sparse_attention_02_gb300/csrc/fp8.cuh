@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "f32x2.cuh"
+
 namespace dsa {
 
 // Smallest power of two not below a positive finite fp32 r (exact, bit level).
@@ -45,6 +47,14 @@ struct ScaleDivider {
         const float q = y * inv;
         return fmaf(fmaf(-q, s, y), inv, q);
     }
+    __device__ __forceinline__ uint16_t codes(float lo, float hi) const // of two quotients
+    {
+        if (plain)
+            return e4m3x2(lo / s, hi / s);
+        const F2 y(lo, hi), q = y * F2(inv);
+        fma2(fma2(q, F2(-s), y), F2(inv), q).get(lo, hi);
+        return e4m3x2(lo, hi);
+    }
 };
 
 // Scale of values whose largest magnitude is amax: amax / 448, or the smallest
@@ -61,7 +71,7 @@ __device__ __forceinline__ float fp8_scale(float amax, int mode)
 // Four values as E4M3 codes over a scale, the first in byte 0.
 __device__ __forceinline__ uint32_t e4m3x4(const ScaleDivider &d, float a, float b, float c, float e)
 {
-    return e4m3x2(d(a), d(b)) | ((uint32_t)e4m3x2(d(c), d(e)) << 16);
+    return d.codes(a, b) | ((uint32_t)d.codes(c, e) << 16);
 }
 
 } // namespace dsa

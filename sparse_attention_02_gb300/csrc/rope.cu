@@ -22,6 +22,7 @@
 // All three kernels move each byte once and are HBM-bound (or, for a decode
 // step, bound by launch and load latency).
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "fp8.cuh"
 #include "launch.h"
 
@@ -73,6 +74,34 @@ __device__ __forceinline__ void unpack8(const uint4 &v, float (&f)[8])
 __device__ __forceinline__ uint4 pack8(const float (&f)[8])
 {
     return make_uint4(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7]));
+}
+
+__device__ __forceinline__ void unpack_pairs(const uint4 &v, F2 (&f)[4])
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        f[i] = F2(bf16_lo(w[i]), bf16_hi(w[i]));
+}
+
+__device__ __forceinline__ uint4 pack_pairs(const F2 (&f)[4])
+{
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float lo, hi;
+        f[i].get(lo, hi);
+        w[i] = bf16_pair(lo, hi);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Largest magnitude in the warp.
+__device__ __forceinline__ float warp_amax(float m)
+{
+    float r;
+    asm volatile("redux.sync.max.abs.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(m));
+    return r;
 }
 
 // ------------------------------------------------------------- cache append
@@ -157,12 +186,13 @@ __global__ void __launch_bounds__(kAppendThreads, 8) cache_append_kernel(CacheAp
             uint4 *dst = reinterpret_cast<uint4 *>(out);
             uint4 v0 = row.v0, v1 = row.v1;
             if (a.kv_weight) {
-                float f0[8], f1[8], ss = 0.f, w0[8], w1[8];
-                unpack8(v0, f0);
-                unpack8(v1, f1);
+                F2 f0[4], f1[4], w0[4], w1[4], sq(0.f);
+                unpack_pairs(v0, f0);
+                unpack_pairs(v1, f1);
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    ss = fmaf(f0[i], f0[i], fmaf(f1[i], f1[i], ss));
+                for (int i = 0; i < 4; ++i)
+                    sq = fma2(f0[i], f0[i], fma2(f1[i], f1[i], sq));
+                float ss = sq.sum();
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1)
                     ss += __shfl_xor_sync(0xffffffffu, ss, o);
@@ -170,22 +200,22 @@ __global__ void __launch_bounds__(kAppendThreads, 8) cache_append_kernel(CacheAp
                 if (W32) {
                     const float *w = static_cast<const float *>(a.kv_weight) + 8 * lane;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        w0[i] = w[i];
-                        w1[i] = w[256 + i];
+                    for (int i = 0; i < 4; ++i) {
+                        w0[i] = F2(w[2 * i], w[2 * i + 1]);
+                        w1[i] = F2(w[256 + 2 * i], w[256 + 2 * i + 1]);
                     }
                 } else {
                     const uint4 *w = static_cast<const uint4 *>(a.kv_weight) + lane;
-                    unpack8(w[0], w0);
-                    unpack8(w[32], w1);
+                    unpack_pairs(w[0], w0);
+                    unpack_pairs(w[32], w1);
                 }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    f0[i] = f0[i] * r * w0[i];
-                    f1[i] = f1[i] * r * w1[i];
+                for (int i = 0; i < 4; ++i) {
+                    f0[i] = f0[i] * F2(r) * w0[i];
+                    f1[i] = f1[i] * F2(r) * w1[i];
                 }
-                v0 = pack8(f0);
-                v1 = pack8(f1);
+                v0 = pack_pairs(f0);
+                v1 = pack_pairs(f1);
             }
             dst[lane] = v0;
             dst[lane + 32] = v1;
@@ -196,9 +226,7 @@ __global__ void __launch_bounds__(kAppendThreads, 8) cache_append_kernel(CacheAp
         if (a.kI) {
             const float k0 = row.k[0] * turn.x - row.k[1] * turn.y, k1 = row.k[0] * turn.y + row.k[1] * turn.x;
             float m = fmaxf(fmaxf(fabsf(k0), fabsf(k1)), fmaxf(fabsf(row.k[2]), fabsf(row.k[3])));
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
-                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            m = warp_amax(m);
             const float sc = fp8_scale(m, a.scale_mode);
             const uint32_t c = e4m3x4(ScaleDivider(sc), k0, k1, row.k[2], row.k[3]);
             uint8_t *codes = a.k8_pool + slot * kIndex;
@@ -328,9 +356,7 @@ __global__ void __launch_bounds__(kQueryThreads, 4) rope_queries_kernel(RopeQuer
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             m = fmaxf(m, fabsf(f[j][i]));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    m = warp_amax(m);
     if ((tid & 31) == 0)
         red[tid >> 5] = m;
     __syncthreads();
