@@ -704,11 +704,18 @@ __global__ void __launch_bounds__(1024) dweight_kernel(const float *part, int np
     grid_dep_wait();
     grid_dep_launch();
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+    constexpr int kAhead = 10; // rows of a warp whose loads are in flight: two CTAs an SM leave it ten
     float t = 0.f;
     if (c < cols)
-#pragma unroll 8
-        for (int p = w; p < nparts; p += 32)
-            t += part[(int64_t)p * cols + c];
+        for (int p = w; p < nparts; p += 32 * kAhead) {
+            float v[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                v[k] = p + 32 * k < nparts ? part[(int64_t)(p + 32 * k) * cols + c] : 0.f;
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                t += v[k];
+        }
     s[w][lane] = t;
     __syncthreads();
     t = s[lane][w]; // warp w: the 32 sums of column w
