@@ -20,7 +20,7 @@ CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(HERE, "_objs")
 LIB = os.path.join(HERE, "libdsa.so")
 FAST = os.path.join(HERE, "_fastcall.so")
-SOURCES = ["api.cu", "quantize.cu", "rmsnorm.cu", "rope.cu", "indexer.cu", "topk.cu", "indexer_topk.cu", "warmup.cu",
+SOURCES = ["api.cu", "quantize.cu", "rmsnorm.cu", "rmsnorm_backward.cu", "rope.cu", "indexer.cu", "topk.cu", "indexer_topk.cu", "warmup.cu",
            "sparse_mla.cu", "dense_mla.cu", "prefill_host.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

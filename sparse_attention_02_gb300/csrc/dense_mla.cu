@@ -27,18 +27,24 @@
 // the 64 heads with the first half of N, lanes 64-127 the same heads with the
 // second: S 2 x 64 columns (two buffers), O 2 x 128.
 //
-// Roles per CTA (8 warps):
-//   load warp    Q once per row, each tile's own 64 keys (9 atoms of 64 columns,
-//                in two groups with barriers of their own), L2 prefetches some
-//                tiles ahead (one instruction: a page is contiguous)
-//   swap warp    the peer's keys' value columns over this CTA's spent ones
-//   MMA warp     (leader CTA only) scores of tile i + 1, then PV of tile i
-//   4 softmax    thread = (head, half of the tile's keys): the two threads of a
-//   warps        head swap their maxima through shared memory, the running
-//                maximum moves only when exceeded by 2^8 (O is then rescaled in
-//                TMEM), P goes to shared memory as bf16.  In a row's last tile
-//                they also zero the value rows past the end, whose stale bytes
-//                might be NaN (0 * NaN).
+// Roles per CTA (12 warps; a wait is polled by all lanes, which answers sooner
+// than one lane polling and a broadcast: 535 us against 607 when it came in):
+//   warp 0       loads: Q once per row, each tile's own 64 keys (9 atoms of 64
+//                columns, as four copies, 0-1, 2-3, 4-5 and 6-8, with barriers of
+//                their own, the halves into what each half of the PV freed), and
+//                behind them an L2 prefetch of the next tile (one instruction: a
+//                page is contiguous; the copy engine takes requests in order)
+//   warp 1       (leader CTA) scores of a tile, group by group as the atoms land;
+//                all lanes of the CTA pair's two warps 1 allocate TMEM
+//   warp 2       swaps: the peer's keys' value columns over this CTA's spent ones
+//   warp 3       (leader CTA) PV.  A thread of its own: a thread that issues both
+//                waits for P with the next scores unissued
+//   warps 4-11   softmax: four threads a head, 32 of the tile's 128 keys each,
+//                which swap their maxima through shared memory; the running maximum
+//                moves only when exceeded by 2^8 (O is then rescaled in TMEM); P
+//                goes to shared memory as bf16, the first 64 keys' over the spent
+//                RoPE atom.  In a row's last tile they also zero the value rows past
+//                the end, whose stale bytes might be NaN (0 * NaN).
 // P is the one intermediate rounded to 16 bits: kind::f16 wants P in V's type.
 // The sum l is that of the unrounded values, in fp32.
 //
@@ -46,6 +52,18 @@
 // share per CTA pair, computed on the device from ctx_len (the host never sees
 // the lengths).  A share that holds part of a row leaves that part, normalised,
 // with its LSE in the workspace, and a second kernel joins the parts.
+//
+// Measured.  64 rows of 128 heads, 8192 to 65536 keys (2.73 GB): 473 us a call in
+// bursts (85 % of measured HBM, 74 % of measured BF16; kernel 460, join 10), 530
+// when calls follow one another for long, the power limit then holding the SM
+// clock near 1.5 GHz.  Without its loads the kernel takes 338 us, with every
+// byte in L2 412: what is left is the chain of a tile (loads, scores, softmax, PV)
+// over the two stages that fit.  9 rows of 16 heads, 1 to 131072 keys, pages of 32:
+// 127 us (79 % of HBM).  One row of 1000 keys, 16 heads: 11.4 us.  Not kept: 64-key
+// tiles over four stages (480 and 555 us where this takes 473 and 530; 123 for the
+// ragged rows; the MMAs of N = 64 run at 78 % of the rate), no prefetch (528 where
+// one tile ahead took 496), two, three and four tiles ahead (504, 518, 557),
+// prefetches by a warp's own loads, a stage's pieces freed one by one.
 #include "common.cuh"
 #include "launch.h"
 

@@ -439,13 +439,18 @@ def test_many_rows(rows, cols, dtype):
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("cols", [9, 24, 127, 129, 520, 1111, 2049, 8190])
 def test_every_misalignment(cols, dtype):
-    """Rows at every element offset from 16 bytes, in every tensor: the values of the aligned call, and nothing beside
-    them."""
+    """Rows at every element offset from 16 bytes, in every tensor: the same values at each, and nothing beside them.
+    Rows of whole chunks that all start at 16 bytes deal their columns to the threads otherwise and so sum them in
+    another order: there the offsets are held to one another, and to fp64 with the bounds of any order."""
     dsa, g = lib(), gen(cols)
     rows = 3
     x, res, w = normal(g, rows, cols, dtype=dtype), normal(g, rows, cols, dtype=dtype), normal(g, cols).to(dtype)
     want = [torch.empty_like(x), torch.empty_like(x), torch.empty((rows, cols), dtype=U8, device=DEV), torch.empty(rows, device=DEV)]
     dsa.dsa_rmsnorm(x, w, EPS, out=want[0], residual=res, residual_out=want[1], codes=want[2], scale=want[3])
+    step = 16 // x.element_size()  # offsets that leave every row at 16 bytes
+    two_orders = cols % 8 == 0
+    aligned = want
+    rh, ry = R.rmsnorm(x, res, w, EPS)
 
     def shifted(t, off, fill=None):
         """A copy of t that begins `off` elements into a larger buffer, and that buffer."""
@@ -459,19 +464,31 @@ def test_every_misalignment(cols, dtype):
         outs = [shifted(t, (off * k) % 16, fill=5) for t, k in zip(want, (7, 1, 9, 1))]
         (o, _), (h, _), (c, _), (s, _) = outs
         dsa.dsa_rmsnorm(xs, ws, EPS, out=o, residual=rs, residual_out=h, codes=c, scale=s)
-        for (view, buf), ref, k in zip(outs, want, (7, 1, 9, 1)):
+        if two_orders and off == 1:
+            assert torch.equal(h, want[1])  # no sum in it
+            R.check_close(o, ry, ry.abs() * (R.half_step(dtype) + REL_Y) + 1e-30, "out")
+            R.check_fp8(c, s, ry, REL_Y, 0, "codes")
+            want = [t.clone() for t in (o, h, c, s)]
+        # the codes' rows start at 8 bytes in the aligned form
+        for (view, buf), ref, k in zip(outs, aligned if off % max(step, 8) == 0 else want, (7, 1, 9, 1)):
             at = (off * k) % 16
             assert torch.equal(view, ref)
             assert (buf[:at] == 7).all() and (buf[at + ref.numel():] == 7).all()
     dy, dw0, dx0 = normal(g, rows, cols, dtype=dtype), torch.empty(cols, device=DEV), torch.empty_like(x)
     dsa.dsa_rmsnorm_backward(dy, x, w, EPS, dx0, dw0, dres=res)
+    dx1, dw1 = dx0, dw0
     for off in range(16):
         dx, buf = shifted(x, (off * 3) % 16, fill=5)
         dw = torch.empty_like(dw0)
         dsa.dsa_rmsnorm_backward(shifted(dy, off)[0], shifted(x, (off * 7) % 16)[0], shifted(w, (off * 5) % 16)[0], EPS, dx, dw,
                                  dres=shifted(res, (off * 9) % 16)[0])
         at = (off * 3) % 16
-        assert torch.equal(dx, dx0) and torch.equal(dw, dw0)
+        if two_orders and off == 1:
+            rx, rw, mag, wmag = R.rmsnorm_backward(dy, x, w, res, EPS)
+            R.check_close(dx, rx, rx.abs() * R.half_step(dtype) + 48 * R.FP32 * mag + 1e-30, "dx")
+            R.check_close(dw, rw, 128 * R.FP32 * wmag + 1e-30, "dweight")
+            dx1, dw1 = dx.clone(), dw.clone()
+        assert all(torch.equal(a, b) for a, b in zip((dx, dw), (dx0, dw0) if off % step == 0 else (dx1, dw1)))
         assert (buf[:at] == 7).all() and (buf[at + dx.numel():] == 7).all()
 
 
