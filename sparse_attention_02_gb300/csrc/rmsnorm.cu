@@ -12,16 +12,22 @@
 //     dx = r (g - xhat mean(g xhat)) + dres,   dweight = sum over rows of dy xhat
 //
 // Both are HBM-bound: every value is read once and written once.  A group of G
-// threads (a warp, or the CTA) owns a row; thread g holds the 8-value chunks
-// c G + g, so a warp's loads are 32 consecutive 16-byte words and 16
-// neighbouring lanes hold one 128-column FP8 block.  Where rows are aligned,
-// long and many, persistent CTAs (two an SM) take them through a ring in shared
-// memory that bulk copies fill while earlier rows are worked on: with the row's
-// values and sums in registers, direct loads left an SM too few threads to keep
-// HBM busy (8191 x 8192 bf16 with residual and block codes: 141 us; backward:
-// 166 us).  Sums are fp32, first within a thread, then by shuffles and shared
-// memory, in an order that depends on sizes and alignment alone: results repeat
-// bit for bit.
+// threads (a warp, or the CTA) owns a row; where rows are aligned thread g holds
+// the 8-value chunks c G + g, so a warp's loads are 32 consecutive 16-byte words
+// and 16 neighbouring lanes hold one 128-column FP8 block.  Where rows are long
+// and many, persistent CTAs take them through a ring in shared memory that bulk
+// copies fill while earlier rows are worked on: with the row's values and sums in
+// registers, direct loads left an SM too few threads to keep HBM busy (8191 x 8192
+// bf16 with residual and block codes: 141 us; backward: 166 us).  Sums are fp32,
+// first within a thread, then by shuffles and shared memory, in an order that
+// depends on sizes and alignment alone: results repeat bit for bit.
+//
+// Measured: 8191 x 8192 bf16, residual, both outputs, block codes 96 us (93 % of
+// measured HBM); backward of 8192 x 8192 with dres 94 us (84 %: four streams, and
+// 5 us of the dweight sum); one row of 4096 2.5 us, launch and one load's latency.
+// At 8191 columns no row but every eighth starts at 16 bytes: 219 us for 9000 rows
+// where 8192 columns take 107 (backward 147 and 80; fp32 240 and 214), bound by
+// instructions: 2-byte loads and stores in every other row.
 #include "rmsnorm.cuh"
 
 namespace dsa {
@@ -187,7 +193,7 @@ int launch_rmsnorm(const RmsNormArgs &a, cudaStream_t stream, char *err, size_t 
     const bool vec = a.cols % 8 == 0 && chunked(a.x, a.ldx * e) && (!a.residual || chunked(a.residual, a.ldr * e)) &&
                      (!a.residual_out || chunked(a.residual_out, a.ldh * e)) && (!a.out || chunked(a.out, a.ldo * e)) &&
                      chunked(a.weight, 0) && (reinterpret_cast<uintptr_t>(a.codes) & 7) == 0;
-    const Shape s = shape_of(a.rows, a.cols, a.residual ? 2 : 1, e, vec);
+    const Shape s = shape_of(a.rows, a.cols, a.residual ? 2 : 1, e, vec, vec);
     unsigned *status = device_status_ptr();
     if (!status) {
         snprintf(err, errlen, "device status word unavailable");

@@ -395,15 +395,20 @@ struct Shape {
 };
 
 // Threads per row, and whether rows (of n tensors of esize-byte values) go
-// through the ring.  Its CTAs have 512 threads an SM together and are as many as
-// leave each two stages; more than 128 KB of stages an SM only slowed the writes
-// among them (99.7 us with three stages, 95.8 with two, at 8191 x 8192).  It pays
-// where an SM has several turns of rows to keep loads ahead of; before that, a
-// chunk a thread is the shorter way, and with short rows it stays so longer, as
-// twice the threads are at work (with residual and block codes, direct and ring,
-// us: 400 x 8192 bf16 8.8, 8.0; 800 x 8192 16.1, 11.3; 800 x 4096 8.0, 7.8;
-// 3200 x 1024 7.0, 14.5; 3200 x 2048 12.9, 14.7; 1600 x 4096 fp32 19.3, 25.6).
-Shape shape_of(int64_t rows, int cols, int n, int esize, bool vec)
+// through the ring.  Its CTAs have 512 threads an SM together, with at most four
+// chunks each, and are as many as leave each two stages: eight of 64 threads took
+// 24000 x 2048 bf16 in 76 us, four of 128 in 96.  More than 128 KB of stages an SM
+// only slowed the writes among them (99.7 us with three stages, 95.8 with two, at
+// 8191 x 8192).  The ring pays where an SM has several turns of rows to keep loads
+// ahead of; before that a chunk a thread is the shorter way, and with short rows it
+// stays so longer, as twice the threads are at work (forward with residual and
+// block codes, direct and ring, us: 400 x 8192 bf16 8.8, 8.0; 800 x 8192 16.1,
+// 11.3; 800 x 4096 8.0, 7.8; 3200 x 1024 7.0, 14.5; 3200 x 2048 12.9, 14.7; 1600 x
+// 4096 fp32 19.3, 25.6), up to 256 columns always (24000 x 256 10.5, 17.1; backward
+// 11.8, 12.7).  So it does in the forward of rows of up to 2048 columns at any
+// address, which instructions bound (wide = false: 24000 x 1111 84, 124; backward
+// 163, 84).
+Shape shape_of(int64_t rows, int cols, int n, int esize, bool vec, bool wide)
 {
     const size_t row = (size_t)n * ring_pitch(cols * esize, vec);
     const auto ring = [&](int threads, int ctas, int group, bool warp) {
@@ -416,14 +421,14 @@ Shape shape_of(int64_t rows, int cols, int n, int esize, bool vec)
             smem = 32 * 8 * 4 * sizeof(float);
         return Shape{nv <= 1 && warp ? 1 : nv <= 2 ? 2 : 4, threads, warp, fit < 2 ? 0 : stages, ctas, kRingBars + smem};
     };
-    if (cols <= 1024 && rows >= 32 * num_sms()) { // rows of single warps: no barrier among them
+    if (cols > 256 && cols <= 1024 && rows >= 32 * num_sms()) { // rows of single warps: no barrier among them
         const Shape s = ring(256, 2, 8, true);
         if (s.stages)
             return s;
     }
     const int direct = (cols + 255) / 256 * 32; // threads a row takes with a chunk each
-    if (cols > 256 && rows * direct >= (cols > 4096 ? 2LL : 8LL) * 1024 * num_sms())
-        for (int ctas = 4; ctas > 0; ctas /= 2)
+    if (cols > (wide ? 256 : 2048) && rows * direct >= (cols > 4096 ? 2LL : 8LL) * 1024 * num_sms())
+        for (int ctas = 8; ctas > 0; ctas /= 2)
             if (cols * ctas <= 32 * 512) { // four chunks a thread at most
                 const Shape s = ring(512 / ctas, ctas, 1, false);
                 if (s.stages)

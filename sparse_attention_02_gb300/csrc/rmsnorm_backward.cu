@@ -205,7 +205,7 @@ size_t rmsnorm_backward_workspace_bytes(int64_t rows, int cols)
     for (int esize = 2; esize <= 4; esize += 2)
         for (int n = 2; n <= 3; ++n)
             for (int vec = 0; vec < 2; ++vec) {
-                const int64_t c = backward_ctas(rows, shape_of(rows, cols, n, esize, vec != 0));
+                const int64_t c = backward_ctas(rows, shape_of(rows, cols, n, esize, vec != 0, true));
                 most = c > most ? c : most;
             }
     return (size_t)most * cols * sizeof(float);
@@ -217,7 +217,7 @@ int launch_rmsnorm_backward(const RmsNormBackwardArgs &a, cudaStream_t stream, c
     const int64_t ld = (int64_t)a.cols * e;
     const bool vec = a.cols % 8 == 0 && chunked(a.h, ld) && chunked(a.dy, ld) && chunked(a.dres, ld) && chunked(a.dx, ld) &&
                      chunked(a.weight, 0); // a null dres counts as aligned
-    const Shape s = shape_of(a.rows, a.cols, a.dres ? 3 : 2, e, vec);
+    const Shape s = shape_of(a.rows, a.cols, a.dres ? 3 : 2, e, vec, true);
     const int grid = (int)backward_ctas(a.rows, s);
     float *part = static_cast<float *>(a.workspace);
     unsigned *status = device_status_ptr();

@@ -503,3 +503,50 @@ def test_quotients_are_those_of_a_division():
         qc, qs = torch.empty_like(codes), torch.empty_like(scale)
         dsa.dsa_quantize_fp8(out, qc, qs, k & 1)
         assert torch.equal(qc, codes) and torch.equal(qs, scale), std
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("rows,cols", [(4900, 300), (5003, 1001), (9800, 1033), (9800, 1040), (4900, 520), (4870, 2051), (4900, 2048),
+                                       (2500, 4096), (2450, 4001), (700, 6001), (420, 8190), (330, 12001), (310, 16383)])
+def test_rows_of_every_ring_shape(rows, cols, dtype):
+    """As above, for the widths and counts at which the ring's CTAs change, whole chunks and rows at any address."""
+    test_many_rows(rows, cols, dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("rows,cols,pad,off", [(4870, 300, 5, 1), (5003, 1001, 1, 3), (4870, 2049, 0, 7), (700, 6000, 3, 2), (700, 6001, 0, 5),
+                                               (640, 4104, 24, 8), (330, 16000, 1, 0)])
+def test_strided_rows_through_the_ring(rows, cols, pad, off, dtype):
+    """Rows `pad` elements apart that begin `off` elements into their buffer, each tensor at another offset: what one
+    call on contiguous rows gives, up to the order of its sums, with nothing written between the rows; in place too."""
+    dsa, g = lib(), gen(rows + cols)
+    ld = cols + pad
+
+    def strided(t, shift, fill):
+        buf = torch.full((rows * ld + 64,), fill, dtype=dtype, device=DEV)
+        view = buf[off + shift:off + shift + rows * ld].view(rows, ld)[:, :cols]
+        if t is not None:
+            view.copy_(t)
+        return view, buf
+
+    x, res, w = normal(g, rows, cols, dtype=dtype), normal(g, rows, cols, dtype=dtype), normal(g, cols).to(dtype)
+    (xs, _), (rs, rbuf) = strided(x, 0, 9.0), strided(res, 3, 9.0)
+    (o, obuf), (h, hbuf) = strided(None, 1, 5.0), strided(None, 2, 5.0)
+    codes, scale = torch.empty((rows, cols), dtype=U8, device=DEV), torch.empty((rows, -(-cols // 128)), device=DEV)
+    dsa.dsa_rmsnorm(xs, w, EPS, out=o, residual=rs, residual_out=h, codes=codes, scale=scale, block=128)
+    pick = sorted({0, 1, 7, 8, rows // 2, rows - 9, rows - 2, rows - 1})
+    rh, ry = R.rmsnorm(x[pick], res[pick], w, EPS)
+    R.check_close(h[pick], rh, rh.abs() * (R.half_step(dtype) + R.FP32) + 1e-30, "h")
+    R.check_close(o[pick], ry, ry.abs() * (R.half_step(dtype) + REL_Y) + 1e-30, "out")
+    for b in range(scale.shape[1]):
+        cut = slice(b * 128, (b + 1) * 128)
+        R.check_fp8(codes[pick][:, cut], scale[pick][:, b], ry[:, cut], REL_Y, 0, f"block {b}")
+    for buf, shift in ((obuf, 1), (hbuf, 2)):
+        rest = buf.clone()
+        rest[off + shift:off + shift + rows * ld].view(rows, ld)[:, :cols] = 5.0
+        assert (rest == 5.0).all()
+    dsa.dsa_rmsnorm(xs, w, EPS, out=xs, residual=rs, residual_out=rs)
+    assert torch.equal(xs, o) and torch.equal(rs, h)
+    rest = rbuf.clone()
+    rest[off + 3:off + 3 + rows * ld].view(rows, ld)[:, :cols] = 9.0
+    assert (rest == 9.0).all()
