@@ -103,7 +103,8 @@ def _load_fastcall(path: str):
     from . import _fastcall
 
     _fastcall.init(path, (torch.bfloat16, torch.float32, torch.float64, torch.int32, torch.uint8), torch._C._cuda_getDevice,
-                   torch._C._cuda_getCurrentRawStream, lambda n, cur: torch.empty(n, dtype=torch.uint8, device=cur))
+                   torch._C._cuda_getCurrentRawStream, torch._C._cuda_cudaCachingAllocator_raw_alloc,
+                   torch._C._cuda_cudaCachingAllocator_raw_delete)
     _fast = _fastcall
 
 

@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <initializer_list>
 #include <mutex>
 #include <stdarg.h>
@@ -49,8 +50,8 @@ bool aligned_to(size_t n, std::initializer_list<const void *> ps)
 
 constexpr int kMaxDevices = 64;
 std::mutex g_mu;
-unsigned *g_status_ptr[kMaxDevices] = {};
-int g_sms[kMaxDevices] = {};
+std::atomic<unsigned *> g_status_ptr[kMaxDevices]; // looked up once a device, by whichever call comes first
+std::atomic<int> g_sms[kMaxDevices];
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 
 int current_device()
@@ -76,14 +77,15 @@ unsigned *device_status_ptr()
     const int d = current_device();
     if (d < 0 || d >= kMaxDevices)
         return nullptr;
-    std::lock_guard<std::mutex> lk(g_mu);
-    if (!g_status_ptr[d]) {
+    unsigned *known = g_status_ptr[d].load(std::memory_order_acquire);
+    if (!known) {
         void *p = nullptr;
         if (cudaGetSymbolAddress(&p, g_device_status) != cudaSuccess)
             return nullptr;
-        g_status_ptr[d] = static_cast<unsigned *>(p);
+        known = static_cast<unsigned *>(p);
+        g_status_ptr[d].store(known, std::memory_order_release);
     }
-    return g_status_ptr[d];
+    return known;
 }
 
 int num_sms()
@@ -91,13 +93,14 @@ int num_sms()
     const int d = current_device();
     if (d < 0 || d >= kMaxDevices)
         return 148;
-    std::lock_guard<std::mutex> lk(g_mu);
-    if (!g_sms[d]) {
+    int known = g_sms[d].load(std::memory_order_relaxed);
+    if (!known) {
         int n = 0;
         cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, d);
-        g_sms[d] = n > 0 ? n : 148;
+        known = n > 0 ? n : 148;
+        g_sms[d].store(known, std::memory_order_relaxed);
     }
-    return g_sms[d];
+    return known;
 }
 
 namespace {
