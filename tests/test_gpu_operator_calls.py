@@ -216,3 +216,32 @@ def test_query_parts_alone_and_together(T):
     dsa.dsa_rope_queries(pos, fr, qI=qI, q8=b[1], q_scale=b[2])
     assert all(torch.equal(x, y) for x, y in zip(a, b))
     assert (a[2][pos < 0] == 0).all() and (a[2][pos >= 0] > 0).all()
+
+
+@pytest.mark.parametrize("with_residual", [False, True])
+@pytest.mark.parametrize("rows,cols", [(5, 1000), (5, 1001), (3, 130), (5000, 520), (4900, 521), (700, 6000), (700, 6001)])
+def test_norm_outputs_in_every_combination(rows, cols, with_residual):
+    """Each subset of the outputs holds what the call with all of them gives; outputs that are not asked for are not
+    needed."""
+    dsa = lib()
+    g = torch.Generator(device=DEV).manual_seed(rows + cols)
+    x, res = (torch.randn((rows, cols), generator=g, device=DEV).to(BF) for _ in range(2))
+    w = torch.randn(cols, generator=g, device=DEV)
+
+    def outs():
+        return dict(out=torch.zeros_like(x), residual_out=torch.zeros_like(x), codes=torch.zeros((rows, cols), dtype=torch.uint8, device=DEV))
+
+    for block in (0, 128):
+        shape = (rows,) if block == 0 else (rows, -(-cols // 128))
+        given = dict(residual=res) if with_residual else {}
+        full, fscale = outs(), torch.zeros(shape, device=DEV)
+        dsa.dsa_rmsnorm(x, w, 1e-6, scale=fscale, block=block, **full, **given)
+        if not with_residual:
+            assert torch.equal(full["residual_out"], x)
+        for k in range(1, 7):
+            some = {n: t for i, (n, t) in enumerate(outs().items()) if k >> i & 1}
+            scale = torch.zeros(shape, device=DEV) if "codes" in some else None
+            dsa.dsa_rmsnorm(x, w, 1e-6, scale=scale, block=block, **some, **given)
+            for n, t in some.items():
+                assert torch.equal(t, full[n]), (n, k)
+            assert scale is None or torch.equal(scale, fscale)
