@@ -92,7 +92,7 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     return lib
 
 
-_fast = None  # the native call path (csrc/fastcall.c), loaded with the library
+_fast = None  # the native call path (csrc/fastcall.cpp), loaded with the library
 
 
 def _load_fastcall(path: str):
@@ -102,9 +102,8 @@ def _load_fastcall(path: str):
         raise RuntimeError(f"{so} is missing: build it with `python -m sparse_attention_02_gb300.build`")
     from . import _fastcall
 
-    _fastcall.init(path, (torch.bfloat16, torch.float32, torch.float64, torch.int32, torch.uint8), torch._C._cuda_getDevice,
-                   torch._C._cuda_getCurrentRawStream, torch._C._cuda_cudaCachingAllocator_raw_alloc,
-                   torch._C._cuda_cudaCachingAllocator_raw_delete)
+    _fastcall.init(path, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream,
+                   torch._C._cuda_cudaCachingAllocator_raw_alloc, torch._C._cuda_cudaCachingAllocator_raw_delete)
     _fast = _fastcall
 
 
@@ -262,11 +261,19 @@ def _refuse(t, cur: int, name: str, dtype, shape, rows: bool = False):
     raise ValueError(f"{name} must be contiguous")
 
 
+def _address(t, name: str) -> int:
+    """Address of a tensor's first element; fake tensors have none, which the library would take for no tensor."""
+    p = t.data_ptr()
+    if not p and t.numel():
+        raise ValueError(f"{name} has no memory behind it")
+    return p
+
+
 # The checks below are one expression each: a call on a few tokens costs the host more than the GPU.
 def _at(t, cur: int, name: str, dtype, shape) -> int:
     """Address of a contiguous CUDA tensor of the current device ``cur``."""
     if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == cur and t.shape == shape and t.is_contiguous():
-        return t.data_ptr()
+        return _address(t, name)
     _refuse(t, cur, name, dtype, shape)
 
 
@@ -274,10 +281,10 @@ def _at_rows(t, cur: int, name: str, dtype, shape):
     """(address, distance of the rows) of a 2-D CUDA tensor whose rows may be apart."""
     if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == cur and t.shape == shape:
         if t.is_contiguous():
-            return t.data_ptr(), shape[1]
+            return _address(t, name), shape[1]
         ld = t.stride(0) if shape[0] > 1 else shape[1]  # a single row's stride says nothing
         if (shape[1] == 1 or t.stride(1) == 1) and ld >= shape[1]:
-            return t.data_ptr(), ld
+            return _address(t, name), ld
     _refuse(t, cur, name, dtype, shape, True)
 
 
@@ -437,7 +444,7 @@ def dsa_rope_queries(pos, inv_freq, q_rope=None, q=None, qI=None, q8=None, q_sca
         if q_rope.dtype is not bf16 or q_rope.get_device() != cur or q_rope.shape != (T, H, 64) or st_d != 1:
             _refuse(q_rope, cur, "q_rope", bf16, (T, H, 64), True)
         # a single token's or head's stride says nothing
-        a_r, st_t, st_h = q_rope.data_ptr(), st_t if T > 1 else 0, st_h if H > 1 else 0
+        a_r, st_t, st_h = _address(q_rope, "q_rope"), st_t if T > 1 else 0, st_h if H > 1 else 0
         a_q = _at(q, cur, "q", bf16, (T, H, 576))
     if qI is not None:
         i_type = _dtype_of(qI, "qI")

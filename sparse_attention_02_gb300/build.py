@@ -3,12 +3,13 @@
 Each translation unit under csrc/ compiles in parallel to an object file, then
 one link step makes ``sparse_attention_02_gb300/libdsa.so``; the host compiler
 makes ``_fastcall.so``, the native part of the Python binding.  Run as a script
-or call ``build()``.  Only the CUDA toolkit, a C compiler and Python's headers
-are needed (no torch, no cmake).
+or call ``build()``.  Only the CUDA toolkit and, for the binding, a C++ compiler,
+Python's headers and PyTorch's are needed (torch itself is not imported; no cmake).
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -53,22 +54,31 @@ def _compile(src: str, extra=()) -> str:
 
 
 def _build_fastcall():
-    src, hdr = os.path.join(CSRC, "fastcall.c"), os.path.join(HERE, "..", "include", "dsa.h")
-    if os.path.exists(FAST) and os.path.getmtime(FAST) >= max(os.path.getmtime(src), os.path.getmtime(hdr)):
+    src, hdr = os.path.join(CSRC, "fastcall.cpp"), os.path.join(HERE, "..", "include", "dsa.h")
+    torch = importlib.util.find_spec("torch")
+    if torch is None:  # no binding without it; the library stands alone
+        return
+    root = list(torch.submodule_search_locations)[0]
+    deps = [src, hdr, os.path.join(root, "version.py")]
+    if os.path.exists(FAST) and os.path.getmtime(FAST) >= max(os.path.getmtime(d) for d in deps):
         return
     tmp = FAST + f".tmp{os.getpid()}"
-    cmd = [os.environ.get("CC", "gcc"), "-O2", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"], src, "-o", tmp, "-ldl"]
+    inc, lib = os.path.join(root, "include"), os.path.join(root, "lib")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"], "-isystem", inc,
+           "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), src, "-o", tmp, "-L", lib, "-lc10", "-ltorch_cpu",
+           "-ltorch_python", f"-Wl,-rpath,{lib}", "-ldl"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"{cmd[0]} failed for fastcall.c:\n{r.stdout}\n{r.stderr}")
+        raise RuntimeError(f"{cmd[0]} failed for fastcall.cpp:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, FAST)
 
 
 def build(verbose: bool = False, extra=()) -> str:
     os.makedirs(OBJ, exist_ok=True)
-    _build_fastcall()
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        fast = ex.submit(_build_fastcall)
         objs = list(ex.map(lambda s: _compile(s, extra), SOURCES))
+        fast.result()
     if not os.path.exists(LIB) or os.path.getmtime(LIB) < max(os.path.getmtime(o) for o in objs):
         tmp = LIB + f".tmp{os.getpid()}"
         cmd = [nvcc(), "-shared", "-o", tmp, *objs] + ARCH + ["-Xcompiler", "-fPIC", "-lcudart"]

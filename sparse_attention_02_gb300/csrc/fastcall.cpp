@@ -3,6 +3,9 @@
  * the marshalling of twenty arguments take the host longer than the kernels
  * take the GPU (a decode step's cache append: 10.6 us of host time in Python).
  *
+ * Tensors are read through PyTorch's own C++ headers (their attributes asked for
+ * in Python take 0.4 us a tensor, and a call has up to ten).
+ *
  * Every function takes the arguments of the binding's function of that name,
  * in order, and either makes the call, returning the library's status, or
  * returns NotImplemented without having done anything, where an argument is
@@ -13,33 +16,70 @@
 #include <Python.h>
 #include <dlfcn.h>
 #include <stdint.h>
+#include <torch/csrc/autograd/python_variable.h>
 
 #include "../../include/dsa.h"
 
-static PyObject *s_dtype, *s_shape, *s_get_device, *s_is_contiguous, *s_data_ptr, *s_stride, *s_cuda_stream;
-static PyObject *t_bf16, *t_fp32, *t_fp64, *t_int32, *t_uint8; /* torch dtypes */
-static PyObject *get_device_fn, *get_stream_fn;               /* current device, its raw stream */
-static PyObject *alloc_fn, *free_fn;                          /* PyTorch's allocator: address of (bytes, stream), its release */
+namespace {
 
-static __typeof__(&dsa_rmsnorm) f_rmsnorm;
-static __typeof__(&dsa_rmsnorm_backward) f_rmsnorm_backward;
-static __typeof__(&dsa_rmsnorm_backward_workspace_size) f_rmsnorm_backward_ws;
-static __typeof__(&dsa_cache_append) f_cache_append;
-static __typeof__(&dsa_rope_queries) f_rope_queries;
-static __typeof__(&dsa_index_rope_backward) f_index_rope_backward;
-static __typeof__(&dsa_mla_decode_paged) f_mla_decode;
-static __typeof__(&dsa_mla_decode_workspace_size) f_mla_decode_ws;
+PyObject *s_cuda_stream;
+PyObject *get_device_fn, *get_stream_fn;               /* current device, its raw stream */
+PyObject *alloc_fn, *free_fn;                          /* PyTorch's allocator: address of (bytes, stream), its release */
+
+decltype(&dsa_rmsnorm) f_rmsnorm;
+decltype(&dsa_rmsnorm_backward) f_rmsnorm_backward;
+decltype(&dsa_rmsnorm_backward_workspace_size) f_rmsnorm_backward_ws;
+decltype(&dsa_cache_append) f_cache_append;
+decltype(&dsa_rope_queries) f_rope_queries;
+decltype(&dsa_index_rope_backward) f_index_rope_backward;
+decltype(&dsa_mla_decode_paged) f_mla_decode;
+decltype(&dsa_mla_decode_workspace_size) f_mla_decode_ws;
+
+/* An address as whatever the library takes it for. */
+struct Address {
+    void *v = nullptr;
+    template <typename T> operator T *() const { return static_cast<T *>(v); }
+};
 
 /* What is known of a tensor argument. */
-typedef struct {
-    int nd;
-    int64_t dim[3], stride[3]; /* stride only after strides() */
-    int dtype;                 /* DSA_BF16, DSA_FP32, or one of the below */
-    void *p;
-} Arg;
+struct Arg {
+    int nd = 0;
+    int64_t dim[3] = {}, stride[3] = {};
+    bool contiguous = false;
+    int dtype = 0; /* DSA_BF16, DSA_FP32, or one of the below */
+    Address p;
+};
 enum { K_FP64 = 10, K_INT32, K_UINT8, K_ANY /* bf16 or fp32 */ };
 
-static int64_t as_int(PyObject *o, int *ok)
+/* What t is; false where it is not a plain tensor of the device with up to 3 dimensions and the type. */
+bool look(PyObject *t, long cur, int want, Arg *a)
+{
+    if (!THPVariable_Check(t))
+        return false;
+    const at::Tensor &v = THPVariable_Unpack(t);
+    switch (v.scalar_type()) {
+    case at::kBFloat16: a->dtype = DSA_BF16; break;
+    case at::kFloat: a->dtype = DSA_FP32; break;
+    case at::kDouble: a->dtype = K_FP64; break;
+    case at::kInt: a->dtype = K_INT32; break;
+    case at::kByte: a->dtype = K_UINT8; break;
+    default: return false;
+    }
+    if (want == K_ANY ? (a->dtype != DSA_BF16 && a->dtype != DSA_FP32) : a->dtype != want)
+        return false;
+    if (!v.is_cuda() || v.layout() != at::kStrided || v.get_device() != cur || v.dim() > 3)
+        return false;
+    a->nd = (int)v.dim();
+    for (int i = 0; i < a->nd; ++i) {
+        a->dim[i] = v.size(i);
+        a->stride[i] = v.stride(i);
+    }
+    a->contiguous = v.is_contiguous();
+    a->p.v = v.data_ptr(); /* throws, or is null, where there is no memory behind it */
+    return a->p.v || v.numel() == 0;
+}
+
+int64_t as_int(PyObject *o, int *ok)
 {
     int64_t v = o ? PyLong_AsLongLong(o) : -1;
     if (!o || (v == -1 && PyErr_Occurred()))
@@ -48,70 +88,24 @@ static int64_t as_int(PyObject *o, int *ok)
     return v;
 }
 
-/* Dtype, device, shape (up to 3 dimensions) and address of t; 0 where it is not a plain tensor of the device. */
-static int look(PyObject *t, long cur, int want, Arg *a)
-{
-    int ok = 1;
-    PyObject *d = PyObject_GetAttr(t, s_dtype);
-    if (!d)
-        return 0;
-    a->dtype = d == t_bf16 ? DSA_BF16 : d == t_fp32 ? DSA_FP32 : d == t_fp64 ? K_FP64 : d == t_int32 ? K_INT32 : d == t_uint8 ? K_UINT8 : -1;
-    Py_DECREF(d);
-    if (want == K_ANY ? (a->dtype != DSA_BF16 && a->dtype != DSA_FP32) : a->dtype != want)
-        return 0;
-    if (as_int(PyObject_CallMethodNoArgs(t, s_get_device), &ok) != cur || !ok)
-        return 0;
-    PyObject *shape = PyObject_GetAttr(t, s_shape);
-    if (!shape)
-        return 0;
-    ok = PyTuple_Check(shape) && PyTuple_GET_SIZE(shape) <= 3;
-    a->nd = ok ? (int)PyTuple_GET_SIZE(shape) : 0;
-    for (int i = 0; i < a->nd; ++i) {
-        a->dim[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(shape, i));
-        if (a->dim[i] < 0)
-            ok = 0;
-    }
-    Py_DECREF(shape);
-    a->p = (void *)(uintptr_t)as_int(PyObject_CallMethodNoArgs(t, s_data_ptr), &ok);
-    return ok && !PyErr_Occurred();
-}
-
-static int contiguous(PyObject *t)
-{
-    PyObject *c = PyObject_CallMethodNoArgs(t, s_is_contiguous);
-    int yes = c == Py_True;
-    Py_XDECREF(c);
-    return yes;
-}
-
-static int strides(PyObject *t, Arg *a)
-{
-    PyObject *s = PyObject_CallMethodNoArgs(t, s_stride);
-    int ok = s && PyTuple_Check(s) && PyTuple_GET_SIZE(s) == a->nd;
-    for (int i = 0; ok && i < a->nd; ++i)
-        a->stride[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(s, i));
-    Py_XDECREF(s);
-    return ok && !PyErr_Occurred();
-}
-
 /* A contiguous tensor of the shape (n1, n2 < 0: fewer dimensions). */
-static int at(PyObject *t, long cur, int want, int64_t n0, int64_t n1, int64_t n2, Arg *a)
+int at(PyObject *t, long cur, int want, int64_t n0, int64_t n1, int64_t n2, Arg *a)
 {
     return look(t, cur, want, a) && a->nd == 1 + (n1 >= 0) + (n2 >= 0) && a->dim[0] == n0 && (n1 < 0 || a->dim[1] == n1) &&
-           (n2 < 0 || a->dim[2] == n2) && contiguous(t);
+           (n2 < 0 || a->dim[2] == n2) && a->contiguous;
 }
 
 /* A 2-D tensor whose rows may be apart; *ld is their distance. */
-static int at_rows(PyObject *t, long cur, int want, int64_t n0, int64_t n1, Arg *a, int64_t *ld)
+int at_rows(PyObject *t, long cur, int want, int64_t n0, int64_t n1, Arg *a, int64_t *ld)
 {
-    if (!look(t, cur, want, a) || a->nd != 2 || a->dim[0] != n0 || a->dim[1] != n1 || !strides(t, a))
+    if (!look(t, cur, want, a) || a->nd != 2 || a->dim[0] != n0 || a->dim[1] != n1)
         return 0;
     *ld = n0 > 1 ? a->stride[0] : n1;
     return (n1 == 1 || a->stride[1] == 1) && *ld >= n1;
 }
 
 /* Device, and the stream of the call: stream's, or the device's current one. */
-static int where(PyObject *stream, long *cur, dsa_stream_t *s)
+int where(PyObject *stream, long *cur, dsa_stream_t *s)
 {
     int ok = 1;
     *cur = (long)as_int(PyObject_CallNoArgs(get_device_fn), &ok);
@@ -132,7 +126,7 @@ static int where(PyObject *stream, long *cur, dsa_stream_t *s)
 /* Workspace of `need` bytes: the caller's, or one of PyTorch's allocator on the call's stream, to be given back
  * (release) once the call is enqueued: what the allocator hands out next on that stream runs after it.  A tensor
  * for it would take the host as long as the rest of a small call (517 x 1111 norm backward: 11.3 us, 6.2 without). */
-static int workspace(PyObject *ws, dsa_stream_t stream, long cur, size_t need, void **p, size_t *bytes, PyObject **keep)
+int workspace(PyObject *ws, dsa_stream_t stream, long cur, size_t need, void **p, size_t *bytes, PyObject **keep)
 {
     Arg a;
     int ok = 1;
@@ -140,7 +134,7 @@ static int workspace(PyObject *ws, dsa_stream_t stream, long cur, size_t need, v
     *p = NULL;
     *bytes = 0;
     if (ws != Py_None) {
-        if (!look(ws, cur, K_UINT8, &a) || a.nd != 1 || !contiguous(ws))
+        if (!look(ws, cur, K_UINT8, &a) || a.nd != 1 || !a.contiguous)
             return 0;
         *p = a.p;
         *bytes = (size_t)a.dim[0];
@@ -157,7 +151,7 @@ static int workspace(PyObject *ws, dsa_stream_t stream, long cur, size_t need, v
     return ok;
 }
 
-static void release(PyObject *keep)
+void release(PyObject *keep)
 {
     if (!keep)
         return;
@@ -169,7 +163,7 @@ static void release(PyObject *keep)
 }
 
 /* Numbers: plain Python ones only. */
-static int number(PyObject *o, double *v)
+int number(PyObject *o, double *v)
 {
     if (!PyFloat_Check(o) && !PyLong_Check(o))
         return 0;
@@ -177,7 +171,7 @@ static int number(PyObject *o, double *v)
     return !(*v == -1.0 && PyErr_Occurred());
 }
 
-static int integer(PyObject *o, int *v)
+int integer(PyObject *o, int *v)
 {
     if (!PyLong_Check(o))
         return 0;
@@ -186,7 +180,7 @@ static int integer(PyObject *o, int *v)
     return x >= INT32_MIN && x <= INT32_MAX && !PyErr_Occurred();
 }
 
-static PyObject *not_plain(PyObject *keep)
+PyObject *not_plain(PyObject *keep)
 {
     PyErr_Clear();
     release(keep);
@@ -203,16 +197,16 @@ static PyObject *not_plain(PyObject *keep)
     } while (0)
 
 /* x, weight, eps, out, residual, residual_out, codes, scale, block, scale_mode, stream */
-static PyObject *py_rmsnorm(PyObject *m, PyObject *const *v, Py_ssize_t n)
+PyObject *py_rmsnorm(PyObject *const *v, Py_ssize_t n)
 {
     long cur;
     dsa_stream_t st;
-    Arg x, w, o = {0}, r = {0}, h = {0}, c = {0}, s = {0};
+    Arg x, w, o, r, h, c, s;
     int64_t ldx, ldo = 0, ldr = 0, ldh = 0;
     double eps;
     int block, mode;
     if (n != 11 || !where(v[10], &cur, &st) || !number(v[2], &eps) || !integer(v[8], &block) || !integer(v[9], &mode) ||
-        !look(v[0], cur, K_ANY, &x) || x.nd != 2 || !FITS(x.dim[1]) || !strides(v[0], &x))
+        !look(v[0], cur, K_ANY, &x) || x.nd != 2 || !FITS(x.dim[1]))
         return not_plain(NULL);
     const int64_t rows = x.dim[0], cols = x.dim[1];
     ldx = rows > 1 ? x.stride[0] : cols;
@@ -224,7 +218,7 @@ static PyObject *py_rmsnorm(PyObject *m, PyObject *const *v, Py_ssize_t n)
         return not_plain(NULL);
     if (v[7] != Py_None) {
         const int64_t parts = block > 0 ? (cols + block - 1) / block : 1;
-        if (!look(v[7], cur, DSA_FP32, &s) || s.dim[0] != rows || !contiguous(v[7]) ||
+        if (!look(v[7], cur, DSA_FP32, &s) || s.dim[0] != rows || !s.contiguous ||
             !((s.nd == 2 && s.dim[1] == parts) || (s.nd == 1 && parts == 1)))
             return not_plain(NULL);
     }
@@ -235,17 +229,17 @@ static PyObject *py_rmsnorm(PyObject *m, PyObject *const *v, Py_ssize_t n)
 }
 
 /* dy, h, weight, eps, dx, dweight, dres, workspace, stream */
-static PyObject *py_rmsnorm_backward(PyObject *m, PyObject *const *v, Py_ssize_t n)
+PyObject *py_rmsnorm_backward(PyObject *const *v, Py_ssize_t n)
 {
     long cur;
     dsa_stream_t st;
-    Arg dy, h, w, dx, dw, e = {0};
+    Arg dy, h, w, dx, dw, e;
     double eps;
     void *ws;
     size_t bytes;
     PyObject *keep = NULL;
     if (n != 9 || !where(v[8], &cur, &st) || !number(v[3], &eps) || !look(v[1], cur, K_ANY, &h) || h.nd != 2 ||
-        !FITS(h.dim[1]) || !contiguous(v[1]))
+        !FITS(h.dim[1]) || !h.contiguous)
         return not_plain(NULL);
     const int64_t rows = h.dim[0], cols = h.dim[1];
     if (!at(v[0], cur, h.dtype, rows, cols, -1, &dy) || !at(v[2], cur, K_ANY, cols, -1, -1, &w) ||
@@ -260,31 +254,31 @@ static PyObject *py_rmsnorm_backward(PyObject *m, PyObject *const *v, Py_ssize_t
 }
 
 /* pos, block_table, inv_freq, kv, kv_pool, kI, k8_pool, ks_pool, seq, kv_weight, eps, scale_mode, stream */
-static PyObject *py_cache_append(PyObject *m, PyObject *const *v, Py_ssize_t n)
+PyObject *py_cache_append(PyObject *const *v, Py_ssize_t n)
 {
     long cur;
     dsa_stream_t st;
-    Arg pos, bt, fr, kv = {0}, kp = {0}, k = {0}, k8 = {0}, ks = {0}, seq = {0}, w = {0};
+    Arg pos, bt, fr, kv, kp, k, k8, ks, seq, w;
     int64_t ld = 0, ldI = 0;
     double eps;
     int mode;
     const int with_kv = n == 13 && v[3] != Py_None, with_k = n == 13 && v[5] != Py_None;
     if (n != 13 || (!with_kv && !with_k) || !where(v[12], &cur, &st) || !number(v[10], &eps) || !integer(v[11], &mode) ||
-        !look(v[0], cur, K_INT32, &pos) || pos.nd != 1 || !FITS(pos.dim[0]) || !contiguous(v[0]) ||
-        !look(v[1], cur, K_INT32, &bt) || bt.nd != 2 || !FITS(bt.dim[0]) || !FITS(bt.dim[1]) || !contiguous(v[1]) ||
+        !look(v[0], cur, K_INT32, &pos) || pos.nd != 1 || !FITS(pos.dim[0]) || !pos.contiguous ||
+        !look(v[1], cur, K_INT32, &bt) || bt.nd != 2 || !FITS(bt.dim[0]) || !FITS(bt.dim[1]) || !bt.contiguous ||
         !at(v[2], cur, K_FP64, 32, -1, -1, &fr))
         return not_plain(NULL);
     const int64_t T = pos.dim[0];
     int64_t pages = 0, page = 0;
     if (with_kv) {
         if (!at_rows(v[3], cur, DSA_BF16, T, 576, &kv, &ld) || !look(v[4], cur, DSA_BF16, &kp) || kp.nd != 3 ||
-            kp.dim[2] != 576 || !contiguous(v[4]) || (v[9] != Py_None && !at(v[9], cur, K_ANY, 512, -1, -1, &w)))
+            kp.dim[2] != 576 || !kp.contiguous || (v[9] != Py_None && !at(v[9], cur, K_ANY, 512, -1, -1, &w)))
             return not_plain(NULL);
         pages = kp.dim[0], page = kp.dim[1];
     }
     if (with_k) {
         if (!at_rows(v[5], cur, K_ANY, T, 128, &k, &ldI) || !look(v[6], cur, K_UINT8, &k8) || k8.nd != 3 || k8.dim[2] != 128 ||
-            !contiguous(v[6]) || (with_kv && (k8.dim[0] != pages || k8.dim[1] != page)))
+            !k8.contiguous || (with_kv && (k8.dim[0] != pages || k8.dim[1] != page)))
             return not_plain(NULL);
         pages = k8.dim[0], page = k8.dim[1];
         if (!at(v[7], cur, DSA_FP32, pages, page, -1, &ks))
@@ -299,27 +293,27 @@ static PyObject *py_cache_append(PyObject *m, PyObject *const *v, Py_ssize_t n)
 }
 
 /* pos, inv_freq, q_rope, q, qI, q8, q_scale, scale_mode, stream */
-static PyObject *py_rope_queries(PyObject *m, PyObject *const *v, Py_ssize_t n)
+PyObject *py_rope_queries(PyObject *const *v, Py_ssize_t n)
 {
     long cur;
     dsa_stream_t st;
-    Arg pos, fr, r = {0}, q = {0}, qi = {0}, q8 = {0}, s = {0};
+    Arg pos, fr, r, q, qi, q8, s;
     int64_t H = 0, HI = 0;
     int mode;
     const int with_r = n == 9 && v[2] != Py_None, with_i = n == 9 && v[4] != Py_None;
     if (n != 9 || (!with_r && !with_i) || !where(v[8], &cur, &st) || !integer(v[7], &mode) || !look(v[0], cur, K_INT32, &pos) ||
-        pos.nd != 1 || !FITS(pos.dim[0]) || !contiguous(v[0]) || !at(v[1], cur, K_FP64, 32, -1, -1, &fr))
+        pos.nd != 1 || !FITS(pos.dim[0]) || !pos.contiguous || !at(v[1], cur, K_FP64, 32, -1, -1, &fr))
         return not_plain(NULL);
     const int64_t T = pos.dim[0];
     if (with_r) {
-        if (!look(v[2], cur, DSA_BF16, &r) || r.nd != 3 || r.dim[0] != T || r.dim[2] != 64 || !strides(v[2], &r) || r.stride[2] != 1)
+        if (!look(v[2], cur, DSA_BF16, &r) || r.nd != 3 || r.dim[0] != T || r.dim[2] != 64 || r.stride[2] != 1)
             return not_plain(NULL);
         H = r.dim[1];
         if (!FITS(H) || !at(v[3], cur, DSA_BF16, T, H, 576, &q))
             return not_plain(NULL);
     }
     if (with_i) {
-        if (!look(v[4], cur, K_ANY, &qi) || qi.nd != 3 || qi.dim[0] != T || qi.dim[2] != 128 || !contiguous(v[4]))
+        if (!look(v[4], cur, K_ANY, &qi) || qi.nd != 3 || qi.dim[0] != T || qi.dim[2] != 128 || !qi.contiguous)
             return not_plain(NULL);
         HI = qi.dim[1];
         if (!FITS(HI) || !at(v[5], cur, K_UINT8, T, HI, 128, &q8) || !at(v[6], cur, DSA_FP32, T, -1, -1, &s))
@@ -332,13 +326,13 @@ static PyObject *py_rope_queries(PyObject *m, PyObject *const *v, Py_ssize_t n)
 }
 
 /* g, pos, inv_freq, dx, stream */
-static PyObject *py_index_rope_backward(PyObject *m, PyObject *const *v, Py_ssize_t n)
+PyObject *py_index_rope_backward(PyObject *const *v, Py_ssize_t n)
 {
     long cur;
     dsa_stream_t st;
     Arg g, pos, fr, dx;
     if (n != 5 || !where(v[4], &cur, &st) || !look(v[0], cur, DSA_FP32, &g) || g.nd < 2 || g.dim[g.nd - 1] != 128 ||
-        !FITS(g.dim[0]) || !FITS(g.dim[1]) || !contiguous(v[0]) || !at(v[1], cur, K_INT32, g.dim[0], -1, -1, &pos) ||
+        !FITS(g.dim[0]) || !FITS(g.dim[1]) || !g.contiguous || !at(v[1], cur, K_INT32, g.dim[0], -1, -1, &pos) ||
         !at(v[2], cur, K_FP64, 32, -1, -1, &fr) || !at(v[3], cur, K_ANY, g.dim[0], g.dim[1], g.nd == 3 ? 128 : -1, &dx))
         return not_plain(NULL);
     int rc;
@@ -347,7 +341,7 @@ static PyObject *py_index_rope_backward(PyObject *m, PyObject *const *v, Py_ssiz
 }
 
 /* q, kv_pool, block_table, ctx_len, sm_scale, out, lse, workspace, stream */
-static PyObject *py_mla_decode_paged(PyObject *m, PyObject *const *v, Py_ssize_t n)
+PyObject *py_mla_decode_paged(PyObject *const *v, Py_ssize_t n)
 {
     long cur;
     dsa_stream_t st;
@@ -357,9 +351,9 @@ static PyObject *py_mla_decode_paged(PyObject *m, PyObject *const *v, Py_ssize_t
     size_t bytes;
     PyObject *keep = NULL;
     if (n != 9 || !where(v[8], &cur, &st) || !number(v[4], &scale) || !look(v[0], cur, DSA_BF16, &q) || q.nd != 3 ||
-        q.dim[2] != 576 || !FITS(q.dim[0]) || !FITS(q.dim[1]) || !contiguous(v[0]) || !look(v[1], cur, DSA_BF16, &kv) ||
-        kv.nd != 3 || kv.dim[2] != 576 || !FITS(kv.dim[0]) || !FITS(kv.dim[1]) || !contiguous(v[1]) ||
-        !look(v[2], cur, K_INT32, &bt) || bt.nd != 2 || bt.dim[0] != q.dim[0] || !FITS(bt.dim[1]) || !contiguous(v[2]) ||
+        q.dim[2] != 576 || !FITS(q.dim[0]) || !FITS(q.dim[1]) || !q.contiguous || !look(v[1], cur, DSA_BF16, &kv) ||
+        kv.nd != 3 || kv.dim[2] != 576 || !FITS(kv.dim[0]) || !FITS(kv.dim[1]) || !kv.contiguous ||
+        !look(v[2], cur, K_INT32, &bt) || bt.nd != 2 || bt.dim[0] != q.dim[0] || !FITS(bt.dim[1]) || !bt.contiguous ||
         !at(v[3], cur, K_INT32, q.dim[0], -1, -1, &ctx) || !at(v[5], cur, DSA_BF16, q.dim[0], q.dim[1], 512, &out) ||
         !at(v[6], cur, DSA_FP32, q.dim[0], q.dim[1], -1, &lse) ||
         !workspace(v[7], st, cur, v[7] == Py_None ? f_mla_decode_ws((int)q.dim[0], (int)q.dim[1]) : 0, &ws, &bytes, &keep))
@@ -371,40 +365,48 @@ static PyObject *py_mla_decode_paged(PyObject *m, PyObject *const *v, Py_ssize_t
     return PyLong_FromLong(rc);
 }
 
-/* init(path of the library, (bf16, fp32, fp64, int32, uint8), current device, raw stream of a device, alloc(bytes, stream),
- * free(address)) */
-static PyObject *py_init(PyObject *m, PyObject *args)
+/* init(path of the library, current device, raw stream of a device, alloc(bytes, stream), free(address)) */
+PyObject *py_init(PyObject *, PyObject *args)
 {
     const char *path;
-    if (!PyArg_ParseTuple(args, "s(OOOOO)OOOO", &path, &t_bf16, &t_fp32, &t_fp64, &t_int32, &t_uint8, &get_device_fn, &get_stream_fn,
-                          &alloc_fn, &free_fn))
+    if (!PyArg_ParseTuple(args, "sOOOO", &path, &get_device_fn, &get_stream_fn, &alloc_fn, &free_fn))
         return NULL;
     void *lib = dlopen(path, RTLD_NOW | RTLD_LOCAL);
     if (!lib) {
         PyErr_SetString(PyExc_RuntimeError, dlerror());
         return NULL;
     }
-    f_rmsnorm = (__typeof__(f_rmsnorm))dlsym(lib, "dsa_rmsnorm");
-    f_rmsnorm_backward = (__typeof__(f_rmsnorm_backward))dlsym(lib, "dsa_rmsnorm_backward");
-    f_rmsnorm_backward_ws = (__typeof__(f_rmsnorm_backward_ws))dlsym(lib, "dsa_rmsnorm_backward_workspace_size");
-    f_cache_append = (__typeof__(f_cache_append))dlsym(lib, "dsa_cache_append");
-    f_rope_queries = (__typeof__(f_rope_queries))dlsym(lib, "dsa_rope_queries");
-    f_index_rope_backward = (__typeof__(f_index_rope_backward))dlsym(lib, "dsa_index_rope_backward");
-    f_mla_decode = (__typeof__(f_mla_decode))dlsym(lib, "dsa_mla_decode_paged");
-    f_mla_decode_ws = (__typeof__(f_mla_decode_ws))dlsym(lib, "dsa_mla_decode_workspace_size");
+    f_rmsnorm = (decltype(f_rmsnorm))dlsym(lib, "dsa_rmsnorm");
+    f_rmsnorm_backward = (decltype(f_rmsnorm_backward))dlsym(lib, "dsa_rmsnorm_backward");
+    f_rmsnorm_backward_ws = (decltype(f_rmsnorm_backward_ws))dlsym(lib, "dsa_rmsnorm_backward_workspace_size");
+    f_cache_append = (decltype(f_cache_append))dlsym(lib, "dsa_cache_append");
+    f_rope_queries = (decltype(f_rope_queries))dlsym(lib, "dsa_rope_queries");
+    f_index_rope_backward = (decltype(f_index_rope_backward))dlsym(lib, "dsa_index_rope_backward");
+    f_mla_decode = (decltype(f_mla_decode))dlsym(lib, "dsa_mla_decode_paged");
+    f_mla_decode_ws = (decltype(f_mla_decode_ws))dlsym(lib, "dsa_mla_decode_workspace_size");
     if (!f_rmsnorm || !f_rmsnorm_backward || !f_rmsnorm_backward_ws || !f_cache_append || !f_rope_queries || !f_index_rope_backward ||
         !f_mla_decode || !f_mla_decode_ws) {
         PyErr_SetString(PyExc_RuntimeError, "the library lacks an entry point");
         return NULL;
     }
-    PyObject *kept[] = {t_bf16, t_fp32, t_fp64, t_int32, t_uint8, get_device_fn, get_stream_fn, alloc_fn, free_fn};
+    PyObject *kept[] = {get_device_fn, get_stream_fn, alloc_fn, free_fn};
     for (size_t i = 0; i < sizeof kept / sizeof *kept; ++i)
         Py_INCREF(kept[i]);
     Py_RETURN_NONE;
 }
 
-#define FAST(name) {#name, (PyCFunction)(void (*)(void))py_##name, METH_FASTCALL, NULL}
-static PyMethodDef methods[] = {FAST(rmsnorm),
+/* What PyTorch throws leaves the call to the Python form, which then raises it. */
+template <PyObject *(*F)(PyObject *const *, Py_ssize_t)> PyObject *entry(PyObject *, PyObject *const *v, Py_ssize_t n)
+{
+    try {
+        return F(v, n);
+    } catch (...) {
+        return not_plain(NULL);
+    }
+}
+
+#define FAST(name) {#name, (PyCFunction)(void (*)(void))entry<py_##name>, METH_FASTCALL, NULL}
+PyMethodDef methods[] = {FAST(rmsnorm),
                                 FAST(rmsnorm_backward),
                                 FAST(cache_append),
                                 FAST(rope_queries),
@@ -412,16 +414,12 @@ static PyMethodDef methods[] = {FAST(rmsnorm),
                                 FAST(mla_decode_paged),
                                 {"init", py_init, METH_VARARGS, NULL},
                                 {NULL, NULL, 0, NULL}};
-static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fastcall", NULL, -1, methods, NULL, NULL, NULL, NULL};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fastcall", NULL, -1, methods, NULL, NULL, NULL, NULL};
+
+} // namespace
 
 PyMODINIT_FUNC PyInit__fastcall(void)
 {
-    s_dtype = PyUnicode_InternFromString("dtype");
-    s_shape = PyUnicode_InternFromString("shape");
-    s_get_device = PyUnicode_InternFromString("get_device");
-    s_is_contiguous = PyUnicode_InternFromString("is_contiguous");
-    s_data_ptr = PyUnicode_InternFromString("data_ptr");
-    s_stride = PyUnicode_InternFromString("stride");
     s_cuda_stream = PyUnicode_InternFromString("cuda_stream");
     return PyModule_Create(&module);
 }

@@ -245,3 +245,23 @@ def test_norm_outputs_in_every_combination(rows, cols, with_residual):
             for n, t in some.items():
                 assert torch.equal(t, full[n]), (n, k)
             assert scale is None or torch.equal(scale, fscale)
+
+
+def test_tensors_without_memory_are_refused():
+    """Meta, sparse and fake tensors: an error from the Python form, nothing launched, and the next call works."""
+    from torch._subclasses.fake_tensor import FakeTensorMode
+
+    dsa = lib()
+    x, w = torch.ones((4, 64), dtype=BF, device=DEV), torch.ones(64, dtype=BF, device=DEV)
+    with FakeTensorMode(allow_non_fake_inputs=True):
+        fake = torch.empty((4, 64), dtype=BF, device=DEV)
+    for bad in (torch.empty((4, 64), dtype=BF, device="meta"), x.to_sparse(), fake, None, 3):
+        out = torch.zeros_like(x)
+        with pytest.raises((TypeError, ValueError, RuntimeError)):
+            dsa.dsa_rmsnorm(bad, w, 1e-6, out=out)
+        with pytest.raises((TypeError, ValueError, RuntimeError)):
+            dsa.dsa_rmsnorm(x, w, 1e-6, out=out, residual=bad if bad is not None else 5)
+        torch.cuda.synchronize()
+        assert (out == 0).all()
+        dsa.dsa_rmsnorm(x, w, 0.0, out=out)
+        assert (out == 1).all()
