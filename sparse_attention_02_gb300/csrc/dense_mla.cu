@@ -113,6 +113,12 @@ constexpr int B_KF = 0,  // L [stage][group]: both CTAs' atoms landed
 
 constexpr uint32_t TM_O = 0, TM_S = 256, kTmemCols = 512;
 
+// A row in parts: the slot of its first, the cluster of its last.  Rows that are
+// whole, and clusters that do not begin a row which others finish, have row = -1.
+struct Split {
+    int row, slot, last, pad;
+};
+
 struct Params {
     const __nv_bfloat16 *q;
     const __nv_bfloat16 *pool;
@@ -122,7 +128,7 @@ struct Params {
     __nv_bfloat16 *out;
     float *lse;
     float *ws_o, *ws_lse; // [2 clusters, H, 512], [2 clusters, H]
-    int2 *row_parts;      // [B] slot of a row's first part (-1: it is whole), cluster of its last
+    Split *splits;        // [min(B, clusters)], of rows where they are fewer than clusters, else of clusters
     unsigned *status;
 };
 
@@ -137,8 +143,10 @@ __device__ __forceinline__ int context(const Params &p, int row)
 __device__ __forceinline__ int tiles_of(int ctx) { return ctx > 0 ? (ctx - 1) / kTile + 1 : 1; }
 
 struct Share {
-    int64_t tiles;      // of this cluster
-    int row, tile;      // where it starts
+    int64_t tiles;        // of this cluster
+    int64_t begin, total; // its first of all tiles
+    int row, tile;        // where it starts
+    int clusters;         // that have shares
 };
 
 struct Unit {
@@ -375,8 +383,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             return total < (1 << 24) ? (int64_t)((uint32_t)total * (uint32_t)c / (uint32_t)n) : total * c / n;
         };
         const int64_t g0 = cid < n ? start(cid) : total, g1 = cid < n ? start(cid + 1) : total;
-        if (threadIdx.x == 0)
+        if (threadIdx.x == 0) {
             share->tiles = g1 - g0;
+            share->begin = g0;
+            share->total = total;
+            share->clusters = n;
+        }
         if (g0 >= before && g0 < before + mine) {
             int64_t at = before;
             int r = r0;
@@ -593,13 +605,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         Walk it(*share);
         Unit un;
         Pages pg;
+        // for the joining kernel: tile g of all lies in cluster ((g + 1) clusters - 1) / total
+        const bool records = rank == 0 && threadIdx.x == 32 * kSoftWarp0, by_row = p.B < p.clusters;
+        if (records && !by_row)
+            p.splits[cid] = {-1, 0, 0, 0};
         while (ok && it.next(p, cid, un)) {
             float m = -INFINITY, l = 0.f;
-            if (rank == 0 && threadIdx.x == 32 * kSoftWarp0) { // for the joining kernel
-                if (un.jb == 0)
-                    p.row_parts[un.row].x = un.slot;
-                if (un.je == tiles_of(un.ctx))
-                    p.row_parts[un.row].y = cid;
+            if (records && un.jb == 0) {
+                const int n = tiles_of(un.ctx);
+                const int64_t end = share->begin + (share->tiles - it.left - un.je) + n; // of the row
+                if (un.slot >= 0)
+                    p.splits[by_row ? un.row : cid] = {un.row, un.slot, (int)((end * share->clusters - 1) / share->total), 0};
+                else if (by_row)
+                    p.splits[un.row].row = -1;
             }
             const int64_t orow = (int64_t)un.row * p.H + h, prow = (int64_t)un.slot * p.H + h;
             const int col0 = 256 * kb + 128 * part; // of O: lanes 0-63 hold columns [0, 256), lanes 64-127 the others
@@ -794,7 +812,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // of the parts.  A CTA takes HEADS heads of a row: with eight and few parts a
 // warp each, else its warps take parts w, w + 8, ... of one head after the
 // other and add up.  A row's parts lie in consecutive clusters; in all but the
-// first the row is the share's first, so its slot is 2 cluster.
+// first the row is the share's first, so its slot is 2 cluster.  At most one row
+// a cluster begins there and ends elsewhere, so the grid has no more rows than
+// clusters: looking at all 200 of a batch took 4 us of 33.
 template <int HEADS>
 __global__ void __launch_bounds__(256) dense_mla_join_kernel(Params p)
 {
@@ -802,12 +822,13 @@ __global__ void __launch_bounds__(256) dense_mla_join_kernel(Params p)
     __shared__ float sum_s[8];
     grid_dep_wait();
     grid_dep_launch();
-    const int row = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int2 rp = p.row_parts[row];
-    if (rp.x < 0)
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const Split sp = p.splits[blockIdx.x];
+    const int row = sp.row, c0 = sp.slot >> 1, np = sp.last - c0 + 1;
+    // after a wait that gave up, records may be missing: nothing is read or written outside the buffers for it
+    if (row < 0 || row >= p.B || sp.slot < 0 || np < 1 || sp.last >= p.clusters)
         return;
-    const int c0 = rp.x >> 1, np = rp.y - c0 + 1;
-    auto slot = [&](int i) { return i == 0 ? rp.x : 2 * (c0 + i); };
+    auto slot = [&](int i) { return i == 0 ? sp.slot : 2 * (c0 + i); };
     const bool alone = HEADS > 1 && np <= 8; // a warp joins a head by itself
     for (int k = alone ? warp : 0; k < HEADS; k += alone ? 8 : 1) {
         const int h = blockIdx.y * HEADS + k;
@@ -879,7 +900,8 @@ size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 size_t dense_mla_workspace_bytes(int B, int H)
 {
     const size_t parts = 2 * (size_t)clusters() * H;
-    return align256(parts * kDv * sizeof(float)) + align256(parts * sizeof(float)) + (size_t)B * sizeof(int2);
+    const size_t splits = B < clusters() ? B : clusters();
+    return align256(parts * kDv * sizeof(float)) + align256(parts * sizeof(float)) + splits * sizeof(Split);
 }
 
 int launch_dense_mla(const DenseMlaArgs &a, cudaStream_t stream, char *err, size_t errlen)
@@ -907,7 +929,7 @@ int launch_dense_mla(const DenseMlaArgs &a, cudaStream_t stream, char *err, size
     uint8_t *ws = static_cast<uint8_t *>(a.workspace);
     p.ws_o = reinterpret_cast<float *>(ws);
     p.ws_lse = reinterpret_cast<float *>(ws + align256(parts * kDv * sizeof(float)));
-    p.row_parts = reinterpret_cast<int2 *>(ws + align256(parts * kDv * sizeof(float)) + align256(parts * sizeof(float)));
+    p.splits = reinterpret_cast<Split *>(ws + align256(parts * kDv * sizeof(float)) + align256(parts * sizeof(float)));
     CUtensorMap tq, tkv2, tkv3;
     const uint64_t rows = (uint64_t)a.num_pages * a.page_size;
     const uint32_t box = a.page_size < 64 ? a.page_size : 64;
@@ -923,10 +945,11 @@ int launch_dense_mla(const DenseMlaArgs &a, cudaStream_t stream, char *err, size
     cudaError_t e = raise_smem_limit_once(dense_mla_kernel, kSmem, raised);
     if (e == cudaSuccess)
         e = launch_pdl(dense_mla_kernel, dim3(2 * p.clusters), dim3(kThreads), kSmem, stream, 1, tq, tkv2, tkv3, p);
+    const int joins = a.B < p.clusters ? a.B : p.clusters; // rows that may be in parts
     if (e == cudaSuccess)
-        e = (int64_t)a.B * a.H <= 8 * num_sms()
-                ? launch_pdl(dense_mla_join_kernel<1>, dim3(a.B, a.H), dim3(256), 0, stream, 1, p)
-                : launch_pdl(dense_mla_join_kernel<8>, dim3(a.B, (a.H + 7) / 8), dim3(256), 0, stream, 1, p);
+        e = joins * a.H <= 8 * num_sms()
+                ? launch_pdl(dense_mla_join_kernel<1>, dim3(joins, a.H), dim3(256), 0, stream, 1, p)
+                : launch_pdl(dense_mla_join_kernel<8>, dim3(joins, (a.H + 7) / 8), dim3(256), 0, stream, 1, p);
     if (e != cudaSuccess) {
         snprintf(err, errlen, "dense MLA launch: %s", cudaGetErrorString(e));
         return DSA_ERR_CUDA;

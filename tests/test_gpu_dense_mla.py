@@ -224,3 +224,18 @@ def test_batches_in_turn_share_a_workspace():
     for (o, l), got in zip(want, outs):
         for go, gl in got:
             assert torch.equal(go, o) and torch.equal(gl, l)
+
+
+@pytest.mark.parametrize("B", [74, 75, 76, 77, 150, 400])
+@pytest.mark.parametrize("H", [3, 100])
+def test_as_many_rows_as_clusters(B, H):
+    """Around the number of CTA pairs, where parts of rows are recorded by row or by pair: rows of one tile, of many and
+    none, over a workspace that holds anything."""
+    g = torch.Generator().manual_seed(B)
+    ctx = torch.randint(0, 140, (B,), generator=g)
+    ctx[torch.randint(0, B, (5,), generator=g)] = torch.tensor([3000, 1500, 129, 128, 700])
+    p = problem(ctx.tolist(), H, 64, B + H)
+    need = lib().dsa_mla_decode_workspace_size(B, H)
+    ws = torch.randint(0, 256, (need,), generator=torch.Generator(device=DEV).manual_seed(B), dtype=torch.uint8, device=DEV)
+    out, lse = call(*p, workspace=ws)
+    check(out, lse, *p)
