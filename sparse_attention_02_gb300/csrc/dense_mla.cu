@@ -125,6 +125,7 @@ struct Params {
     const int32_t *block_table, *ctx_len;
     int num_pages, page_size, max_pages, B, H, clusters;
     float scale_log2;
+    bool wide; // out starts at 32 bytes
     __nv_bfloat16 *out;
     float *lse;
     float *ws_o, *ws_lse; // [2 clusters, H, 512], [2 clusters, H]
@@ -294,6 +295,24 @@ __device__ __forceinline__ void umma_commit_pair(uint32_t bar)
                  : "memory");
 }
 
+// Whether a barrier's phase is over, without waiting for it.
+__device__ __forceinline__ bool mbar_done(uint32_t bar, uint32_t parity)
+{
+    uint32_t done;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(done)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
+    return done != 0;
+}
+
+__device__ __forceinline__ void store32(void *p, const uint32_t (&w)[8])
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t dst, uint32_t ncols)
 {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(ncols) : "memory");
@@ -424,18 +443,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (un.ctx == 0)
                 continue;
             pg.start(p, un, rank);
-            // Q is free once the previous unit's last score MMAs are done
-            if (u > 0 && !mbar_wait_warp(bar(B_SF + ((i - 1) & 1)), ((i - 1) >> 1) & 1, abort_flag, p.status)) {
-                ok = false;
-                break;
-            }
-            if (elect_one()) {
-                if (rank == 0)
-                    mbar_arrive_expect_tx(bar(B_QF), 2 * kStage);
-                load_atoms(sbase + OFF_Q, &tm_q, lead(B_QF), 0, 64 * (int)rank, un.row); // heads past H: zeros
-            }
-            __syncwarp();
-            ++u;
+            // Q is free once the previous unit's last score MMAs are done.  Until then the unit's first tile goes ahead
+            // of it: a row of one tile would otherwise wait for the row before it to load anything.
+            const uint32_t last = i - 1;
+            bool q_due = true;
+            auto load_q = [&] {
+                if (elect_one()) {
+                    if (rank == 0)
+                        mbar_arrive_expect_tx(bar(B_QF), 2 * kStage);
+                    load_atoms(sbase + OFF_Q, &tm_q, lead(B_QF), 0, 64 * (int)rank, un.row); // heads past H: zeros
+                }
+                __syncwarp();
+                q_due = false;
+            };
+            if (u == 0 || __all_sync(0xffffffffu, mbar_done(bar(B_SF + (last & 1)), (last >> 1) & 1)))
+                load_q();
             for (int j = un.jb; j < un.je; ++j, ++i) {
                 const int st = i & 1;
                 pg.advance(p, un, j);
@@ -463,6 +485,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 if (!ok)
                     break;
+                if (q_due) {
+                    if (!mbar_wait_warp(bar(B_SF + (last & 1)), (last >> 1) & 1, abort_flag, p.status)) {
+                        ok = false;
+                        break;
+                    }
+                    load_q();
+                }
                 // behind this tile's loads, the one after the next: the copy engine takes requests in order
                 if (j + kPrefetch < un.je) {
                     const int r0 = pg.get(j + kPrefetch, 0), r1 = pg.get(j + kPrefetch, 1);
@@ -475,6 +504,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     __syncwarp();
                 }
             }
+            ++u;
         }
     } else if (warp == 2) {
         // ------------------------------------------------------------ swaps
@@ -759,22 +789,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 tmem_ld_wait();
                 if (h >= p.H)
                     continue;
+                // a lane's columns are its own row's: 32 bytes a store fill whole sectors
                 if (un.slot < 0) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(p.out + orow * kDv + col0 + c);
+                    __nv_bfloat16 *dst = p.out + orow * kDv + col0 + c;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        uint32_t w[4];
+                    for (int e = 0; e < 2; ++e) {
+                        uint32_t w[8];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            w[k] = pack2(__uint_as_float(o[8 * e + 2 * k]) * inv, __uint_as_float(o[8 * e + 2 * k + 1]) * inv);
-                        dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
+                        for (int k = 0; k < 8; ++k)
+                            w[k] = pack2(__uint_as_float(o[16 * e + 2 * k]) * inv, __uint_as_float(o[16 * e + 2 * k + 1]) * inv);
+                        if (p.wide) {
+                            store32(dst + 16 * e, w);
+                        } else {
+                            reinterpret_cast<uint4 *>(dst)[2 * e] = make_uint4(w[0], w[1], w[2], w[3]);
+                            reinterpret_cast<uint4 *>(dst)[2 * e + 1] = make_uint4(w[4], w[5], w[6], w[7]);
+                        }
                     }
                 } else {
-                    float4 *dst = reinterpret_cast<float4 *>(p.ws_o + prow * kDv + col0 + c);
+                    float *dst = p.ws_o + prow * kDv + col0 + c;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        dst[e] = make_float4(__uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
-                                             __uint_as_float(o[4 * e + 2]) * inv, __uint_as_float(o[4 * e + 3]) * inv);
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t w[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            w[k] = __float_as_uint(__uint_as_float(o[8 * e + k]) * inv);
+                        store32(dst + 8 * e, w);
+                    }
                 }
             }
             tc_fence_before();
@@ -924,6 +964,7 @@ int launch_dense_mla(const DenseMlaArgs &a, cudaStream_t stream, char *err, size
     p.clusters = clusters();
     p.scale_log2 = a.sm_scale * 1.4426950408889634f;
     p.out = static_cast<__nv_bfloat16 *>(a.out);
+    p.wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
     p.lse = a.lse;
     const size_t parts = 2 * (size_t)p.clusters * a.H;
     uint8_t *ws = static_cast<uint8_t *>(a.workspace);
