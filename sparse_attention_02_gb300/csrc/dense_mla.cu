@@ -152,6 +152,7 @@ struct Share {
 
 struct Unit {
     int row, ctx, jb, je; // tiles [jb, je) of the row
+    int64_t left;         // tiles of the share behind it
     int slot;             // -1: the whole row
 };
 
@@ -170,6 +171,7 @@ struct Walk {
         u.je = left < n - tile ? tile + (int)left : n;
         u.slot = u.jb == 0 && u.je == n ? -1 : 2 * cid + (row != first);
         left -= u.je - u.jb;
+        u.left = left;
         ++row;
         tile = 0;
         return true;
@@ -601,13 +603,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         break;
                     }
                     tc_fence_after();
+                    const int64_t valid = (int64_t)un.ctx - (int64_t)j * kTile; // past these P is zero
 #pragma unroll
                     for (int kb = 0; kb < 2; ++kb) {
 #pragma unroll
                         for (int n = 0; n < 2; ++n)
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
-                                umma_f16_pair(tmem + TM_O + 128 * n, (kb ? pd1 : pd0 + so) + 2 * k,
+                                if (64 * kb + 16 * k < valid)
+                                    umma_f16_pair(tmem + TM_O + 128 * n, (kb ? pd1 : pd0 + so) + 2 * k,
                                               vd + so + (((4 * kb + 2 * n) * kAtom + 16 * 128 * k) >> 4), idesc,
                                               kb || k || j > un.jb);
                         umma_commit_pair(bar(B_E + 2 * st + kb));
@@ -639,11 +643,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const bool records = rank == 0 && threadIdx.x == 32 * kSoftWarp0, by_row = p.B < p.clusters;
         if (records && !by_row)
             p.splits[cid] = {-1, 0, 0, 0};
-        while (ok && it.next(p, cid, un)) {
+        bool have = it.next(p, cid, un);
+        if (have)
+            pg.start(p, un, kb);
+        Unit ahead; // the unit after this one, looked up while this one's last PV runs
+        Pages pg_ahead;
+        bool more = false;
+        auto look_ahead = [&] {
+            more = it.next(p, cid, ahead);
+            if (more)
+                pg_ahead.start(p, ahead, kb);
+        };
+        for (; ok && have; have = more, un = ahead, pg = pg_ahead) {
             float m = -INFINITY, l = 0.f;
             if (records && un.jb == 0) {
                 const int n = tiles_of(un.ctx);
-                const int64_t end = share->begin + (share->tiles - it.left - un.je) + n; // of the row
+                const int64_t end = share->begin + (share->tiles - un.left - un.je) + n; // of the row
                 if (un.slot >= 0)
                     p.splits[by_row ? un.row : cid] = {un.row, un.slot, (int)((end * share->clusters - 1) / share->total), 0};
                 else if (by_row)
@@ -659,9 +674,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     if (col0 == 0)
                         p.lse[orow] = -INFINITY;
                 }
+                look_ahead();
                 continue;
             }
-            pg.start(p, un, kb);
             for (int j = un.jb; j < un.je; ++j, ++i) {
                 const int st = i & 1;
                 pg.advance(p, un, j);
@@ -759,6 +774,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             if (!ok)
                 break;
+            look_ahead();
             // ---- the unit's output
             // the sums go where the next tile's maxima do: all four threads have read the ones before
             xmine[256 * (i & 1)] = l;
@@ -782,11 +798,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             ++u;
             const float inv = l == 0.f ? 0.f : 1.f / l; // a NaN key's l is NaN, and so its row
             tc_fence_after();
-#pragma unroll 2
+            uint32_t o0[32], o1[32];
+#pragma unroll
             for (int c = 0; c < 128; c += 32) {
-                uint32_t o[32];
-                tmem_ld32(tmem + lane_off + TM_O + 128 * part + c, o);
-                tmem_ld_wait();
+                uint32_t(&o)[32] = c & 32 ? o1 : o0;
+                if (!(c & 32)) {
+                    tmem_ld32(tmem + lane_off + TM_O + 128 * part + c, o0);
+                    tmem_ld32(tmem + lane_off + TM_O + 128 * part + c + 32, o1);
+                    tmem_ld_wait();
+                }
                 if (h >= p.H)
                     continue;
                 // a lane's columns are its own row's: 32 bytes a store fill whole sectors
