@@ -48,22 +48,25 @@
 // P is the one intermediate rounded to 16 bits: kind::f16 wants P in V's type.
 // The sum l is that of the unrounded values, in fp32.
 //
-// Work split.  The rows' tiles laid end to end are cut into one contiguous
-// share per CTA pair, computed on the device from ctx_len (the host never sees
-// the lengths).  A share that holds part of a row leaves that part, normalised,
-// with its LSE in the workspace, and a second kernel joins the parts.
+// Work split.  The rows' tiles (and their fixed cost, below) laid end to end are
+// cut into one contiguous share per CTA pair, computed on the device from ctx_len
+// (the host never sees the lengths).  A share that holds part of a row leaves that
+// part, normalised, with its LSE in the workspace, and a second kernel joins the
+// parts.
 //
-// Measured.  64 rows of 128 heads, 8192 to 65536 keys (2.73 GB): 473 us a call in
-// bursts (85 % of measured HBM, 74 % of measured BF16; kernel 460, join 10), 530
-// when calls follow one another for long, the power limit then holding the SM
-// clock near 1.5 GHz.  Without its loads the kernel takes 338 us, with every
+// Measured.  64 rows of 128 heads, 8192 to 65536 keys (2.73 GB): 457-486 us a call
+// in bursts (83-88 % of measured HBM, 72-76 % of measured BF16; the join 10 of
+// them), 543 when calls follow one another for long, the power limit then holding
+// the SM clock near 1.5 GHz.  Without its loads the kernel takes 338 us, with every
 // byte in L2 412: what is left is the chain of a tile (loads, scores, softmax, PV)
 // over the two stages that fit.  9 rows of 16 heads, 1 to 131072 keys, pages of 32:
-// 127 us (79 % of HBM).  One row of 1000 keys, 16 heads: 11.4 us.  Not kept: 64-key
-// tiles over four stages (480 and 555 us where this takes 473 and 530; 123 for the
-// ragged rows; the MMAs of N = 64 run at 78 % of the rate), no prefetch (528 where
-// one tile ahead took 496), two, three and four tiles ahead (504, 518, 557),
-// prefetches by a warp's own loads, a stage's pieces freed one by one.
+// 123 us (81 % of HBM).  One row of 1000 keys, 16 heads: 10.7 us.  Many short rows,
+// 200 of 1 to 500 keys, 16 heads: 30.7 us.  Not kept: 64-key tiles over four stages
+// (480 and 555 us where this took 473 and 530; 123 for the ragged rows; the MMAs of
+// N = 64 run at 78 % of the rate), no prefetch (528 where one tile ahead took 496),
+// two, three and four tiles ahead (504, 518, 557), prefetches by a warp's own loads
+// or of the next row's queries (27.7 for 26.4 at 200 rows of one tile), a stage's
+// pieces freed one by one.
 #include "common.cuh"
 #include "launch.h"
 

@@ -239,3 +239,25 @@ def test_as_many_rows_as_clusters(B, H):
     ws = torch.randint(0, 256, (need,), generator=torch.Generator(device=DEV).manual_seed(B), dtype=torch.uint8, device=DEV)
     out, lse = call(*p, workspace=ws)
     check(out, lse, *p)
+
+
+@pytest.mark.parametrize("ctx", [[300, 0, 9000, 64], [20000]])
+def test_tensors_that_start_at_16_bytes(ctx):
+    """q, the pool and out no multiple of 32 bytes: the same bits, and nothing beside out."""
+    q, pool, bt, lens = problem(ctx, 100, 64, 70)
+    want = call(q, pool, bt, lens)
+
+    def shifted(t, fill=0.0):
+        buf = torch.full((t.numel() + 16,), fill, dtype=t.dtype, device=DEV)
+        view = buf[8:8 + t.numel()].view(t.shape)
+        assert view.data_ptr() % 32 == 16
+        view.copy_(t)
+        return view, buf
+
+    out, buf = shifted(torch.empty((len(ctx), 100, 512), dtype=BF), 5.0)
+    lse = torch.empty((len(ctx), 100), device=DEV)
+    buf[:8] = 5.0
+    buf[-8:] = 5.0
+    lib().dsa_mla_decode_paged(shifted(q)[0], shifted(pool)[0], bt.to(DEV), lens.to(DEV), SCALE, out, lse)
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    assert (buf[:8] == 5.0).all() and (buf[-8:] == 5.0).all()
