@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(kAppendThreads, 8) cache_append_kernel(CacheAp
 // ------------------------------------------------------------------ queries
 // A CTA per token.  Everything a thread reads, of both parts, is in flight
 // before the token's position and angles are there.  Main part: eight threads a
-// head, 32 heads at a time.  Index part: four threads a head, thread r of them
+// head, 32 or 16 heads at a time.  Index part: four threads a head, thread r of them
 // with the chunks (8 columns) r and r + 4, which turn into each other, r + 8 and
 // r + 12; no value passes between threads but the token's amax.  HBM-bound: 37.2
 // us for 4096 tokens of 128 and 64 heads, 93 % of measured bandwidth; CTAs of one
@@ -253,7 +253,8 @@ __global__ void __launch_bounds__(kAppendThreads, 8) cache_append_kernel(CacheAp
 // ones with the next token in registers 40.5, pairs of chunks four lanes apart
 // turned by shuffles 42.9.  Up to a token per SM each part has a CTA of its own:
 // 2.5 us instead of 2.8 for 64 tokens, 2.8 and 2.9 for 152, 3.8 and 3.6 for 304.
-constexpr int kQueryThreads = 256;
+// THREADS: 256, or 128 where that many do for the heads of either part (four chunks
+// a thread at most): 4096 tokens of 64 and 32 heads 17.1 us, 23.5 with half of 256 idle.
 
 // Turns chunks a and b (columns 8 r ... and 32 + 8 r ...) into each other by the angles 8 r ... of cs; sign -1: back.
 __device__ __forceinline__ void turn_chunks(float (&a)[8], float (&b)[8], const float2 *cs, int r, float sign)
@@ -292,19 +293,19 @@ template <typename K> struct IndexRow { // a thread's part of a token's index qu
     }
 };
 
-template <typename K>
-__global__ void __launch_bounds__(kQueryThreads, 4) rope_queries_kernel(RopeQueriesArgs a, bool split)
+template <typename K, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) rope_queries_kernel(RopeQueriesArgs a, bool split)
 {
     __shared__ __align__(16) float2 cs[32];
-    __shared__ float red[kQueryThreads / 32];
+    __shared__ float red[THREADS / 32];
     grid_dep_wait();
     grid_dep_launch();
     const int t = split ? blockIdx.x >> 1 : blockIdx.x, tid = threadIdx.x;
     const bool main_part = a.q_rope && (!split || (blockIdx.x & 1)), index_part = a.qI && (!split || !(blockIdx.x & 1));
     const int pos = a.pos[t];
     const double freq = a.inv_freq[tid & 31];
-    // main: eight threads a head, 32 heads at a time
-    constexpr int kMost = 128 * 8 / kQueryThreads, kHeads = kQueryThreads / 8;
+    // main: eight threads a head, as many heads at a time as there are eights
+    constexpr int kMost = 4, kHeads = THREADS / 8;
     const int h0 = tid >> 3, p = tid & 7;
     uint4 v[kMost];
     if (main_part) {
@@ -365,7 +366,7 @@ __global__ void __launch_bounds__(kQueryThreads, 4) rope_queries_kernel(RopeQuer
     __syncthreads();
     m = red[0];
 #pragma unroll
-    for (int w = 1; w < kQueryThreads / 32; ++w)
+    for (int w = 1; w < THREADS / 32; ++w)
         m = fmaxf(m, red[w]);
     const float sc = fp8_scale(m, a.scale_mode);
     const ScaleDivider div(sc);
@@ -484,8 +485,16 @@ int launch_cache_append(const CacheAppendArgs &a, cudaStream_t stream, char *err
 int launch_rope_queries(const RopeQueriesArgs &a, cudaStream_t stream, char *err, size_t errlen)
 {
     const bool split = a.q_rope && a.qI && a.T <= num_sms();
-    auto go = [&](auto kernel) { return launch_pdl(kernel, dim3((unsigned)a.T * (split ? 2 : 1)), dim3(kQueryThreads), 0, stream, 1, a, split); };
-    return finish(a.i32 ? go(rope_queries_kernel<float>) : go(rope_queries_kernel<__nv_bfloat16>), "query rotation", err, errlen);
+    const bool few = (!a.q_rope || a.H <= 64) && (!a.qI || a.HI <= 32);
+    auto go = [&](auto kernel) {
+        return launch_pdl(kernel, dim3((unsigned)a.T * (split ? 2 : 1)), dim3(few ? 128 : 256), 0, stream, 1, a, split);
+    };
+    cudaError_t e;
+    if (a.i32)
+        e = few ? go(rope_queries_kernel<float, 128>) : go(rope_queries_kernel<float, 256>);
+    else
+        e = few ? go(rope_queries_kernel<__nv_bfloat16, 128>) : go(rope_queries_kernel<__nv_bfloat16, 256>);
+    return finish(e, "query rotation", err, errlen);
 }
 
 int launch_index_rope_backward(const IndexRopeBackwardArgs &a, cudaStream_t stream, char *err, size_t errlen)

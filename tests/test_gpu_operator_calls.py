@@ -265,3 +265,24 @@ def test_tensors_without_memory_are_refused():
         assert (out == 0).all()
         dsa.dsa_rmsnorm(x, w, 0.0, out=out)
         assert (out == 1).all()
+
+
+@pytest.mark.parametrize("H,HI", [(64, 32), (65, 32), (64, 33), (1, 1), (7, 31)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_queries_of_few_heads(H, HI, dtype):
+    """Around the heads that half the threads do for, against fp64."""
+    dsa = lib()
+    g = torch.Generator().manual_seed(H * HI)
+    T = 200
+    pos = torch.randint(0, 70000, (T,), generator=g).to(I32)
+    fr = R.inv_freq()
+    qr, qI = torch.randn((T, H, 64), generator=g).to(BF), torch.randn((T, HI, 128), generator=g).to(dtype)
+    q = torch.zeros((T, H, 576), dtype=BF, device=DEV)
+    q8, qs = torch.zeros((T, HI, 128), dtype=torch.uint8, device=DEV), torch.zeros(T, device=DEV)
+    dsa.dsa_rope_queries(pos.to(DEV), fr.to(DEV), qr.to(DEV), q, qI.to(DEV), q8, qs)
+    ref = R.rotate_main(R.d(qr), pos, fr)
+    mag = R.d(qr).abs().unflatten(-1, (32, 2)).sum(-1, keepdim=True).expand(T, H, 32, 2).flatten(-2)
+    R.check_close(q[:, :, 512:], ref, R.BF16 * ref.abs() + 8 * R.FP32 * mag, "main")
+    y = R.rotate_index(R.d(qI), pos, fr).flatten(1)
+    # a rotated value is off by 8 half steps of |a| + |b|, at most twice the pair's larger rotated magnitude and so the amax
+    R.check_fp8(q8.flatten(1), qs, y, 16 * R.FP32, 0, "index")
