@@ -39,8 +39,8 @@
 // Partials rounded to fp16 would halve the swap, but put an error of
 // ~|S| * 2^-11 on every score and hence on LSE.
 //
-// Per 64-key block j (double-buffered S buffers, one P buffer; prefill: two
-// swap buffers and three KV stages, decode: one and four):
+// Per 64-key block j (double-buffered S buffers, one P buffer, two swap buffers,
+// three KV stages):
 //   producer warps  four warps cp.async the 64 selected rows x 576 B into the
 //                   SW128 / SW64 K-major layouts (one 128-byte line per 8
 //                   lanes), zero-fill invalid entries, and arrive on the
@@ -107,14 +107,15 @@ constexpr float kRescaleLog2 = 8.f;      // move the running max only when excee
 
 constexpr int NBAR = 48;
 
-// Shared-memory layout.  Prefill: three KV stages and two swap buffers (the
-// peer's next block may land while this one's is read: 23.0 ms against 23.5 ms
-// with four stages and one buffer at L = 32768).  Decode: four stages and one
-// swap buffer (its rows come from HBM, so the deeper gather ring matters more:
-// 78 us against 85 us at B = 64).
-template <bool PAGED> struct Layout {
-    static constexpr int kNStage = PAGED ? 4 : 3;
-    static constexpr int kNX = PAGED ? 1 : 2;                // swap buffers, 32 KB each
+// Shared-memory layout: three KV stages and two swap buffers (the peer's next
+// block may land while this one's is read: 23.0 ms against 23.5 ms with four stages
+// and one buffer at L = 32768).  Decode had four stages and one buffer (its rows come
+// from HBM: 65.0 us against 69.8 at 64 rows), but with one buffer a call of many
+// short rows gave a wrong row now and then (3204 rows of up to 1250 keys, k = 256:
+// one call in ten, some heads of one row); with two, none in thousands.
+struct Layout {
+    static constexpr int kNStage = 3;
+    static constexpr int kNX = 2;                            // swap buffers, 32 KB each
     static constexpr int OFF_Q = 0;                          // two full Q atoms
     static constexpr int OFF_KV = OFF_Q + kQSmemAtoms * kQAtom;
     static constexpr int OFF_X = OFF_KV + kNStage * kStage;
@@ -275,7 +276,7 @@ template <bool PAGED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     sparse_mla_kernel(const __grid_constant__ CUtensorMap tm_q, Params p)
 {
-    using Lay = Layout<PAGED>;
+    using Lay = Layout;
     constexpr int kNStage = Lay::kNStage, kNX = Lay::kNX;
     constexpr int OFF_Q = Lay::OFF_Q, OFF_KV = Lay::OFF_KV, OFF_X = Lay::OFF_X, OFF_STG = Lay::OFF_STG,
                   OFF_BAR = Lay::OFF_BAR, OFF_MISC = Lay::OFF_MISC;
@@ -1177,7 +1178,7 @@ template <bool PAGED>
 int launch(const MlaArgs &a, cudaStream_t stream, char *err, size_t errlen)
 {
     static std::atomic<bool> attr_set[64];
-    constexpr int kSmem = Layout<PAGED>::kSmem;
+    constexpr int kSmem = Layout::kSmem;
     if (cudaError_t e_attr = raise_smem_limit_once(sparse_mla_kernel<PAGED>, kSmem, attr_set);
         e_attr != cudaSuccess) {
         snprintf(err, errlen, "cudaFuncSetAttribute(sparse_mla): %s", cudaGetErrorString(e_attr));
