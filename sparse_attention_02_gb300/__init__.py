@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 
 import numpy as np
 import torch
@@ -26,6 +27,8 @@ DSA_DEV_BAD_POSITION = 0x2
 DSA_DEV_BAD_PAGE = 0x4
 
 _lib = None
+_fast = None  # the native call path (csrc/fastcall.cpp), there whenever _lib is
+_load_lock = threading.Lock()
 
 
 class DsaError(RuntimeError):
@@ -36,10 +39,19 @@ class DsaError(RuntimeError):
 
 def load_library(path: str | None = None) -> ctypes.CDLL:
     """Load libdsa.so (built by ``sparse_attention_02_gb300.build``)."""
-    global _lib
-    if _lib is not None and path is None:
-        return _lib
-    p = path or LIB_PATH
+    global _lib, _fast
+    if path is not None:
+        return _open(path)
+    if _lib is None:
+        with _load_lock:  # a thread that comes meanwhile waits, and finds both or neither
+            if _lib is None:
+                lib = _open(LIB_PATH)
+                _fast = _load_fastcall(LIB_PATH)
+                _lib = lib
+    return _lib
+
+
+def _open(p: str) -> ctypes.CDLL:
     if not os.path.exists(p):
         raise RuntimeError(f"{p} is missing: build it with `python -m sparse_attention_02_gb300.build` "
                            "(or __graft_entry__.build()); there is no fallback path")
@@ -86,17 +98,10 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
                  "dsa_sparse_mla_decode_paged_noalloc", "dsa_prefill_host", "dsa_prefill_host_trace",
                  "dsa_prefill_host_trace_read", "dsa_get_device_status"):
         getattr(lib, name).restype = i32
-    if path is None:
-        _lib = lib
-        _load_fastcall(p)
     return lib
 
 
-_fast = None  # the native call path (csrc/fastcall.cpp), loaded with the library
-
-
 def _load_fastcall(path: str):
-    global _fast
     so = os.path.join(_HERE, "_fastcall.so")
     if not os.path.exists(so):
         raise RuntimeError(f"{so} is missing: build it with `python -m sparse_attention_02_gb300.build`")
@@ -104,7 +109,7 @@ def _load_fastcall(path: str):
 
     _fastcall.init(path, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream,
                    torch._C._cuda_cudaCachingAllocator_raw_alloc, torch._C._cuda_cudaCachingAllocator_raw_delete)
-    _fast = _fastcall
+    return _fastcall
 
 
 def _check(rc: int):
@@ -235,7 +240,7 @@ def _raw_stream(stream, cur: int) -> int:
 def _native(name: str, *args) -> bool:
     """Makes the call natively where its arguments are plainly right; False leaves it, and what is wrong with it, to
     the Python form."""
-    if _fast is None:
+    if _lib is None:
         load_library()
     rc = getattr(_fast, name)(*args)
     if rc is NotImplemented:

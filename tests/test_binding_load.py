@@ -1,0 +1,82 @@
+"""Loading the library: first calls from several threads, and what a failed load leaves behind (fresh processes, no GPU)."""
+import os
+import subprocess
+import sys
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+def fresh(code: str) -> str:
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr
+    return r.stdout.strip()
+
+
+def test_first_calls_from_several_threads():
+    """Every one of them finds the library whole, also one that comes while another is still loading the extension: the
+    refusal of its argument, and nothing else."""
+    out = fresh("""
+import threading, time
+import sparse_attention_02_gb300 as dsa
+load, loading, seen = dsa._load_fastcall, threading.Event(), []
+def slow(path):
+    loading.set()
+    time.sleep(0.5)
+    return load(path)
+dsa._load_fastcall = slow
+def first():
+    try:
+        dsa.dsa_rmsnorm(None, None, 1e-6)
+    except Exception as e:
+        seen.append(type(e).__name__ + ": " + str(e))
+threads = [threading.Thread(target=first) for _ in range(8)]
+threads[0].start()
+loading.wait()
+[t.start() for t in threads[1:]]
+[t.join() for t in threads]
+assert len(seen) == 8
+print("|".join(sorted(set(seen))))
+""")
+    assert out == "TypeError: x must be a torch.Tensor"
+
+
+def test_a_failed_load_is_told_every_time():
+    """A library that cannot be loaded is named by each call, and one that can be later is loaded then."""
+    out = fresh("""
+import sparse_attention_02_gb300 as dsa
+whole, dsa.LIB_PATH = dsa.LIB_PATH, dsa.LIB_PATH + ".none"
+for _ in range(2):
+    try:
+        dsa.dsa_rmsnorm(None, None, 1e-6)
+    except RuntimeError as e:
+        assert "is missing" in str(e)
+        print("missing")
+dsa.LIB_PATH = whole
+try:
+    dsa.dsa_rmsnorm(None, None, 1e-6)
+except TypeError as e:
+    print(e)
+""")
+    assert out.split("\n") == ["missing", "missing", "x must be a torch.Tensor"]
+
+
+def test_a_failed_extension_is_told_every_time():
+    """What goes wrong while the extension loads is not left for later calls to trip over."""
+    out = fresh("""
+import sparse_attention_02_gb300 as dsa
+load, seen = dsa._load_fastcall, []
+def broken(path):
+    raise OSError("cannot load it")
+dsa._load_fastcall = broken
+for _ in range(2):
+    try:
+        dsa.dsa_rmsnorm(None, None, 1e-6)
+    except Exception as e:
+        print(type(e).__name__, e)
+dsa._load_fastcall = load
+try:
+    dsa.dsa_rmsnorm(None, None, 1e-6)
+except TypeError as e:
+    print(e)
+""")
+    assert out.split("\n") == ["OSError cannot load it"] * 2 + ["x must be a torch.Tensor"]
