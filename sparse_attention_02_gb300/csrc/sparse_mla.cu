@@ -19,17 +19,16 @@
 //   partial-score tiles through distributed shared memory.  Both CTAs then
 //   add the same two halves in the same way, so they hold bit-identical
 //   scores, run the same softmax (identical P, m and l) and each applies P to
-//   its own V quarter.  Stages are 36 KB (three or four in flight); the last
+//   its own V quarter.  Stages are 36 KB (three in flight); the last
 //   160 of this CTA's Q columns live in TMEM (the score MMA reads them as a TMEM
 //   A operand), the first 128 in shared memory.
 
 // The swap carries the raw fp32 partial scores (32 KB per 64-key block).  The
 // sender warps stage them in shared memory and the copy engine moves them
 // (cp.async.bulk into the peer's shared memory, 2 KB per warp and 16-key
-// quarter, two staging slots per warp so staging overlaps the copies, one
-// arrival barrier per quarter so the add starts with the first): remote stores
-// issued by the warps themselves moved a third of that rate, the issue of 2048
-// 16-byte stores per block competing with the gathers.
+// quarter, one arrival barrier per quarter so the add starts with the first):
+// remote stores issued by the warps themselves moved a third of that rate, the
+// issue of 2048 16-byte stores per block competing with the gathers.
 // The softmax warps add the peer's partials to their own in fp32 and apply the
 // log2 softmax scale, (own + peer) * scale: the add commutes, so both CTAs hold
 // bit-identical scores whose error is that of the fp32 accumulation alone, a
@@ -39,8 +38,24 @@
 // Partials rounded to fp16 would halve the swap, but put an error of
 // ~|S| * 2^-11 on every score and hence on LSE.
 //
-// Per 64-key block j (double-buffered S buffers, one P buffer, two swap buffers,
-// three KV stages):
+// What orders the swap.  Such a copy is complete when it has counted its bytes on
+// the PEER's mbarrier; the sender's bulk async-groups do not cover it (those take
+// the copies that complete on groups, out of shared memory into global).  So a
+// staging slot has one use a block, and what frees it for the next block is what
+// frees its place in the swap buffer: the peer's softmax warps have read that half of
+// the block, which they could only once its copies were complete.  They say so by a
+// four-byte st.async, counted on the sender's mbarrier: it comes after the reads (which
+// __syncwarp orders in front of it), and its count is a release at cluster scope, which
+// the senders' wait acquires.  A plain arrival with a release at cluster scope says the
+// same and took 1500 cycles a block here (410 for the st.async, 305 for an arrival that
+// orders nothing): 83.1 us where decode now takes 69.3 (64 rows), 7.5 ms for 5.74 at
+// 8192 prefill rows.  With two slots a warp, each used twice a block behind
+// cp.async.bulk.wait_group, and relaxed arrivals, a slot could be staged anew before the
+// copy engine, busy with queries, had read it; calls of many short rows had wrong rows
+// now and then.
+//
+// Per 64-key block j (double-buffered S buffers, one P buffer, one swap buffer in
+// two halves, three KV stages):
 //   producer warps  four warps cp.async the 64 selected rows x 576 B into the
 //                   SW128 / SW64 K-major layouts (one 128-byte line per 8
 //                   lanes), zero-fill invalid entries, and arrive on the
@@ -61,7 +76,7 @@
 //                   16-key quarter at a time, and a bulk copy per quarter to
 //                   the peer (completion counted in bytes on the peer's
 //                   per-quarter mbarrier) as soon as the peer's softmax warps
-//                   have read the previous block's;
+//                   have read that half of the previous block;
 //   softmax warps   thread = head, two warps per TMEM lane quadrant, each with
 //                   32 of the block's keys: own partial from the S buffer
 //                   (then free for the next score MMAs once the senders have
@@ -107,33 +122,29 @@ constexpr float kRescaleLog2 = 8.f;      // move the running max only when excee
 
 constexpr int NBAR = 48;
 
-// Shared-memory layout: three KV stages and two swap buffers (the peer's next
-// block may land while this one's is read: 23.0 ms against 23.5 ms with four stages
-// and one buffer at L = 32768).  Decode had four stages and one buffer (its rows come
-// from HBM: 65.0 us against 69.8 at 64 rows), but with one buffer a call of many
-// short rows gave a wrong row now and then (3204 rows of up to 1250 keys, k = 256:
-// one call in ten, some heads of one row); with two, none in thousands.
+// Shared-memory layout: three KV stages, the swap buffer and as much staging.
 struct Layout {
     static constexpr int kNStage = 3;
-    static constexpr int kNX = 2;                            // swap buffers, 32 KB each
     static constexpr int OFF_Q = 0;                          // two full Q atoms
     static constexpr int OFF_KV = OFF_Q + kQSmemAtoms * kQAtom;
     static constexpr int OFF_X = OFF_KV + kNStage * kStage;
-    static constexpr int OFF_STG = OFF_X + kNX * kXBuf;      // two 16-key quarters of this CTA's partials, staged
-    static constexpr int OFF_BAR = OFF_STG + kXBuf / 2;
+    static constexpr int OFF_STG = OFF_X + kXBuf;            // a block of this CTA's partials, staged
+    static constexpr int OFF_BAR = OFF_STG + kXBuf;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
     static constexpr int kSmem = OFF_MISC + 64 + 1024;
     static_assert(kSmem <= 232448, "dynamic shared memory above the 227 KB a CTA may hold");
 };
 
 // barrier slots
-// [J & 1] for S buffers, [J % kNX] for swap buffers, [J % kNP] for P buffers
+// [J & 1] for S buffers, [J % kNP] for P buffers
 constexpr int kNP = 1; // P buffers in TMEM (one: its TMEM columns hold a Q atom instead)
-constexpr int B_KVF = 0, B_KVE = 4, B_SF = 8, B_SE = 10, B_XE = 14, B_PF = 16, B_PE = 18,
+constexpr int B_KVF = 0, B_KVE = 4, B_SF = 8, B_SE = 10,
+              B_XE = 14, // [half]: the peer's softmax warps have read this CTA's partials of keys [32 half, + 32)
+              B_PF = 16, B_PE = 18,
               B_QF = 22, B_QE = 23, B_QA = 24, B_OF = 25, B_OE = 26, B_DONE = 27,
               B_RB = 28,  // [quad][parity]: sibling softmax warps swapped their block max
               B_RL = 36,  // [quad]: sibling softmax warps swapped their row sums
-              B_XQ = 40;  // [xb][q]: the peer's partials of keys [16 q, 16 q + 16) landed in swap buffer xb
+              B_XQ = 40;  // [q]: the peer's partials of keys [16 q, 16 q + 16) landed
 
 // TMEM columns
 constexpr uint32_t TM_O = 0;
@@ -269,15 +280,13 @@ __device__ __forceinline__ void bulk_s2cluster(uint32_t dst_cluster, uint32_t sr
                  "r"(src_cta), "r"(bytes), "r"(bar_cluster)
                  : "memory");
 }
-__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait_read1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
 
 template <bool PAGED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     sparse_mla_kernel(const __grid_constant__ CUtensorMap tm_q, Params p)
 {
     using Lay = Layout;
-    constexpr int kNStage = Lay::kNStage, kNX = Lay::kNX;
+    constexpr int kNStage = Lay::kNStage;
     constexpr int OFF_Q = Lay::OFF_Q, OFF_KV = Lay::OFF_KV, OFF_X = Lay::OFF_X, OFF_STG = Lay::OFF_STG,
                   OFF_BAR = Lay::OFF_BAR, OFF_MISC = Lay::OFF_MISC;
     extern __shared__ uint8_t smem_raw[];
@@ -304,17 +313,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(B_SF + i), 1);
             mbar_init(bar(B_SE + i), kSoftWarps + kSendWarps);
-        }
-        for (int i = 0; i < kNX; ++i) {
-            mbar_init(bar(B_XE + i), kSoftWarps); // the peer's softmax warps have read its contents
+            mbar_init(bar(B_XE + i), 1);
+            mbar_arrive_expect_tx(bar(B_XE + i), kSoftWarps / 2 * 4); // armed for block 0
         }
         for (int i = 0; i < kNP; ++i) {
             mbar_init(bar(B_PF + i), kSoftWarps);
             mbar_init(bar(B_PE + i), 1);
         }
-        for (int i = 0; i < 4 * kNX; ++i) {
+        for (int i = 0; i < 4; ++i) {
             mbar_init(bar(B_XQ + i), 1);
-            mbar_arrive_expect_tx(bar(B_XQ + i), kXBuf / 4); // armed for blocks 0 .. kNX - 1
+            mbar_arrive_expect_tx(bar(B_XQ + i), kXBuf / 4); // armed for block 0
         }
         mbar_init(bar(B_QF), 1 + kProdWarps); // the Q TMA (expect_tx) + each producer's TMEM part
         mbar_init(bar(B_QE), 2);
@@ -414,6 +422,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 ok = false;
                 break;
             }
+            tc_fence_after();
             if (pw == 0) {
                 if (u >= 1 && !mbar_wait_warp(bar(B_QA), (u - 1) & 1, abort_flag, p.status)) {
                     ok = false;
@@ -711,23 +720,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // Thread = head (TMEM lane), all 64 keys of each block.  The block's 64
         // partial-score columns are read first (two TMEM loads, one wait), which
         // frees the S buffer, then go to the peer one 16-key quarter at a time:
-        // staged in shared memory (two slots per warp), then a bulk copy of the
+        // staged in shared memory (a slot each per warp), then a bulk copy of the
         // warp's 32 head rows (completion counted in bytes on the peer's
         // per-quarter mbarrier, which the peer's softmax warps wait on and
-        // re-arm).  The next block's copies wait until the peer's softmax warps
+        // re-arm).  A half of the next block waits until the peer's softmax warps
         // have read this one's.  Per-warp handshakes per quarter measured slower (the waits
         // inside the copy loop cost more than the coupling they remove).
         const int quad = warp & 3;
         const int h = quad * 32 + lane;
         const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
-        const uint32_t xe_remote0 = mapa_shared(bar(B_XE), peer);
         // swap buffer: four quarters of 16 keys
         // ([q][head][16 fp32], 64-byte rows, chunk c of head h's row at c ^ ((h >> 1) & 3): eight
-        // consecutive heads storing or reading the same chunk hit eight different banks; staging: two
+        // consecutive heads storing or reading the same chunk hit eight different banks; staging: four
         // 2 KB slots per warp, one quarter of its 32 head rows each)
         const uint32_t qsw = static_cast<uint32_t>((h >> 1) & 3);
-        uint8_t *stg_row = smem + OFF_STG + quad * 4096 + lane * 64;
-        const uint32_t stg_q = sbase + OFF_STG + quad * 4096;
+        uint8_t *stg_row = smem + OFF_STG + quad * 8192 + lane * 64;
+        const uint32_t stg_q = sbase + OFF_STG + quad * 8192;
         const uint32_t x_remote_q = mapa_shared(sbase + OFF_X + quad * 32 * 64, peer);
         const uint32_t xq_remote0 = mapa_shared(bar(B_XQ), peer);
         uint32_t J = 0;
@@ -746,12 +754,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 mbar_arrive(bar(B_QA)); // this token's nb slot has been read
             for (int j = 0; j < nb; ++j, ++J) {
                 const int b = J & 1;
-                const int xb = J % kNX;
                 const uint32_t s_cols = tmem + lane_off + TM_S + 64 * b;
-                // the peer's swap buffer xb must be free (its softmax warps have read block J - kNX)
-                if (!mbar_wait_warp(bar(B_SF + b), (J >> 1) & 1, abort_flag, p.status) ||
-                    (J >= kNX &&
-                     !mbar_wait_warp<true>(bar(B_XE + xb), ((J / kNX) - 1) & 1, abort_flag, p.status))) {
+                if (!mbar_wait_warp(bar(B_SF + b), (J >> 1) & 1, abort_flag, p.status)) {
                     ok = false;
                     break;
                 }
@@ -766,11 +770,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     mbar_arrive(bar(B_SE + b)); // this warp has read the block's partials
 #pragma unroll
                 for (int qq = 0; qq < 4; ++qq) {
-                    // slot qq & 1 is free once the copy issued two quarters ago has read it
-                    if (lane == 0)
-                        bulk_wait_read1();
-                    __syncwarp();
-                    uint8_t *srow = stg_row + (qq & 1) * 2048;
+                    // the peer's softmax warps have read the half of block J - 1: its copies are complete, so their
+                    // slots here are free as well as their places there
+                    if ((qq & 1) == 0 && J >= 1) {
+                        if (!mbar_wait_warp<true>(bar(B_XE + (qq >> 1)), (J - 1) & 1, abort_flag, p.status)) {
+                            ok = false;
+                            break;
+                        }
+                        if (quad == 0 && lane == 0) // armed for this block's
+                            mbar_arrive_expect_tx(bar(B_XE + (qq >> 1)), kSoftWarps / 2 * 4);
+                    }
+                    uint8_t *srow = stg_row + qq * 2048;
 #pragma unroll
                     for (int cc = 0; cc < 4; ++cc) {
                         const int e = 16 * (qq & 1) + 4 * cc;
@@ -780,17 +790,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                     fence_proxy_async_smem(); // the copy engine reads what the generic stores wrote
                     __syncwarp();
-                    if (lane == 0) {
-                        // this warp's 32 head rows of the quarter (2 KB, contiguous in both buffers)
-                        bulk_s2cluster(x_remote_q + xb * kXBuf + qq * (kXBuf / 4), stg_q + (qq & 1) * 2048, 32 * 64,
-                                       xq_remote0 + 8u * (4 * xb + qq));
-                        bulk_commit();
-                    }
+                    if (lane == 0) // this warp's 32 head rows of the quarter (2 KB, contiguous in both buffers)
+                        bulk_s2cluster(x_remote_q + qq * (kXBuf / 4), stg_q + qq * 2048, 32 * 64, xq_remote0 + 8u * qq);
                 }
+                if (!ok)
+                    break;
             }
         }
-        if (lane == 0)
-            asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); // this warp's copies are complete
+        if (ok && J >= 1) // the last hand-backs are stores into this CTA, which must outlive them
+            for (int half = 0; half < 2; ++half)
+                mbar_wait_warp<true>(bar(B_XE + half), (J - 1) & 1, abort_flag, p.status);
         __syncwarp();
     } else {
         // ------------------------------------------------ softmax + epilogue
@@ -803,9 +812,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int h = quad * 32 + lane;                  // head = TMEM lane
         const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
         const uint32_t red = tmem + lane_off + TM_RED;
+        const uint32_t xe_remote = mapa_shared(bar(B_XE + hf), peer);
+        const uint32_t unread_remote = mapa_shared(sbase + OFF_MISC + 32 + 4 * sw, peer); // the word is of no use
         const uint8_t *xq_row = smem + OFF_X + h * 64;
         const uint32_t xqsw = static_cast<uint32_t>((h >> 1) & 3);
-        const uint32_t xe_remote_sm = mapa_shared(bar(B_XE), peer);
         uint32_t J = 0;
         int u = 0, v = 0;
         bool ok = true;
@@ -880,18 +890,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     mbar_arrive(bar(B_SE + b));
                 // the peer's partials of this warp's two quarters, each added as it lands:
                 // (own + peer) * scale in fp32 (the add commutes: both CTAs hold the same bits)
-                const int xb = J % kNX;
                 bool got = true;
 #pragma unroll
                 for (int qh = 0; qh < 2; ++qh) {
-                    if (!mbar_wait_warp<true>(bar(B_XQ + 4 * xb + 2 * hf + qh), (J / kNX) & 1, abort_flag, p.status)) {
+                    if (!mbar_wait_warp<true>(bar(B_XQ + 2 * hf + qh), J & 1, abort_flag, p.status)) {
                         got = false;
                         break;
                     }
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         const float4 pv = *reinterpret_cast<const float4 *>(
-                            xq_row + xb * kXBuf + (2 * hf + qh) * (kXBuf / 4) + ((static_cast<uint32_t>(c) ^ xqsw) << 4));
+                            xq_row + (2 * hf + qh) * (kXBuf / 4) + ((static_cast<uint32_t>(c) ^ xqsw) << 4));
                         const int e0 = 16 * qh + 4 * c;
                         sc[e0] = (sc[e0] + pv.x) * p.scale_log2;
                         sc[e0 + 1] = (sc[e0 + 1] + pv.y) * p.scale_log2;
@@ -905,10 +914,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp(); // every lane has read its rows of the two quarters
                 if (lane == 0) {
-                    if (quad == 0) // both quarters' phases of block J are complete: arm them for block J + kNX
+                    if (quad == 0) // both quarters' phases of block J are complete: arm them for block J + 1
                         for (int q = 2 * hf; q < 2 * hf + 2; ++q)
-                            mbar_arrive_expect_tx(bar(B_XQ + 4 * xb + q), kXBuf / 4);
-                    mbar_arrive_remote_relaxed(xe_remote_sm + 8u * xb); // the peer may send into buffer xb again
+                            mbar_arrive_expect_tx(bar(B_XQ + q), kXBuf / 4);
+                    st_async_b32(unread_remote, 0u, xe_remote); // the peer may send it again
                 }
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -1067,6 +1076,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
     }
 
+    // Every copy and store to the peer was waited for there.  After a wait that gave up in either CTA some may be in
+    // flight: a millisecond is far longer than any takes.
+    __syncwarp();
+    if (*abort_flag) {
+        st_cluster_u32(mapa_shared(sbase + OFF_MISC + 4, peer), 1u);
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < 1000000ull) {
+        }
+    }
     tc_fence_before();
     __syncthreads();
     cluster_sync_all(); // no CTA leaves while its peer may still touch its smem
