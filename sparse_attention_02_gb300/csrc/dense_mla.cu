@@ -97,10 +97,12 @@ constexpr int OFF_X = OFF_P1 + kAtom;             // per-thread maxima (two buff
 constexpr int OFF_BAR = OFF_X + 2 * 256 * 4;
 constexpr int NBAR = 36;
 constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
-constexpr int kSmem = OFF_MISC + 64;
+constexpr int OFF_UNREAD = OFF_MISC + 64;         // where st.async leaves its words
+constexpr int kSmem = OFF_UNREAD + 4 * kSoftWarps;
 static_assert(kSmem <= 232448, "dynamic shared memory above the 227 KB a CTA may hold");
 
-// barriers (L: used in the leader CTA only; both CTAs' roles arrive there)
+// barriers (L: used in the leader CTA only; both CTAs' roles arrive there).  What the other CTA's threads, loads or MMAs
+// signal is waited for with an acquire at cluster scope (all but VL, RB, RL and DONE: 0.3 % of a call).
 constexpr int B_KF = 0,  // L [stage][group]: both CTAs' atoms landed
               B_E = 8,   // [stage][half]: PV of the tile's first / second 64 keys done
               B_SF = 12, // [buffer]: scores done
@@ -267,12 +269,18 @@ __device__ __forceinline__ bool elect_one()
     return r != 0;
 }
 
-// Arrive on a barrier of either CTA of the pair, releasing at CTA scope: what
-// it announces lies in this CTA's shared or tensor memory.  A release at cluster
-// scope waits for more than that and took most of a tile's time.
-__device__ __forceinline__ void arrive_pair(uint32_t cluster_bar)
+// One softmax warp's arrival on a barrier of the leader CTA, which counts kSoftWarps arrivals of its own warps, one of
+// them expecting kSoftWarps * 4 bytes (`arms`), and those bytes from CTA 1's.  What CTA 1 announces (P, value rows, O in its
+// shared and tensor memory) the leader's MMA threads act on, so it takes a release at cluster scope: a four-byte
+// st.async carries one without keeping the warp, where a plain arrival with it took most of a tile's time.
+__device__ __forceinline__ void arrive_leader(uint32_t rank, uint32_t bar, uint32_t lead_bar, uint32_t lead_unread, bool arms)
 {
-    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+    if (rank)
+        st_async_b32(lead_unread, 0u, lead_bar);
+    else if (arms)
+        mbar_arrive_expect_tx(bar, kSoftWarps * 4);
+    else
+        mbar_arrive(bar);
 }
 
 // Atoms of 64 columns (block, block + 1, ... as the map's box has) of consecutive rows into this CTA's shared memory.
@@ -312,7 +320,7 @@ __device__ __forceinline__ void umma_commit_pair(uint32_t bar)
 __device__ __forceinline__ bool mbar_done(uint32_t bar, uint32_t parity)
 {
     uint32_t done;
-    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
                  : "=r"(done)
                  : "r"(bar), "r"(parity)
                  : "memory");
@@ -365,10 +373,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_init(bar(B_SF + i), 1);
             mbar_init(bar(B_QD + i), 1);
             mbar_init(bar(B_VL + i), 1);
-            mbar_init(bar(B_P + i), 2 * kSoftWarps);
+            mbar_init(bar(B_P + i), kSoftWarps);
         }
         mbar_init(bar(B_OF), 1);
-        mbar_init(bar(B_OE), 2 * kSoftWarps);
+        mbar_init(bar(B_OE), kSoftWarps);
         mbar_init(bar(B_QF), 1);
         mbar_init(bar(B_DONE), 2);
         *abort_flag = 0;
@@ -490,7 +498,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 for (int g = 0; g < kGroups; ++g) {
                     // atoms 0-3 hold the value columns of the first 64 keys, 4-7 of the second
                     if ((g & 1) == 0 && i >= 2 &&
-                        !mbar_wait_warp(bar(B_E + 2 * st + (g >> 1)), ((i >> 1) - 1) & 1, abort_flag, p.status)) {
+                        !mbar_wait_warp<true>(bar(B_E + 2 * st + (g >> 1)), ((i >> 1) - 1) & 1, abort_flag, p.status)) {
                         ok = false;
                         break;
                     }
@@ -509,7 +517,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (!ok)
                     break;
                 if (q_due) {
-                    if (!mbar_wait_warp(bar(B_SF + (last & 1)), (last >> 1) & 1, abort_flag, p.status)) {
+                    if (!mbar_wait_warp<true>(bar(B_SF + (last & 1)), (last >> 1) & 1, abort_flag, p.status)) {
                         ok = false;
                         break;
                     }
@@ -546,7 +554,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 pg.advance(p, un, j);
                 const int r[2] = {pg.get(j, 0), pg.get(j, 1)};
                 // CTA 1 gives up atoms 0-3, done with after the first group of score MMAs; CTA 0 atoms 4-7
-                if (!mbar_wait_warp(bar((rank ? B_QD : B_SF) + st), (i >> 1) & 1, abort_flag, p.status)) {
+                if (!mbar_wait_warp<true>(bar((rank ? B_QD : B_SF) + st), (i >> 1) & 1, abort_flag, p.status)) {
                     ok = false;
                     break;
                 }
@@ -575,13 +583,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             uint32_t t = 0;
             bool ok = true;
             for (int u = 0; ok && it.next_filled(p, cid, un); ++u) {
-                ok = mbar_wait(bar(B_QF), u & 1, abort_flag, p.status);
+                ok = mbar_wait<true>(bar(B_QF), u & 1, abort_flag, p.status);
                 for (int j = un.jb; ok && j < un.je; ++j, ++t) {
                     const int st = t & 1;
                     const uint64_t so = (uint64_t)((st * kStage) >> 4);
 #pragma unroll
                     for (int g = 0; g < kGroups; ++g) {
-                        if (!mbar_wait(bar(B_KF + kGroups * st + g), (t >> 1) & 1, abort_flag, p.status)) {
+                        if (!mbar_wait<true>(bar(B_KF + kGroups * st + g), (t >> 1) & 1, abort_flag, p.status)) {
                             ok = false;
                             break;
                         }
@@ -613,13 +621,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             Unit un;
             uint32_t t = 0;
             bool ok = true;
-            for (int u = 0; ok && it.next_filled(p, cid, un); ++u) {
+            int u = 0;
+            for (; ok && it.next_filled(p, cid, un); ++u) {
                 // a unit's first PV overwrites O: the previous unit's must have been read
-                ok = u == 0 || mbar_wait(bar(B_OE), (u - 1) & 1, abort_flag, p.status);
+                ok = u == 0 || mbar_wait<true>(bar(B_OE), (u - 1) & 1, abort_flag, p.status);
                 for (int j = un.jb; ok && j < un.je; ++j, ++t) {
                     const int st = t & 1;
                     const uint64_t so = (uint64_t)((st * kStage) >> 4);
-                    if (!mbar_wait(bar(B_P + st), (t >> 1) & 1, abort_flag, p.status)) {
+                    if (!mbar_wait<true>(bar(B_P + st), (t >> 1) & 1, abort_flag, p.status)) {
                         ok = false;
                         break;
                     }
@@ -641,6 +650,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         umma_commit_pair(bar(B_OF));
                 }
             }
+            if (ok && u > 0) // the last words from CTA 1 are stores into this CTA, which must outlive them
+                mbar_wait<true>(bar(B_OE), (u - 1) & 1, abort_flag, p.status);
             umma_commit_pair(bar(B_DONE));
             mbar_drain(bar(B_DONE), 0);
         }
@@ -654,6 +665,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t lane_off = (uint32_t)(32 * quad) << 16;
         const bool swapped = kb != (int)rank; // this CTA's value columns of key block kb are swapped in
         float *xrow = xs + hl * 4, *xmine = xrow + 2 * kb + part;
+        const uint32_t lead_unread = mapa_shared(sbase + OFF_UNREAD + 4 * (warp - kSoftWarp0), 0);
         uint32_t i = 0;
         int u = 0;
         bool ok = true;
@@ -704,7 +716,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const int64_t left = (int64_t)un.ctx - (int64_t)j * kTile - 64 * kb - 32 * part;
                 // heads past H have Q = 0; P = 0 too costs the MMAs the least power
                 const int valid = bad || left < 0 || h >= p.H ? 0 : left < 32 ? (int)left : 32;
-                if (!mbar_wait_warp(bar(B_SF + st), (i >> 1) & 1, abort_flag, p.status)) {
+                if (!mbar_wait_warp<true>(bar(B_SF + st), (i >> 1) & 1, abort_flag, p.status)) {
                     ok = false;
                     break;
                 }
@@ -738,7 +750,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const bool rescale = !first && __any_sync(0xffffffffu, move);
                 // PV of the previous tile: before O is touched, and before P's second buffer is
                 if ((rescale || (kb == 1 && i > 0)) &&
-                    !mbar_wait_warp(bar(B_E + 2 * (st ^ 1) + 1), ((i - 1) >> 1) & 1, abort_flag, p.status)) {
+                    !mbar_wait_warp<true>(bar(B_E + 2 * (st ^ 1) + 1), ((i - 1) >> 1) & 1, abort_flag, p.status)) {
                     ok = false;
                     break;
                 }
@@ -790,7 +802,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0)
-                    arrive_pair(lead(B_P + st));
+                    arrive_leader(rank, bar(B_P + st), lead(B_P + st), lead_unread, warp == kSoftWarp0);
             }
             if (!ok)
                 break;
@@ -811,7 +823,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (lane == 0)
                 mbar_arrive(bar(B_RL + 2 * pair + 1)); // read
             if (!mbar_wait_warp(bar(B_RL + 2 * pair + 1), u & 1, abort_flag, p.status) ||
-                !mbar_wait_warp(bar(B_OF), u & 1, abort_flag, p.status)) {
+                !mbar_wait_warp<true>(bar(B_OF), u & 1, abort_flag, p.status)) {
                 ok = false;
                 break;
             }
@@ -860,7 +872,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0)
-                arrive_pair(lead(B_OE));
+                arrive_leader(rank, bar(B_OE), lead(B_OE), lead_unread, warp == kSoftWarp0);
             if (h < p.H && col0 == 0) {
                 const float v = l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
                 if (un.slot < 0)
@@ -871,10 +883,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
     }
 
-    // After a wait that gave up, copies may be in flight whose barrier is the other CTA's: a millisecond is far longer
-    // than any takes.
+    // After a wait that gave up in either CTA, copies may be in flight whose barrier is the other's: a millisecond is
+    // far longer than any takes.
     __syncwarp();
     if (*abort_flag) {
+        st_cluster_u32(mapa_shared(sbase + OFF_MISC + 4, rank ^ 1), 1u);
         const uint64_t t0 = global_timer_ns();
         while (global_timer_ns() - t0 < 1000000ull) {
         }

@@ -41,3 +41,11 @@ def test_bulk_groups_wait_for_copies_that_join_them(name):
 def test_no_relaxed_arrivals(name):
     """An arrival tells another thread that reads or writes are done: it releases them."""
     assert not [a for a in asm_strings(name) if re.search(r"mbarrier\.arrive[a-z_.]*\.relaxed", a)]
+
+
+@pytest.mark.parametrize("name", SOURCES)
+def test_arrivals_in_another_cta_release_at_cluster_scope(name):
+    """Scope says which threads synchronise, not where the data lies: an arrival that another CTA's threads act on releases
+    at cluster scope (so do the counts of asynchronous copies and stores), whatever it announces."""
+    remote = [a for a in asm_strings(name) if re.search(r"mbarrier\.arrive[a-z_.:]*shared::cluster", a)]
+    assert all(".release.cluster" in a for a in remote)
