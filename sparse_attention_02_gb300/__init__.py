@@ -14,6 +14,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+import warnings
 
 import numpy as np
 import torch
@@ -27,7 +28,7 @@ DSA_DEV_BAD_POSITION = 0x2
 DSA_DEV_BAD_PAGE = 0x4
 
 _lib = None
-_fast = None  # the native call path (csrc/fastcall.cpp), there whenever _lib is
+_fast = None  # the native call path (csrc/fastcall.cpp), set before _lib; None where it cannot be used
 _load_lock = threading.Lock()
 
 
@@ -102,13 +103,17 @@ def _open(p: str) -> ctypes.CDLL:
 
 
 def _load_fastcall(path: str):
-    so = os.path.join(_HERE, "_fastcall.so")
-    if not os.path.exists(so):
-        raise RuntimeError(f"{so} is missing: build it with `python -m sparse_attention_02_gb300.build`")
-    from . import _fastcall
+    """The native call path, or None where it was not built or PyTorch lacks what it calls: the Python form of every
+    call makes the same library calls, at 5 to 15 us more host time each."""
+    try:
+        from . import _fastcall
 
-    _fastcall.init(path, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream,
-                   torch._C._cuda_cudaCachingAllocator_raw_alloc, torch._C._cuda_cudaCachingAllocator_raw_delete)
+        _fastcall.init(path, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream,
+                       torch._C._cuda_cudaCachingAllocator_raw_alloc, torch._C._cuda_cudaCachingAllocator_raw_delete)
+    except (ImportError, AttributeError) as e:
+        warnings.warn(f"the native call path is not used ({e}): calls on few tokens take the host longer; "
+                      "`python -m sparse_attention_02_gb300.build` builds it", RuntimeWarning, stacklevel=3)
+        return None
     return _fastcall
 
 
@@ -242,6 +247,8 @@ def _native(name: str, *args) -> bool:
     the Python form."""
     if _lib is None:
         load_library()
+    if _fast is None:
+        return False
     rc = getattr(_fast, name)(*args)
     if rc is NotImplemented:
         return False

@@ -3,8 +3,9 @@
 Each translation unit under csrc/ compiles in parallel to an object file, then
 one link step makes ``sparse_attention_02_gb300/libdsa.so``; the host compiler
 makes ``_fastcall.so``, the native part of the Python binding.  Run as a script
-or call ``build()``.  Only the CUDA toolkit and, for the binding, a C++ compiler,
-Python's headers and PyTorch's are needed (torch itself is not imported; no cmake).
+or call ``build()``.  The library needs the CUDA toolkit alone (no cmake).  The
+extension takes a C++ compiler, Python's headers and PyTorch's (torch itself is not
+imported); without the headers it is left out, and the binding does without it.
 """
 from __future__ import annotations
 
@@ -15,6 +16,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -59,6 +61,11 @@ def _build_fastcall():
     if torch is None:  # no binding without it; the library stands alone
         return
     root = list(torch.submodule_search_locations)[0]
+    for need in (os.path.join(sysconfig.get_paths()["include"], "Python.h"),
+                 os.path.join(root, "include", "torch", "csrc", "autograd", "python_variable.h")):
+        if not os.path.exists(need):
+            warnings.warn(f"{need} is missing: _fastcall.so is not built", RuntimeWarning)
+            return
     deps = [src, hdr, os.path.join(root, "version.py")]
     if os.path.exists(FAST) and os.path.getmtime(FAST) >= max(os.path.getmtime(d) for d in deps):
         return

@@ -3,6 +3,8 @@ import os
 import subprocess
 import sys
 
+import pytest
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
@@ -80,3 +82,34 @@ except TypeError as e:
     print(e)
 """)
     assert out.split("\n") == ["OSError cannot load it"] * 2 + ["x must be a torch.Tensor"]
+
+
+def test_without_the_extension_calls_take_the_python_form():
+    """libdsa.so alone serves every entry point; that the extension is missing is said once."""
+    out = fresh("""
+import sys, warnings
+sys.modules["sparse_attention_02_gb300._fastcall"] = None  # its import fails
+import sparse_attention_02_gb300 as dsa
+with warnings.catch_warnings(record=True) as seen:
+    warnings.simplefilter("always")
+    for call in (lambda: dsa.dsa_rmsnorm(None, None, 1e-6), lambda: dsa.dsa_index_rope_backward(None, None, None, None),
+                 lambda: dsa.dsa_quantize_fp8(None, None, None)):
+        try:
+            call()
+        except (TypeError, ValueError, AttributeError) as e:
+            print(type(e).__name__)
+    print(dsa.dsa_mla_decode_workspace_size(2, 16) > 0, dsa.dsa_rmsnorm_backward_workspace_size(4, 64) > 0)
+print([str(w.message).split(" (")[0] for w in seen])
+""")
+    lines = out.split("\n")
+    assert lines[:2] == ["TypeError", "TypeError"] and lines[3:] == ["True True", "['the native call path is not used']"]
+
+
+def test_without_headers_the_extension_is_left_out(monkeypatch, tmp_path):
+    from sparse_attention_02_gb300 import build
+
+    monkeypatch.setattr(build, "FAST", str(tmp_path / "_fastcall.so"))
+    monkeypatch.setattr(build.sysconfig, "get_paths", lambda: {"include": str(tmp_path)})
+    with pytest.warns(RuntimeWarning, match="Python.h is missing"):
+        build._build_fastcall()
+    assert not os.listdir(tmp_path)
