@@ -103,9 +103,14 @@ def _open(p: str) -> ctypes.CDLL:
 
 
 def _load_fastcall(path: str):
-    """The native call path, or None where it was not built or PyTorch lacks what it calls: the Python form of every
-    call makes the same library calls, at 5 to 15 us more host time each."""
+    """The native call path, or None where it was not built for this interpreter and PyTorch (it reads tensors by
+    PyTorch's C++ classes) or PyTorch lacks what it calls: the Python form of every call makes the same library calls, at 5
+    to 15 us more host time each."""
+    from .build import fastcall_abi, fastcall_built_for
+
     try:
+        if fastcall_built_for() != fastcall_abi():  # before its import: another PyTorch's would read the wrong fields
+            raise ImportError("_fastcall.so is not there, or was built for another Python or PyTorch")
         from . import _fastcall
 
         _fastcall.init(path, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream,

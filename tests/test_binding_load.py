@@ -113,3 +113,50 @@ def test_without_headers_the_extension_is_left_out(monkeypatch, tmp_path):
     with pytest.warns(RuntimeWarning, match="Python.h is missing"):
         build._build_fastcall()
     assert not os.listdir(tmp_path)
+
+
+def test_an_extension_for_another_pytorch_is_not_loaded():
+    """It is known by what stands beside it, without importing it."""
+    out = fresh("""
+import sys, warnings
+import sparse_attention_02_gb300 as dsa
+from sparse_attention_02_gb300 import build
+assert build.fastcall_built_for() == build.fastcall_abi()
+build.fastcall_abi = lambda: "another"
+with warnings.catch_warnings(record=True) as seen:
+    warnings.simplefilter("always")
+    dsa.load_library()
+print(dsa._fast, "sparse_attention_02_gb300._fastcall" in sys.modules, len(seen))
+""")
+    assert out == "None False 1"
+
+
+def test_the_extension_is_built_anew_for_another_interpreter_pytorch_or_compiler(monkeypatch, tmp_path):
+    """Whatever its files' times say: a PyTorch that was put back is older than the extension built for the other."""
+    from sparse_attention_02_gb300 import build
+
+    built = []
+
+    def run(cmd, **kw):
+        built.append(cmd[0])
+        open(cmd[cmd.index("-o") + 1], "w").close()
+        return subprocess.CompletedProcess(cmd, 0, "", "")
+
+    monkeypatch.setattr(build, "FAST", str(tmp_path / "_fastcall.so"))
+    monkeypatch.setattr(build, "FAST_KEY", str(tmp_path / "_fastcall.key"))
+    monkeypatch.setattr(build.subprocess, "run", run)
+    monkeypatch.setenv("CXX", "one")
+    for _ in range(2):
+        build._build_fastcall()
+    assert built == ["one"]
+    monkeypatch.setenv("CXX", "two")
+    build._build_fastcall()
+    assert built == ["one", "two"]
+    was = build.fastcall_abi()
+    monkeypatch.setattr(build, "fastcall_abi", lambda: "another")
+    for _ in range(2):
+        build._build_fastcall()
+    assert built == ["one", "two", "two"] and build.fastcall_built_for() == "another" != was
+    os.remove(tmp_path / "_fastcall.key")  # a build that was cut short
+    build._build_fastcall()
+    assert len(built) == 4 and sorted(os.listdir(tmp_path)) == ["_fastcall.key", "_fastcall.so"]
