@@ -175,7 +175,8 @@ int dsa_quantize_fp8(const float *x, int64_t rows, int64_t cols, int scale_mode,
  * three not all.  residual_out may be residual or x itself, and out may be x; no
  * other overlap of an output with another tensor.
  * 1 <= cols <= 16384; rows = 0 is a no-op; eps >= 0 (a row of zeros with eps = 0
- * has no norm: NaN).  Inputs must be finite.  Any alignment of whole elements
+ * has no norm: NaN).  Inputs must be finite, and a row's squares add up within
+ * fp32's range (below 3.4e38; where they do not, y is 0).  Any alignment of whole elements
  * works; 16-byte aligned rows, with cols a multiple of 8, take the vector path.
  * All sums are fp32 in an order fixed by sizes and alignment: results repeat bit
  * for bit on one kind of device.

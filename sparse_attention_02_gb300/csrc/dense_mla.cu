@@ -56,12 +56,12 @@
 //
 // Measured.  64 rows of 128 heads, 8192 to 65536 keys (2.73 GB): 457-486 us a call
 // in bursts (83-88 % of measured HBM, 72-76 % of measured BF16; the join 10 of
-// them), 543 when calls follow one another for long, the power limit then holding
+// them), 542-551 when calls follow one another for long, the power limit then holding
 // the SM clock near 1.5 GHz.  Without its loads the kernel takes 338 us, with every
 // byte in L2 412: what is left is the chain of a tile (loads, scores, softmax, PV)
 // over the two stages that fit.  9 rows of 16 heads, 1 to 131072 keys, pages of 32:
-// 123 us (81 % of HBM).  One row of 1000 keys, 16 heads: 10.7 us.  Many short rows,
-// 200 of 1 to 500 keys, 16 heads: 30.7 us.  Not kept: 64-key tiles over four stages
+// 125 us (80 % of HBM).  One row of 1000 keys, 16 heads: 11.8 us.  Many short rows,
+// 200 of 1 to 500 keys, 16 heads: 30.2 us.  Not kept: 64-key tiles over four stages
 // (480 and 555 us where this took 473 and 530; 123 for the ragged rows; the MMAs of
 // N = 64 run at 78 % of the rate), no prefetch (528 where one tile ahead took 496),
 // two, three and four tiles ahead (504, 518, 557), prefetches by a warp's own loads

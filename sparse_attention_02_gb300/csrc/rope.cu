@@ -19,8 +19,9 @@
 // and cosine.  The same product in fp64 cost five fp64 operations an angle, on
 // a GPU with 1/64 of its fp32 rate.
 //
-// All three kernels move each byte once and are HBM-bound (or, for a decode
-// step, bound by launch and load latency).
+// All three kernels move each byte once.  The queries and the index rotation's
+// backward are HBM-bound, the append by load latency and issue, and a decode step
+// of any by launch and load latency.
 #include "common.cuh"
 #include "f32x2.cuh"
 #include "fp8.cuh"
@@ -110,9 +111,10 @@ __device__ __forceinline__ float warp_amax(float m)
 // 64 + 2l and 65 + 2l: it computes the one angle that both its pairs turn by, and
 // no lane needs another's.  One wave of warps, each with its next token's row in
 // registers; the norm in pairs of fp32, the page size as a shift, quotients by
-// reciprocals.  32768 tokens with norm and both caches: 17.2 us, 76 % of measured
-// HBM; 65536 31.2, 131072 59.7, so a token more takes what its bytes do (93 %) and
-// the rest is 3.5 us of filling and draining.  With rotated chunks of 8 columns
+// reciprocals.  32768 tokens with norm and both caches: 17.2 us, its bytes at 76 % of
+// measured HBM's rate, though they come out of L2 (DRAM at 33 %, 64 % of issue slots,
+// loads the top stall); 65536 31.2, 131072 59.7, so a token more takes what its bytes
+// would from HBM (93 %) and the rest is 3.5 us of filling and draining.  With rotated chunks of 8 columns
 // and angles handed around, instructions bounded it: 22 us.  Pages looked up a
 // token ahead, more or fewer warps: no faster.
 constexpr int kAppendThreads = 128;
