@@ -115,7 +115,7 @@ def _load_fastcall(path: str):
 
         _fastcall.init(path, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream,
                        torch._C._cuda_cudaCachingAllocator_raw_alloc, torch._C._cuda_cudaCachingAllocator_raw_delete)
-    except (ImportError, AttributeError) as e:
+    except (ImportError, AttributeError, OSError) as e:  # OSError: a PyTorch without the file that names its version
         warnings.warn(f"the native call path is not used ({e}): calls on few tokens take the host longer; "
                       "`python -m sparse_attention_02_gb300.build` builds it", RuntimeWarning, stacklevel=3)
         return None

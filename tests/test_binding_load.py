@@ -160,3 +160,17 @@ def test_the_extension_is_built_anew_for_another_interpreter_pytorch_or_compiler
     os.remove(tmp_path / "_fastcall.key")  # a build that was cut short
     build._build_fastcall()
     assert len(built) == 4 and sorted(os.listdir(tmp_path)) == ["_fastcall.key", "_fastcall.so"]
+
+
+def test_a_pytorch_that_does_not_say_its_version_leaves_the_python_form():
+    out = fresh("""
+import warnings
+import sparse_attention_02_gb300 as dsa
+from sparse_attention_02_gb300 import build
+build._torch_root = lambda: "/nowhere"
+with warnings.catch_warnings(record=True) as seen:
+    warnings.simplefilter("always")
+    dsa.load_library()
+print(dsa._fast, len(seen))
+""")
+    assert out == "None 1"
