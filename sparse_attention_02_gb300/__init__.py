@@ -104,8 +104,8 @@ def _open(p: str) -> ctypes.CDLL:
 
 def _load_fastcall(path: str):
     """The native call path, or None where it was not built for this interpreter and PyTorch (it reads tensors by
-    PyTorch's C++ classes) or PyTorch lacks what it calls: the Python form of every call makes the same library calls, at 5
-    to 15 us more host time each."""
+    PyTorch's C++ classes) or PyTorch lacks what it calls: the Python form of every call makes the same library calls, at 6
+    to 12 us more host time each (one-row norm 6.1 and 12.5 us, dense decode of one row 6.2 and 17.6)."""
     from .build import fastcall_abi, fastcall_built_for
 
     try:
