@@ -214,6 +214,95 @@ int dsa_rmsnorm_backward(const void *dy, const void *h, const void *weight, cons
 size_t dsa_rmsnorm_backward_workspace_size(int64_t rows, int cols);
 
 /*
+ * dsa_quantize_fp8_blocks: FP8 operands for dsa_gemm_fp8, from activations,
+ * gradients or weights ("AMD Instinct MI355X GPUs Power DeepSeek-V3.2-Exp",
+ * section "DeepSeek Sparse Attention (DSA)", item 1, for the FP8 arithmetic;
+ * scales per 128 values have no counterpart on the pages).  Writes x [rows,
+ * cols] and/or its transpose as E4M3 codes:
+ *   codes   [rows, cols], scale per 1 x 128 piece of a row (block_rows = 1:
+ *           scale [rows, ceil(cols / 128)]) or per 128 x 128 block (block_rows =
+ *           128: scale [ceil(rows / 128), ceil(cols / 128)])
+ *   codes_t [cols, rows], the same of x transposed: scale_t [cols, ceil(rows /
+ *           128)] or [ceil(cols / 128), ceil(rows / 128)]
+ * with scale = amax / 448 over the piece or block (the last ones may be short),
+ * or the power of two of dsa_quantize_fp8's scale_mode, 1 for zeros, and code =
+ * E4M3 nearest to x / scale (fp32 division, ties to even, saturated).
+ *
+ *   x        bf16 or fp32 (`dtype`), rows ldx elements apart (>= cols)
+ *   codes, codes_t  uint8, rows ld_codes (>= cols) and ld_codes_t (>= rows) apart;
+ *            dsa_gemm_fp8 wants them multiples of 16; what lies between rows is
+ *            left alone
+ * codes (with scale) or codes_t (with scale_t) may be NULL.  rows >= 0 (0 is a
+ * no-op), cols >= 1.  Inputs must be finite.  Any alignment of whole elements works; x
+ * with rows at 16 bytes, codes at 8 and codes_t at 16 take the vector path.
+ * The outputs overlap neither x nor one another.
+ */
+int dsa_quantize_fp8_blocks(const void *x, int64_t ldx, int64_t rows, int64_t cols, int dtype,
+                            int block_rows, int scale_mode, void *codes, int64_t ld_codes, float *scale,
+                            void *codes_t, int64_t ld_codes_t, float *scale_t, dsa_stream_t stream);
+
+/*
+ * dsa_gemm_fp8: product of FP8 operands with a scale for every 128 values along
+ * the summed axis: a projection of tokens (a: dsa_rmsnorm's or dsa_layernorm's
+ * codes with block = 128) by weights, or a product of its backward (operands from
+ * dsa_quantize_fp8_blocks).  Same page, section and item as there.
+ *     out[m, n] = sum_p a_scale[m, p] b_scale[n', p] sum_{k in [128 p, 128 p + 128)} a[m, k] b[n, k]
+ * with n' = n / 128 (b_block_rows = 128: b scaled per 128 x 128 block, as weights
+ * are) or n (b_block_rows = 1: per row, for a weight's gradient, where K runs
+ * over the tokens).  Both operands lie along K: y = x W^T takes W [N, K] as stored,
+ * dx = dy W takes the transpose's codes, dW = dy^T x both transposes'.
+ *
+ *   a [M, K], b [N, K]  E4M3 codes, rows lda and ldb bytes apart
+ *   a_scale [M, ceil(K / 128)], b_scale [N or ceil(N / 128), ceil(K / 128)] fp32
+ *   out [M, N] bf16 or fp32 (`out_dtype`), rows ldo elements apart
+ * 0 <= M, N, K <= 2^30 (M or N = 0 is a no-op, K = 0 writes zeros); a and b
+ * 16-byte aligned, lda >= K and ldb >= K multiples of 16 (that of a single or empty row is not
+ * looked at); out overlaps no input.  Codes behind K in a row are never used.
+ *
+ * Precision: the products of a piece are summed in fp32 by the tensor cores; the
+ * pieces' sums are scaled and added in fp32, in an order fixed by the sizes and
+ * the device: results repeat bit for bit.  A NaN code (or scale) makes NaN of its row's or column's
+ * outputs and no others.
+ */
+int dsa_gemm_fp8(const void *a, int64_t lda, const float *a_scale, const void *b, int64_t ldb,
+                 const float *b_scale, int b_block_rows, int M, int N, int K,
+                 void *out, int64_t ldo, int out_dtype, dsa_stream_t stream);
+
+/*
+ * dsa_layernorm: residual addition, layer norm and FP8 output: the norm of the
+ * indexer's keys in front of dsa_cache_append, or of hidden states (no
+ * counterpart on the pages).  For each row r, in fp32,
+ *     h = x + residual (x when residual is NULL)
+ *     y = (h - mean_c(h)) / sqrt(mean_c((h - mean)^2) + eps) * weight + bias
+ * Tensors, types, strides, outputs, limits, aliasing and the FP8 form of y are those of
+ * dsa_rmsnorm; bias [cols] is of `weight_dtype`, or NULL for none.  A row of
+ * equal values with eps = 0 has no norm (NaN).  The variance is taken about the mean,
+ * so a large common offset costs no more than its own rounding.
+ */
+int dsa_layernorm(const void *x, int64_t ldx, const void *residual, int64_t ldr, const void *weight, const void *bias,
+                  int64_t rows, int cols, int dtype, int weight_dtype, float eps,
+                  void *residual_out, int64_t ldh, void *out, int64_t ldo,
+                  void *codes, float *scale, int block, int scale_mode, dsa_stream_t stream);
+
+/*
+ * dsa_layernorm_backward: gradients of dsa_layernorm (the FP8 output passes
+ * gradients straight through).  With h the saved residual_out (x where there was
+ * no residual), xhat the normed row before weight and bias, g = dy * weight:
+ *     dx = (g - mean_c(g) - xhat mean_c(g xhat)) / sqrt(var + eps) + dres
+ *     dweight[c] = sum over rows of dy xhat,  dbias[c] = sum over rows of dy
+ * Arguments as for dsa_rmsnorm_backward; dbias [cols] fp32, overwritten, or NULL.
+ *   workspace: dsa_layernorm_backward_workspace_size(rows, cols) bytes, 16-byte
+ *   aligned, as there.
+ */
+int dsa_layernorm_backward(const void *dy, const void *h, const void *weight, const void *dres,
+                           int64_t rows, int cols, int dtype, int weight_dtype, float eps,
+                           void *dx, float *dweight, float *dbias, void *workspace, size_t workspace_bytes,
+                           dsa_stream_t stream);
+
+/* Bytes of workspace dsa_layernorm_backward needs on the current device (0 on bad input). */
+size_t dsa_layernorm_backward_workspace_size(int64_t rows, int cols);
+
+/*
  * dsa_cache_append: writes new tokens into the paged caches that the paged
  * entry points read, applying the position rotation on the way ("DeepSeek-
  * V3.2-Exp: Boosting Long-Context Efficiency with DeepSeek Sparse Attention",

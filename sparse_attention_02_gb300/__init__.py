@@ -86,14 +86,20 @@ def _open(p: str) -> ctypes.CDLL:
     lib.dsa_rmsnorm_backward.argtypes = [P, P, P, P, i64, i32, i32, i32, f32, P, P, P, sz, P]
     lib.dsa_rmsnorm_backward_workspace_size.restype = sz
     lib.dsa_rmsnorm_backward_workspace_size.argtypes = [i64, i32]
+    lib.dsa_quantize_fp8_blocks.argtypes = [P, i64, i64, i64, i32, i32, i32, P, i64, P, P, i64, P, P]
+    lib.dsa_gemm_fp8.argtypes = [P, i64, P, P, i64, P, i32, i32, i32, i32, P, i64, i32, P]
+    lib.dsa_layernorm.argtypes = [P, i64, P, i64, P, P, i64, i32, i32, i32, f32, P, i64, P, i64, P, P, i32, i32, P]
+    lib.dsa_layernorm_backward.argtypes = [P, P, P, P, i64, i32, i32, i32, f32, P, P, P, P, sz, P]
+    lib.dsa_layernorm_backward_workspace_size.restype = sz
+    lib.dsa_layernorm_backward_workspace_size.argtypes = [i64, i32]
     lib.dsa_cache_append.argtypes = [P, P, i32, P, i32, i32, i32, i32, P, P, i64, P, i32, f32, P, P, i64, i32, i32, P, P, P]
     lib.dsa_rope_queries.argtypes = [P, P, i32, P, i64, i64, i32, P, P, i32, i32, i32, P, P, P]
     lib.dsa_index_rope_backward.argtypes = [P, P, P, i32, i32, P, i32, P]
     lib.dsa_mla_decode_paged.argtypes = [P, P, i32, i32, P, i32, P, i32, i32, f32, P, P, P, sz, P]
     lib.dsa_mla_decode_workspace_size.restype = sz
     lib.dsa_mla_decode_workspace_size.argtypes = [i32, i32]
-    for name in ("dsa_rmsnorm", "dsa_rmsnorm_backward", "dsa_cache_append", "dsa_rope_queries",
-                 "dsa_index_rope_backward", "dsa_mla_decode_paged", "dsa_quantize_fp8", "dsa_indexer_logits", "dsa_topk", "dsa_indexer_topk", "dsa_indexer_warmup",
+    for name in ("dsa_quantize_fp8_blocks", "dsa_gemm_fp8", "dsa_layernorm", "dsa_layernorm_backward", "dsa_rmsnorm", "dsa_rmsnorm_backward",
+                 "dsa_cache_append", "dsa_rope_queries", "dsa_index_rope_backward", "dsa_mla_decode_paged", "dsa_quantize_fp8", "dsa_indexer_logits", "dsa_topk", "dsa_indexer_topk", "dsa_indexer_warmup",
                  "dsa_sparse_mla_prefill",
                  "dsa_sparse_mla_decode_paged",
                  "dsa_sparse_mla_decode_paged_noalloc", "dsa_prefill_host", "dsa_prefill_host_trace",
@@ -393,6 +399,124 @@ def dsa_rmsnorm_backward(dy, h, weight, eps: float, dx, dweight, dres=None, work
     _check(lib.dsa_rmsnorm_backward(a_dy, a_h, a_w, a_e, rows, cols, _DTYPE[t], _DTYPE[wt], float(eps), a_dx, a_dw, ws, ws_bytes,
                                     _raw_stream(stream, cur)))
     return dx, dweight
+
+
+def dsa_layernorm(x, weight, bias, eps: float, out=None, residual=None, residual_out=None, codes=None, scale=None,
+                  block: int = 0, scale_mode: int = DSA_SCALE_AMAX, stream=None):
+    """h = x + residual; y = (h - mean(h)) / sqrt(var(h) + eps) * weight + bias, over the rows of x [rows, cols] (bf16 or
+    fp32).  bias [cols] is of weight's type, or None; the other arguments are dsa_rmsnorm's.  Returns (residual_out, out,
+    codes, scale) as given."""
+    if _native("layernorm", x, weight, bias, eps, out, residual, residual_out, codes, scale, block, scale_mode, stream):
+        return residual_out, out, codes, scale
+    t = _dtype_of(x, "x")
+    if x.dim() != 2:
+        raise TypeError("x must be 2-D")
+    cur, shape, f32 = _device(), x.shape, torch.float32
+    rows, cols = shape
+    wt = _dtype_of(weight, "weight")
+    a_x, ldx = _at_rows(x, cur, "x", t, shape)
+    a_r = a_h = a_o = a_c = a_s = a_b = None
+    ldr = ldh = ldo = 0
+    if bias is not None:
+        a_b = _at(bias, cur, "bias", wt, (cols,))
+    if residual is not None:
+        a_r, ldr = _at_rows(residual, cur, "residual", t, shape)
+    if residual_out is not None:
+        a_h, ldh = _at_rows(residual_out, cur, "residual_out", t, shape)
+    if out is not None:
+        a_o, ldo = _at_rows(out, cur, "out", t, shape)
+    if codes is not None:
+        a_c = _at(codes, cur, "codes", torch.uint8, shape)
+    if scale is not None:
+        n = -(-cols // block) if block > 0 else 1
+        a_s = _at(scale, cur, "scale", f32, (rows,) if n == 1 and isinstance(scale, torch.Tensor) and scale.dim() == 1 else (rows, n))
+    _check((_lib or load_library()).dsa_layernorm(
+        a_x, ldx, a_r, ldr, _at(weight, cur, "weight", wt, (cols,)), a_b, rows, cols, _DTYPE[t], _DTYPE[wt], float(eps), a_h, ldh, a_o,
+        ldo, a_c, a_s, block, scale_mode, _raw_stream(stream, cur)))
+    return residual_out, out, codes, scale
+
+
+def dsa_layernorm_backward_workspace_size(rows: int, cols: int) -> int:
+    return int(load_library().dsa_layernorm_backward_workspace_size(rows, cols))
+
+
+def dsa_layernorm_backward(dy, h, weight, eps: float, dx, dweight, dbias=None, dres=None, workspace=None, stream=None):
+    """Gradients of dsa_layernorm: dy, h, dres (or None) and dx [rows, cols] bf16 or fp32, h the saved residual_out
+    (x without a residual); dx is the gradient of x and of the residual; dweight and dbias (or None) fp32 [cols].
+    ``workspace``: a CUDA tensor of at least dsa_layernorm_backward_workspace_size(rows, cols) bytes; taken from PyTorch
+    when None."""
+    if _native("layernorm_backward", dy, h, weight, eps, dx, dweight, dbias, dres, workspace, stream):
+        return dx, dweight, dbias
+    t = _dtype_of(h, "h")
+    if h.dim() != 2:
+        raise TypeError("h must be 2-D")
+    cur, shape, wt = _device(), h.shape, _dtype_of(weight, "weight")
+    rows, cols = shape
+    lib = _lib or load_library()
+    a_dy, a_h, a_w = _at(dy, cur, "dy", t, shape), _at(h, cur, "h", t, shape), _at(weight, cur, "weight", wt, (cols,))
+    a_e = None if dres is None else _at(dres, cur, "dres", t, shape)
+    a_dx, a_dw = _at(dx, cur, "dx", t, shape), _at(dweight, cur, "dweight", torch.float32, (cols,))
+    a_db = None if dbias is None else _at(dbias, cur, "dbias", torch.float32, (cols,))
+    need = 0 if workspace is not None else lib.dsa_layernorm_backward_workspace_size(rows, cols)
+    ws, ws_bytes, keep = _workspace(workspace, need, cur, stream)
+    _check(lib.dsa_layernorm_backward(a_dy, a_h, a_w, a_e, rows, cols, _DTYPE[t], _DTYPE[wt], float(eps), a_dx, a_dw, a_db, ws, ws_bytes,
+                                      _raw_stream(stream, cur)))
+    return dx, dweight, dbias
+
+
+def dsa_quantize_fp8_blocks(x, codes=None, scale=None, codes_t=None, scale_t=None, block_rows: int = 1,
+                            scale_mode: int = DSA_SCALE_AMAX, stream=None):
+    """FP8 operands of dsa_gemm_fp8 from x [rows, cols] (bf16 or fp32, rows may be strided): codes uint8 [rows, cols] (E4M3)
+    with scale fp32 [rows, ceil(cols / 128)] (block_rows = 1) or [ceil(rows / 128), ceil(cols / 128)] (block_rows = 128),
+    and/or the same of x transposed: codes_t uint8 [cols, rows] with scale_t [cols, ceil(rows / 128)] or [ceil(cols / 128),
+    ceil(rows / 128)].  Rows of codes and codes_t may be strided: dsa_gemm_fp8 wants them at multiples of 16 bytes.
+    Returns (codes, scale, codes_t, scale_t) as given."""
+    if _native("quantize_fp8_blocks", x, codes, scale, codes_t, scale_t, block_rows, scale_mode, stream):
+        return codes, scale, codes_t, scale_t
+    t = _dtype_of(x, "x")
+    if x.dim() != 2:
+        raise TypeError("x must be 2-D")
+    if block_rows not in (1, 128):
+        raise ValueError("block_rows must be 1 or 128")
+    cur, (rows, cols), u8, f32 = _device(), x.shape, torch.uint8, torch.float32
+    a_x, ldx = _at_rows(x, cur, "x", t, (rows, cols))
+    a_c = a_s = a_t = a_ts = None
+    ldc = ldt = 0
+    if codes is not None:
+        a_c, ldc = _at_rows(codes, cur, "codes", u8, (rows, cols))
+    if scale is not None:
+        a_s = _at(scale, cur, "scale", f32, (-(-rows // block_rows), -(-cols // 128)))
+    if codes_t is not None:
+        a_t, ldt = _at_rows(codes_t, cur, "codes_t", u8, (cols, rows))
+    if scale_t is not None:
+        a_ts = _at(scale_t, cur, "scale_t", f32, (-(-cols // block_rows), -(-rows // 128)))
+    _check((_lib or load_library()).dsa_quantize_fp8_blocks(a_x, ldx, rows, cols, _DTYPE[t], block_rows, scale_mode, a_c, ldc, a_s, a_t, ldt,
+                                                            a_ts, _raw_stream(stream, cur)))
+    return codes, scale, codes_t, scale_t
+
+
+def dsa_gemm_fp8(a, a_scale, b, b_scale, out, stream=None):
+    """out[m, n] = sum over pieces p of 128 along K of a_scale[m, p] b_scale[n', p] (a[m, p] . b[n, p]).
+
+    a uint8 [M, K] and b uint8 [N, K]: E4M3 codes, rows at multiples of 16 bytes (may be strided); a_scale fp32 [M,
+    ceil(K / 128)]; b_scale fp32 [ceil(N / 128), ceil(K / 128)] (per 128 x 128 block, n' = n / 128: weights) or [N, ceil(K / 128)]
+    (n' = n: a weight's gradient, K the tokens); out bf16 or fp32 [M, N], rows may be strided."""
+    if _native("gemm_fp8", a, a_scale, b, b_scale, out, stream):
+        return out
+    u8, f32 = torch.uint8, torch.float32
+    for t, name in ((a, "a"), (b, "b"), (b_scale, "b_scale")):
+        if not isinstance(t, torch.Tensor) or t.dim() != 2:
+            raise TypeError(f"{name} must be a 2-D torch.Tensor")
+    cur, (M, K), N, t = _device(), a.shape, b.shape[0], _dtype_of(out, "out")
+    pieces, blocks = -(-K // 128), -(-N // 128)
+    a_a, lda = _at_rows(a, cur, "a", u8, (M, K))
+    a_b, ldb = _at_rows(b, cur, "b", u8, (N, K))
+    rows = blocks if b_scale.shape[0] == blocks else N
+    a_o, ldo = _at_rows(out, cur, "out", t, (M, N))
+    _check((_lib or load_library()).dsa_gemm_fp8(
+        a_a, lda, _at(a_scale, cur, "a_scale", f32, (M, pieces)), a_b, ldb, _at(b_scale, cur, "b_scale", f32, (rows, pieces)),
+        128 if rows == blocks else 1, M, N, K, a_o, ldo, _DTYPE[t], _raw_stream(stream, cur)))
+    return out
 
 
 def dsa_cache_append(pos, block_table, inv_freq, kv=None, kv_pool=None, kI=None, k8_pool=None, ks_pool=None, seq=None,

@@ -319,10 +319,14 @@ bool too_large(int64_t rows, int64_t ld) { return rows > (int64_t(1) << 40) / ld
 
 } // namespace
 
-int dsa_rmsnorm(const void *x, int64_t ldx, const void *residual, int64_t ldr, const void *weight, int64_t rows, int cols,
-                int dtype, int weight_dtype, float eps, void *residual_out, int64_t ldh, void *out, int64_t ldo, void *codes,
-                float *scale, int block, int scale_mode, dsa_stream_t stream)
+namespace {
+
+// The argument checks of both norms: DSA_OK with *none set where there is nothing to do.
+int check_norm(const void *x, int64_t ldx, const void *residual, int64_t ldr, const void *weight, const void *bias, int64_t rows, int cols,
+               int dtype, int weight_dtype, float eps, const void *residual_out, int64_t ldh, const void *out, int64_t ldo,
+               const void *codes, const float *scale, int block, int scale_mode, bool *none)
 {
+    *none = rows == 0;
     if (rows < 0 || cols < 1)
         return fail(DSA_ERR_INVALID_ARG, "rows must be >= 0 and cols >= 1");
     if (cols > kNormMaxCols)
@@ -336,7 +340,7 @@ int dsa_rmsnorm(const void *x, int64_t ldx, const void *residual, int64_t ldr, c
     if (block != 0 && block != 128)
         return fail(DSA_ERR_INVALID_ARG, "block must be 0 (one scale per row) or 128");
     if (rows == 0)
-        return ok();
+        return DSA_OK;
     if (!x || !weight)
         return fail(DSA_ERR_INVALID_ARG, "null pointer argument");
     if ((codes == nullptr) != (scale == nullptr))
@@ -349,24 +353,14 @@ int dsa_rmsnorm(const void *x, int64_t ldx, const void *residual, int64_t ldr, c
         (residual_out && too_large(rows, ldh)) || (out && too_large(rows, ldo)))
         return fail(DSA_ERR_UNSUPPORTED, "rows too large");
     if (!aligned_to(dtype == DSA_FP32 ? 4 : 2, {x, residual, residual_out, out}) ||
-        !aligned_to(weight_dtype == DSA_FP32 ? 4 : 2, {weight}) || !aligned_to(4, {scale}))
+        !aligned_to(weight_dtype == DSA_FP32 ? 4 : 2, {weight, bias}) || !aligned_to(4, {scale}))
         return fail(DSA_ERR_ALIGNMENT, "tensors must be aligned to their elements");
-    RmsNormArgs a{x, residual, weight, rows, cols, ldx, ldr, ldh, ldo, dtype == DSA_FP32, weight_dtype == DSA_FP32, eps,
-                  residual_out, out, static_cast<uint8_t *>(codes), scale, block, scale_mode};
-    int rc = launch_rmsnorm(a, reinterpret_cast<cudaStream_t>(stream), t_err, sizeof t_err);
-    return rc == DSA_OK ? ok() : rc;
+    return DSA_OK;
 }
 
-size_t dsa_rmsnorm_backward_workspace_size(int64_t rows, int cols)
-{
-    if (rows < 0 || rows > (int64_t)INT32_MAX || cols < 1 || cols > kNormMaxCols)
-        return 0;
-    return rmsnorm_backward_workspace_bytes(rows, cols);
-}
-
-int dsa_rmsnorm_backward(const void *dy, const void *h, const void *weight, const void *dres, int64_t rows, int cols,
-                         int dtype, int weight_dtype, float eps, void *dx, float *dweight, void *workspace,
-                         size_t workspace_bytes, dsa_stream_t stream)
+int check_norm_backward(const void *dy, const void *h, const void *weight, const void *dres, int64_t rows, int cols, int dtype,
+                        int weight_dtype, float eps, const void *dx, const float *dweight, const float *dbias, size_t need,
+                        const void *workspace, size_t workspace_bytes)
 {
     if (rows < 0 || cols < 1)
         return fail(DSA_ERR_INVALID_ARG, "rows must be >= 0 and cols >= 1");
@@ -381,16 +375,159 @@ int dsa_rmsnorm_backward(const void *dy, const void *h, const void *weight, cons
     if (rows > (int64_t)INT32_MAX)
         return fail(DSA_ERR_UNSUPPORTED, "rows too large");
     if (!aligned_to(dtype == DSA_FP32 ? 4 : 2, {dy, h, dres, dx}) || !aligned_to(weight_dtype == DSA_FP32 ? 4 : 2, {weight}) ||
-        !aligned_to(4, {dweight}))
+        !aligned_to(4, {dweight, dbias}))
         return fail(DSA_ERR_ALIGNMENT, "tensors must be aligned to their elements");
-    const size_t need = rmsnorm_backward_workspace_bytes(rows, cols);
     if (need > 0 && (!workspace || workspace_bytes < need))
         return fail(DSA_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace ? workspace_bytes : 0);
     if (!aligned16(workspace))
         return fail(DSA_ERR_ALIGNMENT, "workspace must be 16-byte aligned");
-    RmsNormBackwardArgs a{dy, h, weight, dres, rows, cols, dtype == DSA_FP32, weight_dtype == DSA_FP32, eps, dx, dweight,
-                          workspace};
-    int rc = launch_rmsnorm_backward(a, reinterpret_cast<cudaStream_t>(stream), t_err, sizeof t_err);
+    return DSA_OK;
+}
+
+} // namespace
+
+int dsa_rmsnorm(const void *x, int64_t ldx, const void *residual, int64_t ldr, const void *weight, int64_t rows, int cols,
+                int dtype, int weight_dtype, float eps, void *residual_out, int64_t ldh, void *out, int64_t ldo, void *codes,
+                float *scale, int block, int scale_mode, dsa_stream_t stream)
+{
+    bool none;
+    int rc = check_norm(x, ldx, residual, ldr, weight, nullptr, rows, cols, dtype, weight_dtype, eps, residual_out, ldh, out, ldo, codes,
+                        scale, block, scale_mode, &none);
+    if (rc != DSA_OK)
+        return rc;
+    if (none)
+        return ok();
+    NormArgs a{x, residual, weight, rows, cols, ldx, ldr, ldh, ldo, dtype == DSA_FP32, weight_dtype == DSA_FP32, eps,
+               residual_out, out, static_cast<uint8_t *>(codes), scale, block, scale_mode};
+    rc = launch_rmsnorm(a, reinterpret_cast<cudaStream_t>(stream), t_err, sizeof t_err);
+    return rc == DSA_OK ? ok() : rc;
+}
+
+int dsa_layernorm(const void *x, int64_t ldx, const void *residual, int64_t ldr, const void *weight, const void *bias, int64_t rows, int cols,
+                int dtype, int weight_dtype, float eps, void *residual_out, int64_t ldh, void *out, int64_t ldo, void *codes,
+                float *scale, int block, int scale_mode, dsa_stream_t stream)
+{
+    bool none;
+    int rc = check_norm(x, ldx, residual, ldr, weight, bias, rows, cols, dtype, weight_dtype, eps, residual_out, ldh, out, ldo, codes,
+                        scale, block, scale_mode, &none);
+    if (rc != DSA_OK)
+        return rc;
+    if (none)
+        return ok();
+    NormArgs a{x, residual, weight, rows, cols, ldx, ldr, ldh, ldo, dtype == DSA_FP32, weight_dtype == DSA_FP32, eps,
+               residual_out, out, static_cast<uint8_t *>(codes), scale, block, scale_mode, bias};
+    rc = launch_layernorm(a, reinterpret_cast<cudaStream_t>(stream), t_err, sizeof t_err);
+    return rc == DSA_OK ? ok() : rc;
+}
+
+size_t dsa_rmsnorm_backward_workspace_size(int64_t rows, int cols)
+{
+    if (rows < 0 || rows > (int64_t)INT32_MAX || cols < 1 || cols > kNormMaxCols)
+        return 0;
+    return rmsnorm_backward_workspace_bytes(rows, cols);
+}
+
+int dsa_rmsnorm_backward(const void *dy, const void *h, const void *weight, const void *dres, int64_t rows, int cols,
+                         int dtype, int weight_dtype, float eps, void *dx, float *dweight, void *workspace,
+                         size_t workspace_bytes, dsa_stream_t stream)
+{
+    int rc = check_norm_backward(dy, h, weight, dres, rows, cols, dtype, weight_dtype, eps, dx, dweight, nullptr,
+                                 dsa_rmsnorm_backward_workspace_size(rows, cols), workspace, workspace_bytes);
+    if (rc != DSA_OK)
+        return rc;
+    NormBackwardArgs a{dy, h, weight, dres, rows, cols, dtype == DSA_FP32, weight_dtype == DSA_FP32, eps, dx, dweight,
+                       workspace};
+    rc = launch_rmsnorm_backward(a, reinterpret_cast<cudaStream_t>(stream), t_err, sizeof t_err);
+    return rc == DSA_OK ? ok() : rc;
+}
+
+size_t dsa_layernorm_backward_workspace_size(int64_t rows, int cols)
+{
+    if (rows < 0 || rows > (int64_t)INT32_MAX || cols < 1 || cols > kNormMaxCols)
+        return 0;
+    return layernorm_backward_workspace_bytes(rows, cols);
+}
+
+int dsa_layernorm_backward(const void *dy, const void *h, const void *weight, const void *dres, int64_t rows, int cols,
+                         int dtype, int weight_dtype, float eps, void *dx, float *dweight, float *dbias, void *workspace,
+                         size_t workspace_bytes, dsa_stream_t stream)
+{
+    int rc = check_norm_backward(dy, h, weight, dres, rows, cols, dtype, weight_dtype, eps, dx, dweight, dbias,
+                                 dsa_layernorm_backward_workspace_size(rows, cols), workspace, workspace_bytes);
+    if (rc != DSA_OK)
+        return rc;
+    NormBackwardArgs a{dy, h, weight, dres, rows, cols, dtype == DSA_FP32, weight_dtype == DSA_FP32, eps, dx, dweight,
+                       workspace, dbias};
+    rc = launch_layernorm_backward(a, reinterpret_cast<cudaStream_t>(stream), t_err, sizeof t_err);
+    return rc == DSA_OK ? ok() : rc;
+}
+
+int dsa_quantize_fp8_blocks(const void *x, int64_t ldx, int64_t rows, int64_t cols, int dtype, int block_rows, int scale_mode,
+                            void *codes, int64_t ld_codes, float *scale, void *codes_t, int64_t ld_codes_t, float *scale_t,
+                            dsa_stream_t stream)
+{
+    if (rows < 0 || cols < 1)
+        return fail(DSA_ERR_INVALID_ARG, "rows must be >= 0 and cols >= 1");
+    if (bad_dtype(dtype))
+        return fail(DSA_ERR_INVALID_ARG, "dtype must be DSA_BF16 or DSA_FP32");
+    if (block_rows != 1 && block_rows != 128)
+        return fail(DSA_ERR_INVALID_ARG, "block_rows must be 1 or 128");
+    if (bad_scale_mode(scale_mode))
+        return fail(DSA_ERR_INVALID_ARG, "scale_mode must be DSA_SCALE_AMAX or DSA_SCALE_POW2");
+    if (rows == 0)
+        return ok();
+    if (!x)
+        return fail(DSA_ERR_INVALID_ARG, "null pointer argument");
+    if ((codes == nullptr) != (scale == nullptr) || (codes_t == nullptr) != (scale_t == nullptr))
+        return fail(DSA_ERR_INVALID_ARG, "codes and scale go together, and so do codes_t and scale_t");
+    if (!codes && !codes_t)
+        return fail(DSA_ERR_INVALID_ARG, "no output given");
+    if (ldx < cols || (codes && ld_codes < cols) || (codes_t && ld_codes_t < rows))
+        return fail(DSA_ERR_INVALID_ARG, "a row stride is below the row's width");
+    if (too_large(rows, ldx) || (codes && too_large(rows, ld_codes)) || (codes_t && too_large(cols, ld_codes_t)) ||
+        (rows + 127) / 128 > (int64_t)INT32_MAX / ((cols + 127) / 128))
+        return fail(DSA_ERR_UNSUPPORTED, "rows * cols too large");
+    if (!aligned_to(dtype == DSA_FP32 ? 4 : 2, {x}) || !aligned_to(4, {scale, scale_t}))
+        return fail(DSA_ERR_ALIGNMENT, "tensors must be aligned to their elements");
+    QuantizeBlocksArgs a{x, ldx, rows, cols, dtype == DSA_FP32, block_rows, scale_mode, static_cast<uint8_t *>(codes), ld_codes,
+                         scale, static_cast<uint8_t *>(codes_t), ld_codes_t, scale_t};
+    int rc = launch_quantize_blocks(a, reinterpret_cast<cudaStream_t>(stream), t_err, sizeof t_err);
+    return rc == DSA_OK ? ok() : rc;
+}
+
+int dsa_gemm_fp8(const void *a, int64_t lda, const float *a_scale, const void *b, int64_t ldb, const float *b_scale,
+                 int b_block_rows, int M, int N, int K, void *out, int64_t ldo, int out_dtype, dsa_stream_t stream)
+{
+    constexpr int kMost = 1 << 30;
+    if (M < 0 || N < 0 || K < 0)
+        return fail(DSA_ERR_INVALID_ARG, "M, N and K must not be negative");
+    if (b_block_rows != 1 && b_block_rows != 128)
+        return fail(DSA_ERR_INVALID_ARG, "b_block_rows must be 1 or 128");
+    if (bad_dtype(out_dtype))
+        return fail(DSA_ERR_INVALID_ARG, "out_dtype must be DSA_BF16 or DSA_FP32");
+    if (M > kMost || N > kMost || K > kMost)
+        return fail(DSA_ERR_UNSUPPORTED, "M, N and K must be at most 2^30");
+    if (M == 0 || N == 0)
+        return ok();
+    if (!out || (K > 0 && (!a || !a_scale || !b || !b_scale)))
+        return fail(DSA_ERR_INVALID_ARG, "null pointer argument");
+    // a stride that no address depends on says nothing
+    if (M == 1 || K == 0)
+        lda = ((int64_t)K + 15) & ~int64_t(15);
+    if (N == 1 || K == 0)
+        ldb = ((int64_t)K + 15) & ~int64_t(15);
+    if (lda < K || ldb < K || ldo < N)
+        return fail(DSA_ERR_INVALID_ARG, "a row stride is below the row's width");
+    // a tile of 128 x 16 outputs, by up to 8 CTAs
+    if (too_large(M, lda + 1) || too_large(N, ldb + 1) || too_large(M, ldo) ||
+        ((int64_t)M + 127) / 128 * (((int64_t)N + 127) / 128) > (int64_t)INT32_MAX / 16)
+        return fail(DSA_ERR_UNSUPPORTED, "tensors too large");
+    if (!aligned16(a) || !aligned16(b) || lda % 16 || ldb % 16)
+        return fail(DSA_ERR_ALIGNMENT, "a, b and their row strides must be 16-byte aligned");
+    if (!aligned_to(4, {a_scale, b_scale}) || !aligned_to(out_dtype == DSA_FP32 ? 4 : 2, {out}))
+        return fail(DSA_ERR_ALIGNMENT, "tensors must be aligned to their elements");
+    GemmFp8Args g{a, lda, a_scale, b, ldb, b_scale, b_block_rows == 128, M, N, K, out, ldo, out_dtype == DSA_FP32};
+    int rc = launch_gemm_fp8(g, reinterpret_cast<cudaStream_t>(stream), t_err, sizeof t_err);
     return rc == DSA_OK ? ok() : rc;
 }
 

@@ -251,24 +251,6 @@ __device__ __forceinline__ float exp2_fast(float x)
     return y;
 }
 
-__device__ __forceinline__ uint32_t pack2(float lo, float hi)
-{
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
-// True in one lane of the warp.  The compiler keeps the operands of what this
-// lane issues in uniform registers: the MMAs then go out at the tensor pipe's own
-// rate (32 cycles for N = 128, 64 for N = 256), which a plain lane == 0 does
-// not reach (54 cycles for N = 128 in a loop of MMAs alone).
-__device__ __forceinline__ bool elect_one()
-{
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-    return r != 0;
-}
-
 // One softmax warp's arrival on a barrier of the leader CTA, which counts kSoftWarps arrivals of its own warps, one of
 // them expecting kSoftWarps * 4 bytes (`arms`), and those bytes from CTA 1's.  What CTA 1 announces (P, value rows, O in its
 // shared and tensor memory) the leader's MMA threads act on, so it takes a release at cluster scope: a four-byte
@@ -307,15 +289,6 @@ __device__ __forceinline__ void umma_f16_pair(uint32_t d, uint64_t a, uint64_t b
                  : "memory");
 }
 
-// Arrives on the barrier at this offset in both CTAs once the MMAs issued so far are done.
-__device__ __forceinline__ void umma_commit_pair(uint32_t bar)
-{
-    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-                     bar),
-                 "h"((uint16_t)3)
-                 : "memory");
-}
-
 // Whether a barrier's phase is over, without waiting for it.
 __device__ __forceinline__ bool mbar_done(uint32_t bar, uint32_t parity)
 {
@@ -325,24 +298,6 @@ __device__ __forceinline__ bool mbar_done(uint32_t bar, uint32_t parity)
                  : "r"(bar), "r"(parity)
                  : "memory");
     return done != 0;
-}
-
-__device__ __forceinline__ void store32(void *p, const uint32_t (&w)[8])
-{
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
-                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                 : "memory");
-}
-
-__device__ __forceinline__ void tmem_alloc_pair(uint32_t dst, uint32_t ncols)
-{
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(ncols) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-}
-
-__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols)
-{
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)

@@ -29,6 +29,11 @@ PyObject *alloc_fn, *free_fn;                          /* PyTorch's allocator: a
 decltype(&dsa_rmsnorm) f_rmsnorm;
 decltype(&dsa_rmsnorm_backward) f_rmsnorm_backward;
 decltype(&dsa_rmsnorm_backward_workspace_size) f_rmsnorm_backward_ws;
+decltype(&dsa_layernorm) f_layernorm;
+decltype(&dsa_layernorm_backward) f_layernorm_backward;
+decltype(&dsa_layernorm_backward_workspace_size) f_layernorm_backward_ws;
+decltype(&dsa_quantize_fp8_blocks) f_quantize_blocks;
+decltype(&dsa_gemm_fp8) f_gemm_fp8;
 decltype(&dsa_cache_append) f_cache_append;
 decltype(&dsa_rope_queries) f_rope_queries;
 decltype(&dsa_index_rope_backward) f_index_rope_backward;
@@ -196,60 +201,125 @@ PyObject *not_plain(PyObject *keep)
         Py_END_ALLOW_THREADS                                                                                                        \
     } while (0)
 
-/* x, weight, eps, out, residual, residual_out, codes, scale, block, scale_mode, stream */
-PyObject *py_rmsnorm(PyObject *const *v, Py_ssize_t n)
+/* x, weight, [bias,] eps, out, residual, residual_out, codes, scale, block, scale_mode, stream */
+template <bool LN> PyObject *norm(PyObject *const *v, Py_ssize_t n)
 {
     long cur;
     dsa_stream_t st;
-    Arg x, w, o, r, h, c, s;
+    Arg x, w, b, o, r, h, c, s;
     int64_t ldx, ldo = 0, ldr = 0, ldh = 0;
     double eps;
     int block, mode;
-    if (n != 11 || !where(v[10], &cur, &st) || !number(v[2], &eps) || !integer(v[8], &block) || !integer(v[9], &mode) ||
+    if (n != (LN ? 12 : 11))
+        return not_plain(NULL);
+    PyObject *bias = LN ? v[2] : Py_None;
+    PyObject *const *u = v + (LN ? 1 : 0); /* from eps on */
+    if (!where(u[10], &cur, &st) || !number(u[2], &eps) || !integer(u[8], &block) || !integer(u[9], &mode) ||
         !look(v[0], cur, K_ANY, &x) || x.nd != 2 || !FITS(x.dim[1]))
         return not_plain(NULL);
     const int64_t rows = x.dim[0], cols = x.dim[1];
     ldx = rows > 1 ? x.stride[0] : cols;
     if ((cols != 1 && x.stride[1] != 1) || ldx < cols || !at(v[1], cur, K_ANY, cols, -1, -1, &w) ||
-        (v[3] != Py_None && !at_rows(v[3], cur, x.dtype, rows, cols, &o, &ldo)) ||
-        (v[4] != Py_None && !at_rows(v[4], cur, x.dtype, rows, cols, &r, &ldr)) ||
-        (v[5] != Py_None && !at_rows(v[5], cur, x.dtype, rows, cols, &h, &ldh)) ||
-        (v[6] != Py_None && !at(v[6], cur, K_UINT8, rows, cols, -1, &c)))
+        (bias != Py_None && !at(bias, cur, w.dtype, cols, -1, -1, &b)) ||
+        (u[3] != Py_None && !at_rows(u[3], cur, x.dtype, rows, cols, &o, &ldo)) ||
+        (u[4] != Py_None && !at_rows(u[4], cur, x.dtype, rows, cols, &r, &ldr)) ||
+        (u[5] != Py_None && !at_rows(u[5], cur, x.dtype, rows, cols, &h, &ldh)) ||
+        (u[6] != Py_None && !at(u[6], cur, K_UINT8, rows, cols, -1, &c)))
         return not_plain(NULL);
-    if (v[7] != Py_None) {
+    if (u[7] != Py_None) {
         const int64_t parts = block > 0 ? (cols + block - 1) / block : 1;
-        if (!look(v[7], cur, DSA_FP32, &s) || s.dim[0] != rows || !s.contiguous ||
+        if (!look(u[7], cur, DSA_FP32, &s) || s.dim[0] != rows || !s.contiguous ||
             !((s.nd == 2 && s.dim[1] == parts) || (s.nd == 1 && parts == 1)))
             return not_plain(NULL);
     }
     int rc;
-    CALL(rc, f_rmsnorm(x.p, ldx, r.p, ldr, w.p, rows, (int)cols, x.dtype, w.dtype, (float)eps, h.p, ldh, o.p, ldo,
-                                     c.p, s.p, block, mode, st));
+    if (LN)
+        CALL(rc, f_layernorm(x.p, ldx, r.p, ldr, w.p, b.p, rows, (int)cols, x.dtype, w.dtype, (float)eps, h.p, ldh, o.p, ldo, c.p, s.p,
+                             block, mode, st));
+    else
+        CALL(rc, f_rmsnorm(x.p, ldx, r.p, ldr, w.p, rows, (int)cols, x.dtype, w.dtype, (float)eps, h.p, ldh, o.p, ldo, c.p, s.p, block,
+                           mode, st));
     return PyLong_FromLong(rc);
 }
 
-/* dy, h, weight, eps, dx, dweight, dres, workspace, stream */
-PyObject *py_rmsnorm_backward(PyObject *const *v, Py_ssize_t n)
+PyObject *py_rmsnorm(PyObject *const *v, Py_ssize_t n) { return norm<false>(v, n); }
+PyObject *py_layernorm(PyObject *const *v, Py_ssize_t n) { return norm<true>(v, n); }
+
+/* dy, h, weight, eps, dx, dweight, [dbias,] dres, workspace, stream */
+template <bool LN> PyObject *norm_backward(PyObject *const *v, Py_ssize_t n)
 {
     long cur;
     dsa_stream_t st;
-    Arg dy, h, w, dx, dw, e;
+    Arg dy, h, w, dx, dw, db, e;
     double eps;
     void *ws;
     size_t bytes;
     PyObject *keep = NULL;
-    if (n != 9 || !where(v[8], &cur, &st) || !number(v[3], &eps) || !look(v[1], cur, K_ANY, &h) || h.nd != 2 ||
-        !FITS(h.dim[1]) || !h.contiguous)
+    if (n != (LN ? 10 : 9))
+        return not_plain(NULL);
+    PyObject *dbias = LN ? v[6] : Py_None;
+    PyObject *const *u = v + (LN ? 1 : 0); /* from dres on */
+    if (!where(u[8], &cur, &st) || !number(v[3], &eps) || !look(v[1], cur, K_ANY, &h) || h.nd != 2 || !FITS(h.dim[1]) || !h.contiguous)
         return not_plain(NULL);
     const int64_t rows = h.dim[0], cols = h.dim[1];
     if (!at(v[0], cur, h.dtype, rows, cols, -1, &dy) || !at(v[2], cur, K_ANY, cols, -1, -1, &w) ||
         !at(v[4], cur, h.dtype, rows, cols, -1, &dx) || !at(v[5], cur, DSA_FP32, cols, -1, -1, &dw) ||
-        (v[6] != Py_None && !at(v[6], cur, h.dtype, rows, cols, -1, &e)) ||
-        !workspace(v[7], st, cur, v[7] == Py_None ? f_rmsnorm_backward_ws(rows, (int)cols) : 0, &ws, &bytes, &keep))
+        (dbias != Py_None && !at(dbias, cur, DSA_FP32, cols, -1, -1, &db)) ||
+        (u[6] != Py_None && !at(u[6], cur, h.dtype, rows, cols, -1, &e)) ||
+        !workspace(u[7], st, cur, u[7] == Py_None ? (LN ? f_layernorm_backward_ws : f_rmsnorm_backward_ws)(rows, (int)cols) : 0, &ws,
+                   &bytes, &keep))
         return not_plain(keep);
     int rc;
-    CALL(rc, f_rmsnorm_backward(dy.p, h.p, w.p, e.p, rows, (int)cols, h.dtype, w.dtype, (float)eps, dx.p, dw.p, ws, bytes, st));
+    if (LN)
+        CALL(rc, f_layernorm_backward(dy.p, h.p, w.p, e.p, rows, (int)cols, h.dtype, w.dtype, (float)eps, dx.p, dw.p, db.p, ws, bytes, st));
+    else
+        CALL(rc, f_rmsnorm_backward(dy.p, h.p, w.p, e.p, rows, (int)cols, h.dtype, w.dtype, (float)eps, dx.p, dw.p, ws, bytes, st));
     release(keep);
+    return PyLong_FromLong(rc);
+}
+
+PyObject *py_rmsnorm_backward(PyObject *const *v, Py_ssize_t n) { return norm_backward<false>(v, n); }
+PyObject *py_layernorm_backward(PyObject *const *v, Py_ssize_t n) { return norm_backward<true>(v, n); }
+
+/* x, codes, scale, codes_t, scale_t, block_rows, scale_mode, stream */
+PyObject *py_quantize_fp8_blocks(PyObject *const *v, Py_ssize_t n)
+{
+    long cur;
+    dsa_stream_t st;
+    Arg x, c, s, t, ts;
+    int64_t ldx, ldc = 0, ldt = 0;
+    int block, mode;
+    if (n != 8 || !where(v[7], &cur, &st) || !integer(v[5], &block) || (block != 1 && block != 128) || !integer(v[6], &mode) ||
+        !look(v[0], cur, K_ANY, &x) || x.nd != 2)
+        return not_plain(NULL);
+    const int64_t rows = x.dim[0], cols = x.dim[1];
+    if (!at_rows(v[0], cur, x.dtype, rows, cols, &x, &ldx) || (v[1] != Py_None && !at_rows(v[1], cur, K_UINT8, rows, cols, &c, &ldc)) ||
+        (v[2] != Py_None && !at(v[2], cur, DSA_FP32, (rows + block - 1) / block, (cols + 127) / 128, -1, &s)) ||
+        (v[3] != Py_None && !at_rows(v[3], cur, K_UINT8, cols, rows, &t, &ldt)) ||
+        (v[4] != Py_None && !at(v[4], cur, DSA_FP32, (cols + block - 1) / block, (rows + 127) / 128, -1, &ts)))
+        return not_plain(NULL);
+    int rc;
+    CALL(rc, f_quantize_blocks(x.p, ldx, rows, cols, x.dtype, block, mode, c.p, ldc, s.p, t.p, ldt, ts.p, st));
+    return PyLong_FromLong(rc);
+}
+
+/* a, a_scale, b, b_scale, out, stream */
+PyObject *py_gemm_fp8(PyObject *const *v, Py_ssize_t n)
+{
+    long cur;
+    dsa_stream_t st;
+    Arg a, as, b, bs, o;
+    int64_t lda, ldb, ldo;
+    if (n != 6 || !where(v[5], &cur, &st) || !look(v[0], cur, K_UINT8, &a) || a.nd != 2 || !FITS(a.dim[0]) || !FITS(a.dim[1]) ||
+        !look(v[2], cur, K_UINT8, &b) || b.nd != 2 || !FITS(b.dim[0]) || !look(v[3], cur, DSA_FP32, &bs) || bs.nd != 2 || !bs.contiguous)
+        return not_plain(NULL);
+    const int64_t M = a.dim[0], K = a.dim[1], N = b.dim[0], pieces = (K + 127) / 128, blocks = (N + 127) / 128;
+    if (!at_rows(v[0], cur, K_UINT8, M, K, &a, &lda) || !at_rows(v[2], cur, K_UINT8, N, K, &b, &ldb) ||
+        !at(v[1], cur, DSA_FP32, M, pieces, -1, &as) || (bs.dim[0] != blocks && bs.dim[0] != N) || bs.dim[1] != pieces ||
+        !look(v[4], cur, K_ANY, &o) || !at_rows(v[4], cur, o.dtype, M, N, &o, &ldo))
+        return not_plain(NULL);
+    int rc;
+    CALL(rc, f_gemm_fp8(a.p, lda, as.p, b.p, ldb, bs.p, bs.dim[0] == blocks ? 128 : 1, (int)M, (int)N, (int)K, o.p, ldo, o.dtype, st));
     return PyLong_FromLong(rc);
 }
 
@@ -379,13 +449,19 @@ PyObject *py_init(PyObject *, PyObject *args)
     f_rmsnorm = (decltype(f_rmsnorm))dlsym(lib, "dsa_rmsnorm");
     f_rmsnorm_backward = (decltype(f_rmsnorm_backward))dlsym(lib, "dsa_rmsnorm_backward");
     f_rmsnorm_backward_ws = (decltype(f_rmsnorm_backward_ws))dlsym(lib, "dsa_rmsnorm_backward_workspace_size");
+    f_layernorm = (decltype(f_layernorm))dlsym(lib, "dsa_layernorm");
+    f_layernorm_backward = (decltype(f_layernorm_backward))dlsym(lib, "dsa_layernorm_backward");
+    f_layernorm_backward_ws = (decltype(f_layernorm_backward_ws))dlsym(lib, "dsa_layernorm_backward_workspace_size");
+    f_quantize_blocks = (decltype(f_quantize_blocks))dlsym(lib, "dsa_quantize_fp8_blocks");
+    f_gemm_fp8 = (decltype(f_gemm_fp8))dlsym(lib, "dsa_gemm_fp8");
     f_cache_append = (decltype(f_cache_append))dlsym(lib, "dsa_cache_append");
     f_rope_queries = (decltype(f_rope_queries))dlsym(lib, "dsa_rope_queries");
     f_index_rope_backward = (decltype(f_index_rope_backward))dlsym(lib, "dsa_index_rope_backward");
     f_mla_decode = (decltype(f_mla_decode))dlsym(lib, "dsa_mla_decode_paged");
     f_mla_decode_ws = (decltype(f_mla_decode_ws))dlsym(lib, "dsa_mla_decode_workspace_size");
     if (!f_rmsnorm || !f_rmsnorm_backward || !f_rmsnorm_backward_ws || !f_cache_append || !f_rope_queries || !f_index_rope_backward ||
-        !f_mla_decode || !f_mla_decode_ws) {
+        !f_mla_decode || !f_mla_decode_ws || !f_layernorm || !f_layernorm_backward || !f_layernorm_backward_ws || !f_quantize_blocks ||
+        !f_gemm_fp8) {
         PyErr_SetString(PyExc_RuntimeError, "the library lacks an entry point");
         return NULL;
     }
@@ -408,6 +484,10 @@ template <PyObject *(*F)(PyObject *const *, Py_ssize_t)> PyObject *entry(PyObjec
 #define FAST(name) {#name, (PyCFunction)(void (*)(void))entry<py_##name>, METH_FASTCALL, NULL}
 PyMethodDef methods[] = {FAST(rmsnorm),
                                 FAST(rmsnorm_backward),
+                                FAST(layernorm),
+                                FAST(layernorm_backward),
+                                FAST(quantize_fp8_blocks),
+                                FAST(gemm_fp8),
                                 FAST(cache_append),
                                 FAST(rope_queries),
                                 FAST(index_rope_backward),

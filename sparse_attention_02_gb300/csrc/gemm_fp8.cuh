@@ -1,0 +1,47 @@
+// What the kernels of the FP8 product share.
+#pragma once
+
+#include "common.cuh"
+#include "f32x2.cuh"
+#include "launch.h"
+
+namespace dsa {
+
+constexpr int kGemmPiece = 128; // values along K that share a scale; one row of a 128-byte swizzled tile
+
+// The product by clusters of CTAs that split K between them (gemm_fp8_split.cu), and its
+// form for large products (gemm_fp8_pair.cu).  `cols` is the rows of `a` that a CTA takes.
+int launch_gemm_fp8_split(const GemmFp8Args &a, int cols, int split, cudaStream_t stream, char *err, size_t errlen);
+
+inline bool gemm_fp8_map(CUtensorMap *map, const void *base, int64_t ld, int rows, int K, int box, char *err, size_t errlen)
+{
+    return encode_tmap_2d(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, (uint64_t)K, (uint64_t)rows, (uint64_t)ld, kGemmPiece, box,
+                          CU_TENSOR_MAP_SWIZZLE_128B, err, errlen);
+}
+
+// Waits for this warp's TMEM loads; the values depend on it, so nothing uses them earlier.
+__device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
+                   "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                   "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28])
+                 :
+                 : "memory");
+    asm volatile("" : "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
+}
+
+__device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
+}
+
+__device__ __forceinline__ void tmem_load(uint32_t at, uint32_t (&r)[32]) { tmem_ld32(at, r); }
+__device__ __forceinline__ void tmem_load(uint32_t at, uint32_t (&r)[16]) { tmem_ld16(at, r); }
+
+} // namespace dsa

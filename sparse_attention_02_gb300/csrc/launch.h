@@ -88,7 +88,37 @@ struct QuantizeArgs {
 };
 int launch_quantize(const QuantizeArgs &a, cudaStream_t stream, char *err, size_t errlen);
 
-struct RmsNormArgs {
+struct QuantizeBlocksArgs {
+    const void *x;   // [rows, cols], row stride ldx; bf16, or fp32 with x32
+    int64_t ldx, rows, cols;
+    bool x32;
+    int block_rows;  // 1 or 128
+    int scale_mode;
+    uint8_t *codes;  // [rows, cols], row stride ldc, or null
+    int64_t ldc;
+    float *scale;    // [rows / block_rows, cols / 128], rounded up
+    uint8_t *codes_t; // [cols, rows], row stride ldt, or null
+    int64_t ldt;
+    float *scale_t;  // [cols / block_rows, rows / 128], rounded up
+};
+int launch_quantize_blocks(const QuantizeBlocksArgs &a, cudaStream_t stream, char *err, size_t errlen);
+
+struct GemmFp8Args {
+    const void *a;        // [M, K] E4M3, row stride lda
+    int64_t lda;
+    const float *a_scale; // [M, ceil(K / 128)]
+    const void *b;        // [N, K] E4M3, row stride ldb
+    int64_t ldb;
+    const float *b_scale; // [N, or ceil(N / 128) with b_block; ceil(K / 128)]
+    bool b_block;
+    int M, N, K;
+    void *out;            // [M, N] bf16, or fp32 with o32, row stride ldo
+    int64_t ldo;
+    bool o32;
+};
+int launch_gemm_fp8(const GemmFp8Args &a, cudaStream_t stream, char *err, size_t errlen);
+
+struct NormArgs {
     const void *x;        // [rows, cols], row stride ldx; bf16, or fp32 with x32
     const void *residual; // like x (stride ldr), or null
     const void *weight;   // [cols] bf16, or fp32 with w32
@@ -103,10 +133,12 @@ struct RmsNormArgs {
     float *scale;       // [rows, 1 or ceil(cols / 128)]
     int block;          // 0: one scale a row, 128: one per 128 columns
     int scale_mode;
+    const void *bias = nullptr; // layer norm: like weight, or null
 };
-int launch_rmsnorm(const RmsNormArgs &a, cudaStream_t stream, char *err, size_t errlen);
+int launch_rmsnorm(const NormArgs &a, cudaStream_t stream, char *err, size_t errlen);
+int launch_layernorm(const NormArgs &a, cudaStream_t stream, char *err, size_t errlen);
 
-struct RmsNormBackwardArgs {
+struct NormBackwardArgs {
     const void *dy, *h, *weight, *dres; // [rows, cols] (dres or null); weight [cols]
     int64_t rows;
     int cols;
@@ -115,9 +147,12 @@ struct RmsNormBackwardArgs {
     void *dx;
     float *dweight;
     void *workspace;
+    float *dbias = nullptr; // layer norm; or null
 };
-int launch_rmsnorm_backward(const RmsNormBackwardArgs &a, cudaStream_t stream, char *err, size_t errlen);
+int launch_rmsnorm_backward(const NormBackwardArgs &a, cudaStream_t stream, char *err, size_t errlen);
 size_t rmsnorm_backward_workspace_bytes(int64_t rows, int cols);
+int launch_layernorm_backward(const NormBackwardArgs &a, cudaStream_t stream, char *err, size_t errlen);
+size_t layernorm_backward_workspace_bytes(int64_t rows, int cols);
 
 struct CacheAppendArgs {
     const int32_t *pos;       // [T]
