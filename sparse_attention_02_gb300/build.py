@@ -25,7 +25,7 @@ OBJ = os.path.join(HERE, "_objs")
 LIB = os.path.join(HERE, "libdsa.so")
 FAST = os.path.join(HERE, "_fastcall.so")
 FAST_KEY = os.path.join(HERE, "_fastcall.key")  # what FAST was built for and from
-SOURCES = ["api.cu", "quantize.cu", "quantize_blocks.cu", "gemm_fp8.cu", "gemm_fp8_split.cu", "gemm_fp8_pair.cu", "rmsnorm.cu", "rmsnorm_backward.cu", "layernorm.cu", "layernorm_backward.cu",
+SOURCES = ["api.cu", "quantize.cu", "quantize_blocks.cu", "gemm_fp8.cu", "gemm_fp8_split.cu", "gemm_fp8_tile.cu", "rmsnorm.cu", "rmsnorm_backward.cu", "layernorm.cu", "layernorm_backward.cu",
            "rope.cu", "indexer.cu", "topk.cu", "indexer_topk.cu", "warmup.cu",
            "sparse_mla.cu", "dense_mla.cu", "prefill_host.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -10,9 +10,9 @@ namespace dsa {
 constexpr int kGemmPiece = 128; // values along K that share a scale; one row of a 128-byte swizzled tile
 
 // The product by clusters of CTAs that split K between them (gemm_fp8_split.cu), and its
-// form for large products (gemm_fp8_pair.cu).  `cols` is the rows of `a` that a CTA takes.
+// form for large products (gemm_fp8_tile.cu).  `cols` is the rows of `a` that a CTA takes.
 int launch_gemm_fp8_split(const GemmFp8Args &a, int cols, int split, cudaStream_t stream, char *err, size_t errlen);
-int launch_gemm_fp8_pair(const GemmFp8Args &a, int cols, cudaStream_t stream, char *err, size_t errlen); // cols: rows of `b` a tile takes
+int launch_gemm_fp8_tile(const GemmFp8Args &a, int cols, cudaStream_t stream, char *err, size_t errlen); // cols: rows of `b` a tile takes
 
 inline bool gemm_fp8_map(CUtensorMap *map, const void *base, int64_t ld, int rows, int K, int box, char *err, size_t errlen)
 {

@@ -1,0 +1,396 @@
+// The product of FP8 operands with a scale for every 128 values along the summed
+// axis on sm_103a, where there are enough rows on both sides to fill the GPU with
+// whole tiles (the formula stands in gemm_fp8_split.cu).
+//
+// A CTA's tile is 128 rows of a by BN of b.  A piece of 128 values along K is one stage of
+// shared memory and four MMAs, whose sums stay in TMEM (two buffers of BN columns) only until
+// eight warps have read them, scaled them and added them to running sums in their registers:
+// 128 fp32 a thread, one multiply-add each, in pairs, or a product more where b has a scale
+// for every row.
+#include "gemm_fp8.cuh"
+
+#include <atomic>
+#include <stdio.h>
+
+namespace dsa {
+namespace {
+
+constexpr int kSumWarp0 = 4, kSumWarps = 8;
+constexpr int kThreads = 32 * (kSumWarp0 + kSumWarps);
+constexpr int kGroup = 8;   // tiles along M that neighbouring tiles are taken from
+constexpr int kAuxRegs = 72, kSumRegs = 216; // of 168 a thread at launch
+constexpr int kPatch = 32 * 17 * 4; // 16 columns of a warp's rows, on their way to rows of out that are not aligned
+constexpr int kRows = 128;  // of a
+constexpr int kABytes = kRows * kGemmPiece;
+
+template <int BN, bool ROWS> struct Cfg {
+    static constexpr int kStage = kABytes + BN * kGemmPiece;
+    static constexpr int kStages = BN == 256 ? 4 : 6;
+    static constexpr int kBatch = ROWS ? 4 : 8;                   // pieces whose scales are fetched at once
+    static constexpr int kScaled = kRows + (ROWS ? BN : BN / 128); // scales of a piece: a's, then b's
+    static constexpr int kScales = kStages * kStage;              // two batches
+    static constexpr int kPatches = kScales + 2 * kBatch * kScaled * 4;
+    static constexpr int kBars = (kPatches + kSumWarps * kPatch + 7) / 8 * 8;
+    static constexpr int kNumBars = 2 * kStages + 9;
+    static constexpr int kMisc = kBars + 8 * kNumBars;
+    static constexpr int kSmem = kMisc + 16;
+    static_assert(kSmem <= 232448, "dynamic shared memory above the 227 KB a CTA may hold");
+};
+
+struct Params {
+    const float *a_scale, *b_scale;
+    int M, N, pieces, tiles_m, tiles_n;
+    bool o32;
+    int wide; // bytes that every row of out starts at a multiple of: 32, 16 or less
+    void *out;
+    int64_t ldo;
+    unsigned *status;
+};
+
+__device__ __forceinline__ void tile_at(const Params &p, int tile, int &m, int &n)
+{
+    const int per = kGroup * p.tiles_n, g = tile / per, first = g * kGroup;
+    const int rows = p.tiles_m - first < kGroup ? p.tiles_m - first : kGroup, r = tile - g * per;
+    n = r / rows;
+    m = first + r - n * rows;
+}
+
+// 16 sums of each of a warp's rows to out, from row m (of lane 0) and column n on.
+__device__ __forceinline__ void store_sums(const Params &p, int64_t m, int n, const F2 *acc, float *patch)
+{
+    const int lane = threadIdx.x & 31;
+    float f[16];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        acc[i].get(f[2 * i], f[2 * i + 1]);
+    if (p.N - n >= 16 && p.wide >= 16) { // a lane's columns are its own row's: 32 bytes a store fill whole sectors
+        if (m + lane >= p.M)
+            return;
+        uint32_t w[8];
+        if (p.o32) {
+            float *dst = static_cast<float *>(p.out) + (m + lane) * p.ldo + n;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    w[k] = __float_as_uint(f[8 * e + k]);
+                if (p.wide == 32) {
+                    store32(dst + 8 * e, w);
+                } else {
+                    reinterpret_cast<uint4 *>(dst)[2 * e] = make_uint4(w[0], w[1], w[2], w[3]);
+                    reinterpret_cast<uint4 *>(dst)[2 * e + 1] = make_uint4(w[4], w[5], w[6], w[7]);
+                }
+            }
+        } else {
+            __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) + (m + lane) * p.ldo + n;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                w[k] = pack2(f[2 * k], f[2 * k + 1]);
+            if (p.wide == 32) {
+                store32(dst, w);
+            } else {
+                reinterpret_cast<uint4 *>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                reinterpret_cast<uint4 *>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            }
+        }
+        return;
+    }
+    // by way of shared memory, so that lanes hold neighbouring columns of two rows at a time
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        patch[lane * 17 + i] = f[i];
+    __syncwarp();
+    const int c = lane & 15;
+#pragma unroll 4
+    for (int r = lane >> 4; r < 32; r += 2) {
+        const float v = patch[r * 17 + c];
+        if (m + r < p.M && n + c < p.N) {
+            if (p.o32)
+                static_cast<float *>(p.out)[(m + r) * p.ldo + n + c] = v;
+            else
+                static_cast<__nv_bfloat16 *>(p.out)[(m + r) * p.ldo + n + c] = __float2bfloat16_rn(v);
+        }
+    }
+}
+
+template <int BN, bool ROWS>
+__global__ void __launch_bounds__(kThreads, 1)
+    gemm_fp8_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, Params p)
+{
+    using C = Cfg<BN, ROWS>;
+    extern __shared__ __align__(1024) uint8_t smem[]; // the swizzle's period
+    const uint32_t sbase = smem_u32(smem);
+    auto bar = [&](int i) { return sbase + C::kBars + 8u * i; };
+    constexpr int B_FULL = 0, B_EMPTY = C::kStages, B_TF = 2 * C::kStages, B_TE = B_TF + 2, B_SF = B_TF + 4, B_SE = B_TF + 6,
+                  B_DONE = B_TF + 8;
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + C::kMisc);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::kMisc + 4);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int tiles = p.tiles_m * p.tiles_n;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kStages; ++i) {
+            mbar_init(bar(B_FULL + i), 1);
+            mbar_init(bar(B_EMPTY + i), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(B_TF + i), 1);
+            mbar_init(bar(B_TE + i), kSumWarps);
+            mbar_init(bar(B_SF + i), 64);
+            mbar_init(bar(B_SE + i), kSumWarps);
+        }
+        mbar_init(bar(B_DONE), 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1)
+        tmem_alloc(sbase + C::kMisc, 2 * BN);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_holder;
+    grid_dep_wait(); // no global memory before this
+    grid_dep_launch();
+
+    // each side takes its share of the registers in its own branch: what both run has to fit the smaller
+    if (warp < kSumWarp0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAuxRegs));
+        if (warp == 0) {
+            // -------------------------------------------------------- loads
+            int st = 0, phase = 0;
+            bool ok = true, again = false; // again: every stage was filled once
+            for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
+                int tm, tn;
+                tile_at(p, tile, tm, tn);
+                for (int k = 0; k < p.pieces; ++k) {
+                    if (again && !mbar_wait_warp(bar(B_EMPTY + st), phase ^ 1, abort_flag, p.status)) {
+                        ok = false;
+                        break;
+                    }
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(bar(B_FULL + st), C::kStage);
+                        tma_load_2d(sbase + st * C::kStage, &tm_a, bar(B_FULL + st), k * kGemmPiece, tm * kRows);
+                        tma_load_2d(sbase + st * C::kStage + kABytes, &tm_b, bar(B_FULL + st), k * kGemmPiece, tn * BN);
+                    }
+                    __syncwarp();
+                    if (++st == C::kStages) {
+                        st = 0;
+                        phase ^= 1;
+                        again = true;
+                    }
+                }
+            }
+        } else if (warp == 1) {
+            // --------------------------------------------------------- MMAs
+            if (elect_one()) {
+                constexpr uint32_t idesc = idesc_f32acc(kRows, BN, 0u, false, false);
+                const uint64_t ad = sdesc(sbase, 16, 1024, 2), bd = sdesc(sbase + kABytes, 16, 1024, 2);
+                uint32_t i = 0;
+                int st = 0, phase = 0;
+                bool ok = true;
+                for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x)
+                    for (int k = 0; k < p.pieces; ++k, ++i) {
+                        const uint32_t t = i & 1;
+                        ok = (i < 2 || mbar_wait(bar(B_TE + t), ((i >> 1) - 1) & 1, abort_flag, p.status)) &&
+                             mbar_wait(bar(B_FULL + st), phase, abort_flag, p.status);
+                        if (!ok)
+                            break;
+                        tc_fence_after();
+                        const uint64_t so = (uint64_t)((st * C::kStage) >> 4);
+#pragma unroll
+                        for (int s = 0; s < 4; ++s)
+                            umma_f8f6f4(tmem + t * BN, ad + so + 2 * s, bd + so + 2 * s, idesc, s > 0);
+                        umma_commit(bar(B_TF + t));
+                        umma_commit(bar(B_EMPTY + st));
+                        if (++st == C::kStages) {
+                            st = 0;
+                            phase ^= 1;
+                        }
+                    }
+                umma_commit(bar(B_DONE));
+                mbar_drain(bar(B_DONE), 0);
+            }
+            __syncwarp();
+        } else {
+            // ------------------------------------------------------- scales
+            // Batches of this CTA's pieces, counted through its tiles: kBatch lanes along the pieces, 32 / kBatch rows at
+            // a time; the two warps take half of the rows each.
+            constexpr int R = 32 / C::kBatch;
+            const int kk = lane % C::kBatch, r0 = lane / C::kBatch, half = warp - 2, first = blockIdx.x;
+            const int total = first < tiles ? ((tiles - 1 - first) / (int)gridDim.x + 1) * p.pieces : 0;
+            for (int i = 0; i < total; i += C::kBatch) {
+                const int n = i / C::kBatch, buf = n & 1, mine = i + kk < total ? i + kk : total - 1, nth = mine / p.pieces;
+                const int k = mine - nth * p.pieces;
+                int tm, tn;
+                tile_at(p, first + nth * (int)gridDim.x, tm, tn);
+                if (n >= 2 && !mbar_wait_warp(bar(B_SE + buf), ((n >> 1) - 1) & 1, abort_flag, p.status))
+                    break;
+                float *to = reinterpret_cast<float *>(smem + C::kScales) + (buf * C::kBatch + kk) * C::kScaled;
+                auto fetch = [&](const float *from, int row, int rows, float *dst, int count) {
+                    from += (int64_t)row * p.pieces + k;
+                    const int left = rows - row < count ? rows - row : count;
+#pragma unroll 1
+                    for (int j = r0; j < count; j += 8 * R) {
+                        float v[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            v[e] = j + R * e < left ? from[(int64_t)(j + R * e) * p.pieces] : 0.f;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (j + R * e < count)
+                                dst[j + R * e] = v[e];
+                    }
+                };
+                fetch(p.a_scale, tm * kRows + kRows / 2 * half, p.M, to + kRows / 2 * half, kRows / 2);
+                if (ROWS)
+                    fetch(p.b_scale, tn * BN + BN / 2 * half, p.N, to + kRows + BN / 2 * half, BN / 2);
+                else if (half == 0)
+                    fetch(p.b_scale, tn * (BN / 128), (p.N + 127) / 128, to + kRows, BN / 128);
+                mbar_arrive(bar(B_SF + buf));
+            }
+        }
+    } else {
+        // --------------------------------------------------- scaled sums
+        // Warp: 32 rows (its TMEM lanes) and half of the columns.
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
+        constexpr int W = BN / 2;
+        const int quad = warp & 3, part = (warp - kSumWarp0) >> 2;
+        const uint32_t from = tmem + ((uint32_t)(32 * quad) << 16) + W * part;
+        const float *sc = reinterpret_cast<const float *>(smem + C::kScales);
+        uint32_t i = 0;
+        bool ok = true;
+        for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
+            F2 acc[W / 2];
+#pragma unroll
+            for (int c = 0; c < W / 2; ++c)
+                acc[c] = F2(0.f);
+            for (int k = 0; k < p.pieces; ++k, ++i) {
+                const uint32_t t = i & 1, n = i / C::kBatch;
+                if (i % C::kBatch == 0 && !mbar_wait_warp(bar(B_SF + (n & 1)), (n >> 1) & 1, abort_flag, p.status)) {
+                    ok = false;
+                    break;
+                }
+                const float *slot = sc + i % (2 * C::kBatch) * C::kScaled;
+                const F2 mine(slot[32 * quad + lane] * (ROWS ? 1.f : slot[kRows + W * part / 128]));
+                if (!mbar_wait_warp(bar(B_TF + t), (i >> 1) & 1, abort_flag, p.status)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const float4 *cs = reinterpret_cast<const float4 *>(slot + kRows + W * part);
+                auto add = [&](const uint32_t(&v)[32], int c) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        const F2 v0(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), v1(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
+                        F2 s0 = mine, s1 = mine;
+                        if (ROWS) {
+                            const float4 s = cs[(c + e) / 4];
+                            s0 = mine * F2(s.x, s.y);
+                            s1 = mine * F2(s.z, s.w);
+                        }
+                        acc[(c + e) / 2] = fma2(v0, s0, acc[(c + e) / 2]);
+                        acc[(c + e) / 2 + 1] = fma2(v1, s1, acc[(c + e) / 2 + 1]);
+                    }
+                };
+                // 64 columns in flight
+                uint32_t v0[32], v1[32];
+                tmem_ld32(from + t * BN, v0);
+                tmem_ld32(from + t * BN + 32, v1);
+                tmem_ld_wait_for(v0);
+                tmem_ld_wait_for(v1);
+                if constexpr (W > 64) {
+                    add(v0, 0);
+                    tmem_ld32(from + t * BN + 64, v0);
+                    add(v1, 32);
+                    tmem_ld32(from + t * BN + 96, v1);
+                    tmem_ld_wait_for(v0);
+                    tmem_ld_wait_for(v1);
+                }
+                tc_fence_before(); // read: the buffer may take the piece after the next
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(bar(B_TE + t));
+                add(v0, W - 64);
+                add(v1, W - 32);
+                if (i % C::kBatch == C::kBatch - 1) {
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(bar(B_SE + (n & 1)));
+                }
+            }
+            if (ok) {
+                int tm, tn;
+                tile_at(p, tile, tm, tn);
+                const int64_t row = (int64_t)tm * kRows + 32 * quad;
+                const int col = tn * BN + W * part;
+#pragma unroll
+                for (int c = 0; c < W; c += 16)
+                    if (col + c < p.N)
+                        store_sums(p, row, col + c, acc + c / 2, reinterpret_cast<float *>(smem + C::kPatches + (warp - kSumWarp0) * kPatch));
+            }
+        }
+    }
+
+    __syncwarp();
+    if (*abort_flag) { // copies may be in flight: a millisecond is far longer than any takes
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < 1000000ull) {
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 2 * BN);
+    }
+}
+
+template <int BN, bool ROWS>
+int launch(const GemmFp8Args &a, cudaStream_t stream, char *err, size_t errlen)
+{
+    using C = Cfg<BN, ROWS>;
+    const uintptr_t rows = reinterpret_cast<uintptr_t>(a.out) | (uintptr_t)(a.M > 1 ? a.ldo * (a.o32 ? 4 : 2) : 0);
+    Params p{a.a_scale, a.b_scale, a.M, a.N, (a.K + kGemmPiece - 1) / kGemmPiece, (a.M + kRows - 1) / kRows, (a.N + BN - 1) / BN, a.o32,
+             (int)(rows & 15 ? 0 : rows & 31 ? 16 : 32), a.out, a.ldo, device_status_ptr()};
+    if (!p.status) {
+        snprintf(err, errlen, "device status word unavailable");
+        return DSA_ERR_CUDA;
+    }
+    CUtensorMap ta{}, tb{};
+    if (a.K > 0 && (!gemm_fp8_map(&ta, a.a, a.lda, a.M, a.K, kRows, err, errlen) ||
+                    !gemm_fp8_map(&tb, a.b, a.ldb, a.N, a.K, BN, err, errlen)))
+        return DSA_ERR_CUDA;
+    static std::atomic<bool> raised[64], fits;
+    cudaError_t e = raise_smem_limit_once(gemm_fp8_tile_kernel<BN, ROWS>, C::kSmem, raised);
+    if (e == cudaSuccess && !fits.load(std::memory_order_acquire)) {
+        // the roles' shares of registers are cut from what the block is launched with
+        cudaFuncAttributes f;
+        e = cudaFuncGetAttributes(&f, gemm_fp8_tile_kernel<BN, ROWS>);
+        if (e == cudaSuccess && f.numRegs * kThreads < 32 * (kSumWarp0 * kAuxRegs + kSumWarps * kSumRegs)) {
+            snprintf(err, errlen, "gemm_fp8: built with %d registers a thread, too few to share out", f.numRegs);
+            return DSA_ERR_UNSUPPORTED;
+        }
+        fits.store(e == cudaSuccess, std::memory_order_release);
+    }
+    const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n, most = num_sms();
+    if (e == cudaSuccess)
+        e = launch_pdl(gemm_fp8_tile_kernel<BN, ROWS>, dim3((unsigned)(tiles < most ? tiles : most)), dim3(kThreads), C::kSmem, stream, 1,
+                       ta, tb, p);
+    if (e != cudaSuccess) {
+        snprintf(err, errlen, "gemm_fp8 launch: %s", cudaGetErrorString(e));
+        return DSA_ERR_CUDA;
+    }
+    return DSA_OK;
+}
+
+} // namespace
+
+int launch_gemm_fp8_tile(const GemmFp8Args &a, int cols, cudaStream_t stream, char *err, size_t errlen)
+{
+    if (cols <= 128)
+        return a.b_block ? launch<128, false>(a, stream, err, errlen) : launch<128, true>(a, stream, err, errlen);
+    return a.b_block ? launch<256, false>(a, stream, err, errlen) : launch<256, true>(a, stream, err, errlen);
+}
+
+} // namespace dsa
