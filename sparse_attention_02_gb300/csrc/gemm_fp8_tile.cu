@@ -19,7 +19,7 @@ constexpr int kSumWarp0 = 4, kSumWarps = 8;
 constexpr int kThreads = 32 * (kSumWarp0 + kSumWarps);
 constexpr int kGroup = 8;   // tiles along M that neighbouring tiles are taken from
 constexpr int kAuxRegs = 72, kSumRegs = 216; // of 168 a thread at launch
-constexpr int kPatch = 32 * 17 * 4; // 16 columns of a warp's rows, on their way to rows of out that are not aligned
+constexpr int kPatch = 32 * 64; // 64 bytes of each of a warp's rows of out, on their way there
 constexpr int kRows = 128;  // of a
 constexpr int kABytes = kRows * kGemmPiece;
 
@@ -28,9 +28,9 @@ template <int BN, bool ROWS> struct Cfg {
     static constexpr int kStages = BN == 256 ? 4 : 6;
     static constexpr int kBatch = ROWS ? 4 : 8;                   // pieces whose scales are fetched at once
     static constexpr int kScaled = kRows + (ROWS ? BN : BN / 128); // scales of a piece: a's, then b's
-    static constexpr int kScales = kStages * kStage;              // two batches
-    static constexpr int kPatches = kScales + 2 * kBatch * kScaled * 4;
-    static constexpr int kBars = (kPatches + kSumWarps * kPatch + 7) / 8 * 8;
+    static constexpr int kPatches = kStages * kStage;
+    static constexpr int kScales = kPatches + kSumWarps * kPatch; // two batches
+    static constexpr int kBars = (kScales + 2 * kBatch * kScaled * 4 + 7) / 8 * 8;
     static constexpr int kNumBars = 2 * kStages + 9;
     static constexpr int kMisc = kBars + 8 * kNumBars;
     static constexpr int kSmem = kMisc + 16;
@@ -41,7 +41,7 @@ struct Params {
     const float *a_scale, *b_scale;
     int M, N, pieces, tiles_m, tiles_n;
     bool o32;
-    int wide; // bytes that every row of out starts at a multiple of: 32, 16 or less
+    bool wide; // rows of out start at 16 bytes
     void *out;
     int64_t ldo;
     unsigned *status;
@@ -55,63 +55,48 @@ __device__ __forceinline__ void tile_at(const Params &p, int tile, int &m, int &
     m = first + r - n * rows;
 }
 
-// 16 sums of each of a warp's rows to out, from row m (of lane 0) and column n on.
-__device__ __forceinline__ void store_sums(const Params &p, int64_t m, int n, const F2 *acc, float *patch)
+// Sums of a warp's 32 rows to out, from row m (of lane 0) and column n on: 32 columns as bf16 or 16 as fp32, by way of
+// shared memory, where a row's four 16-byte words stand at place ^ (row / 2) so that neither side meets bank conflicts.
+// Eight rows then leave at a time; straight from the registers, where a lane holds a row, a tile took 5000 cycles.
+template <bool O32>
+__device__ __forceinline__ void store_sums(const Params &p, int64_t m, int n, const F2 *acc, uint8_t *patch)
 {
     const int lane = threadIdx.x & 31;
-    float f[16];
+    constexpr int e = O32 ? 4 : 2, cols = 64 / e;
+    __syncwarp();
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        acc[i].get(f[2 * i], f[2 * i + 1]);
-    if (p.N - n >= 16 && p.wide >= 16) { // a lane's columns are its own row's: 32 bytes a store fill whole sectors
-        if (m + lane >= p.M)
-            return;
-        uint32_t w[8];
-        if (p.o32) {
-            float *dst = static_cast<float *>(p.out) + (m + lane) * p.ldo + n;
+    for (int c = 0; c < 4; ++c) {
+        uint32_t w[4];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    w[k] = __float_as_uint(f[8 * e + k]);
-                if (p.wide == 32) {
-                    store32(dst + 8 * e, w);
-                } else {
-                    reinterpret_cast<uint4 *>(dst)[2 * e] = make_uint4(w[0], w[1], w[2], w[3]);
-                    reinterpret_cast<uint4 *>(dst)[2 * e + 1] = make_uint4(w[4], w[5], w[6], w[7]);
-                }
-            }
-        } else {
-            __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) + (m + lane) * p.ldo + n;
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                w[k] = pack2(f[2 * k], f[2 * k + 1]);
-            if (p.wide == 32) {
-                store32(dst, w);
-            } else {
-                reinterpret_cast<uint4 *>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                reinterpret_cast<uint4 *>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-            }
+        for (int k = 0; k < 4; ++k) {
+            float lo, hi;
+            acc[O32 ? 2 * c + (k >> 1) : 4 * c + k].get(lo, hi);
+            w[k] = !O32 ? pack2(lo, hi) : __float_as_uint(k & 1 ? hi : lo);
         }
+        *reinterpret_cast<uint4 *>(patch + lane * 64 + ((c ^ (lane >> 1 & 3)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __syncwarp();
+    uint8_t *out = static_cast<uint8_t *>(p.out) + (m * p.ldo + n) * e;
+    if (p.wide && p.N - n >= cols) {
+#pragma unroll
+        for (int r = lane >> 2; r < 32; r += 8)
+            if (m + r < p.M)
+                *reinterpret_cast<uint4 *>(out + r * p.ldo * e + 16 * (lane & 3)) =
+                    *reinterpret_cast<const uint4 *>(patch + r * 64 + (((lane & 3) ^ (r >> 1 & 3)) << 4));
         return;
     }
-    // by way of shared memory, so that lanes hold neighbouring columns of two rows at a time
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-        patch[lane * 17 + i] = f[i];
-    __syncwarp();
-    const int c = lane & 15;
+    const int c = lane % cols;
+    if (n + c >= p.N)
+        return;
 #pragma unroll 4
-    for (int r = lane >> 4; r < 32; r += 2) {
-        const float v = patch[r * 17 + c];
-        if (m + r < p.M && n + c < p.N) {
-            if (p.o32)
-                static_cast<float *>(p.out)[(m + r) * p.ldo + n + c] = v;
+    for (int r = lane / cols; r < 32; r += 32 / cols)
+        if (m + r < p.M) {
+            const uint8_t *at = patch + r * 64 + ((c * e / 16 ^ (r >> 1 & 3)) << 4) + c * e % 16;
+            if (O32)
+                *reinterpret_cast<uint32_t *>(out + (r * p.ldo + c) * e) = *reinterpret_cast<const uint32_t *>(at);
             else
-                static_cast<__nv_bfloat16 *>(p.out)[(m + r) * p.ldo + n + c] = __float2bfloat16_rn(v);
+                *reinterpret_cast<uint16_t *>(out + (r * p.ldo + c) * e) = *reinterpret_cast<const uint16_t *>(at);
         }
-    }
 }
 
 template <int BN, bool ROWS>
@@ -183,31 +168,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         } else if (warp == 1) {
             // --------------------------------------------------------- MMAs
+            // One thread, one loop, and nothing carried from turn to turn but its count: the MMAs' operands then come from
+            // uniform registers.  With stage and phase carried, or waits by the whole warp, four MMAs and two commits took
+            // 300 cycles to issue where this takes 50.
             if (elect_one()) {
                 constexpr uint32_t idesc = idesc_f32acc(kRows, BN, 0u, false, false);
-                const uint64_t ad = sdesc(sbase, 16, 1024, 2), bd = sdesc(sbase + kABytes, 16, 1024, 2);
-                uint32_t i = 0;
-                int st = 0, phase = 0;
-                bool ok = true;
-                for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x)
-                    for (int k = 0; k < p.pieces; ++k, ++i) {
-                        const uint32_t t = i & 1;
-                        ok = (i < 2 || mbar_wait(bar(B_TE + t), ((i >> 1) - 1) & 1, abort_flag, p.status)) &&
-                             mbar_wait(bar(B_FULL + st), phase, abort_flag, p.status);
-                        if (!ok)
-                            break;
-                        tc_fence_after();
-                        const uint64_t so = (uint64_t)((st * C::kStage) >> 4);
+                const int first = blockIdx.x, total = first < tiles ? ((tiles - 1 - first) / (int)gridDim.x + 1) * p.pieces : 0;
+                for (int i = 0; i < total; ++i) {
+                    const int st = i % C::kStages, t = i & 1;
+                    if (!mbar_wait(bar(B_FULL + st), (i / C::kStages) & 1, abort_flag, p.status) ||
+                        (i >= 2 && !mbar_wait(bar(B_TE + t), ((i >> 1) - 1) & 1, abort_flag, p.status)))
+                        break;
+                    tc_fence_after();
+                    const uint64_t ad = sdesc(sbase + st * C::kStage, 16, 1024, 2), bd = sdesc(sbase + st * C::kStage + kABytes, 16, 1024, 2);
 #pragma unroll
-                        for (int s = 0; s < 4; ++s)
-                            umma_f8f6f4(tmem + t * BN, ad + so + 2 * s, bd + so + 2 * s, idesc, s > 0);
-                        umma_commit(bar(B_TF + t));
-                        umma_commit(bar(B_EMPTY + st));
-                        if (++st == C::kStages) {
-                            st = 0;
-                            phase ^= 1;
-                        }
-                    }
+                    for (int s = 0; s < 4; ++s)
+                        umma_f8f6f4(tmem + t * BN, ad + 2 * s, bd + 2 * s, idesc, s > 0);
+                    umma_commit(bar(B_TF + t));
+                    umma_commit(bar(B_EMPTY + st));
+                }
                 umma_commit(bar(B_DONE));
                 mbar_drain(bar(B_DONE), 0);
             }
@@ -258,6 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int quad = warp & 3, part = (warp - kSumWarp0) >> 2;
         const uint32_t from = tmem + ((uint32_t)(32 * quad) << 16) + W * part;
         const float *sc = reinterpret_cast<const float *>(smem + C::kScales);
+        uint8_t *patch = smem + C::kPatches + (warp - kSumWarp0) * kPatch;
         uint32_t i = 0;
         bool ok = true;
         for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
@@ -324,10 +304,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tile_at(p, tile, tm, tn);
                 const int64_t row = (int64_t)tm * kRows + 32 * quad;
                 const int col = tn * BN + W * part;
+                if (p.o32) {
 #pragma unroll
-                for (int c = 0; c < W; c += 16)
-                    if (col + c < p.N)
-                        store_sums(p, row, col + c, acc + c / 2, reinterpret_cast<float *>(smem + C::kPatches + (warp - kSumWarp0) * kPatch));
+                    for (int c = 0; c < W; c += 16)
+                        if (col + c < p.N)
+                            store_sums<true>(p, row, col + c, acc + c / 2, patch);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < W; c += 32)
+                        if (col + c < p.N)
+                            store_sums<false>(p, row, col + c, acc + c / 2, patch);
+                }
             }
         }
     }
@@ -352,7 +339,7 @@ int launch(const GemmFp8Args &a, cudaStream_t stream, char *err, size_t errlen)
     using C = Cfg<BN, ROWS>;
     const uintptr_t rows = reinterpret_cast<uintptr_t>(a.out) | (uintptr_t)(a.M > 1 ? a.ldo * (a.o32 ? 4 : 2) : 0);
     Params p{a.a_scale, a.b_scale, a.M, a.N, (a.K + kGemmPiece - 1) / kGemmPiece, (a.M + kRows - 1) / kRows, (a.N + BN - 1) / BN, a.o32,
-             (int)(rows & 15 ? 0 : rows & 31 ? 16 : 32), a.out, a.ldo, device_status_ptr()};
+             (rows & 15) == 0, a.out, a.ldo, device_status_ptr()};
     if (!p.status) {
         snprintf(err, errlen, "device status word unavailable");
         return DSA_ERR_CUDA;
