@@ -36,10 +36,11 @@ template <int BT> struct Cfg {
     static constexpr int kStages = BT <= 16 ? 6 : BT <= 32 ? 5 : BT <= 64 ? 4 : 6;
     static constexpr int kScales = kStages * kStage;            // two batches of [kBatch][BT] fp32
     static constexpr int kBars = kScales + 2 * kBatch * BT * 4;
-    static constexpr int kNumBars = 2 * kStages + 9;
+    static constexpr int kBuffers = BT <= 64 ? 4 : 2;            // of BT columns of TMEM
+    static constexpr int kNumBars = 2 * kStages + 2 * kBuffers + 5;
     static constexpr int kMisc = kBars + 8 * kNumBars;
     static constexpr int kSmem = kMisc + 16;
-    static constexpr int kTmemCols = 2 * BT < 32 ? 32 : 2 * BT;
+    static constexpr int kTmemCols = kBuffers * BT;
     static_assert(BT * kRows * 4 <= kScales, "the split's sums take the stages' place");
 };
 
@@ -51,13 +52,6 @@ struct Params {
     int64_t ldo;
     unsigned *status;
 };
-
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr)
-{
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
-}
 
 __device__ __forceinline__ void put(const Params &p, int64_t m, int64_t n, float v)
 {
@@ -75,8 +69,8 @@ __global__ void __launch_bounds__(kThreads, BT <= 64 ? 2 : 1)
     extern __shared__ __align__(1024) uint8_t smem[]; // the swizzle's period
     const uint32_t sbase = smem_u32(smem);
     auto bar = [&](int i) { return sbase + C::kBars + 8u * i; };
-    constexpr int B_FULL = 0, B_EMPTY = C::kStages, B_TF = 2 * C::kStages, B_TE = B_TF + 2, B_SF = B_TF + 4, B_SE = B_TF + 6,
-                  B_DONE = B_TF + 8;
+    constexpr int B_FULL = 0, B_EMPTY = C::kStages, B_TF = 2 * C::kStages, B_TE = B_TF + C::kBuffers, B_SF = B_TE + C::kBuffers,
+                  B_SE = B_SF + 2, B_DONE = B_SE + 2;
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + C::kMisc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::kMisc + 4);
     float *scales = reinterpret_cast<float *>(smem + C::kScales);
@@ -92,9 +86,11 @@ __global__ void __launch_bounds__(kThreads, BT <= 64 ? 2 : 1)
             mbar_init(bar(B_FULL + i), 1);
             mbar_init(bar(B_EMPTY + i), 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < C::kBuffers; ++i) {
             mbar_init(bar(B_TF + i), 1);
             mbar_init(bar(B_TE + i), kSumWarps);
+        }
+        for (int i = 0; i < 2; ++i) {
             mbar_init(bar(B_SF + i), 32);
             mbar_init(bar(B_SE + i), kSumWarps);
         }
@@ -132,21 +128,20 @@ __global__ void __launch_bounds__(kThreads, BT <= 64 ? 2 : 1)
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------- MMAs
+        // one plain loop, nothing carried but its count: the MMAs' operands come from uniform registers
         if (elect_one()) {
             constexpr uint32_t idesc = idesc_f32acc(128, BT, 0u, false, false);
-            const uint64_t bd = sdesc(sbase, 16, 1024, 2), ad = sdesc(sbase + kRowBytes, 16, 1024, 2);
-            bool ok = true;
-            for (int k = k0, i = 0; ok && k < k1; ++k, ++i) {
-                const int st = i % C::kStages, use = i / C::kStages, t = i & 1;
-                ok = (i < 2 || mbar_wait(bar(B_TE + t), ((i >> 1) - 1) & 1, abort_flag, p.status)) &&
-                     mbar_wait(bar(B_FULL + st), use & 1, abort_flag, p.status);
-                if (!ok)
+            const int total = k1 - k0;
+            for (int i = 0; i < total; ++i) {
+                const int st = i % C::kStages, t = i % C::kBuffers;
+                if (!mbar_wait(bar(B_FULL + st), (i / C::kStages) & 1, abort_flag, p.status) ||
+                    (i >= C::kBuffers && !mbar_wait(bar(B_TE + t), (i / C::kBuffers - 1) & 1, abort_flag, p.status)))
                     break;
                 tc_fence_after();
-                const uint64_t so = (uint64_t)((st * C::kStage) >> 4);
+                const uint64_t bd = sdesc(sbase + st * C::kStage, 16, 1024, 2), ad = sdesc(sbase + st * C::kStage + kRowBytes, 16, 1024, 2);
 #pragma unroll
                 for (int s = 0; s < 4; ++s)
-                    umma_f8f6f4(tmem + t * BT, bd + so + 2 * s, ad + so + 2 * s, idesc, s > 0);
+                    umma_f8f6f4(tmem + t * BT, bd + 2 * s, ad + 2 * s, idesc, s > 0);
                 umma_commit(bar(B_TF + t));
                 umma_commit(bar(B_EMPTY + st));
             }
@@ -193,21 +188,17 @@ __global__ void __launch_bounds__(kThreads, BT <= 64 ? 2 : 1)
             acc[c] = F2(0.f);
         bool ok = true;
         for (int k = k0, i = 0; ok && k < k1; ++k, ++i) {
-            const int t = i & 1, batch = i / kBatch, buf = batch & 1;
+            const int t = i % C::kBuffers, batch = i / kBatch, buf = batch & 1;
             const F2 mine(next);
             next = scaled && k + 1 < k1 ? sb[k + 1] : 1.f;
             if ((i % kBatch == 0 && !mbar_wait_warp(bar(B_SF + buf), (batch >> 1) & 1, abort_flag, p.status)) ||
-                !mbar_wait_warp(bar(B_TF + t), (i >> 1) & 1, abort_flag, p.status)) {
+                !mbar_wait_warp(bar(B_TF + t), (i / C::kBuffers) & 1, abort_flag, p.status)) {
                 ok = false;
                 break;
             }
             tc_fence_after();
             const float4 *cs = reinterpret_cast<const float4 *>(scales + (buf * kBatch + i % kBatch) * BT);
-#pragma unroll
-            for (int c = 0; c < BT; c += W) {
-                uint32_t v[W];
-                tmem_load(from + t * BT + c, v);
-                tmem_ld_wait_for(v);
+            auto add = [&](const uint32_t(&v)[W], int c) {
 #pragma unroll
                 for (int e = 0; e < W; e += 4) {
                     const float4 s = cs[(c + e) / 4];
@@ -220,14 +211,23 @@ __global__ void __launch_bounds__(kThreads, BT <= 64 ? 2 : 1)
                     acc[(c + e) / 2] = fma2(v0, s0, acc[(c + e) / 2]);
                     acc[(c + e) / 2 + 1] = fma2(v1, s1, acc[(c + e) / 2 + 1]);
                 }
+            };
+#pragma unroll
+            for (int c = 0; c < BT; c += W) {
+                uint32_t v[W];
+                tmem_load(from + t * BT + c, v);
+                tmem_ld_wait_for(v);
+                if (c + W == BT) { // read: the buffer may take another product
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(bar(B_TE + t));
+                }
+                add(v, c);
             }
-            tc_fence_before();
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(bar(B_TE + t));
-                if (i % kBatch == kBatch - 1)
-                    mbar_arrive(bar(B_SE + buf));
-            }
+            if (lane == 0 && i % kBatch == kBatch - 1)
+                mbar_arrive(bar(B_SE + buf));
         }
         // every product is done, as the last one is.  Lanes hold consecutive columns of out.
 #pragma unroll
@@ -258,13 +258,14 @@ __global__ void __launch_bounds__(kThreads, BT <= 64 ? 2 : 1)
     if (split == 1)
         return;
     cluster_sync_all();
-    const int r = threadIdx.x & (kRows - 1);
-    for (int t = (int)rank + (int)split * (threadIdx.x >> 7); t < left; t += 2 * split) {
-        float v = 0.f;
-        for (uint32_t c = 0; c < split; ++c)
-            v += ld_cluster_f32(mapa_shared(sbase + (t * kRows + r) * 4, c));
-        if (n0 + r < p.N)
-            put(p, m0 + t, n0 + r, v);
+    const int r = 4 * lane; // a warp takes a column of the sums, a lane four rows
+    for (int t = (int)rank + (int)split * warp; t < left; t += split * (kThreads / 32)) {
+        const float4 v = sums_of_cluster(sbase + (t * kRows + r) * 4, split);
+        const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (n0 + r + e < p.N)
+                put(p, m0 + t, n0 + r + e, f[e]);
     }
     cluster_sync_all(); // no CTA leaves while its peers read its sums
 }

@@ -34,6 +34,7 @@ template <int BN, bool ROWS> struct Cfg {
     static constexpr int kNumBars = 2 * kStages + 9;
     static constexpr int kMisc = kBars + 8 * kNumBars;
     static constexpr int kSmem = kMisc + 16;
+    static_assert((BN + BN / 2 + 1) * kRows * 4 <= kScales, "a split's sums, and what the CTA adds up, take the stages' place");
     static_assert(kSmem <= 232448, "dynamic shared memory above the 227 KB a CTA may hold");
 };
 
@@ -112,7 +113,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + C::kMisc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::kMisc + 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int tiles = p.tiles_m * p.tiles_n;
+    // The CTAs of a cluster share a tile and take a part of its pieces each.
+    const uint32_t rank = cluster_ctarank(), split = cluster_nctarank();
+    const int tiles = p.tiles_m * p.tiles_n, first = blockIdx.x / split, step = gridDim.x / split;
+    const int k0 = (int)((int64_t)p.pieces * rank / split), pieces = (int)((int64_t)p.pieces * (rank + 1) / split) - k0;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kStages; ++i) {
@@ -145,18 +149,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             // -------------------------------------------------------- loads
             int st = 0, phase = 0;
             bool ok = true, again = false; // again: every stage was filled once
-            for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
+            for (int tile = first; ok && tile < tiles; tile += step) {
                 int tm, tn;
                 tile_at(p, tile, tm, tn);
-                for (int k = 0; k < p.pieces; ++k) {
+                for (int k = 0; k < pieces; ++k) {
                     if (again && !mbar_wait_warp(bar(B_EMPTY + st), phase ^ 1, abort_flag, p.status)) {
                         ok = false;
                         break;
                     }
                     if (elect_one()) {
                         mbar_arrive_expect_tx(bar(B_FULL + st), C::kStage);
-                        tma_load_2d(sbase + st * C::kStage, &tm_a, bar(B_FULL + st), k * kGemmPiece, tm * kRows);
-                        tma_load_2d(sbase + st * C::kStage + kABytes, &tm_b, bar(B_FULL + st), k * kGemmPiece, tn * BN);
+                        tma_load_2d(sbase + st * C::kStage, &tm_a, bar(B_FULL + st), (k0 + k) * kGemmPiece, tm * kRows);
+                        tma_load_2d(sbase + st * C::kStage + kABytes, &tm_b, bar(B_FULL + st), (k0 + k) * kGemmPiece, tn * BN);
                     }
                     __syncwarp();
                     if (++st == C::kStages) {
@@ -173,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // 300 cycles to issue where this takes 50.
             if (elect_one()) {
                 constexpr uint32_t idesc = idesc_f32acc(kRows, BN, 0u, false, false);
-                const int first = blockIdx.x, total = first < tiles ? ((tiles - 1 - first) / (int)gridDim.x + 1) * p.pieces : 0;
+                const int total = first < tiles ? ((tiles - 1 - first) / step + 1) * pieces : 0;
                 for (int i = 0; i < total; ++i) {
                     const int st = i % C::kStages, t = i & 1;
                     if (!mbar_wait(bar(B_FULL + st), (i / C::kStages) & 1, abort_flag, p.status) ||
@@ -196,13 +200,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             // Batches of this CTA's pieces, counted through its tiles: kBatch lanes along the pieces, 32 / kBatch rows at
             // a time; the two warps take half of the rows each.
             constexpr int R = 32 / C::kBatch;
-            const int kk = lane % C::kBatch, r0 = lane / C::kBatch, half = warp - 2, first = blockIdx.x;
-            const int total = first < tiles ? ((tiles - 1 - first) / (int)gridDim.x + 1) * p.pieces : 0;
+            const int kk = lane % C::kBatch, r0 = lane / C::kBatch, half = warp - 2;
+            const int total = first < tiles ? ((tiles - 1 - first) / step + 1) * pieces : 0;
             for (int i = 0; i < total; i += C::kBatch) {
-                const int n = i / C::kBatch, buf = n & 1, mine = i + kk < total ? i + kk : total - 1, nth = mine / p.pieces;
-                const int k = mine - nth * p.pieces;
+                const int n = i / C::kBatch, buf = n & 1, mine = i + kk < total ? i + kk : total - 1, nth = mine / pieces;
+                const int k = k0 + mine - nth * pieces;
                 int tm, tn;
-                tile_at(p, first + nth * (int)gridDim.x, tm, tn);
+                tile_at(p, first + nth * step, tm, tn);
                 if (n >= 2 && !mbar_wait_warp(bar(B_SE + buf), ((n >> 1) - 1) & 1, abort_flag, p.status))
                     break;
                 float *to = reinterpret_cast<float *>(smem + C::kScales) + (buf * C::kBatch + kk) * C::kScaled;
@@ -240,12 +244,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint8_t *patch = smem + C::kPatches + (warp - kSumWarp0) * kPatch;
         uint32_t i = 0;
         bool ok = true;
-        for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
+        for (int tile = first; ok && tile < tiles; tile += step) {
             F2 acc[W / 2];
 #pragma unroll
             for (int c = 0; c < W / 2; ++c)
                 acc[c] = F2(0.f);
-            for (int k = 0; k < p.pieces; ++k, ++i) {
+            for (int k = 0; k < pieces; ++k, ++i) {
                 const uint32_t t = i & 1, n = i / C::kBatch;
                 if (i % C::kBatch == 0 && !mbar_wait_warp(bar(B_SF + (n & 1)), (n >> 1) & 1, abort_flag, p.status)) {
                     ok = false;
@@ -299,7 +303,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                         mbar_arrive(bar(B_SE + (n & 1)));
                 }
             }
-            if (ok) {
+            if (split > 1) { // this CTA's sums, over the stages: the last product is done
+#pragma unroll
+                for (int c = 0; c < W / 2; ++c) {
+                    float v[2];
+                    acc[c].get(v[0], v[1]);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        reinterpret_cast<float *>(smem)[(W * part + 2 * c + e) * kRows + 32 * quad + lane] = v[e];
+                }
+            } else if (ok) {
                 int tm, tn;
                 tile_at(p, tile, tm, tn);
                 const int64_t row = (int64_t)tm * kRows + 32 * quad;
@@ -331,10 +344,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         tmem_dealloc(tmem, 2 * BN);
     }
+    if (split == 1)
+        return;
+    // The cluster's CTAs add up the columns of the tile between them, each sum in the CTAs' order: lanes along rows, as the
+    // sums lie, turned in this CTA's own shared memory into lanes along columns, as they leave.
+    cluster_sync_all();
+    int tm, tn;
+    tile_at(p, first, tm, tn);
+    const int cols = BN / split, c0 = cols * rank, pitch = cols + 1;
+    float *turned = reinterpret_cast<float *>(smem) + BN * kRows;
+    for (int x = 4 * threadIdx.x; x < cols * kRows; x += 4 * kThreads) {
+        const float4 v = sums_of_cluster(sbase + 4 * (c0 * kRows + x), split);
+        float *to = turned + x % kRows * pitch + x / kRows;
+        to[0] = v.x, to[pitch] = v.y, to[2 * pitch] = v.z, to[3 * pitch] = v.w;
+    }
+    __syncthreads();
+    for (int x = threadIdx.x; x < cols * kRows; x += kThreads) {
+        const int64_t m = (int64_t)tm * kRows + x / cols, n = (int64_t)tn * BN + c0 + x % cols;
+        const float v = turned[x / cols * pitch + x % cols];
+        if (m < p.M && n < p.N) {
+            if (p.o32)
+                static_cast<float *>(p.out)[m * p.ldo + n] = v;
+            else
+                static_cast<__nv_bfloat16 *>(p.out)[m * p.ldo + n] = __float2bfloat16_rn(v);
+        }
+    }
+    cluster_sync_all(); // no CTA leaves while its peers read its sums
 }
 
 template <int BN, bool ROWS>
-int launch(const GemmFp8Args &a, cudaStream_t stream, char *err, size_t errlen)
+int launch(const GemmFp8Args &a, int split, cudaStream_t stream, char *err, size_t errlen)
 {
     using C = Cfg<BN, ROWS>;
     const uintptr_t rows = reinterpret_cast<uintptr_t>(a.out) | (uintptr_t)(a.M > 1 ? a.ldo * (a.o32 ? 4 : 2) : 0);
@@ -362,8 +401,8 @@ int launch(const GemmFp8Args &a, cudaStream_t stream, char *err, size_t errlen)
     }
     const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n, most = num_sms();
     if (e == cudaSuccess)
-        e = launch_pdl(gemm_fp8_tile_kernel<BN, ROWS>, dim3((unsigned)(tiles < most ? tiles : most)), dim3(kThreads), C::kSmem, stream, 1,
-                       ta, tb, p);
+        e = launch_pdl(gemm_fp8_tile_kernel<BN, ROWS>, dim3((unsigned)(split > 1 ? tiles * split : tiles < most ? tiles : most)),
+                       dim3(kThreads), C::kSmem, stream, split, ta, tb, p);
     if (e != cudaSuccess) {
         snprintf(err, errlen, "gemm_fp8 launch: %s", cudaGetErrorString(e));
         return DSA_ERR_CUDA;
@@ -373,11 +412,11 @@ int launch(const GemmFp8Args &a, cudaStream_t stream, char *err, size_t errlen)
 
 } // namespace
 
-int launch_gemm_fp8_tile(const GemmFp8Args &a, int cols, cudaStream_t stream, char *err, size_t errlen)
+int launch_gemm_fp8_tile(const GemmFp8Args &a, int cols, int split, cudaStream_t stream, char *err, size_t errlen)
 {
     if (cols <= 128)
-        return a.b_block ? launch<128, false>(a, stream, err, errlen) : launch<128, true>(a, stream, err, errlen);
-    return a.b_block ? launch<256, false>(a, stream, err, errlen) : launch<256, true>(a, stream, err, errlen);
+        return a.b_block ? launch<128, false>(a, split, stream, err, errlen) : launch<128, true>(a, split, stream, err, errlen);
+    return a.b_block ? launch<256, false>(a, split, stream, err, errlen) : launch<256, true>(a, split, stream, err, errlen);
 }
 
 } // namespace dsa
