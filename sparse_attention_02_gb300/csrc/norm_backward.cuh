@@ -8,11 +8,12 @@
 namespace dsa {
 namespace {
 
-// One row of the backward; dw: this thread's dweight sums, and behind them its
-// dbias sums.
-template <typename T, typename W, int NV, bool WARP, bool VEC, bool LN>
-__device__ __forceinline__ void norm_backward_row(const NormBackwardArgs &a, const T *hp, const T *dp, const T *ep,
-                                                  int64_t row, float (&dw)[LN ? 2 * NV : NV][8], float *red)
+constexpr int kLayerRowThreads = 512, kLayerRowCtas = 2; // of layer norm whose warps own rows, and CTAs an SM
+
+// One row of the RMS norm's backward; dw: this thread's dweight sums.
+template <typename T, typename W, int NV, bool WARP, bool VEC>
+__device__ __forceinline__ void rmsnorm_backward_row(const NormBackwardArgs &a, const T *hp, const T *dp, const T *ep,
+                                                     int64_t row, float (&dw)[NV][8], float *red)
 {
     const int G = WARP ? 32 : blockDim.x;
     const int g = WARP ? (threadIdx.x & 31) : threadIdx.x;
@@ -26,38 +27,14 @@ __device__ __forceinline__ void norm_backward_row(const NormBackwardArgs &a, con
         load_chunk<VEC>(hv[c], hp, chunk_base<VEC>(c, G, g), cols);
         load_chunk<VEC>(dv[c], dp, chunk_base<VEC>(c, G, g), cols);
     }
-    float mean = 0.f, mean_g = 0.f;
-    if (LN) {
-#pragma unroll
-        for (int c = 0; c < NV; ++c) {
-            float h[8], d[8], w[8], s = 0.f, t = 0.f;
-            load_weights<T, VEC>(w, weight, chunk_base<VEC>(c, G, g), cols);
-            hv[c].get(h);
-            dv[c].get(d);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                s += h[i];
-                t = fmaf(d[i], w[i], t);
-            }
-            ss += s;
-            sg += t;
-        }
-        const float2 sums = group_reduce<WARP, false>(ss, sg, red);
-        mean = sums.x / (float)cols;
-        mean_g = sums.y / (float)cols;
-        ss = sg = 0.f;
-    }
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
-        const int cb = chunk_base<VEC>(c, G, g);
         float h[8], d[8], w[8], s = 0.f, t = 0.f;
-        load_weights<T, VEC>(w, weight, cb, cols);
+        load_weights<T, VEC>(w, weight, chunk_base<VEC>(c, G, g), cols);
         hv[c].get(h);
         dv[c].get(d);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            if (LN)
-                h[i] = (VEC ? cb < cols : column<T, VEC>(cb, i) < cols) ? h[i] - mean : 0.f;
             s = fmaf(h[i], h[i], s);
             t = fmaf(d[i] * w[i], h[i], t);
         }
@@ -76,13 +53,7 @@ __device__ __forceinline__ void norm_backward_row(const NormBackwardArgs &a, con
         dv[c].get(d);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            if (LN) { // past cols d is zero
-                h[i] -= mean;
-                o[i] = r * ((d[i] * w[i] - mean_g) - h[i] * k);
-                dw[NV + c][i] += d[i];
-            } else {
-                o[i] = r * (d[i] * w[i] - h[i] * k);
-            }
+            o[i] = r * (d[i] * w[i] - h[i] * k);
             dw[c][i] = fmaf(d[i], h[i] * r, dw[c][i]);
         }
         if (ep) {
@@ -97,6 +68,132 @@ __device__ __forceinline__ void norm_backward_row(const NormBackwardArgs &a, con
         Vec8<T> v;
         v.set(o);
         store_chunk<VEC>(v, dx, cb, cols);
+    }
+}
+
+template <int N> __device__ __forceinline__ void clear(F2 (&v)[N][4])
+{
+#pragma unroll
+    for (int c = 0; c < N; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v[c][i] = F2(0.f);
+}
+
+template <int N> __device__ __forceinline__ void unpack(const F2 (&v)[N][4], float (&f)[N][8])
+{
+#pragma unroll
+    for (int c = 0; c < N; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v[c][i].get(f[c][2 * i], f[c][2 * i + 1]);
+}
+
+// One row of layer norm's backward.  WARP: LANES lanes own it.  dw: this thread's dweight sums, and behind them its dbias
+// sums.  red: kMoments floats.  Values are unpacked once and worked on in pairs: with a CTA's 512 threads on one row, its
+// instructions and the meeting's latency add up (8192 x 8192 with single operations on values unpacked in each pass 117 us).
+template <typename T, typename W, int NV, bool WARP, bool VEC, int LANES>
+__device__ __forceinline__ void layernorm_backward_row(const NormBackwardArgs &a, const T *hp, const T *dp, const T *ep, int64_t row,
+                                                       bool there, const Held<T, W, NV, VEC> &held, F2 (&dw)[2 * NV][4], float *red)
+{
+    const int G = WARP ? LANES : blockDim.x;
+    const int g = WARP ? (threadIdx.x & (LANES - 1)) : threadIdx.x;
+    const int cols = a.cols;
+    const W *weight = static_cast<const W *>(a.weight);
+    F2 h[NV][4], d[NV][4], gw[NV][4]; // h, dy, dy weight
+    F2 s2(0.f), t2(0.f);
+    {
+        Vec8<T> hv[NV], dv[NV];
+#pragma unroll
+        for (int c = 0; c < NV; ++c) {
+            load_chunk<VEC>(hv[c], hp, chunk_base<VEC>(c, G, g), there ? cols : 0);
+            load_chunk<VEC>(dv[c], dp, chunk_base<VEC>(c, G, g), there ? cols : 0);
+        }
+#pragma unroll
+        for (int c = 0; c < NV; ++c) {
+            float x[8], y[8], w[8];
+            held.get(w, weight, c, chunk_base<VEC>(c, G, g), cols);
+            hv[c].get(x);
+            dv[c].get(y);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                h[c][i] = F2(x[2 * i], x[2 * i + 1]);
+                d[c][i] = F2(y[2 * i], y[2 * i + 1]);
+                gw[c][i] = d[c][i] * F2(w[2 * i], w[2 * i + 1]);
+                s2 = s2 + h[c][i];
+                t2 = t2 + gw[c][i];
+            }
+        }
+    }
+    const float sum = warp_sum<LANES>(s2.sum());
+    float sg = warp_sum<LANES>(t2.sum());
+    const int n = WARP ? cols : warp_columns<NV>(G, g >> 5, cols);
+    float mean = n ? sum / (float)n : 0.f; // the warp's own
+    const F2 back(-mean);
+    s2 = t2 = F2(0.f);
+#pragma unroll
+    for (int c = 0; c < NV; ++c) {
+        const int cb = chunk_base<VEC>(c, G, g);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            h[c][i] = h[c][i] + back;
+            if (VEC ? cb >= cols : column<T, VEC>(cb, 2 * i) >= cols) // past cols: no part of the sum of squares
+                h[c][i] = F2(0.f);
+            else if (!VEC && column<T, VEC>(cb, 2 * i + 1) >= cols) {
+                float lo, hi;
+                h[c][i].get(lo, hi);
+                h[c][i] = F2(lo, 0.f);
+            }
+            s2 = fma2(h[c][i], h[c][i], s2);
+            t2 = fma2(gw[c][i], h[c][i], t2);
+        }
+    }
+    float sq = warp_sum<LANES>(s2.sum()), gd = warp_sum<LANES>(t2.sum());
+    float off = 0.f; // of the row's mean from the warp's
+    if constexpr (!WARP) {
+        const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+        if (lane == 0) {
+            float *to = red + (threadIdx.x >> 5);
+            to[0] = sum, to[32] = sq, to[64] = sg, to[96] = gd;
+        }
+        __syncthreads();
+        const int m = lane < warps ? warp_columns<NV>(G, lane, cols) : 0;
+        const float mine = m ? red[lane] : 0.f, g_mine = m ? red[64 + lane] : 0.f;
+        const float all = warp_sum(mine) / (float)cols;
+        const float dm = m ? mine / (float)m - all : 0.f;
+        sg = warp_sum(g_mine);
+        sq = warp_sum(m ? red[32 + lane] + (float)m * dm * dm : 0.f);
+        gd = warp_sum(m ? fmaf(dm, g_mine, red[96 + lane]) : 0.f);
+        off = mean - all;
+    }
+    const float r = 1.f / sqrtf(sq / (float)cols + a.eps);
+    const float k = gd * r * r / (float)cols, mean_g = sg / (float)cols; // k: mean(g xhat) r
+    if (!there)
+        return;
+    const F2 off2(off), r2(r), k2(-k), mg2(-mean_g);
+#pragma unroll
+    for (int c = 0; c < NV; ++c) {
+        const int cb = chunk_base<VEC>(c, G, g);
+        float o[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) { // past cols d is zero
+            const F2 x = h[c][i] + off2;
+            (fma2(x, k2, gw[c][i] + mg2) * r2).get(o[2 * i], o[2 * i + 1]);
+            dw[c][i] = fma2(d[c][i], x * r2, dw[c][i]);
+            dw[NV + c][i] = dw[NV + c][i] + d[c][i];
+        }
+        if (ep) {
+            float e[8];
+            Vec8<T> ev;
+            load_chunk<VEC>(ev, ep, cb, cols);
+            ev.get(e);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                o[i] += e[i];
+        }
+        Vec8<T> v;
+        v.set(o);
+        store_chunk<VEC>(v, static_cast<T *>(a.dx) + row * cols, cb, cols);
     }
 }
 
@@ -148,30 +245,77 @@ template <int NV> __device__ __forceinline__ bool join_warps(float (&dw)[NV][8],
     return true;
 }
 
+// Layer norm's form: every warp's sums side by side, [warps][32 * 8 * N] floats, added up column by column.
+template <int N, int LANES> __device__ __forceinline__ bool join_warps_at_once(float (&dw)[N][8], float *sums)
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int c = 0; c < N; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (LANES == 16) // both halves hold the same columns
+                dw[c][i] += __shfl_xor_sync(0xffffffffu, dw[c][i], 16);
+            sums[((threadIdx.x >> 5) * N + c) * 256 + i * 32 + lane] = dw[c][i];
+        }
+    __syncthreads();
+    for (int x = threadIdx.x; x < 256 * N; x += blockDim.x) {
+        float t = sums[x];
+        for (int w = 1; w < (int)blockDim.x >> 5; ++w)
+            t += sums[w * 256 * N + x];
+        sums[x] = t;
+    }
+    __syncthreads();
+    if (threadIdx.x >= LANES)
+        return false;
+#pragma unroll
+    for (int c = 0; c < N; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            dw[c][i] = sums[c * 256 + i * 32 + lane];
+    return true;
+}
+
 // Backward.  Each CTA walks rows b, b + grid, ... with its dweight sums in
 // registers.
-template <typename T, typename W, int NV, bool WARP, bool VEC, bool LN>
-__global__ void __launch_bounds__(WARP ? kRowThreads : 1024)
+// LANES: 16 where layer norm's rows are that many chunks (two rows a warp: 32767 x 128 fp32 20 us with one).
+template <typename T, typename W, int NV, bool WARP, bool VEC, bool LN, int LANES>
+__global__ void __launch_bounds__(WARP ? (LN ? kLayerRowThreads : kRowThreads) : 1024, WARP && LN ? kLayerRowCtas : 1)
     norm_backward_kernel(NormBackwardArgs a, float *part)
 {
-    __shared__ float red[64];
-    constexpr int N = LN ? 2 * NV : NV;
-    __shared__ float dws[WARP ? 32 * 8 * N : 1];
+    constexpr int N = LN ? 2 * NV : NV, kOwners = (LN ? kLayerRowThreads : kRowThreads) / LANES; // rows a CTA has at work
+    __shared__ float red[LN ? 2 * kMoments : 64];
+    __shared__ float dws[WARP ? 32 * 8 * N * (LN ? kLayerRowThreads / 32 : 1) : 1];
     grid_dep_wait();
     grid_dep_launch();
-    const int G = WARP ? 32 : blockDim.x;
-    const int g = WARP ? (threadIdx.x & 31) : threadIdx.x;
-    const int64_t row0 = WARP ? (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5) : blockIdx.x;
-    const int64_t step = (int64_t)gridDim.x * (WARP ? kRowThreads / 32 : 1);
+    const int G = WARP ? LANES : blockDim.x;
+    const int g = WARP ? (threadIdx.x & (LANES - 1)) : threadIdx.x;
+    const int64_t row0 = WARP ? (int64_t)blockIdx.x * kOwners + threadIdx.x / LANES : blockIdx.x;
+    const int64_t step = (int64_t)gridDim.x * (WARP ? kOwners : 1);
     const int cols = a.cols;
+    const T *h = static_cast<const T *>(a.h), *dy = static_cast<const T *>(a.dy), *dres = static_cast<const T *>(a.dres);
+    [[maybe_unused]] F2 dw2[N][4];
     float dw[N][8] = {};
-    for (int64_t row = row0; row < a.rows; row += step)
-        norm_backward_row<T, W, NV, WARP, VEC, LN>(a, static_cast<const T *>(a.h) + row * cols,
-                                                  static_cast<const T *>(a.dy) + row * cols,
-                                                  a.dres ? static_cast<const T *>(a.dres) + row * cols : nullptr, row, dw, red);
-    if (WARP && !join_warps<N>(dw, dws))
-        return;
-    store_part<T, VEC, NV>(part, dw, G, g, cols);
+    if constexpr (LN) {
+        Held<T, W, NV, VEC> held;
+        clear(dw2);
+        held.load(static_cast<const W *>(a.weight), G, g, cols);
+        int turn = 0;
+        // a warp's two rows walk together: its lanes add up among themselves
+        for (int64_t row = row0; row - (WARP ? threadIdx.x % 32 / LANES : 0) < a.rows; row += step, turn ^= 1)
+            layernorm_backward_row<T, W, NV, WARP, VEC, LANES>(a, h + row * cols, dy + row * cols, dres ? dres + row * cols : nullptr,
+                                                               row, LANES == 32 || row < a.rows, held, dw2, red + turn * kMoments);
+        unpack(dw2, dw);
+    } else {
+        for (int64_t row = row0; row < a.rows; row += step)
+            rmsnorm_backward_row<T, W, NV, WARP, VEC>(a, h + row * cols, dy + row * cols, dres ? dres + row * cols : nullptr, row, dw, red);
+    }
+    bool mine = true;
+    if constexpr (WARP && LN)
+        mine = join_warps_at_once<N, LANES>(dw, dws);
+    else if constexpr (WARP)
+        mine = join_warps<N>(dw, dws);
+    if (mine)
+        store_part<T, VEC, NV>(part, dw, G, g, cols);
 }
 
 template <typename T, typename W, int NV, bool WARP, bool VEC, bool LN>
@@ -179,20 +323,40 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, WARP ? 2 : 1)
     norm_backward_ring_kernel(NormBackwardArgs a, float *part, int stages, unsigned *status)
 {
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ float red[64];
+    __shared__ float red[LN ? kMoments : 64]; // rows have a barrier between them
     const int bytes = a.cols * (int)sizeof(T), group = WARP ? blockDim.x >> 5 : 1, w = WARP ? threadIdx.x >> 5 : 0;
     const Ring<VEC> ring{{static_cast<const uint8_t *>(a.h), static_cast<const uint8_t *>(a.dy), static_cast<const uint8_t *>(a.dres)},
                          {bytes, bytes, bytes}, a.dres ? 3 : 2, group, bytes, stages, a.rows};
     constexpr int N = LN ? 2 * NV : NV;
+    const int G = WARP ? 32 : blockDim.x, g = WARP ? threadIdx.x & 31 : threadIdx.x;
+    [[maybe_unused]] F2 dw2[N][4];
+    clear(dw2);
     float dw[N][8] = {};
+    [[maybe_unused]] Held<T, W, NV, VEC> held;
+    [[maybe_unused]] bool first = true;
     ring.walk(smem, status, [&](uint8_t *stage, int64_t row) {
         auto at = [&](int k) { return reinterpret_cast<const T *>(stage + ring.at(k, row, w)); };
-        if (row + w < a.rows)
-            norm_backward_row<T, W, NV, WARP, VEC, LN>(a, at(0), at(1), a.dres ? at(2) : nullptr, row + w, dw, red);
+        if constexpr (LN) {
+            if (first) // not before the walk has waited for the kernel in front
+                held.load(static_cast<const W *>(a.weight), G, g, a.cols);
+            first = false;
+        }
+        if (row + w < a.rows) {
+            if constexpr (LN)
+                layernorm_backward_row<T, W, NV, WARP, VEC, 32>(a, at(0), at(1), a.dres ? at(2) : nullptr, row + w, true, held, dw2, red);
+            else
+                rmsnorm_backward_row<T, W, NV, WARP, VEC>(a, at(0), at(1), a.dres ? at(2) : nullptr, row + w, dw, red);
+        }
     });
-    if (WARP && !join_warps<N>(dw, reinterpret_cast<float *>(smem + kRingBars)))
-        return;
-    store_part<T, VEC, NV>(part, dw, WARP ? 32 : blockDim.x, WARP ? threadIdx.x & 31 : threadIdx.x, a.cols);
+    if constexpr (LN)
+        unpack(dw2, dw);
+    bool mine = true;
+    if constexpr (WARP && LN)
+        mine = join_warps_at_once<N, 32>(dw, reinterpret_cast<float *>(smem + kRingBars));
+    else if constexpr (WARP)
+        mine = join_warps<N>(dw, reinterpret_cast<float *>(smem + kRingBars));
+    if (mine)
+        store_part<T, VEC, NV>(part, dw, G, g, a.cols);
 }
 
 // dweight[c] = sum of the nparts partial rows, ld apart: 32 columns a CTA, the
@@ -231,9 +395,21 @@ __global__ void __launch_bounds__(1024) dweight_kernel(const float *part, int np
 }
 
 // CTAs of a backward: a row of the workspace each.
-int64_t backward_ctas(int64_t rows, const Shape &s)
+template <bool LN> int64_t backward_ctas(int64_t rows, const Shape &s)
 {
-    return rows_grid(rows, s, (int64_t)(s.stages ? s.ctas : s.warp ? 4 : 2) * num_sms());
+    return rows_grid(rows, s, (int64_t)(s.stages ? s.ctas : s.warp ? (LN ? kLayerRowCtas : 4) : 2) * num_sms());
+}
+
+template <bool LN> Shape backward_shape(int64_t rows, int cols, int n, int esize, bool vec)
+{
+    Shape s = shape_of(rows, cols, n, esize, vec, true, !LN);
+    if (LN && s.warp && !s.stages)
+        s.threads = kLayerRowThreads;
+    if (LN && s.warp && s.stages) { // room for the warps' sums
+        const size_t join = kRingBars + (size_t)(s.threads / 32) * 2 * s.nv * 256 * sizeof(float);
+        s.smem = s.smem < join ? join : s.smem;
+    }
+    return s;
 }
 
 // The most that any alignment, type and dres needs: which of them a call has is
@@ -244,7 +420,7 @@ template <bool LN> size_t norm_backward_workspace(int64_t rows, int cols)
     for (int esize = 2; esize <= 4; esize += 2)
         for (int n = 2; n <= 3; ++n)
             for (int vec = 0; vec < 2; ++vec) {
-                const int64_t c = backward_ctas(rows, shape_of(rows, cols, n, esize, vec != 0, true));
+                const int64_t c = backward_ctas<LN>(rows, backward_shape<LN>(rows, cols, n, esize, vec != 0));
                 most = c > most ? c : most;
             }
     return (size_t)most * cols * (LN ? 2 : 1) * sizeof(float);
@@ -257,8 +433,8 @@ int launch_norm_backward(const NormBackwardArgs &a, const char *name, cudaStream
     const int64_t ld = (int64_t)a.cols * e;
     const bool vec = a.cols % 8 == 0 && chunked(a.h, ld) && chunked(a.dy, ld) && chunked(a.dres, ld) && chunked(a.dx, ld) &&
                      chunked(a.weight, 0); // a null dres counts as aligned
-    const Shape s = shape_of(a.rows, a.cols, a.dres ? 3 : 2, e, vec, true);
-    const int grid = (int)backward_ctas(a.rows, s);
+    const Shape s = backward_shape<LN>(a.rows, a.cols, a.dres ? 3 : 2, e, vec);
+    const int grid = (int)backward_ctas<LN>(a.rows, s);
     float *part = static_cast<float *>(a.workspace);
     unsigned *status = device_status_ptr();
     if (!status) {
@@ -272,7 +448,7 @@ int launch_norm_backward(const NormBackwardArgs &a, const char *name, cudaStream
             using W = std::remove_pointer_t<decltype(w)>;
             constexpr int NV = decltype(nv)::value;
             constexpr bool WARP = decltype(warp)::value;
-            if constexpr (WARP || NV != 1)
+            if constexpr ((WARP || NV != 1) && !(LN && WARP && NV == 4))
                 if (s.stages) {
                     auto go = [&](auto kernel, std::atomic<bool>(&raised)[64]) {
                         cudaError_t r = raise_smem_limit_once(kernel, kRingSmemMost, raised);
@@ -287,8 +463,11 @@ int launch_norm_backward(const NormBackwardArgs &a, const char *name, cudaStream
             auto go = [&](auto kernel) {
                 return launch_pdl(kernel, dim3((unsigned)grid), dim3(s.threads), 0, stream, 1, a, part);
             };
+            if constexpr (NV == 1 && WARP && LN)
+                if (vec && a.cols <= 128)
+                    return go(norm_backward_kernel<T, W, NV, WARP, true, LN, 16>);
             if constexpr (NV == 1 || (NV == 2 && !WARP))
-                return vec ? go(norm_backward_kernel<T, W, NV, WARP, true, LN>) : go(norm_backward_kernel<T, W, NV, WARP, false, LN>);
+                return vec ? go(norm_backward_kernel<T, W, NV, WARP, true, LN, 32>) : go(norm_backward_kernel<T, W, NV, WARP, false, LN, 32>);
             return cudaErrorInvalidValue; // the others: the ring alone
         });
     if (rc == cudaSuccess) // no rows: the sum of nothing, zeros

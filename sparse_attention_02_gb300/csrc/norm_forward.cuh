@@ -8,9 +8,10 @@ namespace dsa {
 namespace {
 
 // One row: x and res (null: none) point at it, in global memory or a stage of the
-// ring.
-template <typename T, typename W, int NV, bool WARP, bool VEC, bool LN>
-__device__ __forceinline__ void norm_row(const NormArgs &a, const T *x, const T *res, int64_t row, float *red)
+// ring.  A CTA's rows have a barrier between them (the ring), or there is but one.
+template <typename T, typename W, int NV, bool WARP, bool VEC, bool LN, bool HELD = false>
+__device__ __forceinline__ void norm_row(const NormArgs &a, const T *x, const T *res, int64_t row, float *red,
+                                         const Held<T, W, NV, VEC> *held = nullptr) // HELD: of the weight, of the bias
 {
     const int G = WARP ? 32 : blockDim.x;
     const int g = WARP ? (threadIdx.x & 31) : threadIdx.x;
@@ -54,45 +55,61 @@ __device__ __forceinline__ void norm_row(const NormArgs &a, const T *x, const T 
             store_chunk<VEC>(v, ho, chunk_base<VEC>(c, G, g), cols);
         }
     }
-    ss = group_reduce<WARP, false>(ss, 0.f, red).x;
-    if (LN) { // ss becomes the sum of squares about the mean, in a second pass over the registers
-        const float mean = ss / (float)cols;
-        float sd = 0.f;
-        ss = 0.f;
+    if (LN) {
+        // about the warp's own mean first, from the registers
+        ss = warp_sum(ss);
+        const int n = warp_columns<NV>(G, g >> 5, cols);
+        float mean = n ? ss / (float)n : 0.f, sq = 0.f;
 #pragma unroll
         for (int c = 0; c < NV; ++c) {
             const int cb = chunk_base<VEC>(c, G, g);
-            float s = 0.f, t = 0.f;
+            float s = 0.f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const bool in = VEC ? cb < cols : column<T, VEC>(cb, i) < cols;
-                h[c][i] = in ? h[c][i] - mean : 0.f;
-                s = fmaf(h[c][i], h[c][i], s);
-                t += h[c][i];
+                const float d = h[c][i] - mean;
+                s = (VEC ? cb < cols : column<T, VEC>(cb, i) < cols) ? fmaf(d, d, s) : s;
             }
-            ss += s;
-            sd += t;
+            sq += s;
         }
-        const float2 sums = group_reduce<WARP, false>(ss, sd, red);
-        // what the mean's own rounding left: sd is the sum of what would add up to zero
-        const float off = sums.y / (float)cols;
-        ss = fmaxf(sums.x - sums.y * off, 0.f);
+        sq = warp_sum(sq);
+        if (!WARP) {
+            const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+            if (lane == 0) {
+                red[64 + (threadIdx.x >> 5)] = ss;
+                red[96 + (threadIdx.x >> 5)] = sq;
+            }
+            __syncthreads();
+            const int m = lane < warps ? warp_columns<NV>(G, lane, cols) : 0;
+            ss = m ? red[64 + lane] : 0.f;
+            mean = warp_sum(ss) / (float)cols;
+            const float d = m ? ss / (float)m - mean : 0.f;
+            sq = warp_sum(m ? red[96 + lane] + (float)m * d * d : 0.f);
+        }
+        ss = sq;
 #pragma unroll
         for (int c = 0; c < NV; ++c)
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                h[c][i] -= off;
+                h[c][i] -= mean;
+    } else {
+        ss = group_reduce<WARP, false>(ss, 0.f, red).x;
     }
     const float r = 1.f / sqrtf(ss / (float)cols + a.eps);
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
         float w[8];
-        load_weights<T, VEC>(w, weight, chunk_base<VEC>(c, G, g), cols);
+        if (HELD)
+            held[0].get(w, weight, c, chunk_base<VEC>(c, G, g), cols);
+        else
+            load_weights<T, VEC>(w, weight, chunk_base<VEC>(c, G, g), cols);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             h[c][i] = h[c][i] * r * w[i];
         if (LN && a.bias) {
-            load_weights<T, VEC>(w, static_cast<const W *>(a.bias), chunk_base<VEC>(c, G, g), cols);
+            if (HELD)
+                held[1].get(w, static_cast<const W *>(a.bias), c, chunk_base<VEC>(c, G, g), cols);
+            else
+                load_weights<T, VEC>(w, static_cast<const W *>(a.bias), chunk_base<VEC>(c, G, g), cols);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 h[c][i] += w[i];
@@ -163,7 +180,7 @@ __device__ __forceinline__ void norm_row(const NormArgs &a, const T *x, const T 
 template <typename T, typename W, int NV, bool WARP, bool VEC, bool LN>
 __global__ void __launch_bounds__(WARP ? kRowThreads : 1024) norm_kernel(NormArgs a)
 {
-    __shared__ float red[64];
+    __shared__ float red[LN ? 128 : 64];
     grid_dep_wait();
     grid_dep_launch();
     const int64_t row0 = WARP ? (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5) : blockIdx.x;
@@ -179,16 +196,25 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, WARP ? 2 : 1)
     norm_ring_kernel(NormArgs a, int stages, unsigned *status)
 {
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ float red[64];
+    __shared__ float red[LN ? 128 : 64];
     const int bytes = a.cols * (int)sizeof(T), group = WARP ? blockDim.x >> 5 : 1, w = WARP ? threadIdx.x >> 5 : 0;
     const Ring<VEC> ring{{static_cast<const uint8_t *>(a.x), static_cast<const uint8_t *>(a.residual), nullptr},
                          {a.ldx * (int64_t)sizeof(T), a.ldr * (int64_t)sizeof(T), 0},
                          a.residual ? 2 : 1, group, bytes, stages, a.rows};
+    [[maybe_unused]] Held<T, W, NV, VEC> held[LN ? 2 : 1];
+    [[maybe_unused]] bool first = true;
     ring.walk(smem, status, [&](uint8_t *stage, int64_t row) {
+        if (LN && first) { // not before the walk has waited for the kernel in front
+            const int G = WARP ? 32 : blockDim.x, g = WARP ? threadIdx.x & 31 : threadIdx.x;
+            held[0].load(static_cast<const W *>(a.weight), G, g, a.cols);
+            if (a.bias)
+                held[LN ? 1 : 0].load(static_cast<const W *>(a.bias), G, g, a.cols);
+            first = false;
+        }
         if (row + w < a.rows)
-            norm_row<T, W, NV, WARP, VEC, LN>(a, reinterpret_cast<const T *>(stage + ring.at(0, row, w)),
-                                             a.residual ? reinterpret_cast<const T *>(stage + ring.at(1, row, w)) : nullptr,
-                                             row + w, red);
+            norm_row<T, W, NV, WARP, VEC, LN, LN>(a, reinterpret_cast<const T *>(stage + ring.at(0, row, w)),
+                                                  a.residual ? reinterpret_cast<const T *>(stage + ring.at(1, row, w)) : nullptr,
+                                                  row + w, red, held);
     });
 }
 

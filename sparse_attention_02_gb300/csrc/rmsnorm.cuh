@@ -199,6 +199,26 @@ template <typename T, bool VEC, typename W> __device__ __forceinline__ void load
     }
 }
 
+// Weights that a thread keeps for all its rows, as loaded: an SM's L1 beside a ring holds little else.
+template <typename T, typename W, int NV, bool VEC> struct Held {
+    static constexpr bool kHolds = (VEC || sizeof(W) == sizeof(T)) && sizeof(W) * NV <= 8;
+    Vec8<W> v[kHolds ? NV : 1];
+    __device__ __forceinline__ void load(const W *row, int G, int g, int cols)
+    {
+        if constexpr (kHolds)
+#pragma unroll
+            for (int c = 0; c < NV; ++c)
+                load_chunk<VEC>(v[c], row, chunk_base<VEC>(c, G, g), cols);
+    }
+    __device__ __forceinline__ void get(float (&f)[8], const W *row, int c, int cb, int cols) const
+    {
+        if constexpr (kHolds)
+            v[c].get(f);
+        else
+            load_weights<T, VEC>(f, row, cb, cols);
+    }
+};
+
 // The codes of a chunk of T's columns.
 template <typename T, bool VEC> __device__ __forceinline__ void store_codes(uint32_t lo, uint32_t hi, uint8_t *row, int cb, int cols)
 {
@@ -258,6 +278,33 @@ __device__ __forceinline__ float2 group_reduce(float a, float b, float *red)
     }
     return make_float2(a, b);
 }
+
+// ---- sums about the mean (layer norm)
+//
+// A row's mean and sum of squares about it, from one meeting of its warps: each warp takes the sums about its own mean,
+// and n (its mean - the row's)^2 is what that leaves out (T. Chan, G. Golub, R. LeVeque, "Algorithms for computing the
+// sample variance", 1983).
+template <int LANES = 32> __device__ __forceinline__ float warp_sum(float a)
+{
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1)
+        a += __shfl_xor_sync(0xffffffffu, a, o);
+    return a;
+}
+
+// Columns of a row that warp w of a row's G threads holds.
+template <int NV> __device__ __forceinline__ int warp_columns(int G, int w, int cols)
+{
+    int n = 0;
+#pragma unroll
+    for (int c = 0; c < NV; ++c) {
+        const int left = cols - (c * G + 32 * w) * 8;
+        n += left < 0 ? 0 : left < 256 ? left : 256;
+    }
+    return n;
+}
+
+constexpr int kMoments = 4 * 32; // floats that a meeting takes; the next of the same CTA takes others
 
 // ---- the ring of rows in shared memory
 constexpr int kRingMost = 8;   // stages at most
@@ -408,7 +455,10 @@ struct Shape {
 // 11.8, 12.7).  So it does in the forward of rows of up to 2048 columns at any
 // address, which instructions bound (wide = false: 24000 x 1111 84, 124; backward
 // 163, 84).
-Shape shape_of(int64_t rows, int cols, int n, int esize, bool vec, bool wide)
+//
+// Layer norm's backward holds two sums a column, and so takes twice the threads for a row (light = false: 8192 x 8192
+// with four chunks a thread, whose sums then spill, 157 us).
+Shape shape_of(int64_t rows, int cols, int n, int esize, bool vec, bool wide, bool light = true)
 {
     const size_t row = (size_t)n * ring_pitch(cols * esize, vec);
     const auto ring = [&](int threads, int ctas, int group, bool warp) {
@@ -421,7 +471,7 @@ Shape shape_of(int64_t rows, int cols, int n, int esize, bool vec, bool wide)
             smem = 32 * 8 * 4 * sizeof(float);
         return Shape{nv <= 1 && warp ? 1 : nv <= 2 ? 2 : 4, threads, warp, fit < 2 ? 0 : stages, ctas, kRingBars + smem};
     };
-    if (cols > 256 && cols <= 1024 && rows >= 32 * num_sms()) { // rows of single warps: no barrier among them
+    if (cols > 256 && cols <= (light ? 1024 : 512) && rows >= 32 * num_sms()) { // rows of single warps: no barrier among them
         const Shape s = ring(256, 2, 8, true);
         if (s.stages)
             return s;
@@ -429,7 +479,7 @@ Shape shape_of(int64_t rows, int cols, int n, int esize, bool vec, bool wide)
     const int direct = (cols + 255) / 256 * 32; // threads a row takes with a chunk each
     if (cols > (wide ? 256 : 2048) && rows * direct >= (cols > 4096 ? 2LL : 8LL) * 1024 * num_sms())
         for (int ctas = 8; ctas > 0; ctas /= 2)
-            if (cols * ctas <= 32 * 512) { // four chunks a thread at most
+            if (cols * ctas <= (light || ctas == 1 ? 32 : 16) * 512) { // four chunks a thread at most
                 const Shape s = ring(512 / ctas, ctas, 1, false);
                 if (s.stages)
                     return s;
