@@ -17,22 +17,30 @@ int launch_gemm_fp8(const GemmFp8Args &a, cudaStream_t stream, char *err, size_t
             split *= 2;
         return launch_gemm_fp8_split(a, cols, split, stream, err, errlen);
     }
-    // Time of a tile kernel's call, us, from what a piece, an output and a cluster's sum were measured at: 128 x 704 x 4096 of
-    // 128 columns takes 13.5 whole, 10.2 split in 4 and 8.8 in 8; 1024 x 4096 x 1024 10.7 with 128 columns and 9.1 with
-    // 256; 8192 x 8192 x 8192 537 and 436.  Clusters of eight find room for two thirds of the SMs.
-    int best_cols = 256, best_split = 1;
-    float best = 1e30f;
-    for (int cols = 128; cols <= 256; cols *= 2)
+    // By tiles: the widths of a tile and the splits of K by the time that they take, in us, from what a piece, a tile's
+    // output and a cluster's sum were measured at (128 x 704 x 4096 bf16: 13.1 by tiles of 128, 14.9 of 192, 8.6 with K split
+    // in 8; 4096 x 704 x 4096 25.0, 16.7 and, of 256, 19.5; 2048 x 2048 x 2048 15.1, 17.6, 12.3; 8191 x 8192 x 8192 534,
+    // 458, 422).  Clusters of eight find room on two thirds of the SMs.
+    struct Width {
+        int cols;
+        float piece, rows_piece, out, join; // rows_piece: with a scale for every row of b
+    };
+    constexpr Width widths[] = {{128, 0.32f, 0.44f, 1.0f, 4.0f}, {192, 0.38f, 0.60f, 1.6f, 4.6f}, {256, 0.455f, 0.f, 2.4f, 7.f}};
+    int best_cols = 0, best_split = 1;
+    float best = 0.f;
+    for (const Width &w : widths) {
+        if (!a.b_block && w.cols == 256) // a multiply more a sum: more registers than its threads have
+            continue;
         for (int split = 1; split <= 8; split *= 2) {
-            const int64_t ctas = (((int64_t)a.M + 127) / 128) * (((int64_t)a.N + cols - 1) / cols) * split;
+            const int64_t ctas = (((int64_t)a.M + 127) / 128) * (((int64_t)a.N + w.cols - 1) / w.cols) * split;
             if (split > 1 && (ctas > (split == 8 ? sms * 2 / 3 : sms) || pieces < 2 * split))
                 break;
-            const float piece = cols == 128 ? (a.b_block ? 0.34f : 0.48f) : (a.b_block ? 0.48f : 0.87f);
-            const float turn = piece * (float)((pieces + split - 1) / split) + (cols == 128 ? 0.7f : 1.2f);
-            const float t = (float)((ctas + sms - 1) / sms) * turn + (split > 1 ? (cols == 128 ? 4.5f : 7.5f) : 0.f);
-            if (t < best)
-                best = t, best_cols = cols, best_split = split;
+            const float turn = (a.b_block ? w.piece : w.rows_piece) * (float)((pieces + split - 1) / split) + w.out * (a.o32 ? 2.f : 1.f);
+            const float t = (float)((ctas + sms - 1) / sms) * turn + (split > 1 ? w.join : 0.f);
+            if (!best_cols || t < best)
+                best = t, best_cols = w.cols, best_split = split;
         }
+    }
     return launch_gemm_fp8_tile(a, best_cols, best_split, stream, err, errlen);
 }
 

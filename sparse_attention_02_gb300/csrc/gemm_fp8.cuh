@@ -34,6 +34,28 @@ __device__ __forceinline__ float4 sums_of_cluster(uint32_t addr, uint32_t split)
     return v[0];
 }
 
+// mbar_wait_warp with every branch decided by the whole warp: a wait for what is over costs it one poll and one vote.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int *abort_flag, unsigned *status)
+{
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity)))
+        return true;
+    const uint64_t t0 = global_timer_ns();
+    for (uint32_t n = 1;; ++n) {
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity)))
+            return true;
+        if ((n & 15) == 0) {
+            const bool late = global_timer_ns() - t0 > DSA_WAIT_LIMIT_NS;
+            if (__any_sync(0xffffffffu, late)) {
+                atomicOr(status, DSA_DEV_TIMEOUT);
+                *abort_flag = 1;
+                return false;
+            }
+            if (__any_sync(0xffffffffu, *abort_flag != 0))
+                return false;
+        }
+    }
+}
+
 inline bool gemm_fp8_map(CUtensorMap *map, const void *base, int64_t ld, int rows, int K, int box, char *err, size_t errlen)
 {
     return encode_tmap_2d(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, (uint64_t)K, (uint64_t)rows, (uint64_t)ld, kGemmPiece, box,

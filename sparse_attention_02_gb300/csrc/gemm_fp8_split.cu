@@ -1,6 +1,5 @@
 // Product of FP8 operands with a scale for every 128 values along the summed axis,
-// on sm_103a: few rows of `a` (the tokens of a decode step or a short prompt), or a
-// product too small to fill the GPU with whole tiles.
+// on sm_103a, for few rows of `a` (the tokens of a decode step).
 //
 //     out[m, n] = sum_p sa[m, p] sb[n, p] sum_{k in piece p} a[m, k] b[n, k]
 //
@@ -13,6 +12,10 @@
 // tokens leave no part of it idle but the columns up to 16.  K is split over the
 // CTAs of a cluster, each of which takes whole pieces; their sums meet through
 // distributed shared memory, added in the CTAs' order: results repeat bit for bit.
+//
+// Measured: 1 x 704 x 4096 4.1 us (launch, a load's latency, four pieces and the meeting; 2.9 MB),
+// 1 x 24576 x 1536 9.6 (58 % of measured HBM), 1 x 8192 x 8192 14.8 (67 %),
+// 32 x 4096 x 7168 10.4 (44 %).
 //
 // Roles per CTA (8 warps): 0 loads, 1 MMAs, 2 column scales, 4-7 scaling and sums
 // (a thread holds one row of b and all BT columns).
@@ -32,11 +35,11 @@ constexpr int kRowBytes = kRows * kGemmPiece;
 
 template <int BT> struct Cfg {
     static constexpr int kStage = kRowBytes + BT * kGemmPiece;
-    // two CTAs an SM up to 64 columns
-    static constexpr int kStages = BT <= 16 ? 6 : BT <= 32 ? 5 : BT <= 64 ? 4 : 6;
+    // two CTAs an SM
+    static constexpr int kStages = BT <= 16 ? 6 : BT <= 32 ? 5 : 4;
     static constexpr int kScales = kStages * kStage;            // two batches of [kBatch][BT] fp32
     static constexpr int kBars = kScales + 2 * kBatch * BT * 4;
-    static constexpr int kBuffers = BT <= 64 ? 4 : 2;            // of BT columns of TMEM
+    static constexpr int kBuffers = 4;                           // of BT columns of TMEM
     static constexpr int kNumBars = 2 * kStages + 2 * kBuffers + 5;
     static constexpr int kMisc = kBars + 8 * kNumBars;
     static constexpr int kSmem = kMisc + 16;
@@ -62,7 +65,7 @@ __device__ __forceinline__ void put(const Params &p, int64_t m, int64_t n, float
 }
 
 template <int BT>
-__global__ void __launch_bounds__(kThreads, BT <= 64 ? 2 : 1)
+__global__ void __launch_bounds__(kThreads, 2)
     gemm_fp8_split_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, Params p)
 {
     using C = Cfg<BT>;
@@ -115,7 +118,7 @@ __global__ void __launch_bounds__(kThreads, BT <= 64 ? 2 : 1)
         bool ok = true;
         for (int k = k0, i = 0; ok && k < k1; ++k, ++i) {
             const int st = i % C::kStages, use = i / C::kStages;
-            if (use > 0 && !mbar_wait_warp(bar(B_EMPTY + st), (use - 1) & 1, abort_flag, p.status)) {
+            if (use > 0 && !wait_warp(bar(B_EMPTY + st), (use - 1) & 1, abort_flag, p.status)) {
                 ok = false;
                 break;
             }
@@ -165,7 +168,7 @@ __global__ void __launch_bounds__(kThreads, BT <= 64 ? 2 : 1)
                 const int m = m0 + 4 * j + (lane >> 3);
                 v[j] = in && m < p.M ? p.a_scale[(int64_t)m * p.pieces + k + kk] * sb : 0.f;
             }
-            if (i >= 2 && !mbar_wait_warp(bar(B_SE + buf), ((i >> 1) - 1) & 1, abort_flag, p.status)) {
+            if (i >= 2 && !wait_warp(bar(B_SE + buf), ((i >> 1) - 1) & 1, abort_flag, p.status)) {
                 ok = false;
                 break;
             }
@@ -191,8 +194,8 @@ __global__ void __launch_bounds__(kThreads, BT <= 64 ? 2 : 1)
             const int t = i % C::kBuffers, batch = i / kBatch, buf = batch & 1;
             const F2 mine(next);
             next = scaled && k + 1 < k1 ? sb[k + 1] : 1.f;
-            if ((i % kBatch == 0 && !mbar_wait_warp(bar(B_SF + buf), (batch >> 1) & 1, abort_flag, p.status)) ||
-                !mbar_wait_warp(bar(B_TF + t), (i / C::kBuffers) & 1, abort_flag, p.status)) {
+            if ((i % kBatch == 0 && !wait_warp(bar(B_SF + buf), (batch >> 1) & 1, abort_flag, p.status)) ||
+                !wait_warp(bar(B_TF + t), (i / C::kBuffers) & 1, abort_flag, p.status)) {
                 ok = false;
                 break;
             }
@@ -302,8 +305,7 @@ int launch_gemm_fp8_split(const GemmFp8Args &a, int cols, int split, cudaStream_
 {
     return cols <= 16   ? launch<16>(a, split, stream, err, errlen)
            : cols <= 32 ? launch<32>(a, split, stream, err, errlen)
-           : cols <= 64 ? launch<64>(a, split, stream, err, errlen)
-                        : launch<128>(a, split, stream, err, errlen);
+                        : launch<64>(a, split, stream, err, errlen);
 }
 
 } // namespace dsa

@@ -3,10 +3,29 @@
 // whole tiles (the formula stands in gemm_fp8_split.cu).
 //
 // A CTA's tile is 128 rows of a by BN of b.  A piece of 128 values along K is one stage of
-// shared memory and four MMAs, whose sums stay in TMEM (two buffers of BN columns) only until
-// eight warps have read them, scaled them and added them to running sums in their registers:
-// 128 fp32 a thread, one multiply-add each, in pairs, or a product more where b has a scale
-// for every row.
+// shared memory and four MMAs, whose sums stay in TMEM (2 buffers of 256 or 192 columns, 4 of 128)
+// only until warps have read them, scaled them and added them to running sums in their registers:
+// a thread holds 128 columns (BN = 256) or 64 of one row, one multiply-add each, in pairs, or
+// a product more where b has a scale for every row.
+//
+// Bounds.  A piece of 128 x 256 takes the tensor pipe 512 cycles and the FP32 pipe 256.  What a step
+// of the loop takes is the way round: MMAs (512 and 150 until the sums are seen), 128 columns read in two
+// halves, as 64 are what a thread's registers hold beside its sums, and 200 until the next MMAs go
+// out; two buffers share that, 840 cycles a piece.  BN = 192 has registers for all of a
+// piece at once, but more pieces, and takes the product with a scale for every row, which the FP32
+// pipe would bound at 256 (4096 x 4096 x 8191 217 us by 128 x 256, 199 by 128 x 192).
+//
+// Measured: 8191 x 8192 x 8192 bf16 417 us, 2.64 PFLOP/s (140 % of measured BF16).  Without the additions the
+// same loop takes 375, without the loads 390.  Not kept: pairs of CTAs on one tile
+// (cta_group::2, 256 x 256: 468 us, words between CTAs in the way round; in halves of 128
+// columns with four buffers 655: more meetings), 16 warps of 64 columns (500, registers
+// spill), the first columns of the next piece asked for among the additions (486: the reading waits),
+// scales fetched by each warp for itself (610, spills).
+//
+// Roles per CTA (12 or 16 warps): 0 loads, 1 MMAs, 2 and 3 scales, the others scaling, sums and output.
+// Persistent where a tile is a CTA's own: CTA c takes tiles c, c + CTAs, ..., ordered so that those
+// under way at one time share rows of a and of b in L2.  With few tiles the CTAs of a cluster
+// share one, a part of K each, and add up their sums in the CTAs' order.
 #include "gemm_fp8.cuh"
 
 #include <atomic>
@@ -15,26 +34,32 @@
 namespace dsa {
 namespace {
 
-constexpr int kSumWarp0 = 4, kSumWarps = 8;
-constexpr int kThreads = 32 * (kSumWarp0 + kSumWarps);
+constexpr int kSumWarp0 = 4;
 constexpr int kGroup = 8;   // tiles along M that neighbouring tiles are taken from
-constexpr int kAuxRegs = 72, kSumRegs = 216; // of 168 a thread at launch
 constexpr int kPatch = 32 * 64; // 64 bytes of each of a warp's rows of out, on their way there
 constexpr int kRows = 128;  // of a
 constexpr int kABytes = kRows * kGemmPiece;
 
 template <int BN, bool ROWS> struct Cfg {
+    static constexpr int kCols = BN == 256 ? 128 : 64;   // that a warp of sums takes, of 32 rows
+    static constexpr int kSumWarps = 4 * BN / kCols;
+    static constexpr int kThreads = 32 * (kSumWarp0 + kSumWarps);
+    static constexpr int kBuffers = BN == 128 ? 4 : 2; // of BN columns of TMEM
+    // Where sums fill them, the threads' registers are not shared evenly: of 168 a thread at launch 72 and 216 (BN = 256),
+    // of 128 56 and 152 (192).
+    static constexpr bool kShares = BN > 128;
+    static constexpr int kAuxRegs = BN == 256 ? 72 : 56, kSumRegs = BN == 256 ? 216 : 152;
     static constexpr int kStage = kABytes + BN * kGemmPiece;
-    static constexpr int kStages = BN == 256 ? 4 : 6;
-    static constexpr int kBatch = ROWS ? 4 : 8;                   // pieces whose scales are fetched at once
-    static constexpr int kScaled = kRows + (ROWS ? BN : BN / 128); // scales of a piece: a's, then b's
+    static constexpr int kStages = BN == 128 ? 5 : 4;
+    static constexpr int kBatch = 8;                               // pieces whose scales are fetched at once
+    static constexpr int kScaled = kRows + (ROWS ? BN : 4);        // scales of a piece: a's, then b's
     static constexpr int kPatches = kStages * kStage;
-    static constexpr int kScales = kPatches + kSumWarps * kPatch; // two batches
+    static constexpr int kScales = kPatches + kSumWarps * kPatch;  // two batches
     static constexpr int kBars = (kScales + 2 * kBatch * kScaled * 4 + 7) / 8 * 8;
-    static constexpr int kNumBars = 2 * kStages + 9;
+    static constexpr int kNumBars = 2 * kStages + 2 * kBuffers + 5;
     static constexpr int kMisc = kBars + 8 * kNumBars;
     static constexpr int kSmem = kMisc + 16;
-    static_assert((BN + BN / 2 + 1) * kRows * 4 <= kScales, "a split's sums, and what the CTA adds up, take the stages' place");
+    static_assert((BN + BN / 2 + 1) * kRows * 4 <= kBars, "a split's sums, and what the CTA adds up, take the stages' place");
     static_assert(kSmem <= 232448, "dynamic shared memory above the 227 KB a CTA may hold");
 };
 
@@ -101,15 +126,15 @@ __device__ __forceinline__ void store_sums(const Params &p, int64_t m, int n, co
 }
 
 template <int BN, bool ROWS>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<BN, ROWS>::kThreads, 1)
     gemm_fp8_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, Params p)
 {
     using C = Cfg<BN, ROWS>;
     extern __shared__ __align__(1024) uint8_t smem[]; // the swizzle's period
     const uint32_t sbase = smem_u32(smem);
     auto bar = [&](int i) { return sbase + C::kBars + 8u * i; };
-    constexpr int B_FULL = 0, B_EMPTY = C::kStages, B_TF = 2 * C::kStages, B_TE = B_TF + 2, B_SF = B_TF + 4, B_SE = B_TF + 6,
-                  B_DONE = B_TF + 8;
+    constexpr int B_FULL = 0, B_EMPTY = C::kStages, B_TF = 2 * C::kStages, B_TE = B_TF + C::kBuffers,
+                  B_SF = B_TE + C::kBuffers, B_SE = B_SF + 2, B_DONE = B_SE + 2;
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + C::kMisc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::kMisc + 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -123,18 +148,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(bar(B_FULL + i), 1);
             mbar_init(bar(B_EMPTY + i), 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < C::kBuffers; ++i) {
             mbar_init(bar(B_TF + i), 1);
-            mbar_init(bar(B_TE + i), kSumWarps);
+            mbar_init(bar(B_TE + i), C::kSumWarps);
+        }
+        for (int i = 0; i < 2; ++i) {
             mbar_init(bar(B_SF + i), 64);
-            mbar_init(bar(B_SE + i), kSumWarps);
+            mbar_init(bar(B_SE + i), C::kSumWarps);
         }
         mbar_init(bar(B_DONE), 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
     if (warp == 1)
-        tmem_alloc(sbase + C::kMisc, 2 * BN);
+        tmem_alloc(sbase + C::kMisc, 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -144,7 +171,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // each side takes its share of the registers in its own branch: what both run has to fit the smaller
     if (warp < kSumWarp0) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAuxRegs));
+        if constexpr (C::kShares)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kAuxRegs));
         if (warp == 0) {
             // -------------------------------------------------------- loads
             int st = 0, phase = 0;
@@ -153,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 int tm, tn;
                 tile_at(p, tile, tm, tn);
                 for (int k = 0; k < pieces; ++k) {
-                    if (again && !mbar_wait_warp(bar(B_EMPTY + st), phase ^ 1, abort_flag, p.status)) {
+                    if (again && !wait_warp(bar(B_EMPTY + st), phase ^ 1, abort_flag, p.status)) {
                         ok = false;
                         break;
                     }
@@ -179,9 +207,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 constexpr uint32_t idesc = idesc_f32acc(kRows, BN, 0u, false, false);
                 const int total = first < tiles ? ((tiles - 1 - first) / step + 1) * pieces : 0;
                 for (int i = 0; i < total; ++i) {
-                    const int st = i % C::kStages, t = i & 1;
+                    const int st = i % C::kStages, t = i % C::kBuffers;
                     if (!mbar_wait(bar(B_FULL + st), (i / C::kStages) & 1, abort_flag, p.status) ||
-                        (i >= 2 && !mbar_wait(bar(B_TE + t), ((i >> 1) - 1) & 1, abort_flag, p.status)))
+                        (i >= C::kBuffers && !mbar_wait(bar(B_TE + t), (i / C::kBuffers - 1) & 1, abort_flag, p.status)))
                         break;
                     tc_fence_after();
                     const uint64_t ad = sdesc(sbase + st * C::kStage, 16, 1024, 2), bd = sdesc(sbase + st * C::kStage + kABytes, 16, 1024, 2);
@@ -207,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int k = k0 + mine - nth * pieces;
                 int tm, tn;
                 tile_at(p, first + nth * step, tm, tn);
-                if (n >= 2 && !mbar_wait_warp(bar(B_SE + buf), ((n >> 1) - 1) & 1, abort_flag, p.status))
+                if (n >= 2 && !wait_warp(bar(B_SE + buf), ((n >> 1) - 1) & 1, abort_flag, p.status))
                     break;
                 float *to = reinterpret_cast<float *>(smem + C::kScales) + (buf * C::kBatch + kk) * C::kScaled;
                 auto fetch = [&](const float *from, int row, int rows, float *dst, int count) {
@@ -229,15 +257,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (ROWS)
                     fetch(p.b_scale, tn * BN + BN / 2 * half, p.N, to + kRows + BN / 2 * half, BN / 2);
                 else if (half == 0)
-                    fetch(p.b_scale, tn * (BN / 128), (p.N + 127) / 128, to + kRows, BN / 128);
+                    fetch(p.b_scale, tn * BN / 128, (p.N + 127) / 128, to + kRows, 2);
                 mbar_arrive(bar(B_SF + buf));
             }
         }
     } else {
         // --------------------------------------------------- scaled sums
-        // Warp: 32 rows (its TMEM lanes) and half of the columns.
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
-        constexpr int W = BN / 2;
+        // Warp: 32 rows (its TMEM lanes) and W columns, 64 of which are in flight from TMEM at a time.  The last are read
+        // before they are added: the next product in their buffer does not wait for that.
+        if constexpr (C::kShares)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSumRegs));
+        constexpr int W = C::kCols;
         const int quad = warp & 3, part = (warp - kSumWarp0) >> 2;
         const uint32_t from = tmem + ((uint32_t)(32 * quad) << 16) + W * part;
         const float *sc = reinterpret_cast<const float *>(smem + C::kScales);
@@ -245,19 +275,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t i = 0;
         bool ok = true;
         for (int tile = first; ok && tile < tiles; tile += step) {
+            int block = kRows + W * part / 128; // where in a piece's scales that of these columns of b is
+            if constexpr (BN == 192 && !ROWS) {
+                int tm, tn;
+                tile_at(p, tile, tm, tn);
+                block = kRows + ((tn * BN + W * part) >> 7) - (tn * BN >> 7);
+            }
             F2 acc[W / 2];
 #pragma unroll
             for (int c = 0; c < W / 2; ++c)
                 acc[c] = F2(0.f);
             for (int k = 0; k < pieces; ++k, ++i) {
-                const uint32_t t = i & 1, n = i / C::kBatch;
-                if (i % C::kBatch == 0 && !mbar_wait_warp(bar(B_SF + (n & 1)), (n >> 1) & 1, abort_flag, p.status)) {
+                const uint32_t t = i % C::kBuffers, n = i / C::kBatch;
+                if (i % C::kBatch == 0 && !wait_warp(bar(B_SF + (n & 1)), (n >> 1) & 1, abort_flag, p.status)) {
                     ok = false;
                     break;
                 }
                 const float *slot = sc + i % (2 * C::kBatch) * C::kScaled;
-                const F2 mine(slot[32 * quad + lane] * (ROWS ? 1.f : slot[kRows + W * part / 128]));
-                if (!mbar_wait_warp(bar(B_TF + t), (i >> 1) & 1, abort_flag, p.status)) {
+                const F2 mine(slot[32 * quad + lane] * (ROWS ? 1.f : slot[block]));
+                if (!wait_warp(bar(B_TF + t), (i / C::kBuffers) & 1, abort_flag, p.status)) {
                     ok = false;
                     break;
                 }
@@ -266,24 +302,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 auto add = [&](const uint32_t(&v)[32], int c) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) {
-                        const F2 v0(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), v1(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
                         F2 s0 = mine, s1 = mine;
                         if (ROWS) {
                             const float4 s = cs[(c + e) / 4];
                             s0 = mine * F2(s.x, s.y);
                             s1 = mine * F2(s.z, s.w);
                         }
-                        acc[(c + e) / 2] = fma2(v0, s0, acc[(c + e) / 2]);
-                        acc[(c + e) / 2 + 1] = fma2(v1, s1, acc[(c + e) / 2 + 1]);
+                        acc[(c + e) / 2] = fma2(F2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), s0, acc[(c + e) / 2]);
+                        acc[(c + e) / 2 + 1] = fma2(F2(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])), s1, acc[(c + e) / 2 + 1]);
                     }
                 };
-                // 64 columns in flight
                 uint32_t v0[32], v1[32];
                 tmem_ld32(from + t * BN, v0);
                 tmem_ld32(from + t * BN + 32, v1);
                 tmem_ld_wait_for(v0);
                 tmem_ld_wait_for(v1);
-                if constexpr (W > 64) {
+                if constexpr (W == 128) {
                     add(v0, 0);
                     tmem_ld32(from + t * BN + 64, v0);
                     add(v1, 32);
@@ -291,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_ld_wait_for(v0);
                     tmem_ld_wait_for(v1);
                 }
-                tc_fence_before(); // read: the buffer may take the piece after the next
+                tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(bar(B_TE + t));
@@ -342,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, 2 * BN);
+        tmem_dealloc(tmem, 512);
     }
     if (split == 1)
         return;
@@ -353,13 +387,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     tile_at(p, first, tm, tn);
     const int cols = BN / split, c0 = cols * rank, pitch = cols + 1;
     float *turned = reinterpret_cast<float *>(smem) + BN * kRows;
-    for (int x = 4 * threadIdx.x; x < cols * kRows; x += 4 * kThreads) {
+    for (int x = 4 * threadIdx.x; x < cols * kRows; x += 4 * C::kThreads) {
         const float4 v = sums_of_cluster(sbase + 4 * (c0 * kRows + x), split);
         float *to = turned + x % kRows * pitch + x / kRows;
         to[0] = v.x, to[pitch] = v.y, to[2 * pitch] = v.z, to[3 * pitch] = v.w;
     }
     __syncthreads();
-    for (int x = threadIdx.x; x < cols * kRows; x += kThreads) {
+    for (int x = threadIdx.x; x < cols * kRows; x += C::kThreads) {
         const int64_t m = (int64_t)tm * kRows + x / cols, n = (int64_t)tn * BN + c0 + x % cols;
         const float v = turned[x / cols * pitch + x % cols];
         if (m < p.M && n < p.N) {
@@ -389,11 +423,11 @@ int launch(const GemmFp8Args &a, int split, cudaStream_t stream, char *err, size
         return DSA_ERR_CUDA;
     static std::atomic<bool> raised[64], fits;
     cudaError_t e = raise_smem_limit_once(gemm_fp8_tile_kernel<BN, ROWS>, C::kSmem, raised);
-    if (e == cudaSuccess && !fits.load(std::memory_order_acquire)) {
+    if (C::kShares && e == cudaSuccess && !fits.load(std::memory_order_acquire)) {
         // the roles' shares of registers are cut from what the block is launched with
         cudaFuncAttributes f;
         e = cudaFuncGetAttributes(&f, gemm_fp8_tile_kernel<BN, ROWS>);
-        if (e == cudaSuccess && f.numRegs * kThreads < 32 * (kSumWarp0 * kAuxRegs + kSumWarps * kSumRegs)) {
+        if (e == cudaSuccess && f.numRegs * C::kThreads < 32 * (kSumWarp0 * C::kAuxRegs + C::kSumWarps * C::kSumRegs)) {
             snprintf(err, errlen, "gemm_fp8: built with %d registers a thread, too few to share out", f.numRegs);
             return DSA_ERR_UNSUPPORTED;
         }
@@ -402,7 +436,7 @@ int launch(const GemmFp8Args &a, int split, cudaStream_t stream, char *err, size
     const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n, most = num_sms();
     if (e == cudaSuccess)
         e = launch_pdl(gemm_fp8_tile_kernel<BN, ROWS>, dim3((unsigned)(split > 1 ? tiles * split : tiles < most ? tiles : most)),
-                       dim3(kThreads), C::kSmem, stream, split, ta, tb, p);
+                       dim3(C::kThreads), C::kSmem, stream, split, ta, tb, p);
     if (e != cudaSuccess) {
         snprintf(err, errlen, "gemm_fp8 launch: %s", cudaGetErrorString(e));
         return DSA_ERR_CUDA;
@@ -414,9 +448,11 @@ int launch(const GemmFp8Args &a, int split, cudaStream_t stream, char *err, size
 
 int launch_gemm_fp8_tile(const GemmFp8Args &a, int cols, int split, cudaStream_t stream, char *err, size_t errlen)
 {
-    if (cols <= 128)
+    if (cols == 128)
         return a.b_block ? launch<128, false>(a, split, stream, err, errlen) : launch<128, true>(a, split, stream, err, errlen);
-    return a.b_block ? launch<256, false>(a, split, stream, err, errlen) : launch<256, true>(a, split, stream, err, errlen);
+    if (!a.b_block)
+        return launch<192, true>(a, split, stream, err, errlen);
+    return cols == 192 ? launch<192, false>(a, split, stream, err, errlen) : launch<256, false>(a, split, stream, err, errlen);
 }
 
 } // namespace dsa
