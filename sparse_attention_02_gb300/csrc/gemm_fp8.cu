@@ -20,12 +20,12 @@ int launch_gemm_fp8(const GemmFp8Args &a, cudaStream_t stream, char *err, size_t
     // By tiles: the widths of a tile and the splits of K by the time that they take, in us, from what a piece, a tile's
     // output and a cluster's sum were measured at (128 x 704 x 4096 bf16: 13.1 by tiles of 128, 14.9 of 192, 8.6 with K split
     // in 8; 4096 x 704 x 4096 25.0, 16.7 and, of 256, 19.5; 2048 x 2048 x 2048 15.1, 17.6, 12.3; 8191 x 8192 x 8192 534,
-    // 458, 422).  Clusters of eight find room on two thirds of the SMs.
+    // 458, 422).  Clusters of eight find room on two thirds of the SMs.  What is worth a split is too small for tiles of 256.
     struct Width {
         int cols;
-        float piece, rows_piece, out, join; // rows_piece: with a scale for every row of b
+        float piece, rows_piece, out, join; // rows_piece: with a scale for every row of b; join: of a split
     };
-    constexpr Width widths[] = {{128, 0.32f, 0.44f, 1.0f, 4.0f}, {192, 0.38f, 0.60f, 1.6f, 4.6f}, {256, 0.455f, 0.f, 2.4f, 7.f}};
+    constexpr Width widths[] = {{128, 0.32f, 0.44f, 1.0f, 4.0f}, {192, 0.38f, 0.60f, 1.6f, 4.6f}, {256, 0.455f, 0.f, 2.4f, 0.f}};
     int best_cols = 0, best_split = 1;
     float best = 0.f;
     for (const Width &w : widths) {
@@ -33,7 +33,7 @@ int launch_gemm_fp8(const GemmFp8Args &a, cudaStream_t stream, char *err, size_t
             continue;
         for (int split = 1; split <= 8; split *= 2) {
             const int64_t ctas = (((int64_t)a.M + 127) / 128) * (((int64_t)a.N + w.cols - 1) / w.cols) * split;
-            if (split > 1 && (ctas > (split == 8 ? sms * 2 / 3 : sms) || pieces < 2 * split))
+            if (split > 1 && (w.cols == 256 || ctas > (split == 8 ? sms * 2 / 3 : sms) || pieces < 2 * split))
                 break;
             const float turn = (a.b_block ? w.piece : w.rows_piece) * (float)((pieces + split - 1) / split) + w.out * (a.o32 ? 2.f : 1.f);
             const float t = (float)((ctas + sms - 1) / sms) * turn + (split > 1 ? w.join : 0.f);
