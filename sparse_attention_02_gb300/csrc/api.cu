@@ -403,9 +403,9 @@ int dsa_rmsnorm(const void *x, int64_t ldx, const void *residual, int64_t ldr, c
     return rc == DSA_OK ? ok() : rc;
 }
 
-int dsa_layernorm(const void *x, int64_t ldx, const void *residual, int64_t ldr, const void *weight, const void *bias, int64_t rows, int cols,
-                int dtype, int weight_dtype, float eps, void *residual_out, int64_t ldh, void *out, int64_t ldo, void *codes,
-                float *scale, int block, int scale_mode, dsa_stream_t stream)
+int dsa_layernorm(const void *x, int64_t ldx, const void *residual, int64_t ldr, const void *weight, const void *bias,
+                  int64_t rows, int cols, int dtype, int weight_dtype, float eps, void *residual_out, int64_t ldh, void *out,
+                  int64_t ldo, void *codes, float *scale, int block, int scale_mode, dsa_stream_t stream)
 {
     bool none;
     int rc = check_norm(x, ldx, residual, ldr, weight, bias, rows, cols, dtype, weight_dtype, eps, residual_out, ldh, out, ldo, codes,
@@ -449,8 +449,8 @@ size_t dsa_layernorm_backward_workspace_size(int64_t rows, int cols)
 }
 
 int dsa_layernorm_backward(const void *dy, const void *h, const void *weight, const void *dres, int64_t rows, int cols,
-                         int dtype, int weight_dtype, float eps, void *dx, float *dweight, float *dbias, void *workspace,
-                         size_t workspace_bytes, dsa_stream_t stream)
+                           int dtype, int weight_dtype, float eps, void *dx, float *dweight, float *dbias, void *workspace,
+                           size_t workspace_bytes, dsa_stream_t stream)
 {
     int rc = check_norm_backward(dy, h, weight, dres, rows, cols, dtype, weight_dtype, eps, dx, dweight, dbias,
                                  dsa_layernorm_backward_workspace_size(rows, cols), workspace, workspace_bytes);

@@ -49,7 +49,7 @@ template <int BT> struct Cfg {
 
 struct Params {
     const float *a_scale, *b_scale;
-    int M, N, K, pieces, tiles_m;
+    int M, N, pieces;
     bool b_block, o32;
     void *out;
     int64_t ldo;
@@ -79,8 +79,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     float *scales = reinterpret_cast<float *>(smem + C::kScales);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank(), split = cluster_nctarank();
-    const uint32_t tile = blockIdx.x / split;
-    const int m0 = (int)(tile % p.tiles_m) * BT, n0 = (int)(tile / p.tiles_m) * kRows;
+    const int n0 = (int)(blockIdx.x / split) * kRows; // all rows of a: they are BT at most
     // this CTA's pieces
     const int k0 = (int)((int64_t)p.pieces * rank / split), k1 = (int)((int64_t)p.pieces * (rank + 1) / split);
 
@@ -110,7 +109,6 @@ __global__ void __launch_bounds__(kThreads, 2)
     grid_dep_wait(); // no global memory before this
     grid_dep_launch();
 
-    const int left = p.M - m0 < BT ? p.M - m0 : BT;
     float *part = reinterpret_cast<float *>(smem); // [BT][kRows]: a CTA's sums, over the stages once they are done with
 
     if (warp == 0) {
@@ -125,7 +123,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             if (elect_one()) {
                 mbar_arrive_expect_tx(bar(B_FULL + st), C::kStage);
                 tma_load_2d(sbase + st * C::kStage, &tm_b, bar(B_FULL + st), k * kGemmPiece, n0);
-                tma_load_2d(sbase + st * C::kStage + kRowBytes, &tm_a, bar(B_FULL + st), k * kGemmPiece, m0);
+                tma_load_2d(sbase + st * C::kStage + kRowBytes, &tm_a, bar(B_FULL + st), k * kGemmPiece, 0);
             }
             __syncwarp();
         }
@@ -165,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             float v[BT / 4];
 #pragma unroll
             for (int j = 0; j < BT / 4; ++j) {
-                const int m = m0 + 4 * j + (lane >> 3);
+                const int m = 4 * j + (lane >> 3);
                 v[j] = in && m < p.M ? p.a_scale[(int64_t)m * p.pieces + k + kk] * sb : 0.f;
             }
             if (i >= 2 && !wait_warp(bar(B_SE + buf), ((i >> 1) - 1) & 1, abort_flag, p.status)) {
@@ -241,8 +239,8 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (int e = 0; e < 2; ++e) {
                 if (split > 1)
                     part[(2 * c + e) * kRows + 32 * quad + lane] = v[e];
-                else if (row < p.N && 2 * c + e < left)
-                    put(p, m0 + 2 * c + e, row, v[e]);
+                else if (row < p.N && 2 * c + e < p.M)
+                    put(p, 2 * c + e, row, v[e]);
             }
         }
     }
@@ -262,13 +260,13 @@ __global__ void __launch_bounds__(kThreads, 2)
         return;
     cluster_sync_all();
     const int r = 4 * lane; // a warp takes a column of the sums, a lane four rows
-    for (int t = (int)rank + (int)split * warp; t < left; t += split * (kThreads / 32)) {
+    for (int t = (int)rank + (int)split * warp; t < p.M; t += split * (kThreads / 32)) {
         const float4 v = sums_of_cluster(sbase + (t * kRows + r) * 4, split);
         const float f[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             if (n0 + r + e < p.N)
-                put(p, m0 + t, n0 + r + e, f[e]);
+                put(p, t, n0 + r + e, f[e]);
     }
     cluster_sync_all(); // no CTA leaves while its peers read its sums
 }
@@ -277,13 +275,13 @@ template <int BT>
 int launch(const GemmFp8Args &a, int split, cudaStream_t stream, char *err, size_t errlen)
 {
     using C = Cfg<BT>;
-    Params p{a.a_scale, a.b_scale, a.M, a.N, a.K, (a.K + kGemmPiece - 1) / kGemmPiece, (a.M + BT - 1) / BT, a.b_block, a.o32, a.out,
+    Params p{a.a_scale, a.b_scale, a.M, a.N, (a.K + kGemmPiece - 1) / kGemmPiece, a.b_block, a.o32, a.out,
              a.ldo, device_status_ptr()};
     if (!p.status) {
         snprintf(err, errlen, "device status word unavailable");
         return DSA_ERR_CUDA;
     }
-    const int64_t grid = (int64_t)p.tiles_m * ((a.N + kRows - 1) / kRows) * split;
+    const int64_t grid = ((int64_t)a.N + kRows - 1) / kRows * split;
     CUtensorMap ta{}, tb{};
     if (a.K > 0 && (!gemm_fp8_map(&ta, a.a, a.lda, a.M, a.K, BT, err, errlen) ||
                     !gemm_fp8_map(&tb, a.b, a.ldb, a.N, a.K, kRows, err, errlen)))

@@ -91,7 +91,7 @@ template <int N> __device__ __forceinline__ void unpack(const F2 (&v)[N][4], flo
 
 // One row of layer norm's backward.  WARP: LANES lanes own it.  dw: this thread's dweight sums, and behind them its dbias
 // sums.  red: kMoments floats.  Values are unpacked once and worked on in pairs: with a CTA's 512 threads on one row, its
-// instructions and the meeting's latency add up (8192 x 8192 with single operations on values unpacked in each pass 117 us).
+// instructions and the meeting's latency add up.
 template <typename T, typename W, int NV, bool WARP, bool VEC, int LANES>
 __device__ __forceinline__ void layernorm_backward_row(const NormBackwardArgs &a, const T *hp, const T *dp, const T *ep, int64_t row,
                                                        bool there, const Held<T, W, NV, VEC> &held, F2 (&dw)[2 * NV][4], float *red)

@@ -123,10 +123,7 @@ template <> struct Chunk<float> {
         for (int i = 0; i < 8; ++i)
             f[i] = t.f[i];
     }
-    __device__ __forceinline__ static Tops none()
-    {
-        return Tops{};
-    }
+    __device__ __forceinline__ static Tops none() { return Tops{}; }
 };
 
 // Eight values from p on, zeros from the ncol-th on.  !VEC: p is aligned to its elements only, and eight values are cut
@@ -399,7 +396,7 @@ template <typename T, bool VEC> __global__ void __launch_bounds__(256, 4) quanti
     const bool aligned = ((reinterpret_cast<uintptr_t>(a.codes) | a.ldc) & 7) == 0;
     const uint8_t *lo = static_cast<const uint8_t *>(a.x), *hi = end_of<T>(a);
     for (int64_t p0 = ((int64_t)blockIdx.x * 16 + (threadIdx.x >> 4)) * N; p0 - N * half < pieces; p0 += step) { // whole warps
-        int64_t row = pieces <= UINT32_MAX ? (uint32_t)p0 / (uint32_t)cblocks : p0 / cblocks;
+        int64_t row = pieces <= INT32_MAX ? (uint32_t)p0 / (uint32_t)cblocks : p0 / cblocks;
         int at = (int)(p0 - row * cblocks);
         C v[N];
         int64_t rows[N];
