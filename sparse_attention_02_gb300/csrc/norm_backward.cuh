@@ -94,7 +94,7 @@ template <int N> __device__ __forceinline__ void unpack(const F2 (&v)[N][4], flo
 // instructions and the meeting's latency add up.
 template <typename T, typename W, int NV, bool WARP, bool VEC, int LANES>
 __device__ __forceinline__ void layernorm_backward_row(const NormBackwardArgs &a, const T *hp, const T *dp, const T *ep, int64_t row,
-                                                       bool there, const Held<T, W, NV, VEC> &held, F2 (&dw)[2 * NV][4], float *red)
+                                                       bool there, const Held<T, W, NV, VEC> &held, const Counts &n, F2 (&dw)[2 * NV][4], float *red)
 {
     const int G = WARP ? LANES : blockDim.x;
     const int g = WARP ? (threadIdx.x & (LANES - 1)) : threadIdx.x;
@@ -125,61 +125,69 @@ __device__ __forceinline__ void layernorm_backward_row(const NormBackwardArgs &a
             }
         }
     }
-    const float sum = warp_sum<LANES>(s2.sum());
-    float sg = warp_sum<LANES>(t2.sum());
-    const int n = WARP ? cols : warp_columns<NV>(G, g >> 5, cols);
-    float mean = n ? sum / (float)n : 0.f; // the warp's own
-    const F2 back(-mean);
+    float sum, sg, sums = 0.f;
+    if constexpr (WARP) {
+        sums = half_sums<LANES>(s2.sum(), t2.sum());
+        sum = from_half<LANES, 0>(sums);
+    } else { // four sums beside one another: what counts is how long a row's meeting takes
+        sum = warp_sum(s2.sum());
+        sg = warp_sum(t2.sum());
+    }
+    const float mean = sum * n.inv_mine; // the warp's own
     s2 = t2 = F2(0.f);
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
         const int cb = chunk_base<VEC>(c, G, g);
+        const F2 back(!VEC || cb < cols ? -mean : 0.f); // past cols: no part of the sum of squares
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             h[c][i] = h[c][i] + back;
-            if (VEC ? cb >= cols : column<T, VEC>(cb, 2 * i) >= cols) // past cols: no part of the sum of squares
-                h[c][i] = F2(0.f);
-            else if (!VEC && column<T, VEC>(cb, 2 * i + 1) >= cols) {
+            if (!VEC && column<T, VEC>(cb, 2 * i + 1) >= cols) {
                 float lo, hi;
                 h[c][i].get(lo, hi);
-                h[c][i] = F2(lo, 0.f);
+                h[c][i] = F2(column<T, VEC>(cb, 2 * i) < cols ? lo : 0.f, 0.f);
             }
             s2 = fma2(h[c][i], h[c][i], s2);
             t2 = fma2(gw[c][i], h[c][i], t2);
         }
     }
-    float sq = warp_sum<LANES>(s2.sum()), gd = warp_sum<LANES>(t2.sum());
-    float off = 0.f; // of the row's mean from the warp's
-    if constexpr (!WARP) {
-        const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+    float off = 0.f, sq, gd; // off: of the row's mean from the warp's
+    if constexpr (WARP) {
+        const float squares = half_sums<LANES>(s2.sum(), t2.sum());
+        sq = from_half<LANES, 0>(squares);
+        gd = from_half<LANES, 1>(squares);
+        sg = from_half<LANES, 1>(sums);
+    } else {
+        sq = warp_sum(s2.sum());
+        gd = warp_sum(t2.sum());
+        const int lane = threadIdx.x & 31;
         if (lane == 0) {
             float *to = red + (threadIdx.x >> 5);
             to[0] = sum, to[32] = sq, to[64] = sg, to[96] = gd;
         }
         __syncthreads();
-        const int m = lane < warps ? warp_columns<NV>(G, lane, cols) : 0;
-        const float mine = m ? red[lane] : 0.f, g_mine = m ? red[64 + lane] : 0.f;
-        const float all = warp_sum(mine) / (float)cols;
-        const float dm = m ? mine / (float)m - all : 0.f;
-        sg = warp_sum(g_mine);
-        sq = warp_sum(m ? red[32 + lane] + (float)m * dm * dm : 0.f);
-        gd = warp_sum(m ? fmaf(dm, g_mine, red[96 + lane]) : 0.f);
+        const bool is = n.other > 0.f;
+        const float its = is ? red[lane] : 0.f, its_g = is ? red[64 + lane] : 0.f;
+        const float all = warp_sum(its) * n.inv_all, dm = is ? its * n.inv_other - all : 0.f;
+        sg = warp_sum(its_g);
+        sq = warp_sum(is ? red[32 + lane] + n.other * dm * dm : 0.f);
+        gd = warp_sum(is ? fmaf(dm, its_g, red[96 + lane]) : 0.f);
         off = mean - all;
     }
-    const float r = 1.f / sqrtf(sq / (float)cols + a.eps);
-    const float k = gd * r * r / (float)cols, mean_g = sg / (float)cols; // k: mean(g xhat) r
+    const float r = rsqrtf(sq * n.inv_all + a.eps);
+    const float k = gd * n.inv_all * r * r, mean_g = sg * n.inv_all; // k: mean(g xhat) r
     if (!there)
         return;
-    const F2 off2(off), r2(r), k2(-k), mg2(-mean_g);
+    const F2 off2(off * r), r2(r), k2(-k), mg2(-mean_g * r);
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
         const int cb = chunk_base<VEC>(c, G, g);
-        float o[8];
+        F2 o2[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) { // past cols d is zero
-            const F2 x = h[c][i] + off2;
-            (fma2(x, k2, gw[c][i] + mg2) * r2).get(o[2 * i], o[2 * i + 1]);
-            dw[c][i] = fma2(d[c][i], x * r2, dw[c][i]);
+            const F2 xhat = fma2(h[c][i], r2, off2);
+            o2[i] = fma2(xhat, k2, fma2(gw[c][i], r2, mg2));
+            dw[c][i] = fma2(d[c][i], xhat, dw[c][i]);
             dw[NV + c][i] = dw[NV + c][i] + d[c][i];
         }
         if (ep) {
@@ -188,9 +196,13 @@ __device__ __forceinline__ void layernorm_backward_row(const NormBackwardArgs &a
             load_chunk<VEC>(ev, ep, cb, cols);
             ev.get(e);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                o[i] += e[i];
+            for (int i = 0; i < 4; ++i)
+                o2[i] = o2[i] + F2(e[2 * i], e[2 * i + 1]);
         }
+        float o[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            o2[i].get(o[2 * i], o[2 * i + 1]);
         Vec8<T> v;
         v.set(o);
         store_chunk<VEC>(v, static_cast<T *>(a.dx) + row * cols, cb, cols);
@@ -297,13 +309,14 @@ __global__ void __launch_bounds__(WARP ? (LN ? kLayerRowThreads : kRowThreads) :
     float dw[N][8] = {};
     if constexpr (LN) {
         Held<T, W, NV, VEC> held;
+        const Counts n = Counts::of<NV, WARP>(G, cols);
         clear(dw2);
         held.load(static_cast<const W *>(a.weight), G, g, cols);
         int turn = 0;
         // a warp's two rows walk together: its lanes add up among themselves
         for (int64_t row = row0; row - (WARP ? threadIdx.x % 32 / LANES : 0) < a.rows; row += step, turn ^= 1)
             layernorm_backward_row<T, W, NV, WARP, VEC, LANES>(a, h + row * cols, dy + row * cols, dres ? dres + row * cols : nullptr,
-                                                               row, LANES == 32 || row < a.rows, held, dw2, red + turn * kMoments);
+                                                               row, LANES == 32 || row < a.rows, held, n, dw2, red + turn * kMoments);
         unpack(dw2, dw);
     } else {
         for (int64_t row = row0; row < a.rows; row += step)
@@ -333,6 +346,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, WARP ? 2 : 1)
     clear(dw2);
     float dw[N][8] = {};
     [[maybe_unused]] Held<T, W, NV, VEC> held;
+    [[maybe_unused]] const Counts n = Counts::of<NV, WARP>(G, a.cols);
     [[maybe_unused]] bool first = true;
     ring.walk(smem, status, [&](uint8_t *stage, int64_t row) {
         auto at = [&](int k) { return reinterpret_cast<const T *>(stage + ring.at(k, row, w)); };
@@ -343,7 +357,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, WARP ? 2 : 1)
         }
         if (row + w < a.rows) {
             if constexpr (LN)
-                layernorm_backward_row<T, W, NV, WARP, VEC, 32>(a, at(0), at(1), a.dres ? at(2) : nullptr, row + w, true, held, dw2, red);
+                layernorm_backward_row<T, W, NV, WARP, VEC, 32>(a, at(0), at(1), a.dres ? at(2) : nullptr, row + w, true, held, n, dw2, red);
             else
                 rmsnorm_backward_row<T, W, NV, WARP, VEC>(a, at(0), at(1), a.dres ? at(2) : nullptr, row + w, dw, red);
         }

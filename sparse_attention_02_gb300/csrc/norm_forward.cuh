@@ -7,24 +7,36 @@
 namespace dsa {
 namespace {
 
+struct Meet {
+    __device__ __forceinline__ bool operator()() const
+    {
+        __syncthreads();
+        return true;
+    }
+};
+
 // One row: x and res (null: none) point at it, in global memory or a stage of the
-// ring.  A CTA's rows have a barrier between them (the ring), or there is but one.
-template <typename T, typename W, int NV, bool WARP, bool VEC, bool LN, bool HELD = false>
+// ring.  A CTA's rows have a barrier between them (the RMS norm's ring), or there is but one.
+// RING (layer norm): held, of the weight and of the bias; meet, the threads' one meeting, after which the stage is not read;
+// there: whether this warp has a row.  moments: of this row, 64 floats.
+template <typename T, typename W, int NV, bool WARP, bool VEC, bool LN, bool RING = false, typename M = Meet>
 __device__ __forceinline__ void norm_row(const NormArgs &a, const T *x, const T *res, int64_t row, float *red,
-                                         const Held<T, W, NV, VEC> *held = nullptr) // HELD: of the weight, of the bias
+                                         [[maybe_unused]] float *moments = nullptr, [[maybe_unused]] const Held<T, W, NV, VEC> *held = nullptr,
+                                         [[maybe_unused]] bool there = true, M meet = M())
 {
     const int G = WARP ? 32 : blockDim.x;
     const int g = WARP ? (threadIdx.x & 31) : threadIdx.x;
     const int cols = a.cols;
     const W *weight = static_cast<const W *>(a.weight);
+    const int mine = !RING || !WARP || there ? cols : 0; // of the stage's columns
     Vec8<T> xv[NV], rv[NV];
 #pragma unroll
     for (int c = 0; c < NV; ++c)
-        load_chunk<VEC>(xv[c], x, chunk_base<VEC>(c, G, g), cols);
+        load_chunk<VEC>(xv[c], x, chunk_base<VEC>(c, G, g), mine);
     if (res) {
 #pragma unroll
         for (int c = 0; c < NV; ++c)
-            load_chunk<VEC>(rv[c], res, chunk_base<VEC>(c, G, g), cols);
+            load_chunk<VEC>(rv[c], res, chunk_base<VEC>(c, G, g), mine);
     }
     float h[NV][8];
     float ss = 0.f;
@@ -43,6 +55,10 @@ __device__ __forceinline__ void norm_row(const NormArgs &a, const T *x, const T 
         for (int i = 0; i < 8; ++i)
             s = LN ? s + h[c][i] : fmaf(h[c][i], h[c][i], s);
         ss += s;
+    }
+    if (RING && WARP) { // as soon as the stage is read
+        if (!meet() || !there)
+            return;
     }
     // a tensor may be overwritten in place: each value is written by the
     // thread that read it
@@ -75,15 +91,16 @@ __device__ __forceinline__ void norm_row(const NormArgs &a, const T *x, const T 
         if (!WARP) {
             const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
             if (lane == 0) {
-                red[64 + (threadIdx.x >> 5)] = ss;
-                red[96 + (threadIdx.x >> 5)] = sq;
+                moments[threadIdx.x >> 5] = ss;
+                moments[32 + (threadIdx.x >> 5)] = sq;
             }
-            __syncthreads();
+            if (!meet())
+                return;
             const int m = lane < warps ? warp_columns<NV>(G, lane, cols) : 0;
-            ss = m ? red[64 + lane] : 0.f;
+            ss = m ? moments[lane] : 0.f;
             mean = warp_sum(ss) / (float)cols;
             const float d = m ? ss / (float)m - mean : 0.f;
-            sq = warp_sum(m ? red[96 + lane] + (float)m * d * d : 0.f);
+            sq = warp_sum(m ? moments[32 + lane] + (float)m * d * d : 0.f);
         }
         ss = sq;
 #pragma unroll
@@ -98,7 +115,7 @@ __device__ __forceinline__ void norm_row(const NormArgs &a, const T *x, const T 
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
         float w[8];
-        if (HELD)
+        if (RING)
             held[0].get(w, weight, c, chunk_base<VEC>(c, G, g), cols);
         else
             load_weights<T, VEC>(w, weight, chunk_base<VEC>(c, G, g), cols);
@@ -106,7 +123,7 @@ __device__ __forceinline__ void norm_row(const NormArgs &a, const T *x, const T 
         for (int i = 0; i < 8; ++i)
             h[c][i] = h[c][i] * r * w[i];
         if (LN && a.bias) {
-            if (HELD)
+            if (RING)
                 held[1].get(w, static_cast<const W *>(a.bias), c, chunk_base<VEC>(c, G, g), cols);
             else
                 load_weights<T, VEC>(w, static_cast<const W *>(a.bias), chunk_base<VEC>(c, G, g), cols);
@@ -180,14 +197,14 @@ __device__ __forceinline__ void norm_row(const NormArgs &a, const T *x, const T 
 template <typename T, typename W, int NV, bool WARP, bool VEC, bool LN>
 __global__ void __launch_bounds__(WARP ? kRowThreads : 1024) norm_kernel(NormArgs a)
 {
-    __shared__ float red[LN ? 128 : 64];
+    __shared__ float red[64], moments[LN ? 64 : 1];
     grid_dep_wait();
     grid_dep_launch();
     const int64_t row0 = WARP ? (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5) : blockIdx.x;
     const int64_t step = (int64_t)gridDim.x * (WARP ? kRowThreads / 32 : 1);
     for (int64_t row = row0; row < a.rows; row += step)
         norm_row<T, W, NV, WARP, VEC, LN>(a, static_cast<const T *>(a.x) + row * a.ldx,
-                                         a.residual ? static_cast<const T *>(a.residual) + row * a.ldr : nullptr, row, red);
+                                         a.residual ? static_cast<const T *>(a.residual) + row * a.ldr : nullptr, row, red, moments);
 }
 
 // WARP: a stage is a row for each warp.
@@ -196,26 +213,33 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, WARP ? 2 : 1)
     norm_ring_kernel(NormArgs a, int stages, unsigned *status)
 {
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ float red[LN ? 128 : 64];
+    __shared__ float red[64], moments[LN ? 128 : 1]; // of two rows: one meeting lies between them
     const int bytes = a.cols * (int)sizeof(T), group = WARP ? blockDim.x >> 5 : 1, w = WARP ? threadIdx.x >> 5 : 0;
     const Ring<VEC> ring{{static_cast<const uint8_t *>(a.x), static_cast<const uint8_t *>(a.residual), nullptr},
                          {a.ldx * (int64_t)sizeof(T), a.ldr * (int64_t)sizeof(T), 0},
                          a.residual ? 2 : 1, group, bytes, stages, a.rows};
-    [[maybe_unused]] Held<T, W, NV, VEC> held[LN ? 2 : 1];
-    [[maybe_unused]] bool first = true;
-    ring.walk(smem, status, [&](uint8_t *stage, int64_t row) {
-        if (LN && first) { // not before the walk has waited for the kernel in front
-            const int G = WARP ? 32 : blockDim.x, g = WARP ? threadIdx.x & 31 : threadIdx.x;
-            held[0].load(static_cast<const W *>(a.weight), G, g, a.cols);
-            if (a.bias)
-                held[LN ? 1 : 0].load(static_cast<const W *>(a.bias), G, g, a.cols);
-            first = false;
-        }
-        if (row + w < a.rows)
-            norm_row<T, W, NV, WARP, VEC, LN, LN>(a, reinterpret_cast<const T *>(stage + ring.at(0, row, w)),
-                                                  a.residual ? reinterpret_cast<const T *>(stage + ring.at(1, row, w)) : nullptr,
-                                                  row + w, red, held);
-    });
+    auto at = [&](int k, uint8_t *stage, int64_t row) { return reinterpret_cast<const T *>(stage + ring.at(k, row, w)); };
+    if constexpr (LN) {
+        Held<T, W, NV, VEC> held[2];
+        int turn = -1; // before the first row
+        ring.template walk<true>(smem, status, [&](uint8_t *stage, int64_t row, auto meet) {
+            if (turn < 0) { // not before the walk has waited for the kernel in front
+                const int G = WARP ? 32 : blockDim.x, g = WARP ? threadIdx.x & 31 : threadIdx.x;
+                held[0].load(static_cast<const W *>(a.weight), G, g, a.cols);
+                if (a.bias)
+                    held[1].load(static_cast<const W *>(a.bias), G, g, a.cols);
+                turn = 0;
+            }
+            norm_row<T, W, NV, WARP, VEC, true, true>(a, at(0, stage, row), a.residual ? at(1, stage, row) : nullptr, row + w, red,
+                                                      moments + 64 * turn, held, row + w < a.rows, meet);
+            turn ^= 1;
+        });
+    } else {
+        ring.walk(smem, status, [&](uint8_t *stage, int64_t row) {
+            if (row + w < a.rows)
+                norm_row<T, W, NV, WARP, VEC, false>(a, at(0, stage, row), a.residual ? at(1, stage, row) : nullptr, row + w, red);
+        });
+    }
 }
 
 template <bool LN> int launch_norm(const NormArgs &a, const char *name, cudaStream_t stream, char *err, size_t errlen)

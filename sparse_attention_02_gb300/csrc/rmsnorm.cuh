@@ -292,6 +292,22 @@ template <int LANES = 32> __device__ __forceinline__ float warp_sum(float a)
     return a;
 }
 
+// Sums of a and of b over the LANES lanes of a row together: where a lane ends with a's in the lower half, with b's in the
+// upper one.
+template <int LANES = 32> __device__ __forceinline__ float half_sums(float a, float b)
+{
+    const bool upper = threadIdx.x & (LANES / 2);
+    const float give = upper ? a : b;
+    a = (upper ? b : a) + __shfl_xor_sync(0xffffffffu, give, LANES / 2);
+    return warp_sum<LANES / 2>(a);
+}
+
+// What lane 0 (HALF = 0) or the upper half (1) of LANES lanes has.
+template <int LANES, int HALF> __device__ __forceinline__ float from_half(float a)
+{
+    return __shfl_sync(0xffffffffu, a, HALF * (LANES / 2), LANES);
+}
+
 // Columns of a row that warp w of a row's G threads holds.
 template <int NV> __device__ __forceinline__ int warp_columns(int G, int w, int cols)
 {
@@ -304,7 +320,18 @@ template <int NV> __device__ __forceinline__ int warp_columns(int G, int w, int 
     return n;
 }
 
-constexpr int kMoments = 4 * 32; // floats that a meeting takes; the next of the same CTA takes others
+// What a thread knows of its row's columns before the first row: of its warp's, and of those of warp `lane`.
+struct Counts {
+    float inv_mine, other, inv_other, inv_all;
+    template <int NV, bool WARP> static __device__ __forceinline__ Counts of(int G, int cols)
+    {
+        const int lane = threadIdx.x & 31;
+        const int n = WARP ? cols : warp_columns<NV>(G, threadIdx.x >> 5, cols), m = WARP || 32 * lane >= G ? 0 : warp_columns<NV>(G, lane, cols);
+        return {n ? 1.f / (float)n : 0.f, (float)m, m ? 1.f / (float)m : 0.f, 1.f / (float)cols};
+    }
+};
+
+constexpr int kMoments = 4 * 32; // floats that a meeting takes, at most; the next of the same CTA takes others
 
 // ---- the ring of rows in shared memory
 constexpr int kRingMost = 8;   // stages at most
@@ -388,7 +415,10 @@ template <bool VEC> struct Ring {
     }
     // Walks the groups blockIdx.x, + gridDim.x, ...; row_fn(stage, first row) works on one with every thread of the CTA
     // and ends with its values in registers or written.  All threads meet before a stage is filled again.
-    template <typename F> __device__ __forceinline__ void walk(uint8_t *smem, unsigned *status, F &&row_fn) const
+    // MEETS: row_fn(stage, first row, meet) calls meet() once, when it has read the stage, as the threads' one meeting in a
+    // row: the stage may be filled again, and what the threads wrote to shared memory before can be read.  Where that returns
+    // false the stage never came, and the walk ends.
+    template <bool MEETS = false, typename F> __device__ __forceinline__ void walk(uint8_t *smem, unsigned *status, F &&row_fn) const
     {
         const uint32_t bar0 = smem_u32(smem);
         volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + 8 * kRingMost);
@@ -410,12 +440,27 @@ template <bool VEC> struct Ring {
         int st = 0, phase = 0;
         for (int64_t row = first; row < rows; row += step) {
             const bool ok = mbar_wait(bar0 + 8 * st, phase, abort_flag, status);
-            if (!__syncthreads_and(ok))
-                break;
-            row_fn(data + st * stage_bytes(), row);
-            __syncthreads();
-            if (threadIdx.x == 0 && row + stages * step < rows)
-                load(row + stages * step, data + st * stage_bytes(), bar0 + 8 * st);
+            auto fill = [&] {
+                if (threadIdx.x == 0 && row + stages * step < rows)
+                    load(row + stages * step, data + st * stage_bytes(), bar0 + 8 * st);
+            };
+            if constexpr (MEETS) {
+                bool all = false;
+                row_fn(data + st * stage_bytes(), row, [&] {
+                    all = __syncthreads_and(ok);
+                    if (all)
+                        fill();
+                    return all;
+                });
+                if (!all)
+                    break;
+            } else {
+                if (!__syncthreads_and(ok))
+                    break;
+                row_fn(data + st * stage_bytes(), row);
+                __syncthreads();
+                fill();
+            }
             if (++st == stages) {
                 st = 0;
                 phase ^= 1;
