@@ -17,13 +17,21 @@
 // beside a ring an SM's L1 does not hold both (8191 x 8192 with residual, both outputs
 // and block codes 127 us when each row read them again, 111 so).
 //
-// Measured: 8191 x 8192 bf16, residual, both outputs, block codes 111 us (81 % of
-// measured HBM; the RMS norm 96).  64 x 128 3.2 us.  Backward of 8192 x 8192 with dres
-// 117 us (68 %): its two sums a column leave room for one CTA of 512 threads an SM, and
-// what a row's instructions (2200 cycles' issue) and its meeting take is not hidden by
-// another's.  Not kept: two rows at once there (146, spills), more stages (118).
-// 32767 x 128 fp32 backward 14.5 us (7 of them the dweight sum's own launch), two rows a
-// warp; 24.5 with one row a warp and as many CTAs as the RMS norm.
+// An SM has a row of 8192 columns at work at a time, so that a row's instructions are
+// what bytes wait for: arithmetic goes in pairs, counts are divided by once a call
+// (mean_of, rsqrtf), what lies past the columns is kept out by a chunk's offset instead of
+// a choice a value, and the ring's threads meet once a row instead of three times (all of
+// that 111 -> 99 us, and backward 116 -> 98).
+//
+// Measured: 8191 x 8192 bf16, residual, both outputs, block codes 99 us (90 % of
+// measured HBM; the RMS norm 96); without residual and codes 46 (86 %).  64 x 128 3.2 us.
+// Backward of 8192 x 8192 with dres 98 us (81 %): its two sums a column leave room for
+// one CTA of 512 threads an SM, and what a row's meeting takes is not hidden by another's.
+// Not kept there: two rows at once (146, spills), more stages (118 of 116 then), dres read before
+// the meeting for the ring's single one (115, but 16384 x 2048 56 -> 60: registers).
+// 32767 x 128 fp32 backward 13.4 us (7 of them the dweight sum's own launch), two rows a
+// warp, whose half-warps add up two quantities at once; 24.5 with one row a warp and as many
+// CTAs as the RMS norm.
 #include "norm_forward.cuh"
 
 namespace dsa {

@@ -21,7 +21,7 @@ struct Meet {
 // there: whether this warp has a row.  moments: of this row, 64 floats.
 template <typename T, typename W, int NV, bool WARP, bool VEC, bool LN, bool RING = false, typename M = Meet>
 __device__ __forceinline__ void norm_row(const NormArgs &a, const T *x, const T *res, int64_t row, float *red,
-                                         [[maybe_unused]] float *moments = nullptr, [[maybe_unused]] const Held<T, W, NV, VEC> *held = nullptr,
+                                         [[maybe_unused]] float *moments = nullptr, [[maybe_unused]] const Counts &n = Counts(), [[maybe_unused]] const Held<T, W, NV, VEC> *held = nullptr,
                                          [[maybe_unused]] bool there = true, M meet = M())
 {
     const int G = WARP ? 32 : blockDim.x;
@@ -50,11 +50,19 @@ __device__ __forceinline__ void norm_row(const NormArgs &a, const T *x, const T 
             for (int i = 0; i < 8; ++i)
                 h[c][i] += r[i];
         }
-        float s = 0.f; // 8 values at a time, so no long fp32 chain
+        if (LN) {
+            F2 s(0.f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            s = LN ? s + h[c][i] : fmaf(h[c][i], h[c][i], s);
-        ss += s;
+            for (int i = 0; i < 8; i += 2)
+                s = s + F2(h[c][i], h[c][i + 1]);
+            ss += s.sum();
+        } else {
+            float s = 0.f; // 8 values at a time, so no long fp32 chain
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                s = fmaf(h[c][i], h[c][i], s);
+            ss += s;
+        }
     }
     if (RING && WARP) { // as soon as the stage is read
         if (!meet() || !there)
@@ -74,62 +82,63 @@ __device__ __forceinline__ void norm_row(const NormArgs &a, const T *x, const T 
     if (LN) {
         // about the warp's own mean first, from the registers
         ss = warp_sum(ss);
-        const int n = warp_columns<NV>(G, g >> 5, cols);
-        float mean = n ? ss / (float)n : 0.f, sq = 0.f;
+        float mean = mean_of(ss, n.mine, n.inv_mine);
+        F2 sq2(0.f);
 #pragma unroll
         for (int c = 0; c < NV; ++c) {
             const int cb = chunk_base<VEC>(c, G, g);
-            float s = 0.f;
+            const F2 back(!VEC || cb < cols ? -mean : 0.f); // past cols: no part of the sum of squares
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float d = h[c][i] - mean;
-                s = (VEC ? cb < cols : column<T, VEC>(cb, i) < cols) ? fmaf(d, d, s) : s;
+            for (int i = 0; i < 8; i += 2) {
+                F2 d = F2(h[c][i], h[c][i + 1]) + back;
+                if (!VEC && column<T, VEC>(cb, i + 1) >= cols)
+                    d = F2(column<T, VEC>(cb, i) < cols ? h[c][i] - mean : 0.f, 0.f);
+                sq2 = fma2(d, d, sq2);
             }
-            sq += s;
         }
-        sq = warp_sum(sq);
+        float sq = warp_sum(sq2.sum());
         if (!WARP) {
-            const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+            const int lane = threadIdx.x & 31;
             if (lane == 0) {
                 moments[threadIdx.x >> 5] = ss;
                 moments[32 + (threadIdx.x >> 5)] = sq;
             }
             if (!meet())
                 return;
-            const int m = lane < warps ? warp_columns<NV>(G, lane, cols) : 0;
-            ss = m ? moments[lane] : 0.f;
-            mean = warp_sum(ss) / (float)cols;
-            const float d = m ? ss / (float)m - mean : 0.f;
-            sq = warp_sum(m ? moments[32 + lane] + (float)m * d * d : 0.f);
+            const bool is = n.other > 0.f;
+            ss = is ? moments[lane] : 0.f;
+            mean = mean_of(warp_sum(ss), n.all, n.inv_all);
+            const float d = mean_of(ss, n.other, n.inv_other) - mean;
+            sq = warp_sum(is ? moments[32 + lane] + n.other * d * d : 0.f);
         }
-        ss = sq;
+        const F2 r2(rsqrtf(sq * n.inv_all + a.eps)), back(-mean);
 #pragma unroll
-        for (int c = 0; c < NV; ++c)
+        for (int c = 0; c < NV; ++c) {
+            float w[8], b[8] = {};
+            if (RING)
+                held[0].get(w, weight, c, chunk_base<VEC>(c, G, g), cols);
+            else
+                load_weights<T, VEC>(w, weight, chunk_base<VEC>(c, G, g), cols);
+            if (a.bias) {
+                if (RING)
+                    held[1].get(b, static_cast<const W *>(a.bias), c, chunk_base<VEC>(c, G, g), cols);
+                else
+                    load_weights<T, VEC>(b, static_cast<const W *>(a.bias), chunk_base<VEC>(c, G, g), cols);
+            }
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                h[c][i] -= mean;
+            for (int i = 0; i < 8; i += 2)
+                fma2((F2(h[c][i], h[c][i + 1]) + back) * r2, F2(w[i], w[i + 1]), F2(b[i], b[i + 1])).get(h[c][i], h[c][i + 1]);
+        }
     } else {
         ss = group_reduce<WARP, false>(ss, 0.f, red).x;
-    }
-    const float r = 1.f / sqrtf(ss / (float)cols + a.eps);
+        const float r = 1.f / sqrtf(ss / (float)cols + a.eps);
 #pragma unroll
-    for (int c = 0; c < NV; ++c) {
-        float w[8];
-        if (RING)
-            held[0].get(w, weight, c, chunk_base<VEC>(c, G, g), cols);
-        else
+        for (int c = 0; c < NV; ++c) {
+            float w[8];
             load_weights<T, VEC>(w, weight, chunk_base<VEC>(c, G, g), cols);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            h[c][i] = h[c][i] * r * w[i];
-        if (LN && a.bias) {
-            if (RING)
-                held[1].get(w, static_cast<const W *>(a.bias), c, chunk_base<VEC>(c, G, g), cols);
-            else
-                load_weights<T, VEC>(w, static_cast<const W *>(a.bias), chunk_base<VEC>(c, G, g), cols);
-#pragma unroll
             for (int i = 0; i < 8; ++i)
-                h[c][i] += w[i];
+                h[c][i] = h[c][i] * r * w[i];
         }
     }
     if (a.out) {
@@ -202,9 +211,10 @@ __global__ void __launch_bounds__(WARP ? kRowThreads : 1024) norm_kernel(NormArg
     grid_dep_launch();
     const int64_t row0 = WARP ? (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5) : blockIdx.x;
     const int64_t step = (int64_t)gridDim.x * (WARP ? kRowThreads / 32 : 1);
+    [[maybe_unused]] const Counts n = LN ? Counts::of<NV, WARP>(WARP ? 32 : blockDim.x, a.cols) : Counts();
     for (int64_t row = row0; row < a.rows; row += step)
         norm_row<T, W, NV, WARP, VEC, LN>(a, static_cast<const T *>(a.x) + row * a.ldx,
-                                         a.residual ? static_cast<const T *>(a.residual) + row * a.ldr : nullptr, row, red, moments);
+                                         a.residual ? static_cast<const T *>(a.residual) + row * a.ldr : nullptr, row, red, moments, n);
 }
 
 // WARP: a stage is a row for each warp.
@@ -221,6 +231,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, WARP ? 2 : 1)
     auto at = [&](int k, uint8_t *stage, int64_t row) { return reinterpret_cast<const T *>(stage + ring.at(k, row, w)); };
     if constexpr (LN) {
         Held<T, W, NV, VEC> held[2];
+        const Counts n = Counts::of<NV, WARP>(WARP ? 32 : blockDim.x, a.cols);
         int turn = -1; // before the first row
         ring.template walk<true>(smem, status, [&](uint8_t *stage, int64_t row, auto meet) {
             if (turn < 0) { // not before the walk has waited for the kernel in front
@@ -231,7 +242,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, WARP ? 2 : 1)
                 turn = 0;
             }
             norm_row<T, W, NV, WARP, VEC, true, true>(a, at(0, stage, row), a.residual ? at(1, stage, row) : nullptr, row + w, red,
-                                                      moments + 64 * turn, held, row + w < a.rows, meet);
+                                                      moments + 64 * turn, n, held, row + w < a.rows, meet);
             turn ^= 1;
         });
     } else {

@@ -4,6 +4,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "fp8.cuh"
 #include "launch.h"
 
@@ -320,16 +321,24 @@ template <int NV> __device__ __forceinline__ int warp_columns(int G, int w, int 
     return n;
 }
 
-// What a thread knows of its row's columns before the first row: of its warp's, and of those of warp `lane`.
+// How many columns there are, and the counts' reciprocals, before the first row: of a thread's warp, of warp `lane`, of the row.
 struct Counts {
-    float inv_mine, other, inv_other, inv_all;
+    float mine, inv_mine, other, inv_other, all, inv_all;
     template <int NV, bool WARP> static __device__ __forceinline__ Counts of(int G, int cols)
     {
         const int lane = threadIdx.x & 31;
         const int n = WARP ? cols : warp_columns<NV>(G, threadIdx.x >> 5, cols), m = WARP || 32 * lane >= G ? 0 : warp_columns<NV>(G, lane, cols);
-        return {n ? 1.f / (float)n : 0.f, (float)m, m ? 1.f / (float)m : 0.f, 1.f / (float)cols};
+        return {(float)n, n ? 1.f / (float)n : 0.f, (float)m, m ? 1.f / (float)m : 0.f, (float)cols, 1.f / (float)cols};
     }
 };
+
+// s / n with n's correctly rounded reciprocal, correctly rounded (P. Markstein, "Computation of elementary functions on the IBM
+// RISC System/6000 processor", 1990): the mean of equal values is that value.
+__device__ __forceinline__ float mean_of(float s, float n, float inv)
+{
+    const float q = s * inv;
+    return fmaf(fmaf(-q, n, s), inv, q);
+}
 
 constexpr int kMoments = 4 * 32; // floats that a meeting takes, at most; the next of the same CTA takes others
 
