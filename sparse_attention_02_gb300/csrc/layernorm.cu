@@ -21,15 +21,15 @@
 // what bytes wait for: arithmetic goes in pairs, counts are divided by once a call
 // (mean_of, rsqrtf), what lies past the columns is kept out by a chunk's offset instead of
 // a choice a value, and the ring's threads meet once a row instead of three times (all of
-// that 111 -> 99 us, and backward 116 -> 98).
+// that 111 -> 99 us, and backward 116 -> 96).
 //
 // Measured: 8191 x 8192 bf16, residual, both outputs, block codes 99 us (90 % of
 // measured HBM; the RMS norm 96); without residual and codes 46 (86 %).  64 x 128 3.2 us.
-// Backward of 8192 x 8192 with dres 98 us (81 %): its two sums a column leave room for
+// Backward of 8192 x 8192 with dres 96 us (82 %): its two sums a column leave room for
 // one CTA of 512 threads an SM, and what a row's meeting takes is not hidden by another's.
 // Not kept there: two rows at once (146, spills), more stages (118 of 116 then), dres read before
 // the meeting for the ring's single one (115, but 16384 x 2048 56 -> 60: registers).
-// 32767 x 128 fp32 backward 13.4 us (7 of them the dweight sum's own launch), two rows a
+// 32767 x 128 fp32 backward 13.5 us (4 to 5 of them the sums' own launch), two rows a
 // warp, whose half-warps add up two quantities at once; 24.5 with one row a warp and as many
 // CTAs as the RMS norm.
 #include "norm_forward.cuh"

@@ -373,19 +373,14 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, WARP ? 2 : 1)
         store_part<T, VEC, NV>(part, dw, G, g, a.cols);
 }
 
-// dweight[c] = sum of the nparts partial rows, ld apart: 32 columns a CTA, the
-// rows dealt to 32 warps, whose sums are added in order.  Grid row 1: dbias, from
-// the rows' second half.
-__global__ void __launch_bounds__(1024) dweight_kernel(const float *part, int nparts, int cols, int ld, float *dweight, float *dbias)
+// dweight[c] = sum of the nparts partial rows: 32 columns a CTA, the rows dealt
+// to 32 warps, whose sums are added in order.
+__global__ void __launch_bounds__(1024) dweight_kernel(const float *part, int nparts, int cols, float *dweight)
 {
     __shared__ float s[32][33];
     grid_dep_wait();
     grid_dep_launch();
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
-    if (blockIdx.y) {
-        part += cols;
-        dweight = dbias;
-    }
     constexpr int kAhead = 10; // rows of a warp whose loads are in flight: two CTAs an SM leave it ten
     float t = 0.f;
     if (c < cols)
@@ -393,7 +388,7 @@ __global__ void __launch_bounds__(1024) dweight_kernel(const float *part, int np
             float v[kAhead];
 #pragma unroll
             for (int k = 0; k < kAhead; ++k)
-                v[k] = p + 32 * k < nparts ? part[(int64_t)(p + 32 * k) * ld + c] : 0.f;
+                v[k] = p + 32 * k < nparts ? part[(int64_t)(p + 32 * k) * cols + c] : 0.f;
 #pragma unroll
             for (int k = 0; k < kAhead; ++k)
                 t += v[k];
@@ -406,6 +401,41 @@ __global__ void __launch_bounds__(1024) dweight_kernel(const float *part, int np
         t += __shfl_xor_sync(0xffffffffu, t, o);
     if (lane == 0 && blockIdx.x * 32 + w < cols)
         dweight[blockIdx.x * 32 + w] = t;
+}
+
+// Layer norm's: twice the columns, dweight's and dbias's.  WARPS: 32 for the shortest way through few columns, 16 where the
+// CTAs of 32 would take turns (a whole backward of 8192 x 8192 97.6 us with 32, 95.8 so; of 4096 x 4096 30.6 and 31.8).
+template <int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, 64 / WARPS) norm_sums_kernel(const float *part, int nparts, int cols, float *dweight, float *dbias)
+{
+    __shared__ float s[WARPS][32];
+    grid_dep_wait();
+    grid_dep_launch();
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+    constexpr int kAhead = 10; // rows of a warp whose loads are in flight
+    float t = 0.f;
+    if (c < 2 * cols)
+        for (int p = w; p < nparts; p += WARPS * kAhead) {
+            float v[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                v[k] = p + WARPS * k < nparts ? part[(int64_t)(p + WARPS * k) * 2 * cols + c] : 0.f;
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                t += v[k];
+        }
+    s[w][lane] = t;
+    __syncthreads();
+    if (w > 0 || c >= 2 * cols)
+        return;
+    t = s[0][lane];
+#pragma unroll
+    for (int k = 1; k < WARPS; ++k)
+        t += s[k][lane];
+    if (c < cols)
+        dweight[c] = t;
+    else if (dbias)
+        dbias[c - cols] = t;
 }
 
 // CTAs of a backward: a row of the workspace each.
@@ -484,9 +514,18 @@ int launch_norm_backward(const NormBackwardArgs &a, const char *name, cudaStream
                 return vec ? go(norm_backward_kernel<T, W, NV, WARP, true, LN, 32>) : go(norm_backward_kernel<T, W, NV, WARP, false, LN, 32>);
             return cudaErrorInvalidValue; // the others: the ring alone
         });
-    if (rc == cudaSuccess) // no rows: the sum of nothing, zeros
-        rc = launch_pdl(dweight_kernel, dim3((unsigned)((a.cols + 31) / 32), LN && a.dbias ? 2 : 1), dim3(1024), 0, stream, 1,
-                        (const float *)part, grid, a.cols, LN ? 2 * a.cols : a.cols, a.dweight, a.dbias);
+    if (rc == cudaSuccess) { // no rows: the sum of nothing, zeros
+        if constexpr (LN) {
+            const int ctas = ((a.dbias ? 2 : 1) * a.cols + 31) / 32;
+            auto go = [&](auto kernel, int warps) {
+                return launch_pdl(kernel, dim3((unsigned)ctas), dim3(32 * warps), 0, stream, 1, (const float *)part, grid, a.cols, a.dweight,
+                                  a.dbias);
+            };
+            rc = ctas <= 2 * num_sms() ? go(norm_sums_kernel<32>, 32) : go(norm_sums_kernel<16>, 16);
+        } else
+            rc = launch_pdl(dweight_kernel, dim3((unsigned)((a.cols + 31) / 32)), dim3(1024), 0, stream, 1, (const float *)part, grid, a.cols,
+                            a.dweight);
+    }
     if (rc != cudaSuccess) {
         snprintf(err, errlen, "%s launch: %s", name, cudaGetErrorString(rc));
         return DSA_ERR_CUDA;
