@@ -21,13 +21,14 @@
 //   Quotients are correctly rounded, three operations a pair (fp8.cuh); a tile with a
 //   scale so small that its reciprocal overflows divides.
 // Without the transpose and with a scale a piece, half-warps take pieces by themselves,
-// with no barrier and no tile to fill (64 x 4096 8.9 us by tiles, 1.9 so).
+// with no barrier and no tile to fill (64 x 4096 8.9 us by tiles, 1.6 so).
 //
 // Measured: 8191 x 8192 bf16 with its transpose 56 us (70 % of measured HBM; 84 with
 // every lane working out its rows' scales and shared words unpacked once a use), four
 // CTAs an SM (three 65, five 73: registers spill), 4096 x 7168 fp32 by blocks both ways 32 us
 // (80 %; three CTAs of 512 threads 71), 8192 x 8192 without the transpose bf16 51 us (58 %)
-// and fp32 57 (87 %): what bf16 waits for is not bytes but conversions and their stores.
+// and fp32 57 (87 %): bf16 issues 19 instructions a value, 66 % of an SM's slots; loads a
+// turn ahead (56) or a CTA for every 32 pieces (57) gave nothing.
 #include "rmsnorm.cuh"
 
 namespace dsa {
@@ -381,13 +382,10 @@ __global__ void __launch_bounds__(16 * kTile / rows_a_thread<T>(), sizeof(T) == 
     }
 }
 
-constexpr int kEach = 2;
-
-// Pieces of 128 values of a row, by half-warps: two on end each, then the next two that are its.
-template <typename T, bool VEC> __global__ void __launch_bounds__(256, 4) quantize_pieces_kernel(QuantizeBlocksArgs a)
+// Pieces of 128 values of a row, by half-warps: N on end each, then the next N that are its.
+template <typename T, bool VEC, int N> __global__ void __launch_bounds__(256, 4) quantize_pieces_kernel(QuantizeBlocksArgs a)
 {
     using C = Chunk<T>;
-    constexpr int N = kEach;
     grid_dep_wait();
     grid_dep_launch();
     const int cblocks = (int)((a.cols + kTile - 1) / kTile);
@@ -443,12 +441,20 @@ int launch_quantize_blocks(const QuantizeBlocksArgs &a, cudaStream_t stream, cha
 {
     const int64_t rblocks = (a.rows + kTile - 1) / kTile, cblocks = (a.cols + kTile - 1) / kTile;
     const bool vec = chunked(a.x, a.ldx * (a.x32 ? 4 : 2)), pieces = !a.codes_t && a.block_rows == 1;
-    const int64_t all = (a.rows * cblocks + 16 * kEach - 1) / (16 * kEach), most = (int64_t)num_sms() * 4;
     auto go = [&](auto t, auto v) {
         using T = std::remove_pointer_t<decltype(t)>;
         constexpr bool VEC = decltype(v)::value;
-        if (pieces)
-            return launch_pdl(quantize_pieces_kernel<T, VEC>, dim3((unsigned)(all < most ? all : most)), dim3(256), 0, stream, 1, a);
+        if (pieces) {
+            // a piece a half-warp where that is a CTA an SM at most, the shortest way; else two, which share what finding a
+            // scale takes (bf16, us, one and two: 64 x 4096 1.6, 2.0; 256 x 4096 2.6, 2.1; 8192 x 8192 79, 51; four 48, but
+            // 512 x 8192 6.0 for 5.3)
+            auto by = [&](auto n) {
+                constexpr int N = decltype(n)::value;
+                const int64_t all = (a.rows * cblocks + 16 * N - 1) / (16 * N), most = (int64_t)num_sms() * 4;
+                return launch_pdl(quantize_pieces_kernel<T, VEC, N>, dim3((unsigned)(all < most ? all : most)), dim3(256), 0, stream, 1, a);
+            };
+            return a.rows * cblocks <= 16 * num_sms() ? by(std::integral_constant<int, 1>()) : by(std::integral_constant<int, 2>());
+        }
         const dim3 tiles((unsigned)(rblocks * cblocks)), threads(16 * kTile / rows_a_thread<T>());
         return a.block_rows == 1 ? launch_pdl(quantize_blocks_kernel<T, VEC, false>, tiles, threads, 0, stream, 1, a)
                                  : launch_pdl(quantize_blocks_kernel<T, VEC, true>, tiles, threads, 0, stream, 1, a);
