@@ -20,15 +20,15 @@
 //   patterns is that of the magnitudes.
 //   Quotients are correctly rounded, three operations a pair (fp8.cuh); a tile with a
 //   scale so small that its reciprocal overflows divides.
-// Without the transpose and with a scale a piece, half-warps take pieces by themselves,
-// with no barrier and no tile to fill (64 x 4096 8.9 us by tiles, 1.6 so).
+// Few pieces without the transpose go to half-warps by themselves, with no barrier and no
+// tile to fill.
 //
 // Measured: 8191 x 8192 bf16 with its transpose 56 us (70 % of measured HBM; 84 with
 // every lane working out its rows' scales and shared words unpacked once a use), four
 // CTAs an SM (three 65, five 73: registers spill), 4096 x 7168 fp32 by blocks both ways 32 us
-// (80 %; three CTAs of 512 threads 71), 8192 x 8192 without the transpose bf16 51 us (58 %)
-// and fp32 57 (87 %): bf16 issues 19 instructions a value, 66 % of an SM's slots; loads a
-// turn ahead (56) or a CTA for every 32 pieces (57) gave nothing.
+// (80 %; three CTAs of 512 threads 71), 8192 x 8192 without the transpose bf16 39 us (77 %)
+// and fp32 55 (90 %), 64 x 4096 1.6: 17 instructions a value both ways in bf16, 60 % of an
+// SM's slots, are what bytes wait for there.
 #include "rmsnorm.cuh"
 
 namespace dsa {
@@ -389,13 +389,13 @@ template <typename T, bool VEC, int N> __global__ void __launch_bounds__(256, 4)
     grid_dep_wait();
     grid_dep_launch();
     const int cblocks = (int)((a.cols + kTile - 1) / kTile);
-    const int64_t pieces = a.rows * cblocks, step = (int64_t)gridDim.x * 16 * N;
+    const int pieces = (int)a.rows * cblocks, step = gridDim.x * 16 * N; // few (launch_quantize_blocks)
     const int c = threadIdx.x & 15, half = threadIdx.x >> 4 & 1;
     const bool aligned = ((reinterpret_cast<uintptr_t>(a.codes) | a.ldc) & 7) == 0;
     const uint8_t *lo = static_cast<const uint8_t *>(a.x), *hi = end_of<T>(a);
-    for (int64_t p0 = ((int64_t)blockIdx.x * 16 + (threadIdx.x >> 4)) * N; p0 - N * half < pieces; p0 += step) { // whole warps
-        int64_t row = pieces <= INT32_MAX ? (uint32_t)p0 / (uint32_t)cblocks : p0 / cblocks;
-        int at = (int)(p0 - row * cblocks);
+    for (int p0 = (blockIdx.x * 16 + (threadIdx.x >> 4)) * N; p0 - N * half < pieces; p0 += step) { // whole warps
+        int64_t row = p0 / cblocks;
+        int at = p0 - (int)row * cblocks;
         C v[N];
         int64_t rows[N];
         int ats[N], ncol[N]; // columns of this lane; -1: no such piece
@@ -440,14 +440,14 @@ template <typename T, bool VEC, int N> __global__ void __launch_bounds__(256, 4)
 int launch_quantize_blocks(const QuantizeBlocksArgs &a, cudaStream_t stream, char *err, size_t errlen)
 {
     const int64_t rblocks = (a.rows + kTile - 1) / kTile, cblocks = (a.cols + kTile - 1) / kTile;
-    const bool vec = chunked(a.x, a.ldx * (a.x32 ? 4 : 2)), pieces = !a.codes_t && a.block_rows == 1;
+    const bool vec = chunked(a.x, a.ldx * (a.x32 ? 4 : 2)), pieces = !a.codes_t && a.block_rows == 1 && rblocks * cblocks < 2 * num_sms();
     auto go = [&](auto t, auto v) {
         using T = std::remove_pointer_t<decltype(t)>;
         constexpr bool VEC = decltype(v)::value;
         if (pieces) {
             // a piece a half-warp where that is a CTA an SM at most, the shortest way; else two, which share what finding a
-            // scale takes (bf16, us, one and two: 64 x 4096 1.6, 2.0; 256 x 4096 2.6, 2.1; 8192 x 8192 79, 51; four 48, but
-            // 512 x 8192 6.0 for 5.3)
+            // scale takes, until tiles fill the GPU (bf16, us, one, two, tiles: 64 x 4096 1.6, 2.0, 2.7; 256 x 4096 2.6,
+            // 2.1, 3.1; 512 x 8192 6.9, 5.3, 5.3; 2048 x 8192 21, 15, 13; 8192 x 8192 79, 51, 39)
             auto by = [&](auto n) {
                 constexpr int N = decltype(n)::value;
                 const int64_t all = (a.rows * cblocks + 16 * N - 1) / (16 * N), most = (int64_t)num_sms() * 4;
