@@ -177,3 +177,21 @@ def test_product_of_a_tensor_with_itself(M, K):
     dsa.dsa_gemm_fp8(a, sa, a.as_strided(a.shape, a.stride()), sa.clone(), want)
     assert torch.equal(out, want)
     check_gemm(out, a, sa, a, sa, "a a^T")
+
+
+@pytest.mark.parametrize("rows, cols", [(19, 16385), (130, 2431), (300, 4099), (2433, 2003), (2500, 2000), (40001, 100)])
+@pytest.mark.parametrize("t", [BF, F32])
+def test_codes_alone_are_those_beside_the_transpose(rows, cols, t):
+    """... whichever of the ways a number of pieces goes."""
+    dsa, g = lib(), gen(8)
+    x = (torch.randn((rows, cols), generator=g, device=DEV) * torch.exp(torch.randn((rows, 1), generator=g, device=DEV))).to(t)
+    got = []
+    for turned in (True, False):
+        codes, scale = P.padded(rows, cols, DEV), torch.full((rows, P.pieces(cols)), -1.0, device=DEV)
+        codes_t, scale_t = (P.padded(cols, rows, DEV), torch.empty((cols, P.pieces(rows)), device=DEV)) if turned else (None, None)
+        dsa.dsa_quantize_fp8_blocks(x, codes, scale, codes_t, scale_t)
+        got.append((codes, scale))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    s = got[0][1].double().repeat_interleave(128, 1)[:, :cols]
+    ref = x.double() / s
+    assert ((P.values(got[0][0]) - ref).abs() <= ref.abs() * (R.E4M3 * (1 + 1e-5)) + 2.0 ** -10).all()
