@@ -81,25 +81,42 @@ __device__ __forceinline__ void tile_at(const Params &p, int tile, int &m, int &
     m = first + r - n * rows;
 }
 
-// Sums of a warp's 32 rows to out, from row m (of lane 0) and column n on: 32 columns as bf16 or 16 as fp32, by way of
+// Sums of a warp's 32 rows to out, from row m (of the first) and column n on: 32 columns as bf16 or 16 as fp32, by way of
 // shared memory, where a row's four 16-byte words stand at place ^ (row / 2) so that neither side meets bank conflicts.
 // Eight rows then leave at a time; straight from the registers, where a lane holds a row, a tile took 5000 cycles.
-template <bool O32>
+// QUADS: lanes hold pairs of columns of four rows (tmem_ld_quads), else a row each.
+template <bool O32, bool QUADS>
 __device__ __forceinline__ void store_sums(const Params &p, int64_t m, int n, const F2 *acc, uint8_t *patch)
 {
     const int lane = threadIdx.x & 31;
     constexpr int e = O32 ? 4 : 2, cols = 64 / e;
     __syncwarp();
+    if constexpr (QUADS) {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        uint32_t w[4];
+        for (int j = 0; j < cols / 8; ++j)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            float lo, hi;
-            acc[O32 ? 2 * c + (k >> 1) : 4 * c + k].get(lo, hi);
-            w[k] = !O32 ? pack2(lo, hi) : __float_as_uint(k & 1 ? hi : lo);
+            for (int k = 0; k < 4; ++k) {
+                const int r = 8 * k + (lane >> 2), byte = (8 * j + 2 * (lane & 3)) * e;
+                uint8_t *to = patch + r * 64 + ((byte >> 4 ^ (r >> 1 & 3)) << 4) + (byte & 15);
+                float lo, hi;
+                acc[4 * j + k].get(lo, hi);
+                if (O32)
+                    *reinterpret_cast<float2 *>(to) = make_float2(lo, hi);
+                else
+                    *reinterpret_cast<uint32_t *>(to) = pack2(lo, hi);
+            }
+    } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float lo, hi;
+                acc[O32 ? 2 * c + (k >> 1) : 4 * c + k].get(lo, hi);
+                w[k] = !O32 ? pack2(lo, hi) : __float_as_uint(k & 1 ? hi : lo);
+            }
+            *reinterpret_cast<uint4 *>(patch + lane * 64 + ((c ^ (lane >> 1 & 3)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        *reinterpret_cast<uint4 *>(patch + lane * 64 + ((c ^ (lane >> 1 & 3)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
     }
     __syncwarp();
     uint8_t *out = static_cast<uint8_t *>(p.out) + (m * p.ldo + n) * e;
@@ -123,6 +140,20 @@ __device__ __forceinline__ void store_sums(const Params &p, int64_t m, int n, co
             else
                 *reinterpret_cast<uint16_t *>(out + (r * p.ldo + c) * e) = *reinterpret_cast<const uint16_t *>(at);
         }
+}
+
+// 64 columns of 16 rows from TMEM, as quads of lanes hold them: lane l gets columns 8 j + 2 (l % 4) and the next of rows l / 4
+// (v[4 j], v[4 j + 1]) and l / 4 + 8 (v[4 j + 2], v[4 j + 3]).
+__device__ __forceinline__ void tmem_ld_quads(uint32_t at, uint32_t (&v)[32])
+{
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+                   "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
+                   "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+                   "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+                 : "r"(at));
 }
 
 template <int BN, bool ROWS>
@@ -292,45 +323,61 @@ __global__ void __launch_bounds__(Cfg<BN, ROWS>::kThreads, 1)
                     break;
                 }
                 const float *slot = sc + i % (2 * C::kBatch) * C::kScaled;
-                const F2 mine(slot[32 * quad + lane] * (ROWS ? 1.f : slot[block]));
                 if (!wait_warp(bar(B_TF + t), (i / C::kBuffers) & 1, abort_flag, p.status)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const float4 *cs = reinterpret_cast<const float4 *>(slot + kRows + W * part);
-                auto add = [&](const uint32_t(&v)[32], int c) {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        F2 s0 = mine, s1 = mine;
-                        if (ROWS) {
-                            const float4 s = cs[(c + e) / 4];
-                            s0 = mine * F2(s.x, s.y);
-                            s1 = mine * F2(s.z, s.w);
-                        }
-                        acc[(c + e) / 2] = fma2(F2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), s0, acc[(c + e) / 2]);
-                        acc[(c + e) / 2 + 1] = fma2(F2(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])), s1, acc[(c + e) / 2 + 1]);
-                    }
+                auto read = [&] { // the buffer may take another product
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(bar(B_TE + t));
                 };
                 uint32_t v0[32], v1[32];
-                tmem_ld32(from + t * BN, v0);
-                tmem_ld32(from + t * BN + 32, v1);
-                tmem_ld_wait_for(v0);
-                tmem_ld_wait_for(v1);
-                if constexpr (W == 128) {
-                    add(v0, 0);
-                    tmem_ld32(from + t * BN + 64, v0);
-                    add(v1, 32);
-                    tmem_ld32(from + t * BN + 96, v1);
+                if constexpr (ROWS) {
+                    tmem_ld_quads(from + t * BN, v0);
+                    tmem_ld_quads(from + (16u << 16) + t * BN, v1);
+                    F2 mine[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mine[k] = F2(slot[32 * quad + 8 * k + (lane >> 2)]);
+                    const float2 *cs = reinterpret_cast<const float2 *>(slot + kRows + W * part + 2 * (lane & 3));
                     tmem_ld_wait_for(v0);
                     tmem_ld_wait_for(v1);
+                    read();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float2 s = cs[4 * j];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t *v = (k < 2 ? v0 : v1) + 4 * j + 2 * (k & 1);
+                            acc[4 * j + k] = fma2(F2(__uint_as_float(v[0]), __uint_as_float(v[1])), mine[k] * F2(s.x, s.y), acc[4 * j + k]);
+                        }
+                    }
+                } else {
+                    const F2 mine(slot[32 * quad + lane] * slot[block]);
+                    auto add = [&](const uint32_t(&v)[32], int c) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2)
+                            acc[(c + e) / 2] = fma2(F2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), mine, acc[(c + e) / 2]);
+                    };
+                    tmem_ld32(from + t * BN, v0);
+                    tmem_ld32(from + t * BN + 32, v1);
+                    tmem_ld_wait_for(v0);
+                    tmem_ld_wait_for(v1);
+                    if constexpr (W == 128) {
+                        add(v0, 0);
+                        tmem_ld32(from + t * BN + 64, v0);
+                        add(v1, 32);
+                        tmem_ld32(from + t * BN + 96, v1);
+                        tmem_ld_wait_for(v0);
+                        tmem_ld_wait_for(v1);
+                    }
+                    read();
+                    add(v0, W - 64);
+                    add(v1, W - 32);
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(bar(B_TE + t));
-                add(v0, W - 64);
-                add(v1, W - 32);
                 if (i % C::kBatch == C::kBatch - 1) {
                     __syncwarp();
                     if (lane == 0)
@@ -344,7 +391,8 @@ __global__ void __launch_bounds__(Cfg<BN, ROWS>::kThreads, 1)
                     acc[c].get(v[0], v[1]);
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
-                        reinterpret_cast<float *>(smem)[(W * part + 2 * c + e) * kRows + 32 * quad + lane] = v[e];
+                        reinterpret_cast<float *>(smem)[ROWS ? (W * part + 8 * (c / 4) + 2 * (lane & 3) + e) * kRows + 32 * quad + 8 * (c & 3) + (lane >> 2)
+                                                             : (W * part + 2 * c + e) * kRows + 32 * quad + lane] = v[e];
                 }
             } else if (ok) {
                 int tm, tn;
@@ -355,12 +403,12 @@ __global__ void __launch_bounds__(Cfg<BN, ROWS>::kThreads, 1)
 #pragma unroll
                     for (int c = 0; c < W; c += 16)
                         if (col + c < p.N)
-                            store_sums<true>(p, row, col + c, acc + c / 2, patch);
+                            store_sums<true, ROWS>(p, row, col + c, acc + c / 2, patch);
                 } else {
 #pragma unroll
                     for (int c = 0; c < W; c += 32)
                         if (col + c < p.N)
-                            store_sums<false>(p, row, col + c, acc + c / 2, patch);
+                            store_sums<false, ROWS>(p, row, col + c, acc + c / 2, patch);
                 }
             }
         }
