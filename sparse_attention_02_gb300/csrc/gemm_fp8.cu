@@ -25,7 +25,7 @@ int launch_gemm_fp8(const GemmFp8Args &a, cudaStream_t stream, char *err, size_t
         int cols;
         float piece, rows_piece, out, join; // rows_piece: with a scale for every row of b; join: of a split
     };
-    constexpr Width widths[] = {{128, 0.32f, 0.44f, 1.0f, 4.0f}, {192, 0.38f, 0.60f, 1.6f, 4.6f}, {256, 0.455f, 0.f, 2.4f, 0.f}};
+    constexpr Width widths[] = {{128, 0.32f, 0.44f, 1.0f, 4.0f}, {192, 0.38f, 0.505f, 1.6f, 4.6f}, {256, 0.455f, 0.f, 2.4f, 0.f}};
     int best_cols = 0, best_split = 1;
     float best = 0.f;
     for (const Width &w : widths) {

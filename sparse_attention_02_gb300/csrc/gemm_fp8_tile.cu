@@ -12,15 +12,19 @@
 // of the loop takes is the way round: MMAs (512 and 150 until the sums are seen), 128 columns read in two
 // halves, as 64 are what a thread's registers hold beside its sums, and 200 until the next MMAs go
 // out; two buffers share that, 840 cycles a piece.  BN = 192 has registers for all of a
-// piece at once, but more pieces, and takes the product with a scale for every row, which the FP32
-// pipe would bound at 256 (4096 x 4096 x 8191 217 us by 128 x 256, 199 by 128 x 192).
+// piece at once, but more pieces, and takes the product with a scale for every row of b.  Those scales
+// are read by quads of lanes, each of which holds pairs of columns of four rows: 20 words a thread and piece
+// instead of 64 (lanes of one row each, 4096 x 4096 over 8191: 198 us, 178 so; without the product of the two
+// scales 144; with scales by blocks 129).
 //
-// Measured: 8191 x 8192 x 8192 bf16 417 us, 2.64 PFLOP/s (140 % of measured BF16).  Without the additions the
-// same loop takes 375, without the loads 390.  Not kept: pairs of CTAs on one tile
-// (cta_group::2, 256 x 256: 468 us, words between CTAs in the way round; in halves of 128
+// Measured: 8191 x 8192 x 8192 bf16 406 to 417 us in bursts, 2.7 PFLOP/s (143 % of
+// measured BF16), 461 to 470 call after call, where power limits the clock.  Without the
+// additions the same loop takes 375, without the loads 390.  Not kept: pairs of CTAs on one
+// tile (cta_group::2, 256 x 256: 468, words between CTAs in the way round; in halves of 128
 // columns with four buffers 655: more meetings), 16 warps of 64 columns (500, registers
-// spill), the first columns of the next piece asked for among the additions (486: the reading waits),
-// scales fetched by each warp for itself (610, spills).
+// spill), the first columns of the next piece asked for among the additions (486: the
+// reading waits), scales fetched by each warp for itself (610, spills), 16 loads of a scale
+// warp's lanes in flight for 8 (597, spills).
 //
 // Roles per CTA (12 or 16 warps): 0 loads, 1 MMAs, 2 and 3 scales, the others scaling, sums and output.
 // Persistent where a tile is a CTA's own: CTA c takes tiles c, c + CTAs, ..., ordered so that those
