@@ -18,7 +18,7 @@ int launch_gemm_fp8(const GemmFp8Args &a, cudaStream_t stream, char *err, size_t
         return launch_gemm_fp8_split(a, cols, split, stream, err, errlen);
     }
     // By tiles: the widths of a tile and the splits of K by the time that they take, in us, from what a piece, a tile's
-    // output and a cluster's sum were measured at (128 x 704 x 4096 bf16: 13.1 by tiles of 128, 14.9 of 192, 8.6 with K split
+    // output and a cluster's sum were measured at (128 x 704 x 4096 bf16: 13.1 by tiles of 128, 14.9 of 192, 7.9 with K split
     // in 8; 4096 x 704 x 4096 25.0, 16.7 and, of 256, 19.5; 2048 x 2048 x 2048 15.1, 17.6, 12.3; 8191 x 8192 x 8192 534,
     // 458, 422).  Clusters of eight find room on two thirds of the SMs.  What is worth a split is too small for tiles of 256.
     struct Width {

@@ -15,25 +15,6 @@ constexpr int kGemmPiece = 128; // values along K that share a scale; one row of
 int launch_gemm_fp8_split(const GemmFp8Args &a, int cols, int split, cudaStream_t stream, char *err, size_t errlen);
 int launch_gemm_fp8_tile(const GemmFp8Args &a, int cols, int split, cudaStream_t stream, char *err, size_t errlen);
 
-// The sums of what the `split` (at most 8) CTAs of a cluster have in four words of their shared memory, in the CTAs' order,
-// with all loads in flight at once (one word after the other, a tile's sums took 15 us).
-__device__ __forceinline__ float4 sums_of_cluster(uint32_t addr, uint32_t split)
-{
-    float4 v[8];
-#pragma unroll
-    for (uint32_t k = 0; k < 8; ++k)
-        if (k < split)
-            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                         : "=f"(v[k].x), "=f"(v[k].y), "=f"(v[k].z), "=f"(v[k].w)
-                         : "r"(mapa_shared(addr, k))
-                         : "memory");
-#pragma unroll
-    for (uint32_t k = 1; k < 8; ++k)
-        if (k < split)
-            v[0] = make_float4(v[0].x + v[k].x, v[0].y + v[k].y, v[0].z + v[k].z, v[0].w + v[k].w);
-    return v[0];
-}
-
 // mbar_wait_warp with every branch decided by the whole warp: a wait for what is over costs it one poll and one vote.
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int *abort_flag, unsigned *status)
 {

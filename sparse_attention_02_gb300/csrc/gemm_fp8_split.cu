@@ -64,6 +64,25 @@ __device__ __forceinline__ void put(const Params &p, int64_t m, int64_t n, float
         static_cast<__nv_bfloat16 *>(p.out)[m * p.ldo + n] = __float2bfloat16_rn(v);
 }
 
+// The sums of what the `split` (at most 8) CTAs of a cluster have in four words of their shared memory, in the CTAs' order,
+// with all loads in flight at once (one word after the other, a tile's sums took 15 us).
+__device__ __forceinline__ float4 sums_of_cluster(uint32_t addr, uint32_t split)
+{
+    float4 v[8];
+#pragma unroll
+    for (uint32_t k = 0; k < 8; ++k)
+        if (k < split)
+            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(v[k].x), "=f"(v[k].y), "=f"(v[k].z), "=f"(v[k].w)
+                         : "r"(mapa_shared(addr, k))
+                         : "memory");
+#pragma unroll
+    for (uint32_t k = 1; k < 8; ++k)
+        if (k < split)
+            v[0] = make_float4(v[0].x + v[k].x, v[0].y + v[k].y, v[0].z + v[k].z, v[0].w + v[k].w);
+    return v[0];
+}
+
 template <int BT>
 __global__ void __launch_bounds__(kThreads, 2)
     gemm_fp8_split_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, Params p)

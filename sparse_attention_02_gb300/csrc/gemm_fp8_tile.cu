@@ -63,7 +63,7 @@ template <int BN, bool ROWS> struct Cfg {
     static constexpr int kNumBars = 2 * kStages + 2 * kBuffers + 5;
     static constexpr int kMisc = kBars + 8 * kNumBars;
     static constexpr int kSmem = kMisc + 16;
-    static_assert((BN + BN / 2 + 1) * kRows * 4 <= kBars, "a split's sums, and what the CTA adds up, take the stages' place");
+    static_assert(BN == 256 || (BN + BN / 2 + 1) * kRows * 4 <= kBars, "a split's sums, and what the CTA adds up, take the stages' place");
     static_assert(kSmem <= 232448, "dynamic shared memory above the 227 KB a CTA may hold");
 };
 
@@ -158,6 +158,66 @@ __device__ __forceinline__ void tmem_ld_quads(uint32_t at, uint32_t (&v)[32])
                    "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
                    "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
                  : "r"(at));
+}
+
+// What the SPLIT CTAs of a cluster have in four words of their shared memory, with all loads in flight at once, and
+// its sum in the CTAs' order.
+template <int SPLIT> __device__ __forceinline__ void words_of_cluster(uint32_t addr, float4 (&v)[SPLIT])
+{
+#pragma unroll
+    for (uint32_t k = 0; k < SPLIT; ++k)
+        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(v[k].x), "=f"(v[k].y), "=f"(v[k].z), "=f"(v[k].w)
+                     : "r"(mapa_shared(addr, k))
+                     : "memory");
+}
+
+template <int SPLIT> __device__ __forceinline__ float4 sum_of(const float4 (&v)[SPLIT])
+{
+    float4 t = v[0];
+#pragma unroll
+    for (int k = 1; k < SPLIT; ++k)
+        t = make_float4(t.x + v[k].x, t.y + v[k].y, t.z + v[k].z, t.w + v[k].w);
+    return t;
+}
+
+// The CTAs of a cluster add up the columns of their tile between them, each sum in the CTAs' order: lanes along rows, as the
+// sums lie, turned in this CTA's own shared memory into lanes along columns, as they leave.  The warps of sums do it: the
+// others have given their registers away.
+template <int BN, int SPLIT, int THREADS>
+__device__ __forceinline__ void join(const Params &p, uint8_t *smem, int tm, int tn, uint32_t rank)
+{
+    constexpr int cols = BN / SPLIT, pitch = cols + 1, words = cols * kRows, A = 8 / SPLIT; // A: words of a thread in flight
+    const uint32_t mine = smem_u32(smem) + 4 * words * rank;
+    const int thread = threadIdx.x - 32 * kSumWarp0;
+    float *turned = reinterpret_cast<float *>(smem) + BN * kRows;
+    for (int x0 = 4 * thread; x0 < words; x0 += 4 * THREADS * A) {
+        float4 v[A][SPLIT];
+#pragma unroll
+        for (int i = 0; i < A; ++i)
+            if (x0 + 4 * THREADS * i < words)
+                words_of_cluster(mine + 4 * (x0 + 4 * THREADS * i), v[i]);
+#pragma unroll
+        for (int i = 0; i < A; ++i) {
+            const int x = x0 + 4 * THREADS * i;
+            if (x < words) {
+                const float4 t = sum_of(v[i]);
+                float *to = turned + x % kRows * pitch + x / kRows;
+                to[0] = t.x, to[pitch] = t.y, to[2 * pitch] = t.z, to[3 * pitch] = t.w;
+            }
+        }
+    }
+    named_bar_sync(1, THREADS);
+    for (int x = thread; x < words; x += THREADS) {
+        const int64_t m = (int64_t)tm * kRows + x / cols, n = (int64_t)tn * BN + cols * (int)rank + x % cols;
+        const float v = turned[x / cols * pitch + x % cols];
+        if (m < p.M && n < p.N) {
+            if (p.o32)
+                static_cast<float *>(p.out)[m * p.ldo + n] = v;
+            else
+                static_cast<__nv_bfloat16 *>(p.out)[m * p.ldo + n] = __float2bfloat16_rn(v);
+        }
+    }
 }
 
 template <int BN, bool ROWS>
@@ -388,7 +448,7 @@ __global__ void __launch_bounds__(Cfg<BN, ROWS>::kThreads, 1)
                         mbar_arrive(bar(B_SE + (n & 1)));
                 }
             }
-            if (split > 1) { // this CTA's sums, over the stages: the last product is done
+            if (BN != 256 && split > 1) { // this CTA's sums, over the stages: the last product is done
 #pragma unroll
                 for (int c = 0; c < W / 2; ++c) {
                     float v[2];
@@ -430,30 +490,18 @@ __global__ void __launch_bounds__(Cfg<BN, ROWS>::kThreads, 1)
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
-    if (split == 1)
+    if (BN == 256 || split == 1) // 256: never split (launch_gemm_fp8)
         return;
-    // The cluster's CTAs add up the columns of the tile between them, each sum in the CTAs' order: lanes along rows, as the
-    // sums lie, turned in this CTA's own shared memory into lanes along columns, as they leave.
     cluster_sync_all();
     int tm, tn;
     tile_at(p, first, tm, tn);
-    const int cols = BN / split, c0 = cols * rank, pitch = cols + 1;
-    float *turned = reinterpret_cast<float *>(smem) + BN * kRows;
-    for (int x = 4 * threadIdx.x; x < cols * kRows; x += 4 * C::kThreads) {
-        const float4 v = sums_of_cluster(sbase + 4 * (c0 * kRows + x), split);
-        float *to = turned + x % kRows * pitch + x / kRows;
-        to[0] = v.x, to[pitch] = v.y, to[2 * pitch] = v.z, to[3 * pitch] = v.w;
-    }
-    __syncthreads();
-    for (int x = threadIdx.x; x < cols * kRows; x += C::kThreads) {
-        const int64_t m = (int64_t)tm * kRows + x / cols, n = (int64_t)tn * BN + c0 + x % cols;
-        const float v = turned[x / cols * pitch + x % cols];
-        if (m < p.M && n < p.N) {
-            if (p.o32)
-                static_cast<float *>(p.out)[m * p.ldo + n] = v;
-            else
-                static_cast<__nv_bfloat16 *>(p.out)[m * p.ldo + n] = __float2bfloat16_rn(v);
-        }
+    if (warp >= kSumWarp0) {
+        if (split == 2)
+            join<BN, 2, 32 * C::kSumWarps>(p, smem, tm, tn, rank);
+        else if (split == 4)
+            join<BN, 4, 32 * C::kSumWarps>(p, smem, tm, tn, rank);
+        else
+            join<BN, 8, 32 * C::kSumWarps>(p, smem, tm, tn, rank);
     }
     cluster_sync_all(); // no CTA leaves while its peers read its sums
 }
