@@ -451,12 +451,12 @@ __global__ void __launch_bounds__(Cfg<BN, ROWS>::kThreads, 1)
             if (BN != 256 && split > 1) { // this CTA's sums, over the stages: the last product is done
 #pragma unroll
                 for (int c = 0; c < W / 2; ++c) {
+                    const int col = ROWS ? 8 * (c / 4) + 2 * (lane & 3) : 2 * c, row = ROWS ? 8 * (c & 3) + (lane >> 2) : lane;
                     float v[2];
                     acc[c].get(v[0], v[1]);
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
-                        reinterpret_cast<float *>(smem)[ROWS ? (W * part + 8 * (c / 4) + 2 * (lane & 3) + e) * kRows + 32 * quad + 8 * (c & 3) + (lane >> 2)
-                                                             : (W * part + 2 * c + e) * kRows + 32 * quad + lane] = v[e];
+                        reinterpret_cast<float *>(smem)[(W * part + col + e) * kRows + 32 * quad + row] = v[e];
                 }
             } else if (ok) {
                 int tm, tn;

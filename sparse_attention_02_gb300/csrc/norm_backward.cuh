@@ -94,7 +94,8 @@ template <int N> __device__ __forceinline__ void unpack(const F2 (&v)[N][4], flo
 // instructions and the meeting's latency add up.
 template <typename T, typename W, int NV, bool WARP, bool VEC, int LANES>
 __device__ __forceinline__ void layernorm_backward_row(const NormBackwardArgs &a, const T *hp, const T *dp, const T *ep, int64_t row,
-                                                       bool there, const Held<T, W, NV, VEC> &held, const Counts &n, F2 (&dw)[2 * NV][4], float *red)
+                                                       bool there, const Held<T, W, NV, VEC> &held, const Counts &n,
+                                                       F2 (&dw)[2 * NV][4], float *red)
 {
     const int G = WARP ? LANES : blockDim.x;
     const int g = WARP ? (threadIdx.x & (LANES - 1)) : threadIdx.x;

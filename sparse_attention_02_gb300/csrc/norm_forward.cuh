@@ -21,7 +21,8 @@ struct Meet {
 // there: whether this warp has a row.  moments: of this row, 64 floats.
 template <typename T, typename W, int NV, bool WARP, bool VEC, bool LN, bool RING = false, typename M = Meet>
 __device__ __forceinline__ void norm_row(const NormArgs &a, const T *x, const T *res, int64_t row, float *red,
-                                         [[maybe_unused]] float *moments = nullptr, [[maybe_unused]] const Counts &n = Counts(), [[maybe_unused]] const Held<T, W, NV, VEC> *held = nullptr,
+                                         [[maybe_unused]] float *moments = nullptr, [[maybe_unused]] const Counts &n = Counts(),
+                                         [[maybe_unused]] const Held<T, W, NV, VEC> *held = nullptr,
                                          [[maybe_unused]] bool there = true, M meet = M())
 {
     const int G = WARP ? 32 : blockDim.x;

@@ -53,7 +53,8 @@ def test_codes_of_rows_far_apart(t, block_rows):
         return codes, s, codes_t, st
 
     want = run(x, torch.zeros((rows, cols), dtype=U8, device=DEV), torch.zeros((cols, rows), dtype=U8, device=DEV))
-    got = run(far(rows, cols, (1 << 32) // 40, t, x), far(rows, cols, (1 << 32) // 40 // 16 * 16, U8), far(cols, rows, (1 << 32) // 240 // 16 * 16, U8))
+    ld, ld_t = (1 << 32) // 40 // 16 * 16, (1 << 32) // 240 // 16 * 16
+    got = run(far(rows, cols, (1 << 32) // 40, t, x), far(rows, cols, ld, U8), far(cols, rows, ld_t, U8))
     assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 

@@ -69,7 +69,8 @@ def test_serving_projections(T):
     R.check_close(kI, ref, ref.abs() * R.BF16 + 40 * R.FP32 * mag + 1e-30, "index keys")
     pages = -(-T // PAGE)
     table = torch.arange(pages, dtype=I32, device=DEV).view(1, pages)
-    kv, k8, ks = torch.zeros((pages, PAGE, 576), dtype=BF, device=DEV), torch.zeros((pages, PAGE, 128), dtype=U8, device=DEV), torch.zeros((pages, PAGE), device=DEV)
+    kv = torch.zeros((pages, PAGE, 576), dtype=BF, device=DEV)
+    k8, ks = torch.zeros((pages, PAGE, 128), dtype=U8, device=DEV), torch.zeros((pages, PAGE), device=DEV)
     pos = torch.arange(T, dtype=I32, device=DEV)
     dsa.dsa_cache_append(pos, table, R.inv_freq().to(DEV), kv=out[:, :576], kv_pool=kv, kI=kI, k8_pool=k8, ks_pool=ks,
                          seq=torch.zeros(T, dtype=I32, device=DEV))
@@ -138,7 +139,8 @@ def test_padded_batch_in_one_graph():
     proj = Projection(dsa, N, D, g)
     w, kw, kb = (torch.randn(k, generator=g, device=DEV).to(BF) for k in (D, 128, 128))
     x = torch.zeros((T, D), dtype=BF, device=DEV)
-    codes, scale, out, kI = torch.empty((T, D), dtype=U8, device=DEV), torch.empty((T, D // 128), device=DEV), torch.empty((T, N), dtype=BF, device=DEV), torch.empty((T, 128), dtype=BF, device=DEV)
+    codes, scale = torch.empty((T, D), dtype=U8, device=DEV), torch.empty((T, D // 128), device=DEV)
+    out, kI = torch.empty((T, N), dtype=BF, device=DEV), torch.empty((T, 128), dtype=BF, device=DEV)
 
     def step(x, codes, scale, out, kI):
         dsa.dsa_rmsnorm(x, w, EPS, codes=codes, scale=scale, block=128)
