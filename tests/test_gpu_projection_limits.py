@@ -169,6 +169,17 @@ def test_norm_in_place_of_its_inputs(cols, t):
     assert all(torch.equal(a, b) for a, b in zip(twice, run(x, x.clone(), torch.empty_like(x), torch.empty_like(x))))
 
 
+@pytest.mark.parametrize("M, N, K", [(3, 5, (1 << 20) + 5), (70, 40, (1 << 20) + 5), (1, (1 << 20) + 3, 130), (60, 100001, 20), ((1 << 20) + 3, 1, 130)])
+@pytest.mark.parametrize("block", [128, 1])
+def test_product_of_long_sides(M, N, K, block):
+    dsa, g = lib(), gen(9)
+    ops = operands(M, N, K, block, g)
+    out = torch.full((M, N), float("nan"), device=DEV)
+    dsa.dsa_gemm_fp8(*ops, out)
+    check_gemm(out, *ops, "long")
+    assert dsa.dsa_get_device_status() == 0
+
+
 @pytest.mark.parametrize("M, K", [(5, 300), (50, 1000), (300, 700), (2050, 1100)])
 def test_product_of_a_tensor_with_itself(M, K):
     dsa, g = lib(), gen(7)
@@ -180,7 +191,7 @@ def test_product_of_a_tensor_with_itself(M, K):
     check_gemm(out, a, sa, a, sa, "a a^T")
 
 
-@pytest.mark.parametrize("rows, cols", [(19, 16385), (130, 2431), (300, 4099), (2433, 2003), (2500, 2000), (40001, 100)])
+@pytest.mark.parametrize("rows, cols", [(19, 16385), (130, 2431), (300, 4099), (2433, 2003), (2500, 2000), (40001, 100), (1, 3000001)])
 @pytest.mark.parametrize("t", [BF, F32])
 def test_codes_alone_are_those_beside_the_transpose(rows, cols, t):
     """... whichever of the ways a number of pieces goes."""
