@@ -105,3 +105,14 @@ print("captured first")
 def test_first_calls_of_a_process_captured():
     r = subprocess.run([sys.executable, "-c", FIRST], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "captured first" in r.stdout, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("M", [1, 20, 50])
+@pytest.mark.parametrize("tiles", [16, 34, 35, 38, 68, 69, 76, 77, 152, 153])
+def test_few_rows_by_every_number_of_tiles(M, tiles):
+    """... with K split in 8, 4, 2 and not at all."""
+    dsa, g = lib(), gen(tiles)
+    ops = operands(M, 128 * tiles - 5, 2100, 128, g)
+    out = torch.full((M, 128 * tiles - 5), float("nan"), device=DEV)
+    dsa.dsa_gemm_fp8(*ops, out)
+    check(out, *ops, f"{M} rows, {tiles} tiles")
