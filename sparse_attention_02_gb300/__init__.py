@@ -23,6 +23,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libdsa.so")
 
 DSA_OK = 0
+DSA_ERR_UNSUPPORTED = 2
 DSA_DEV_TIMEOUT = 0x1
 DSA_DEV_BAD_POSITION = 0x2
 DSA_DEV_BAD_PAGE = 0x4
@@ -52,14 +53,34 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     return _lib
 
 
+class _Int:
+    """An int argument of the library.  ctypes' own c_int cuts larger numbers to their low 32 bits, which the library then
+    takes for other sizes."""
+
+    @staticmethod
+    def from_param(v):
+        if type(v) is int:
+            if -0x80000000 <= v <= 0x7FFFFFFF:
+                return v
+            raise OverflowError(f"{v} is more than the library's int holds")
+        return ctypes.c_int.from_param(v)
+
+
+def _sizes(*sizes):
+    """Refuses what the library counts in an int and would refuse itself, could it be told."""
+    for n in sizes:
+        if n > 0x7FFFFFFF:
+            raise DsaError(DSA_ERR_UNSUPPORTED, f"a size of {n} is more than the library takes")
+
+
 def _open(p: str) -> ctypes.CDLL:
     if not os.path.exists(p):
         raise RuntimeError(f"{p} is missing: build it with `python -m sparse_attention_02_gb300.build` "
                            "(or __graft_entry__.build()); there is no fallback path")
     lib = ctypes.CDLL(p)
-    P, i32, i64, f32, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
+    P, i32, i64, f32, sz = ctypes.c_void_p, _Int, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
     lib.dsa_last_error.restype = ctypes.c_char_p
-    lib.dsa_version.restype = i32
+    lib.dsa_version.restype = ctypes.c_int
     lib.dsa_get_device_status.argtypes = [P, ctypes.POINTER(ctypes.c_uint32)]
     lib.dsa_quantize_fp8.argtypes = [P, i64, i64, i32, P, P, P]
     lib.dsa_indexer_logits.argtypes = [P, P, P, i32, i32, i32, P, P, i32, P, i32, i32, i32, P, P, i64, P]
@@ -71,9 +92,9 @@ def _open(p: str) -> ctypes.CDLL:
     lib.dsa_prefill_host_workspace_size.restype = sz
     lib.dsa_prefill_host_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32, i32]
     lib.dsa_prefill_host_trace.argtypes = [i32]
-    lib.dsa_prefill_host_trace_read.argtypes = [P, P, P, i32, ctypes.POINTER(i32)]
+    lib.dsa_prefill_host_trace_read.argtypes = [P, P, P, i32, ctypes.POINTER(ctypes.c_int)]
     lib.dsa_selftest_wait_timeout.argtypes = [ctypes.c_uint32, P]
-    lib.dsa_selftest_wait_timeout.restype = i32
+    lib.dsa_selftest_wait_timeout.restype = ctypes.c_int
     lib.dsa_sparse_mla_decode_workspace_size.restype = sz
     lib.dsa_sparse_mla_decode_workspace_size.argtypes = [i32, i32, i32]
     lib.dsa_indexer_topk.argtypes = [P, P, P, i32, i32, i32, P, P, i32, P, i32, P, P, sz, P]
@@ -104,7 +125,7 @@ def _open(p: str) -> ctypes.CDLL:
                  "dsa_sparse_mla_decode_paged",
                  "dsa_sparse_mla_decode_paged_noalloc", "dsa_prefill_host", "dsa_prefill_host_trace",
                  "dsa_prefill_host_trace_read", "dsa_get_device_status"):
-        getattr(lib, name).restype = i32
+        getattr(lib, name).restype = ctypes.c_int
     return lib
 
 
@@ -354,6 +375,7 @@ def dsa_rmsnorm(x, weight, eps: float, out=None, residual=None, residual_out=Non
         raise TypeError("x must be 2-D")
     cur, shape, f32 = _device(), x.shape, torch.float32
     rows, cols = shape
+    _sizes(cols)
     wt = _dtype_of(weight, "weight")
     a_x, ldx = _at_rows(x, cur, "x", t, shape)
     a_r = a_h = a_o = a_c = a_s = None
@@ -376,6 +398,7 @@ def dsa_rmsnorm(x, weight, eps: float, out=None, residual=None, residual_out=Non
 
 
 def dsa_rmsnorm_backward_workspace_size(rows: int, cols: int) -> int:
+    _sizes(cols)
     return int(load_library().dsa_rmsnorm_backward_workspace_size(rows, cols))
 
 
@@ -390,6 +413,7 @@ def dsa_rmsnorm_backward(dy, h, weight, eps: float, dx, dweight, dres=None, work
         raise TypeError("h must be 2-D")
     cur, shape, wt = _device(), h.shape, _dtype_of(weight, "weight")
     rows, cols = shape
+    _sizes(cols)
     lib = _lib or load_library()
     a_dy, a_h, a_w = _at(dy, cur, "dy", t, shape), _at(h, cur, "h", t, shape), _at(weight, cur, "weight", wt, (cols,))
     a_e = None if dres is None else _at(dres, cur, "dres", t, shape)
@@ -413,6 +437,7 @@ def dsa_layernorm(x, weight, bias, eps: float, out=None, residual=None, residual
         raise TypeError("x must be 2-D")
     cur, shape, f32 = _device(), x.shape, torch.float32
     rows, cols = shape
+    _sizes(cols)
     wt = _dtype_of(weight, "weight")
     a_x, ldx = _at_rows(x, cur, "x", t, shape)
     a_r = a_h = a_o = a_c = a_s = a_b = None
@@ -437,6 +462,7 @@ def dsa_layernorm(x, weight, bias, eps: float, out=None, residual=None, residual
 
 
 def dsa_layernorm_backward_workspace_size(rows: int, cols: int) -> int:
+    _sizes(cols)
     return int(load_library().dsa_layernorm_backward_workspace_size(rows, cols))
 
 
@@ -452,6 +478,7 @@ def dsa_layernorm_backward(dy, h, weight, eps: float, dx, dweight, dbias=None, d
         raise TypeError("h must be 2-D")
     cur, shape, wt = _device(), h.shape, _dtype_of(weight, "weight")
     rows, cols = shape
+    _sizes(cols)
     lib = _lib or load_library()
     a_dy, a_h, a_w = _at(dy, cur, "dy", t, shape), _at(h, cur, "h", t, shape), _at(weight, cur, "weight", wt, (cols,))
     a_e = None if dres is None else _at(dres, cur, "dres", t, shape)
@@ -508,6 +535,7 @@ def dsa_gemm_fp8(a, a_scale, b, b_scale, out, stream=None):
         if not isinstance(t, torch.Tensor) or t.dim() != 2:
             raise TypeError(f"{name} must be a 2-D torch.Tensor")
     cur, (M, K), N, t = _device(), a.shape, b.shape[0], _dtype_of(out, "out")
+    _sizes(M, N, K)
     pieces, blocks = -(-K // 128), -(-N // 128)
     a_a, lda = _at_rows(a, cur, "a", u8, (M, K))
     a_b, ldb = _at_rows(b, cur, "b", u8, (N, K))
