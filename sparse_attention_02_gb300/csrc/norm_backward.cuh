@@ -134,7 +134,7 @@ __device__ __forceinline__ void layernorm_backward_row(const NormBackwardArgs &a
         sum = warp_sum(s2.sum());
         sg = warp_sum(t2.sum());
     }
-    const float mean = sum * n.inv_mine; // the warp's own
+    const float mean = n.mine.mean_by_parts(sum); // the warp's own
     s2 = t2 = F2(0.f);
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
@@ -167,16 +167,16 @@ __device__ __forceinline__ void layernorm_backward_row(const NormBackwardArgs &a
             to[0] = sum, to[32] = sq, to[64] = sg, to[96] = gd;
         }
         __syncthreads();
-        const bool is = n.other > 0.f;
+        const bool is = n.other.n > 0.f;
         const float its = is ? red[lane] : 0.f, its_g = is ? red[64 + lane] : 0.f;
-        const float all = warp_sum(its) * n.inv_all, dm = is ? its * n.inv_other - all : 0.f;
+        const float all = n.all.mean_by_parts(warp_sum(its)), dm = is ? n.other.mean_by_parts(its) - all : 0.f;
         sg = warp_sum(its_g);
-        sq = warp_sum(is ? red[32 + lane] + n.other * dm * dm : 0.f);
+        sq = warp_sum(is ? red[32 + lane] + n.other.n * dm * dm : 0.f);
         gd = warp_sum(is ? fmaf(dm, its_g, red[96 + lane]) : 0.f);
         off = mean - all;
     }
-    const float r = rsqrtf(sq * n.inv_all + a.eps);
-    const float k = gd * n.inv_all * r * r, mean_g = sg * n.inv_all; // k: mean(g xhat) r
+    const float r = rsqrtf(sq * n.all.inv + a.eps);
+    const float k = gd * n.all.inv * r * r, mean_g = sg * n.all.inv; // k: mean(g xhat) r
     if (!there)
         return;
     const F2 off2(off * r), r2(r), k2(-k), mg2(-mean_g * r);

@@ -83,7 +83,7 @@ __device__ __forceinline__ void norm_row(const NormArgs &a, const T *x, const T 
     if (LN) {
         // about the warp's own mean first, from the registers
         ss = warp_sum(ss);
-        float mean = mean_of(ss, n.mine, n.inv_mine);
+        float mean = n.mine.mean_by_remainder(ss);
         F2 sq2(0.f);
 #pragma unroll
         for (int c = 0; c < NV; ++c) {
@@ -106,13 +106,13 @@ __device__ __forceinline__ void norm_row(const NormArgs &a, const T *x, const T 
             }
             if (!meet())
                 return;
-            const bool is = n.other > 0.f;
+            const bool is = n.other.n > 0.f;
             ss = is ? moments[lane] : 0.f;
-            mean = mean_of(warp_sum(ss), n.all, n.inv_all);
-            const float d = mean_of(ss, n.other, n.inv_other) - mean;
-            sq = warp_sum(is ? moments[32 + lane] + n.other * d * d : 0.f);
+            mean = n.all.mean_by_remainder(warp_sum(ss));
+            const float d = n.other.mean_by_remainder(ss) - mean;
+            sq = warp_sum(is ? moments[32 + lane] + n.other.n * d * d : 0.f);
         }
-        const F2 r2(rsqrtf(sq * n.inv_all + a.eps)), back(-mean);
+        const F2 r2(rsqrtf(sq * n.all.inv + a.eps)), back(-mean);
 #pragma unroll
         for (int c = 0; c < NV; ++c) {
             float w[8], b[8] = {};
