@@ -19,7 +19,7 @@
 //
 // An SM has a row of 8192 columns at work at a time, so that a row's instructions are
 // what bytes wait for: arithmetic goes in pairs, counts are divided by once a call
-// (Count, rsqrtf), what lies past the columns is kept out by a chunk's offset instead of
+// (Count), the root taken by inv_sqrt, what lies past the columns is kept out by a chunk's offset instead of
 // a choice a value, and the ring's threads meet once a row instead of three times (all of
 // that 111 -> 99 us, and backward 116 -> 96).
 //

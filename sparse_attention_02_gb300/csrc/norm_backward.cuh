@@ -175,7 +175,7 @@ __device__ __forceinline__ void layernorm_backward_row(const NormBackwardArgs &a
         gd = warp_sum(is ? fmaf(dm, its_g, red[96 + lane]) : 0.f);
         off = mean - all;
     }
-    const float r = rsqrtf(sq * n.all.inv + a.eps);
+    const float r = inv_sqrt(sq * n.all.inv + a.eps);
     const float k = gd * n.all.inv * r * r, mean_g = sg * n.all.inv; // k: mean(g xhat) r
     if (!there)
         return;

@@ -112,7 +112,7 @@ __device__ __forceinline__ void norm_row(const NormArgs &a, const T *x, const T 
             const float d = n.other.mean_by_remainder(ss) - mean;
             sq = warp_sum(is ? moments[32 + lane] + n.other.n * d * d : 0.f);
         }
-        const F2 r2(rsqrtf(sq * n.all.inv + a.eps)), back(-mean);
+        const F2 r2(inv_sqrt(sq * n.all.inv + a.eps)), back(-mean);
 #pragma unroll
         for (int c = 0; c < NV; ++c) {
             float w[8], b[8] = {};

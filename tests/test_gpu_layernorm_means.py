@@ -39,3 +39,31 @@ def test_rows_of_one_short_value(rows, cols, t):
     mean, r = grad.mean(-1, keepdim=True), EPS ** -0.5
     ref, mag = r * (grad - mean), r * (grad.abs() + grad.abs().mean(-1, keepdim=True))
     R.check_close(dx, ref, ref.abs() * R.half_step(t) + steps(cols) * mag * (1 + R.half_step(t)), "dx")
+
+
+def test_the_root_is_rounded_once():
+    """Rows of 1 and -1 have variance 1 and give 1 / sqrt(1 + eps) itself: off by its rounding and little more."""
+    dsa = lib()
+    for cols in (2, 512):
+        x = torch.tensor([1.0, -1.0], device=DEV).repeat(cols // 2).expand(3, cols).contiguous()
+        w, out, dx, dw = torch.ones(cols, device=DEV), torch.empty_like(x), torch.empty_like(x), torch.empty(cols, device=DEV)
+        for eps in [float(e) for e in 4.0 ** (torch.rand(200, generator=torch.Generator().manual_seed(cols)) * 16 - 15)]:
+            v = torch.tensor(1.0) + torch.tensor(eps)  # as fp32 rounds it
+            ref = 1.0 / torch.sqrt(v.double())
+            dsa.dsa_layernorm(x, w, None, eps, out=out)
+            assert ((R.d(out).abs() - ref).abs() <= ref * R.FP32 * (1 + 2.0 ** -10)).all(), eps
+            dsa.dsa_layernorm_backward(x[:1], x[:1], w, eps, dx[:1], dw)  # dweight = dy xhat
+            assert ((R.d(dw) - ref).abs() <= ref * R.FP32 * (1 + 2.0 ** -10)).all(), eps
+
+
+def test_rows_whose_variance_ends_in_infinity_or_zero():
+    """1 / sqrt of what fp32 cannot hold: nothing of the row but the bias; of nothing, no number."""
+    dsa, inf = lib(), float("inf")
+    for cols in (2, 512, 8192):
+        x = torch.tensor([1.0, -1.0], device=DEV).repeat(cols // 2).expand(2, cols) * torch.tensor([[2.0 ** 70], [0.0]], device=DEV)
+        w, b, out = torch.ones(cols, device=DEV), torch.full((cols,), 0.5, device=DEV), torch.empty_like(x.contiguous())
+        dsa.dsa_layernorm(x.contiguous(), w, b, 0.0, out=out)
+        assert (out[0] == 0.5).all() and torch.isnan(out[1]).all()
+        tiny = x[:1].contiguous() * 2.0 ** -75 * 2.0 ** -75  # its squares are below fp32's smallest (2^-150 itself is 0 in fp32)
+        dsa.dsa_layernorm(tiny, w, b, 0.0, out=out[:1])
+        assert (out[0].abs() == inf).all()
