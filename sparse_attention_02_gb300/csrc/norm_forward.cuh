@@ -18,7 +18,8 @@ struct Meet {
 // One row: x and res (null: none) point at it, in global memory or a stage of the
 // ring.  A CTA's rows have a barrier between them (the RMS norm's ring), or there is but one.
 // RING (layer norm): held, of the weight and of the bias; meet, the threads' one meeting, after which the stage is not read;
-// there: whether this warp has a row.  moments: of this row, 64 floats.
+// there: whether this warp has a row, and its wait for the stage ended with it: nothing is written of a row that never came.
+// moments: of this row, 64 floats.
 template <typename T, typename W, int NV, bool WARP, bool VEC, bool LN, bool RING = false, typename M = Meet>
 __device__ __forceinline__ void norm_row(const NormArgs &a, const T *x, const T *res, int64_t row, float *red,
                                          [[maybe_unused]] float *moments = nullptr, [[maybe_unused]] const Counts &n = Counts(),
@@ -71,7 +72,7 @@ __device__ __forceinline__ void norm_row(const NormArgs &a, const T *x, const T 
     }
     // a tensor may be overwritten in place: each value is written by the
     // thread that read it
-    if (a.residual_out) {
+    if (a.residual_out && there) {
         T *ho = static_cast<T *>(a.residual_out) + row * a.ldh;
 #pragma unroll
         for (int c = 0; c < NV; ++c) {
@@ -234,7 +235,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, WARP ? 2 : 1)
         Held<T, W, NV, VEC> held[2];
         const Counts n = Counts::of<NV, WARP>(WARP ? 32 : blockDim.x, a.cols);
         int turn = -1; // before the first row
-        ring.template walk<true>(smem, status, [&](uint8_t *stage, int64_t row, auto meet) {
+        ring.template walk<true>(smem, status, [&](uint8_t *stage, int64_t row, bool came, auto meet) {
             if (turn < 0) { // not before the walk has waited for the kernel in front
                 const int G = WARP ? 32 : blockDim.x, g = WARP ? threadIdx.x & 31 : threadIdx.x;
                 held[0].load(static_cast<const W *>(a.weight), G, g, a.cols);
@@ -243,7 +244,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, WARP ? 2 : 1)
                 turn = 0;
             }
             norm_row<T, W, NV, WARP, VEC, true, true>(a, at(0, stage, row), a.residual ? at(1, stage, row) : nullptr, row + w, red,
-                                                      moments + 64 * turn, n, held, row + w < a.rows, meet);
+                                                      moments + 64 * turn, n, held, came && row + w < a.rows, meet);
             turn ^= 1;
         });
     } else {

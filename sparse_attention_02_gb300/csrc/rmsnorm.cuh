@@ -444,9 +444,9 @@ template <bool VEC> struct Ring {
     }
     // Walks the groups blockIdx.x, + gridDim.x, ...; row_fn(stage, first row) works on one with every thread of the CTA
     // and ends with its values in registers or written.  All threads meet before a stage is filled again.
-    // MEETS: row_fn(stage, first row, meet) calls meet() once, when it has read the stage, as the threads' one meeting in a
+    // MEETS: row_fn(stage, first row, came, meet) calls meet() once, when it has read the stage, as the threads' one meeting in a
     // row: the stage may be filled again, and what the threads wrote to shared memory before can be read.  Where that returns
-    // false the stage never came, and the walk ends.
+    // false the stage never came for one of them, and the walk ends; came says so of this thread, before the meeting.
     template <bool MEETS = false, typename F> __device__ __forceinline__ void walk(uint8_t *smem, unsigned *status, F &&row_fn) const
     {
         const uint32_t bar0 = smem_u32(smem);
@@ -475,7 +475,7 @@ template <bool VEC> struct Ring {
             };
             if constexpr (MEETS) {
                 bool all = false;
-                row_fn(data + st * stage_bytes(), row, [&] {
+                row_fn(data + st * stage_bytes(), row, ok, [&] {
                     all = __syncthreads_and(ok);
                     if (all)
                         fill();
