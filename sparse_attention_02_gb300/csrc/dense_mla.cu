@@ -866,7 +866,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 template <int HEADS>
 __global__ void __launch_bounds__(256) dense_mla_join_kernel(Params p)
 {
-    __shared__ float acc_s[8][kDv];
+    __shared__ __align__(16) float acc_s[8][kDv];
     __shared__ float sum_s[8];
     grid_dep_wait();
     grid_dep_launch();

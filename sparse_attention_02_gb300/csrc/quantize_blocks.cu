@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(16 * kTile / rows_a_thread<T>(), sizeof(T) == 
     constexpr int RPT = rows_a_thread<T>(), kThreads = kTile / RPT * 16, kWarps = kThreads / 32; // rows a thread
     using C = Chunk<T>;
     __shared__ __align__(16) uint8_t turned[kTile * kTile];
-    __shared__ float tops[BLOCK ? 1 : kWarps][BLOCK ? kWarps : kTile + 4];
+    __shared__ __align__(16) float tops[BLOCK ? 1 : kWarps][BLOCK ? kWarps : kTile + 4];
     __shared__ __align__(16) float col_scale[kTile], col_inv[kTile];
     grid_dep_wait();
     grid_dep_launch();

@@ -1,6 +1,9 @@
-"""What a kernel may write of a row whose copy never came, by the text of the sources: it does not show in a run that goes well."""
+"""What a kernel may write of a row whose copy never came, and how its shared memory is laid out, by the text of the sources:
+neither shows in a run that goes well."""
 import os
 import re
+
+import pytest
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "sparse_attention_02_gb300", "csrc")
 
@@ -37,3 +40,17 @@ def test_layer_norm_writes_no_row_that_never_came():
     assert "came && row + w < a.rows, meet)" in ring
     walk = body(source("rmsnorm.cuh"), "void walk(")
     assert re.search(r"const bool ok = mbar_wait\(", walk) and "row_fn(data + st * stage_bytes(), row, ok, [&]" in walk
+
+
+WORDS = {"float2": 8, "uint2": 8, "int2": 8, "float4": 16, "uint4": 16, "int4": 16, "uint64_t": 8, "double": 8}
+
+
+@pytest.mark.parametrize("name", sorted(f for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh"))))
+def test_shared_arrays_read_as_words_are_aligned_to_them(name):
+    """An array of floats is aligned to a float unless it says more: where it is read or written by wider words, it has to."""
+    text = source(name)
+    for m in re.finditer(r"__shared__\s+(?:__align__\((\d+)\)\s+)?(\w+)\s+([^;]*);", text):
+        align = int(m.group(1) or WORDS.get(m.group(2), 4))
+        for array in re.findall(r"(\w+)\s*\[\]", re.sub(r"\[[^\]]*\]", "[]", m.group(3)) + " "):
+            for word in re.findall(r"reinterpret_cast<(?:const\s+)?(\w+)\s*\*>\(\s*&?\s*" + array + r"\b", text):
+                assert WORDS.get(word, 4) <= align, f"{name}: {array} is aligned to {align} bytes and read as {word}"
