@@ -275,9 +275,11 @@ int dsa_gemm_fp8(const void *a, int64_t lda, const float *a_scale, const void *b
  *     h = x + residual (x when residual is NULL)
  *     y = (h - mean_c(h)) / sqrt(mean_c((h - mean)^2) + eps) * weight + bias
  * Tensors, types, strides, outputs, limits, aliasing and the FP8 form of y are those of
- * dsa_rmsnorm; bias [cols] is of `weight_dtype`, or NULL for none.  A row of
- * equal values with eps = 0 has no norm (NaN).  The variance is taken about the mean,
- * so a large common offset costs no more than its own rounding.
+ * dsa_rmsnorm; bias [cols] is of `weight_dtype`, or NULL for none.  The variance is
+ * taken about the mean, so a large common offset costs no more than the mean's own
+ * rounding: none for a row of equal values whose sum is exact in fp32 (bf16 values
+ * without a residual), which gives the bias, and with eps = 0 has no norm (NaN); else
+ * that of a sum in fp32, over sqrt(var + eps).
  */
 int dsa_layernorm(const void *x, int64_t ldx, const void *residual, int64_t ldr, const void *weight, const void *bias,
                   int64_t rows, int cols, int dtype, int weight_dtype, float eps,

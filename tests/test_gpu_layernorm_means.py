@@ -41,6 +41,28 @@ def test_rows_of_one_short_value(rows, cols, t):
     R.check_close(dx, ref, ref.abs() * R.half_step(t) + steps(cols) * mag * (1 + R.half_step(t)), "dx")
 
 
+@pytest.mark.parametrize("rows, cols", SHAPES)
+def test_rows_of_one_short_value_have_no_norm_without_eps(rows, cols):
+    dsa, g = lib(), gen(cols + 2)
+    x = short_values(rows, g).expand(rows, cols).contiguous().to(BF)
+    w, out = torch.ones(cols, dtype=BF, device=DEV), torch.zeros_like(x)
+    dsa.dsa_layernorm(x, w, None, 0.0, out=out)
+    assert torch.isnan(out).all()
+
+
+@pytest.mark.parametrize("rows, cols", SHAPES)
+def test_rows_of_one_long_value(rows, cols):
+    """Sums of fp32 values round, and the mean is off by as much: no more than that shows."""
+    dsa, g = lib(), gen(cols + 1)
+    v = torch.rand((rows, 1), generator=g, device=DEV) + 0.01
+    x = v.expand(rows, cols).contiguous()
+    w, b = torch.randn(cols, generator=g, device=DEV), torch.randn(cols, generator=g, device=DEV)
+    out = torch.empty_like(x)
+    dsa.dsa_layernorm(x, w, b, EPS, out=out)
+    xhat = steps(cols) * R.d(v) * EPS ** -0.5
+    R.check_close(out, R.d(b).expand(rows, cols), xhat * R.d(w).abs() * 1.01 + 3 * R.FP32 * R.d(b).abs(), "out")
+
+
 def test_the_root_is_rounded_once():
     """Rows of 1 and -1 have variance 1 and give 1 / sqrt(1 + eps) itself: off by its rounding and little more."""
     dsa = lib()
