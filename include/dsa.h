@@ -262,7 +262,10 @@ int dsa_quantize_fp8_blocks(const void *x, int64_t ldx, int64_t rows, int64_t co
  * Precision: the products of a piece are summed in fp32 by the tensor cores; the
  * pieces' sums are scaled and added in fp32, in an order fixed by the sizes and
  * the device: results repeat bit for bit.  A NaN code (or scale) makes NaN of its row's or column's
- * outputs and no others.
+ * outputs and no others.  A piece's two scales are multiplied first, in fp32: the product
+ * has to be 0, or at least 2^-126 and finite (as of scales of 0 and 2^-63 to 2^63).
+ * Beyond, it loses bits, is 0 or is infinite (NaN with a sum of 0), although the term
+ * itself may fit fp32.
  */
 int dsa_gemm_fp8(const void *a, int64_t lda, const float *a_scale, const void *b, int64_t ldb,
                  const float *b_scale, int b_block_rows, int M, int N, int K,
