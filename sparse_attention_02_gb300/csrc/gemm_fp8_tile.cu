@@ -9,17 +9,21 @@
 // a product more where b has a scale for every row.
 //
 // Bounds.  A piece of 128 x 256 takes the tensor pipe 512 cycles and the FP32 pipe 256.  What a step
-// of the loop takes is the way round: MMAs (512 and 150 until the sums are seen), 128 columns read in two
-// halves, as 64 are what a thread's registers hold beside its sums, and 200 until the next MMAs go
-// out; two buffers share that, 840 cycles a piece.  BN = 192 has registers for all of a
-// piece at once, but more pieces, and takes the product with a scale for every row of b.  Those scales
+// of the loop takes is longer: 840 cycles a piece.  A buffer's way round is MMAs (512 and 150 until the sums
+// are seen), 128 columns read in two halves, as 64 are what a thread's registers hold beside its sums, and 200
+// until the next MMAs go out, and two buffers (all of TMEM) share that.  A warp of sums in turn waits, reads,
+// waits and adds, piece by piece: with BN = 128, whose four buffers hide the way round, a piece still takes 660
+// cycles for 256 of the tensor pipe.  Which of the two holds BN = 256 is not measured apart.  BN = 192 has
+// registers for all of a piece at once, but more pieces, and takes the product with a scale for every row of
+// b.  Those scales
 // are read by quads of lanes, each of which holds pairs of columns of four rows: 20 words a thread and piece
 // instead of 64 (lanes of one row each, 4096 x 4096 over 8191: 198 us, 178 so; without the product of the two
 // scales 144; with scales by blocks 129).
 //
-// Measured: 8191 x 8192 x 8192 bf16 406 to 417 us in bursts, 2.7 PFLOP/s (143 % of
-// measured BF16), 461 to 470 call after call, where power limits the clock.  Without the
-// additions the same loop takes 375, without the loads 390.  Not kept: pairs of CTAs on one
+// Measured: 8191 x 8192 x 8192 bf16 461 to 474 us call after call, where power limits the
+// clock (by what the codes are: evenly spread ones 440), 396 to 417 in bursts, 2.7 PFLOP/s
+// (143 % of measured BF16).  Of 417, the same loop takes 375 without the additions and 390
+// without the loads.  Not kept: pairs of CTAs on one
 // tile (cta_group::2, 256 x 256: 468, words between CTAs in the way round; in halves of 128
 // columns with four buffers 655: more meetings), 16 warps of 64 columns (500, registers
 // spill), the first columns of the next piece asked for among the additions (486: the

@@ -19,14 +19,18 @@
 //
 // An SM has a row of 8192 columns at work at a time, so that a row's instructions are
 // what bytes wait for: arithmetic goes in pairs, counts are divided by once a call
-// (Count), the root taken by inv_sqrt, what lies past the columns is kept out by a chunk's offset instead of
-// a choice a value, and the ring's threads meet once a row instead of three times (all of
-// that 111 -> 99 us, and backward 116 -> 96).
+// (Count), the root costs a Newton step (inv_sqrt), what lies past the columns is kept out
+// by a chunk's offset instead of a choice a value, and the ring's threads meet once a row
+// instead of three times (all of that 111 -> 99 us, and backward 116 -> 96).
 //
 // Measured: 8191 x 8192 bf16, residual, both outputs, block codes 99 us (90 % of
-// measured HBM; the RMS norm 96); without residual and codes 46 (86 %).  64 x 128 3.2 us.
+// measured HBM; the RMS norm 96); without residual and codes 46 (86 %).  64 x 128 3.1 us.
+// Rows off 16 bytes are bound by 2-byte accesses: 9000 x 8191 100 us without and 145 with
+// residual (43 and 60 %), 253 with block codes too (39 %).
 // Backward of 8192 x 8192 with dres 96 us (82 %): its two sums a column leave room for
 // one CTA of 512 threads an SM, and what a row's meeting takes is not hidden by another's.
+// Beyond 8192 columns four chunks a thread and their sums do not fit its 128 registers, and
+// spill: 2048 x 16384 102 us bf16 (39 %), 184 fp32 (43 %).
 // Not kept there: two rows at once (146, spills), more stages (118 of 116 then), dres read before
 // the meeting for the ring's single one (115, but 16384 x 2048 56 -> 60: registers).
 // 32767 x 128 fp32 backward 13.5 us (4 to 5 of them the sums' own launch), two rows a

@@ -25,9 +25,10 @@
 //
 // Measured: 8191 x 8192 bf16 with its transpose 56 us (70 % of measured HBM; 84 with
 // every lane working out its rows' scales and shared words unpacked once a use), four
-// CTAs an SM (three 65, five 73: registers spill), 4096 x 7168 fp32 by blocks both ways 32 us
+// CTAs an SM, whose 64 registers a thread hold all but the division path, which spills
+// (three CTAs 65, five 73), 4096 x 7168 fp32 by blocks both ways 32 us
 // (80 %; three CTAs of 512 threads 71), 8192 x 8192 without the transpose bf16 39 us (77 %)
-// and fp32 55 (90 %), 64 x 4096 1.6: 17 instructions a value both ways in bf16, 60 % of an
+// and fp32 55 (90 %), the transpose alone 42 (72 %) and 63 (79 %), 64 x 4096 1.6: 17 instructions a value both ways in bf16, 60 % of an
 // SM's slots, are what bytes wait for there.
 #include "rmsnorm.cuh"
 
