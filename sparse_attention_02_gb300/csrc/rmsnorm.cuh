@@ -351,13 +351,13 @@ struct Counts {
     }
 };
 
-// 1 / sqrt(v), off by hardly more than its rounding: rsqrtf, up to 2 ulp off, and one of Newton's steps, r + r (1 - v r^2) / 2 with
-// r^2 in two parts.  0, infinity and NaN, whose residual is NaN, keep rsqrtf's result.  1 / sqrtf(v) is further off, and took the
-// backward of 8192 x 8192 from 95 to 108 us; this 96.
+// 1 / sqrt(v), off by hardly more than its rounding: rsqrtf, up to 2 ulp off, and one of Newton's steps, r + r (1 - v r r) / 2
+// with v r (which neither over- nor underflows) in two parts.  0, infinity and NaN, whose residual is NaN, keep rsqrtf's
+// result.  1 / sqrtf(v) is further off, and took the backward of 8192 x 8192 from 95 to 108 us; this 96.
 __device__ __forceinline__ float inv_sqrt(float v)
 {
-    const float r = rsqrtf(v), h = 0.5f * v, q = r * r;
-    return fmaf(r, fminf(fmaf(-h, fmaf(r, r, -q), fmaf(-h, q, 0.5f)), 1.f), r); // fminf drops a NaN
+    const float r = rsqrtf(v), q = v * r;
+    return fmaf(0.5f * r, fminf(fmaf(-fmaf(v, r, -q), r, fmaf(-q, r, 1.f)), 1.f), r); // fminf drops a NaN
 }
 
 constexpr int kMoments = 4 * 32; // floats that a meeting takes, at most; the next of the same CTA takes others

@@ -89,3 +89,16 @@ def test_rows_whose_variance_ends_in_infinity_or_zero():
         tiny = x[:1].contiguous() * 2.0 ** -75 * 2.0 ** -75  # its squares are below fp32's smallest (2^-150 itself is 0 in fp32)
         dsa.dsa_layernorm(tiny, w, b, 0.0, out=out[:1])
         assert (out[0].abs() == inf).all()
+
+
+def test_the_root_of_the_smallest_and_largest_variances():
+    """Rows of 2^k and -2^k: their variance is 4^k, below fp32's normal numbers and up to its largest."""
+    dsa = lib()
+    for cols in (2, 512, 8192):
+        x = torch.tensor([1.0, -1.0], device=DEV).repeat(cols // 2).expand(127, cols) * torch.exp2(torch.arange(-74, 53, device=DEV))[:, None]
+        x = x.contiguous()
+        w, out, dx, dw = torch.ones(cols, device=DEV), torch.empty_like(x), torch.empty_like(x), torch.empty(cols, device=DEV)
+        dsa.dsa_layernorm(x, w, None, 0.0, out=out)
+        assert torch.equal(out, x.sign())
+        dsa.dsa_layernorm_backward(torch.ones_like(x), x, w, 0.0, dx, dw)
+        assert torch.equal(dw, 127 * x[0].sign())
