@@ -59,7 +59,7 @@ class _Int:
 
     @staticmethod
     def from_param(v):
-        if type(v) is int:
+        if isinstance(v, int):
             if -0x80000000 <= v <= 0x7FFFFFFF:
                 return v
             raise OverflowError(f"{v} is more than the library's int holds")
